@@ -527,6 +527,153 @@ tv_status tv_tree_attention(int32_t B, int32_t total_nodes, int32_t max_nodes, i
                             size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
+ * tv_qcache_* -- a KV cache of the attention layers held in 4 bits, in pages.
+ *
+ * The attention layers of a hybrid model keep a KV cache beside the recurrent
+ * layers' states (Bole summary page, "Why existing tree speculation fails on hybrid
+ * models": all branches share the prefix's KV and each adds only its own).  These
+ * calls keep it quantised: tv_qcache_write stores new rows (a prompt or a chunk of
+ * one), tv_qcache_commit the accepted path's rows after a verification (the attention
+ * layers' counterpart of tv_commit), tv_qcache_read gives positions back as bf16 and
+ * tv_qcache_attention attends over it.
+ *
+ * Format.  A page holds TV_QCACHE_PAGE positions of one request; the cache is
+ * [num_pages][Hkv] records, one per (page, KV head), of tv_qcache_bytes(1, 1, d)
+ * contiguous bytes:
+ *     K codes   [d/32][64][16 B]   the 32 channels of a group at one position
+ *     K scales  [64][d/32]
+ *     V codes   [2][d][16 B]       32 positions (a half page) of one channel
+ *     V scales  [d/32][64]
+ * TV_QCACHE_GROUP channels of a position share a scale byte b: s = (8 + b % 8) *
+ * 2^(b / 8 - 25) for b < 255 (so 2^-22 .. 896); b = 255 marks a group that holds a NaN
+ * and reads back as NaN.  A value is s * (c - 8) with its code c in 1..15.  The 32
+ * codes of 16 bytes fill four little-endian 32-bit words of 8 elements, element 2p of
+ * a word in its nibble p and element 2p + 1 in nibble p + 4.
+ * Quantising: s = (largest |x| of the group) / 7 rounded to four significant bits
+ * (ties to even) and clamped to the range above; c = 8 + sign(x) * min(7, |x| / s
+ * rounded, halves away from zero).  A value is at most s / 2 off, unless it is beyond
+ * 7.5 * 896 = 6720, infinities included, and saturates at 6272.  Every value is exact
+ * in bf16.  Unlike a cache of bf16 a position takes 17/64 of the bytes.
+ *
+ * Pages.  page_table [B][max_pages] int32 (device): page_table[b][p] is the page that
+ * holds request b's positions 64 p .. 64 p + 63.  Only the entries of positions that
+ * a call touches are read; the others may hold anything.  Pages may be shared between
+ * requests that only read them; a page being written belongs to one request.  Cache
+ * and page table are caller memory, 16-byte aligned; new pages need no clearing.
+ */
+#define TV_QCACHE_PAGE 64
+#define TV_QCACHE_GROUP 32
+
+/* Bytes of a cache of num_pages pages (0 for invalid sizes); d is 64 or 128. */
+size_t tv_qcache_bytes(int32_t num_pages, int32_t Hkv, int32_t d);
+
+/*
+ * tv_qcache_write -- quantise new rows into the cache.
+ *   B, total_rows (R)   requests, and rows in all
+ *   Hkv, d              KV heads and head width (64 or 128)
+ *   num_pages, max_pages  pages in the cache, and the row length of page_table
+ *   row_offsets [B+1]   int32 (device): rows row_offsets[b] .. row_offsets[b+1]-1 are
+ *                       request b's, like node_offsets
+ *   start [B]           int32 (device): the position of request b's first row
+ *   page_table          see above
+ *   k, v                bf16 rows: row r, head h, channel c at k[r * row_stride +
+ *                       h * d + c]; row_stride >= Hkv * d, a multiple of 8 (so rows
+ *                       may be views into a fused projection)
+ *   cache               the cache; positions that are not written keep their values
+ * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for sizes out of range
+ * (row_stride too); TV_ERR_UNSUPPORTED for d not in {64, 128}.  Device-detected errors:
+ * unusable row_offsets give TV_ERR_TREE and rows that do not fit into [0, 64 *
+ * max_pages) or a page outside [0, num_pages) give TV_ERR_SHAPE; the rows concerned
+ * are not written (with unusable offsets also rows of other requests may be left out).
+ */
+tv_status tv_qcache_write(int32_t B, int32_t total_rows, int32_t Hkv, int32_t d,
+                          int32_t num_pages, int32_t max_pages, const int32_t *row_offsets,
+                          const int32_t *start, const int32_t *page_table, const void *k,
+                          const void *v, int64_t row_stride, void *cache, int32_t *dev_status,
+                          void *stream);
+
+/*
+ * tv_qcache_commit -- the accepted path's keys and values into the cache.
+ * Row m of request b's path (node path[b][m] of its tree, m < accept_len[b]) is
+ * quantised into position ctx_len[b] + m, and new_len[b] = ctx_len[b] + accept_len[b].
+ *   node_offsets [B+1]; path [B][max_depth], accept_len [B]   as tv_accept_greedy
+ *                       wrote them
+ *   ctx_len [B]         int32 (device): committed positions before the step
+ *   k_tree, v_tree      bf16 rows of the tree nodes, strided as in tv_qcache_write
+ *   new_len [B]         int32 out; may be ctx_len itself (the lengths advance in place)
+ *   other arguments as in tv_qcache_write
+ * Device-detected errors: bad offsets, an accept_len outside [0, max_depth] or a path
+ * entry outside the tree give TV_ERR_TREE; a length that leaves [0, 64 * max_pages] or
+ * a page outside [0, num_pages) gives TV_ERR_SHAPE.  Such a request commits nothing:
+ * its cache is untouched and new_len[b] = ctx_len[b].
+ */
+tv_status tv_qcache_commit(int32_t B, int32_t total_nodes, int32_t max_nodes, int32_t max_depth,
+                           int32_t Hkv, int32_t d, int32_t num_pages, int32_t max_pages,
+                           const int32_t *node_offsets, const int32_t *path,
+                           const int32_t *accept_len, const int32_t *ctx_len,
+                           const int32_t *page_table, const void *k_tree, const void *v_tree,
+                           int64_t row_stride, void *cache, int32_t *new_len,
+                           int32_t *dev_status, void *stream);
+
+/*
+ * tv_qcache_read -- positions of the cache as bf16 rows.
+ * Row r of request b (r counted from row_offsets[b]) is position start[b] + r; a row at
+ * or past ctx_len[b] is written as zeros, without its page being looked up.
+ *   k, v    out: bf16 rows, strided as in tv_qcache_write
+ *   other arguments as in tv_qcache_write
+ * Errors as tv_qcache_write; rows of a page outside [0, num_pages), or of a request
+ * whose rows or ctx_len leave [0, 64 * max_pages], are written as zeros.
+ */
+tv_status tv_qcache_read(int32_t B, int32_t total_rows, int32_t Hkv, int32_t d,
+                         int32_t num_pages, int32_t max_pages, const int32_t *row_offsets,
+                         const int32_t *start, const int32_t *ctx_len, const int32_t *page_table,
+                         const void *cache, void *k, void *v, int64_t row_stride,
+                         int32_t *dev_status, void *stream);
+
+/*
+ * tv_qcache_attention -- tv_tree_attention over the 4-bit cache, with an optional
+ * sliding window and first positions that stay visible (sinks).
+ * Node i at depth n (1 for a child of the context) stands at position ctx_len[b] + n - 1.
+ * With window W > 0 it sees the W positions that end with its own, and the positions
+ * below `sinks`; with W = 0 all of them.  Query row (i, h) attends to the cached
+ * positions below ctx_len[b] and the nodes of i's root path (i included) that it sees:
+ *     out[i][h] = sum_j softmax_j(scale * q[i][h] . k_j) v_j.
+ * A step of plain decoding is a tree of one node.
+ *
+ *   B, total_nodes (T), max_nodes, H, Hkv, d, node_offsets, parent, ctx_len, scale
+ *              as in tv_tree_attention, and H / Hkv any number from 1 to 128
+ *   num_pages, max_pages, page_table, cache   as in tv_qcache_write; entries of pages
+ *              without a visible position are not read (they may have been given up)
+ *   window, sinks   >= 0; sinks has no effect without a window
+ *   q          bf16 rows: node i, head h, channel c at q[i * q_stride + h * d + c];
+ *              q_stride >= H * d, a multiple of 8
+ *   k_tree, v_tree   bf16 rows of the tree nodes, strided by kv_stride as in
+ *              tv_qcache_write
+ *   out_dtype  TV_BF16 or TV_F32: the type of out [T][H][d]
+ *   workspace  device memory, 16-byte aligned, of at least
+ *              tv_qcache_attention_workspace_bytes bytes (scratch: partial results of
+ *              contexts that are shared out over several CTAs)
+ * Arithmetic: cache values are exact in bf16; scores, softmax sums and outputs
+ * accumulate in fp32; softmax weights enter the value sums as a bf16 hi + lo pair.
+ * Positions that a request's nodes do not see may hold anything; a NaN or an infinity
+ * in one that some of them see may reach the outputs of the request's other rows.
+ * Host errors: as tv_tree_attention, plus TV_ERR_DTYPE for out_dtype, TV_ERR_NULL for a
+ * missing and TV_ERR_SHAPE for a small workspace, TV_ERR_SHAPE for the strides, pages,
+ * window and sinks.  Device-detected errors: as tv_tree_attention; a page outside
+ * [0, num_pages) gives TV_ERR_SHAPE and zero rows for that request.
+ */
+size_t tv_qcache_attention_workspace_bytes(int32_t B, int32_t total_nodes, int32_t max_nodes,
+                                           int32_t H, int32_t Hkv, int32_t d, int32_t max_pages);
+tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes, int32_t H,
+                              int32_t Hkv, int32_t d, int32_t num_pages, int32_t max_pages,
+                              const int32_t *node_offsets, const int32_t *parent,
+                              const int32_t *ctx_len, const int32_t *page_table, int32_t window,
+                              int32_t sinks, const void *q, int64_t q_stride, const void *cache,
+                              const void *k_tree, const void *v_tree, int64_t kv_stride,
+                              float scale, int32_t out_dtype, void *out, void *workspace,
+                              size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
  * tv_verify_variant -- the kernel tv_verify (TV_VARIANT_AUTO) would launch for
  * this problem: TV_VARIANT_TC_STREAM, TV_VARIANT_TC, TV_VARIANT_TC_TILED (trees too
  * large for TV_VARIANT_TC's shared-memory plan, and per-channel decay trees of 64

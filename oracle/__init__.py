@@ -12,7 +12,8 @@ against), the greedy acceptance walk (LLM Primer VI ch. 9, §9.1) and the
 commit of the accepted path's state (Bole §2).  This file builds the C source,
 marshals arrays and splits work over threads; the functions for the wider rows
 of the path are plain numpy here: the argmax of logits rows, best-first tree
-construction, stochastic acceptance and tree-masked softmax attention.
+construction, stochastic acceptance, tree-masked softmax attention and the 4-bit KV
+cache (its quantiser, its records, windowed attention over it).
 
 Parity pins for each function are in ``tests/test_oracle_pins.py``.
 """
@@ -455,6 +456,121 @@ def tree_attention(node_offsets, parent, q, k_cache, v_cache, ctx_len, k_tree, v
             W = W / W.sum(axis=1, keepdims=True)
             out[s:e, h] = W @ V
     return out
+
+
+QCACHE_PAGE, QCACHE_GROUP = 64, 32
+
+
+def qcache_quantise(x):
+    """Codes (1..15) and scale bytes of rows x [..., d], groups of 32 channels: the step
+    is (largest |x|) / 7 rounded to four significant bits, ties to even, clamped to
+    [2^-22, 1.75 * 2^9]; the code is 8 + |x| / step rounded with halves away from zero,
+    at most 7, with x's sign.  A group with a NaN gets scale byte 255 and codes 8.
+    Doubles: both quotients are exact wherever a rounding has a tie."""
+    x = np.asarray(x, dtype=np.float64)
+    g = x.reshape(x.shape[:-1] + (-1, QCACHE_GROUP))
+    top = np.abs(g).max(axis=-1)
+    nan = np.isnan(top)
+    top = np.where(nan, 0.0, top)
+    m, e = np.frexp(np.minimum(top, 1e6) / 7.0)             # m in [0.5, 1), or 0
+    step = np.clip(np.ldexp(np.rint(m * 16.0), e - 4), 2.0 ** -22, 1.75 * 2.0 ** 9)
+    m, e = np.frexp(step)                                   # step = (8 + low) 2^(E - 25)
+    byte = ((e - 1 + 22) * 8 + (m * 16.0 - 8.0).astype(np.int64)).astype(np.int64)
+    with np.errstate(invalid="ignore"):
+        r = np.abs(np.where(nan[..., None], 0.0, g)) / step[..., None]
+    n = np.minimum(np.floor(r + 0.5), 7.0)
+    code = (8 + np.where(g < 0, -n, n)).astype(np.uint8)
+    return code.reshape(x.shape), np.where(nan, 255, byte).astype(np.uint8)
+
+
+def qcache_values(code, byte):
+    """Values (fp64) of codes [..., d] and scale bytes [..., d / 32]."""
+    byte = np.asarray(byte).astype(np.int64)
+    step = np.ldexp((8 + byte % 8).astype(np.float64), byte // 8 - 25)
+    step = np.where(byte == 255, np.nan, step)
+    c = np.asarray(code).astype(np.float64) - 8.0
+    return c * np.repeat(step, QCACHE_GROUP, axis=-1)
+
+
+def _qcache_places(d):
+    """For element (position p, channel c) of a record: byte and shift of its K code and
+    its V code, and the bytes of its two scales."""
+    G = d // QCACHE_GROUP
+    codes, scales = QCACHE_PAGE * d // 2, QCACHE_PAGE * G
+    p, c = np.meshgrid(np.arange(QCACHE_PAGE), np.arange(d), indexing="ij")
+
+    def nibble(e):  # element e of 32 in a 16-byte line
+        n = (e % 8) // 2 + 4 * (e % 2)
+        return (e // 8) * 4 + n // 2, 4 * (n % 2)
+
+    kb, ks = nibble(c % 32)
+    vb, vs = nibble(p % 32)
+    k_at = ((c // 32) * QCACHE_PAGE + p) * 16 + kb
+    v_at = codes + scales + ((p // 32) * d + c) * 16 + vb
+    ps, gs = np.meshgrid(np.arange(QCACHE_PAGE), np.arange(G), indexing="ij")
+    k_sc = codes + ps * G + gs
+    v_sc = 2 * codes + scales + gs * QCACHE_PAGE + ps
+    return k_at, ks, v_at, vs, k_sc, v_sc
+
+
+def qcache_put(record, d, p, k, v):
+    """Row k, v [d] at place p of one record (uint8, changed in place)."""
+    k_at, ks, v_at, vs, k_sc, v_sc = _qcache_places(d)
+    for x, at, sh, sc in ((k, k_at, ks, k_sc), (v, v_at, vs, v_sc)):
+        code, byte = qcache_quantise(x)
+        for c in range(d):
+            i, s = at[p, c], int(sh[p, c])
+            record[i] = (int(record[i]) & ~(15 << s) & 255) | (int(code[c]) << s)
+        record[sc[p]] = byte
+
+
+def qcache_get(records, d):
+    """K, V values (fp64 [..., 64, d]) of records [..., bytes]."""
+    k_at, ks, v_at, vs, k_sc, v_sc = _qcache_places(d)
+    r = np.asarray(records)
+    return (qcache_values((r[..., k_at] >> ks) & 15, r[..., k_sc]),
+            qcache_values((r[..., v_at] >> vs) & 15, r[..., v_sc]))
+
+
+def qcache_attention(node_offsets, parent, q, k_cache, v_cache, ctx_len, k_tree, v_tree,
+                     scale: float, window: int = 0, sinks: int = 0, bounds: bool = False):
+    """tree_attention with a sliding window and sinks: node i at depth n stands at position
+    ctx_len + n - 1 and, with window > 0, sees the `window` positions that end with its
+    own and those below `sinks` (among its context and its root path).  Arguments as
+    tree_attention, the cache as values; invisible keys and values are left out of the
+    arithmetic, so whatever they hold does not matter.  With bounds=True also returns,
+    per row, the largest scale * sum_c |q_c k_c| of a visible key, the largest visible
+    |v| of any channel and the number of visible keys."""
+    q, kt, vt = (np.asarray(x, dtype=np.float64) for x in (q, k_tree, v_tree))
+    T, H, d = q.shape
+    Hkv = kt.shape[1]
+    grp = H // Hkv
+    out = np.zeros((T, H, d))
+    smax, vmax, count = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
+    for b in range(len(ctx_len)):
+        s, e, L = int(node_offsets[b]), int(node_offsets[b + 1]), int(ctx_len[b])
+        for i in range(e - s):
+            path, j = [], i
+            while j >= 0:
+                path.append(j)
+                j = int(parent[s + j])
+            path.reverse()
+            me = L + len(path) - 1
+            see = lambda pos: window == 0 or me - window < pos <= me or pos < sinks  # noqa: E731
+            ctx = [pos for pos in range(L) if see(pos)] if window else slice(0, L)
+            on = [s + t for depth, t in enumerate(path) if see(L + depth)]
+            for kv in range(Hkv):
+                K = np.concatenate([k_cache[b, kv][ctx], kt[on, kv]], axis=0)
+                V = np.concatenate([v_cache[b, kv][ctx], vt[on, kv]], axis=0)
+                hs = slice(kv * grp, (kv + 1) * grp)
+                S = scale * (q[s + i, hs] @ K.T)
+                W = np.exp(S - S.max(axis=1, keepdims=True))
+                out[s + i, hs] = (W @ V) / W.sum(axis=1, keepdims=True)
+                if bounds:
+                    smax[s + i, hs] = scale * (np.abs(q[s + i, hs]) @ np.abs(K).T).max(axis=1)
+                    vmax[s + i, hs] = np.abs(V).max()
+                    count[s + i, hs] = len(K)
+    return (out, smax, vmax, count) if bounds else out
 
 
 def commit(batch, accept_len, path, units: Optional[Sequence[int]] = None, threads: int = 1,

@@ -12,6 +12,10 @@ include/treeverify.h; this package is the ctypes binding):
 * ``tv_accept_stochastic`` acceptance by min(1, p/q) with residual resampling
 * ``tv_tree_attention`` tree-masked softmax attention over a shared-prefix KV cache
   (the attention layers of a hybrid model)
+* ``tv_qcache_write``, ``tv_qcache_commit``, ``tv_qcache_read`` a paged KV cache in
+  4 bits: rows or an accepted path quantised into it, positions read back
+* ``tv_qcache_attention`` tree attention over that cache, with an optional sliding
+  window and sinks
 * ``tv_verify_serial``  the naive node-by-node verification with per-node states
   (a baseline for the closed form)
 * ``tv_commit_verify`` the previous step's commit applied to the state in place,
@@ -28,6 +32,8 @@ from .binding import (  # noqa: F401
     tv_accept_commit_verify,
     tv_verify_serial, tv_verify_serial_workspace_bytes, tv_verify_serial_static, tv_build_tree,
     tv_accept_stochastic, tv_tree_attention, tv_tree_attention_workspace_bytes,
+    tv_qcache_bytes, tv_qcache_write, tv_qcache_commit, tv_qcache_read, tv_qcache_attention,
+    tv_qcache_attention_workspace_bytes, TV_QCACHE_PAGE, TV_QCACHE_GROUP,
     TV_SERIAL_STATIC_BYTES,
     tv_problem, tv_status_string, tv_verify, tv_verify_variant, tv_verify_supports, tv_version, EXPORTED,
     TV_OK, TV_ERR_NULL, TV_ERR_SHAPE, TV_ERR_DTYPE, TV_ERR_ALIGN, TV_ERR_UNSUPPORTED,

@@ -28,6 +28,7 @@ TV_VARIANT_TC_TILED = 4
 TV_VARIANT_TEST_EXPIRE_WAIT = 0x100
 TV_MAX_NODES, TV_MAX_DEPTH, TV_MAX_DIM = 256, 32, 256
 TV_SERIAL_STATIC_BYTES = 16 << 20
+TV_QCACHE_PAGE, TV_QCACHE_GROUP = 64, 32
 
 EXPORTED = ("tv_verify", "tv_verify_ex", "tv_verify_variant", "tv_verify_supports",
             "tv_workspace_bytes",
@@ -36,6 +37,8 @@ EXPORTED = ("tv_verify", "tv_verify_ex", "tv_verify_variant", "tv_verify_support
             "tv_accept_greedy_logits", "tv_verify_serial",
             "tv_verify_serial_workspace_bytes", "tv_verify_serial_static", "tv_build_tree",
             "tv_accept_stochastic", "tv_tree_attention", "tv_tree_attention_workspace_bytes",
+            "tv_qcache_bytes", "tv_qcache_write", "tv_qcache_commit", "tv_qcache_read",
+            "tv_qcache_attention", "tv_qcache_attention_workspace_bytes",
             "tv_status_string", "tv_version")
 
 
@@ -96,6 +99,16 @@ def load(path: Optional[str] = None):
                                                                 ctypes.c_size_t, vp, vp])
         L.tv_tree_attention_workspace_bytes.argtypes = [i32] * 7
         L.tv_tree_attention_workspace_bytes.restype = ctypes.c_size_t
+        i64, size = ctypes.c_int64, ctypes.c_size_t
+        L.tv_qcache_bytes.argtypes = [i32] * 3
+        L.tv_qcache_bytes.restype = size
+        L.tv_qcache_write.argtypes = [i32] * 6 + [vp] * 5 + [i64] + [vp] * 3
+        L.tv_qcache_commit.argtypes = [i32] * 8 + [vp] * 7 + [i64] + [vp] * 4
+        L.tv_qcache_read.argtypes = [i32] * 6 + [vp] * 7 + [i64] + [vp] * 2
+        L.tv_qcache_attention_workspace_bytes.argtypes = [i32] * 7
+        L.tv_qcache_attention_workspace_bytes.restype = size
+        L.tv_qcache_attention.argtypes = ([i32] * 8 + [vp] * 4 + [i32] * 2 + [vp, i64] + [vp] * 3 +
+                                          [i64, ctypes.c_float, i32, vp, vp, size, vp, vp])
         L.tv_verify_serial_workspace_bytes.argtypes = [P]
         L.tv_verify_serial_workspace_bytes.restype = ctypes.c_size_t
         L.tv_workspace_bytes.argtypes = [P]
@@ -104,7 +117,8 @@ def load(path: Optional[str] = None):
                   L.tv_accept_commit, L.tv_commit_verify, L.tv_accept_commit_verify,
                   L.tv_accept_greedy_logits,
                   L.tv_verify_serial, L.tv_verify_serial_static, L.tv_build_tree,
-                  L.tv_accept_stochastic, L.tv_tree_attention):
+                  L.tv_accept_stochastic, L.tv_tree_attention, L.tv_qcache_write,
+                  L.tv_qcache_commit, L.tv_qcache_read, L.tv_qcache_attention):
             f.restype = ctypes.c_int32
         L.tv_status_string.argtypes = [i32]
         L.tv_status_string.restype = ctypes.c_char_p
@@ -232,6 +246,63 @@ def tv_tree_attention(B, total_nodes, max_nodes, H, Hkv, d, P, node_offsets, par
                                   _ptr(v_tree), float(scale), _ptr(out), _ptr(workspace),
                                   int(workspace_bytes), _ptr(dev_status), _stream(stream))
     return _check(rc, "tv_tree_attention", check)
+
+
+def tv_qcache_bytes(num_pages, Hkv, d) -> int:
+    """Bytes of a 4-bit KV cache of num_pages pages (0 for invalid sizes)."""
+    return int(load().tv_qcache_bytes(int(num_pages), int(Hkv), int(d)))
+
+
+def tv_qcache_write(B, total_rows, Hkv, d, num_pages, max_pages, row_offsets, start, page_table, k,
+                    v, row_stride, cache, dev_status, stream=None, check: bool = True) -> int:
+    rc = load().tv_qcache_write(int(B), int(total_rows), int(Hkv), int(d), int(num_pages),
+                                int(max_pages), _ptr(row_offsets), _ptr(start), _ptr(page_table),
+                                _ptr(k), _ptr(v), int(row_stride), _ptr(cache), _ptr(dev_status),
+                                _stream(stream))
+    return _check(rc, "tv_qcache_write", check)
+
+
+def tv_qcache_commit(B, total_nodes, max_nodes, max_depth, Hkv, d, num_pages, max_pages,
+                     node_offsets, path, accept_len, ctx_len, page_table, k_tree, v_tree,
+                     row_stride, cache, new_len, dev_status, stream=None,
+                     check: bool = True) -> int:
+    rc = load().tv_qcache_commit(int(B), int(total_nodes), int(max_nodes), int(max_depth),
+                                 int(Hkv), int(d), int(num_pages), int(max_pages),
+                                 _ptr(node_offsets), _ptr(path), _ptr(accept_len), _ptr(ctx_len),
+                                 _ptr(page_table), _ptr(k_tree), _ptr(v_tree), int(row_stride),
+                                 _ptr(cache), _ptr(new_len), _ptr(dev_status), _stream(stream))
+    return _check(rc, "tv_qcache_commit", check)
+
+
+def tv_qcache_read(B, total_rows, Hkv, d, num_pages, max_pages, row_offsets, start, ctx_len,
+                   page_table, cache, k, v, row_stride, dev_status, stream=None,
+                   check: bool = True) -> int:
+    rc = load().tv_qcache_read(int(B), int(total_rows), int(Hkv), int(d), int(num_pages),
+                               int(max_pages), _ptr(row_offsets), _ptr(start), _ptr(ctx_len),
+                               _ptr(page_table), _ptr(cache), _ptr(k), _ptr(v), int(row_stride),
+                               _ptr(dev_status), _stream(stream))
+    return _check(rc, "tv_qcache_read", check)
+
+
+def tv_qcache_attention_workspace_bytes(B, total_nodes, max_nodes, H, Hkv, d, max_pages) -> int:
+    return int(load().tv_qcache_attention_workspace_bytes(int(B), int(total_nodes),
+                                                          int(max_nodes), int(H), int(Hkv),
+                                                          int(d), int(max_pages)))
+
+
+def tv_qcache_attention(B, total_nodes, max_nodes, H, Hkv, d, num_pages, max_pages, node_offsets,
+                        parent, ctx_len, page_table, window, sinks, q, q_stride, cache, k_tree,
+                        v_tree, kv_stride, scale, out_dtype, out, workspace=None,
+                        workspace_bytes=0, dev_status=None, stream=None,
+                        check: bool = True) -> int:
+    rc = load().tv_qcache_attention(int(B), int(total_nodes), int(max_nodes), int(H), int(Hkv),
+                                    int(d), int(num_pages), int(max_pages), _ptr(node_offsets),
+                                    _ptr(parent), _ptr(ctx_len), _ptr(page_table), int(window),
+                                    int(sinks), _ptr(q), int(q_stride), _ptr(cache),
+                                    _ptr(k_tree), _ptr(v_tree), int(kv_stride), float(scale),
+                                    int(out_dtype), _ptr(out), _ptr(workspace),
+                                    int(workspace_bytes), _ptr(dev_status), _stream(stream))
+    return _check(rc, "tv_qcache_attention", check)
 
 
 def tv_build_tree(B, C, depth_cap, n, marginals, cost, parent, token, rho, count, stream=None,

@@ -564,3 +564,169 @@ tv_status tv_accept_commit_verify(const tv_problem *p, const tv_pending *prev,
 }
 
 }  // extern "C"
+
+namespace {
+
+tv_status qcache_dims(int32_t B, int32_t rows, int32_t Hkv, int32_t d, int32_t num_pages,
+                      int32_t max_pages) {
+    if (B < 0 || rows < 0 || Hkv < 1 || d < 1 || num_pages < 1 || max_pages < 1)
+        return TV_ERR_SHAPE;
+    if (d != 64 && d != 128) return TV_ERR_UNSUPPORTED;
+    // positions and work items are counted in 32 bits
+    if (max_pages > 0x7fffffff / tv::kQPage) return TV_ERR_UNSUPPORTED;
+    if (((int64_t)rows / tv::kQPage + 2LL * B) * Hkv * (d / tv::kQGroup) > 0x7fffffffLL)
+        return TV_ERR_UNSUPPORTED;
+    return TV_OK;
+}
+
+bool bad_stride(int64_t stride, int32_t heads, int32_t d) {
+    return stride < (int64_t)heads * d || stride % 8;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tv_qcache_bytes(int32_t num_pages, int32_t Hkv, int32_t d) {
+    if (num_pages < 1 || Hkv < 1 || (d != 64 && d != 128)) return 0;
+    return (size_t)num_pages * Hkv * tv::qrec_bytes(d);
+}
+
+tv_status tv_qcache_write(int32_t B, int32_t total_rows, int32_t Hkv, int32_t d,
+                          int32_t num_pages, int32_t max_pages, const int32_t *row_offsets,
+                          const int32_t *start, const int32_t *page_table, const void *k,
+                          const void *v, int64_t row_stride, void *cache, int32_t *dev_status,
+                          void *stream) {
+    tv_status st = qcache_dims(B, total_rows, Hkv, d, num_pages, max_pages);
+    if (st != TV_OK) return st;
+    if (bad_stride(row_stride, Hkv, d)) return TV_ERR_SHAPE;
+    if (!dev_status) return TV_ERR_NULL;
+    if (B == 0 || total_rows == 0) return TV_OK;
+    st = check_ptrs({row_offsets, start, page_table, k, v, cache, dev_status});
+    if (st != TV_OK) return st;
+    tv::QRowsArgs a{B, total_rows, Hkv, d, num_pages, max_pages, row_offsets, start, nullptr,
+                    page_table, const_cast<void *>(k), const_cast<void *>(v), row_stride,
+                    static_cast<uint8_t *>(cache), dev_status};
+    cudaError_t e = tv::launch_qcache_write(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+tv_status tv_qcache_read(int32_t B, int32_t total_rows, int32_t Hkv, int32_t d,
+                         int32_t num_pages, int32_t max_pages, const int32_t *row_offsets,
+                         const int32_t *start, const int32_t *ctx_len, const int32_t *page_table,
+                         const void *cache, void *k, void *v, int64_t row_stride,
+                         int32_t *dev_status, void *stream) {
+    tv_status st = qcache_dims(B, total_rows, Hkv, d, num_pages, max_pages);
+    if (st != TV_OK) return st;
+    if (bad_stride(row_stride, Hkv, d)) return TV_ERR_SHAPE;
+    if (!dev_status) return TV_ERR_NULL;
+    if (B == 0 || total_rows == 0) return TV_OK;
+    st = check_ptrs({row_offsets, start, ctx_len, page_table, cache, k, v, dev_status});
+    if (st != TV_OK) return st;
+    tv::QRowsArgs a{B, total_rows, Hkv, d, num_pages, max_pages, row_offsets, start, ctx_len,
+                    page_table, k, v, row_stride,
+                    static_cast<uint8_t *>(const_cast<void *>(cache)), dev_status};
+    cudaError_t e = tv::launch_qcache_read(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+tv_status tv_qcache_commit(int32_t B, int32_t total_nodes, int32_t max_nodes, int32_t max_depth,
+                           int32_t Hkv, int32_t d, int32_t num_pages, int32_t max_pages,
+                           const int32_t *node_offsets, const int32_t *path,
+                           const int32_t *accept_len, const int32_t *ctx_len,
+                           const int32_t *page_table, const void *k_tree, const void *v_tree,
+                           int64_t row_stride, void *cache, int32_t *new_len,
+                           int32_t *dev_status, void *stream) {
+    tv_status st = qcache_dims(B, total_nodes, Hkv, d, num_pages, max_pages);
+    if (st != TV_OK) return st;
+    if (max_nodes < 1 || max_depth < 1) return TV_ERR_SHAPE;
+    if (max_nodes > TV_MAX_NODES || max_depth > TV_MAX_DEPTH) return TV_ERR_UNSUPPORTED;
+    if ((int64_t)total_nodes > (int64_t)B * max_nodes) return TV_ERR_SHAPE;
+    if (bad_stride(row_stride, Hkv, d)) return TV_ERR_SHAPE;
+    if (!dev_status) return TV_ERR_NULL;
+    if (B == 0) return TV_OK;
+    st = check_ptrs({node_offsets, path, accept_len, ctx_len, page_table, cache, new_len,
+                     dev_status});
+    if (st != TV_OK) return st;
+    if (total_nodes > 0) {
+        st = check_ptrs({k_tree, v_tree});
+        if (st != TV_OK) return st;
+    }
+    tv::QCommitArgs a{B, total_nodes, max_nodes, max_depth, Hkv, d, num_pages, max_pages,
+                      node_offsets, path, accept_len, ctx_len, page_table, k_tree, v_tree,
+                      row_stride, static_cast<uint8_t *>(cache), new_len, dev_status};
+    cudaError_t e = tv::launch_qcache_commit(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+tv_status qattn_dims(int32_t B, int32_t T, int32_t max_nodes, int32_t H, int32_t Hkv, int32_t d,
+                     int32_t max_pages) {
+    if (max_nodes < 1 || H < 1) return TV_ERR_SHAPE;
+    tv_status st = qcache_dims(B, T, Hkv, d, 1, max_pages);
+    if (st != TV_OK) return st;
+    if (H % Hkv || (int64_t)T > (int64_t)B * max_nodes) return TV_ERR_SHAPE;
+    if (H / Hkv > 128 || max_nodes > TV_MAX_NODES) return TV_ERR_UNSUPPORTED;
+    if ((int64_t)B * Hkv * max_pages * tv::kQPage > 0x7fffffffLL ||
+        (int64_t)B * max_nodes * H > 0x7fffffffLL)
+        return TV_ERR_UNSUPPORTED;
+    return TV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tv_qcache_attention_workspace_bytes(int32_t B, int32_t total_nodes, int32_t max_nodes,
+                                           int32_t H, int32_t Hkv, int32_t d, int32_t max_pages) {
+    if (qattn_dims(B, total_nodes, max_nodes, H, Hkv, d, max_pages) != TV_OK || B == 0 ||
+        total_nodes == 0)
+        return 0;
+    tv::QAttnArgs a{};
+    a.B = B;
+    a.T = total_nodes;
+    a.max_nodes = max_nodes;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.max_pages = max_pages;
+    return tv::qcache_attention_workspace_bytes(a);
+}
+
+tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes, int32_t H,
+                              int32_t Hkv, int32_t d, int32_t num_pages, int32_t max_pages,
+                              const int32_t *node_offsets, const int32_t *parent,
+                              const int32_t *ctx_len, const int32_t *page_table, int32_t window,
+                              int32_t sinks, const void *q, int64_t q_stride, const void *cache,
+                              const void *k_tree, const void *v_tree, int64_t kv_stride,
+                              float scale, int32_t out_dtype, void *out, void *workspace,
+                              size_t workspace_bytes, int32_t *dev_status, void *stream) {
+    tv_status st = qattn_dims(B, total_nodes, max_nodes, H, Hkv, d, max_pages);
+    if (st != TV_OK) return st;
+    if (num_pages < 1 || window < 0 || sinks < 0) return TV_ERR_SHAPE;
+    if (bad_stride(q_stride, H, d) || bad_stride(kv_stride, Hkv, d)) return TV_ERR_SHAPE;
+    if (!(scale > 0.f) || scale > 3.0e38f) return TV_ERR_SHAPE;  // positive and finite
+    if (out_dtype != TV_BF16 && out_dtype != TV_F32) return TV_ERR_DTYPE;
+    if (!dev_status) return TV_ERR_NULL;
+    if (B == 0 || total_nodes == 0) return TV_OK;
+    st = check_ptrs({node_offsets, parent, ctx_len, page_table, q, cache, k_tree, v_tree, out,
+                     dev_status});
+    if (st != TV_OK) return st;
+    tv::QAttnArgs a{B, total_nodes, max_nodes, H, Hkv, d, num_pages, max_pages,
+                    node_offsets, parent, ctx_len, page_table, window, sinks, q, q_stride,
+                    static_cast<const uint8_t *>(cache), k_tree, v_tree, kv_stride, scale,
+                    out_dtype == TV_F32, out, static_cast<float *>(workspace), dev_status};
+    const size_t need = tv::qcache_attention_workspace_bytes(a);
+    if (need > 0) {
+        st = check_ptrs({workspace});
+        if (st != TV_OK) return st;
+        if (workspace_bytes < need) return TV_ERR_SHAPE;
+    }
+    cudaError_t e = tv::launch_qcache_attention(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -72,6 +72,56 @@ struct AttnArgs {
 size_t tree_attention_workspace_bytes(const AttnArgs &a);
 cudaError_t launch_tree_attention(const AttnArgs &a, cudaStream_t s);
 
+// The paged 4-bit KV cache (tv_qcache_*): one record per (page, KV head).
+constexpr int kQPage = TV_QCACHE_PAGE;
+constexpr int kQGroup = TV_QCACHE_GROUP;
+__host__ __device__ constexpr uint32_t qrec_codes(int d) { return kQPage * d / 2; }
+__host__ __device__ constexpr uint32_t qrec_scales(int d) { return kQPage * (d / kQGroup); }
+__host__ __device__ constexpr uint32_t qrec_bytes(int d) {
+    return 2 * (qrec_codes(d) + qrec_scales(d));
+}
+
+// Rows of k and v are `stride` elements apart; `len` is read by commit and read only.
+struct QRowsArgs {
+    int32_t B, T, Hkv, d, num_pages, max_pages;
+    const int32_t *offsets, *start, *len, *table;
+    void *k, *v;  // bf16 rows: inputs of a write, outputs of a read
+    int64_t stride;
+    uint8_t *cache;
+    int32_t *status;
+};
+cudaError_t launch_qcache_write(const QRowsArgs &a, cudaStream_t s);
+cudaError_t launch_qcache_read(const QRowsArgs &a, cudaStream_t s);
+
+struct QCommitArgs {
+    int32_t B, T, max_nodes, max_depth, Hkv, d, num_pages, max_pages;
+    const int32_t *node_offsets, *path, *accept_len, *ctx_len, *table;
+    const void *k, *v;
+    int64_t stride;
+    uint8_t *cache;
+    int32_t *new_len;
+    int32_t *status;
+};
+cudaError_t launch_qcache_commit(const QCommitArgs &a, cudaStream_t s);
+
+struct QAttnArgs {
+    int32_t B, T, max_nodes, H, Hkv, d, num_pages, max_pages;
+    const int32_t *node_offsets, *parent, *ctx_len, *table;
+    int32_t window, sinks;
+    const void *q;
+    int64_t q_stride;
+    const uint8_t *cache;
+    const void *k_tree, *v_tree;
+    int64_t kv_stride;
+    float scale;
+    int32_t out_f32;
+    void *out;
+    float *ws;
+    int32_t *status;
+};
+size_t qcache_attention_workspace_bytes(const QAttnArgs &a);
+cudaError_t launch_qcache_attention(const QAttnArgs &a, cudaStream_t s);
+
 // Best-first draft-tree construction (tv_build_tree).
 struct BuildArgs {
     int32_t B, C, depth_cap, n;

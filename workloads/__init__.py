@@ -525,6 +525,13 @@ def attention_inputs(batch: Batch, H: int, Hkv: int, d: int, ctx_len: Sequence[i
     return out
 
 
+def qcache_pages(rng, B: int, max_pages: int, spare: int = 3):
+    """A page table [B][max_pages] (int32) of distinct pages in random order, and the
+    number of pages (spare ones belong to nobody)."""
+    pages = B * max_pages + spare
+    return rng.permutation(pages)[:B * max_pages].reshape(B, max_pages).astype(np.int32), pages
+
+
 def random_batch(rng, sizes: Sequence[int], H: int, dk: int, dv: int, *, decay="scalar",
                  qkv_dtype="bf16", g_kind=None, depth_cap: int = 32, vocab: int = 4,
                  h0_std: float = 0.05, max_depth: Optional[int] = None,
