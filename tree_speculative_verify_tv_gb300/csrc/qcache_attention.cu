@@ -3,166 +3,1043 @@
 // Query row (node i, head h) of request b sees the cached positions below ctx_len[b] and
 // the nodes of i's root path, within the window or among the sinks:
 //   o = sum_j softmax_j(scale * q . k_j) v_j.
-// One CTA per query row: keys in tiles of 64 (a page, or 64 nodes of the root path), one
-// thread per key for the scores, one per channel for the value sums, the running maximum
-// and sum in fp32.
+//
+// Keys are the M dimension of both products, so that the dequantised operands are A
+// operands in tensor memory and never pass through shared memory:
+//   S^T = K Q^T    M = 128 keys (lane = key), N = R query rows, K = d; B = Q, K-major in
+//                  shared memory, loaded once per unit;
+//   O^T += V^T P^T M = 128 channels (lane = channel), N = R rows per part, K = 128 keys;
+//                  B = P, written by the softmax threads as [key][row], MN-major.
+// A tile is 128 keys: two pages, or 128 tree nodes.  A page of one KV head is one record of
+// 17/64 of its bf16 size and comes by one bulk copy; K codes are laid out so that the
+// thread of a key, and V codes so that the thread of a channel, reads its 4-bit codes in
+// 16-byte pieces without bank conflicts and stores them to its own tensor-memory lane:
+//   two codes at once: ((word >> 4 p) & 0x000F000F) | 0x43004300 is the bf16 pair
+//   (128 + c0, 128 + c1), and one packed fma with s and -136 s gives s (c - 8), exactly
+//   (at most 7 significant bits; 136 s has at most 8).
+// Work: the tiles of all (request, KV head, tile of R rows) units are laid end to end and
+// every CTA (one per SM) takes an equal share; a unit that is cut leaves (O, m, l) pieces
+// in the workspace, joined by a second kernel.
+//
+// Warp roles: NSW = R / 32 softmax groups of 4 warps (32 rows each, lane = key), one group
+// that dequantises K, one for V, a producer warp (page table, bulk copies), a warp that
+// issues the products.  The reference maximum m of a row is raised only when a score
+// exceeds it by more than 8 (log2 units); all 128 threads of a group vote per tile.  Weights
+// enter the value product as NP bf16 parts; sums l are kept in fp32 from the same weights.
+// Every mbarrier wait is bounded, as in tree_attention.cu.
+#include <algorithm>
+
 #include "qcache.cuh"
+#include "tc_common.cuh"
 
 namespace tv {
 namespace {
 
-__device__ __forceinline__ float block_max(float x, float *s) {
+using tcc::kWaitLimit;
+
+constexpr int kKeys = 128;             // keys per tile
+constexpr int kChunkB = 2048;          // requests per launch (their tile counts are in smem)
+constexpr uint32_t kSlab = kKeys * 128;  // 128 keys x 128 bytes
+constexpr float kHeadroom = 8.f;
+constexpr float kNoMax = 1e30f;        // -m of a row that has seen no key
+constexpr uint32_t kTmemCols = 512;
+
+struct QParams {
+    QAttnArgs a;
+    int b0, nb;   // this launch's requests
+    int grp, grid;
+    float sl2;    // scale * log2(e)
+};
+
+// One request: its rows, the pages that any of its nodes sees, its tiles.
+struct Req {
+    int off, n;      // first node, nodes (0 when its offsets are unusable)
+    int ctx;         // 0 when out of range (then bad)
+    bool range, bad;
+    int sp, lp, np;  // linear page i is page i below sp, else i - sp + lp; np of them
+    int nct, nt;     // context tiles, all tiles
+    int mts;         // tiles of R rows
+};
+
+template <int R>
+__device__ __forceinline__ Req request(const QParams &P, int b) {
+    const QAttnArgs &a = P.a;
+    Req r{};
+    r.range = request_range(a.node_offsets, b, a.T, a.max_nodes, r.off, r.n);
+    if (!r.range) r.n = 0;
+    r.ctx = a.ctx_len[b];
+    r.bad = r.ctx < 0 || r.ctx > (long long)a.max_pages * kQPage;
+    if (r.bad) r.ctx = 0;
+    const int cp = (r.ctx + kQPage - 1) / kQPage;
+    if (a.window > 0) {
+        const long long lo = (long long)r.ctx + 1 - a.window;  // seen by a node at depth 1
+        r.lp = lo >= r.ctx ? cp : lo > 0 ? (int)lo / kQPage : 0;
+        r.sp = min((min(a.sinks, r.ctx) + kQPage - 1) / kQPage, r.lp);
+    }
+    r.np = r.sp + cp - r.lp;
+    r.nct = (r.np + 1) / 2;
+    r.nt = r.n > 0 ? r.nct + (r.n + kKeys - 1) / kKeys : 0;
+    r.mts = (int)(((long long)r.n * P.grp + R - 1) / R);
+    return r;
+}
+
+__device__ __forceinline__ int page_of(const Req &r, int i) { return i < r.sp ? i : i - r.sp + r.lp; }
+
+// A run of tiles [j0, j1) of one unit.
+struct Seg {
+    Req r;
+    int b, kvh, mt, j0, j1;
+};
+
+// Walks this CTA's share [t, t1) of the tiles.
+template <int R>
+struct Walk {
+    int t, t1;
+    __device__ bool next(const QParams &P, const int *cum, Seg &s) {
+        if (t >= t1) return false;
+        int lo = 0, hi = P.nb - 1;  // the last request whose tiles begin at or before t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cum[mid] <= t)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        s.b = P.b0 + lo;
+        s.r = request<R>(P, s.b);
+        const int rem = t - cum[lo], unit = rem / s.r.nt;
+        s.j0 = rem % s.r.nt;
+        s.j1 = min(s.r.nt, s.j0 + (t1 - t));
+        s.kvh = unit / s.r.mts;
+        s.mt = unit % s.r.mts;
+        t += s.j1 - s.j0;
+        return true;
+    }
+};
+
+// Shared memory.  P: two buffers of NP parts; at R = 64 a part fills a 128-byte row, at
+// R = 32 two parts share one.
+template <int D, int R, int NP>
+struct Lay {
+    static constexpr int kSW = R / 32;                     // softmax groups
+    static constexpr int kWarps = 4 * kSW + 8 + 2;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr uint32_t kRec = qrec_bytes(D);
+    static constexpr uint32_t kPSlabs = (NP * R + 63) / 64;
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kP = kQ + R * D * 2;
+    static constexpr uint32_t kRing = kP + 2 * kPSlabs * kSlab;
+    static constexpr uint32_t kMiscBytes = 18 * 1024;
+    static constexpr int kStages =
+        (int)std::min<uint32_t>(16, (227 * 1024 - 1024 - kMiscBytes - kRing) / (2 * kRec));
+    static constexpr uint32_t kCum = kRing + kStages * 2 * kRec;       // int [kChunkB + 1]
+    static constexpr uint32_t kPar = kCum + (kChunkB + 4) * 4;         // int16 [kSW][256]
+    static constexpr uint32_t kAnc = kPar + kSW * kMaxNodes * 2;       // u32 [kSW][32][8]
+    static constexpr uint32_t kLo = kAnc + kSW * 32 * 8 * 4;           // int [kSW][32]
+    static constexpr uint32_t kNm = kLo + kSW * 128;                   // float [kSW][32]
+    static constexpr uint32_t kAl = kNm + kSW * 128;                   // float [kSW][32]
+    static constexpr uint32_t kRed = kAl + kSW * 128;                  // float [kSW][4][32]
+    static constexpr uint32_t kVs = kRed + kSW * 512;                  // uint2 [4][2][32]
+    static constexpr uint32_t kBar = kVs + 4 * 2 * 32 * 8;
+    // mbarriers: ring full / empty; K and V operands written; Q loaded; S ready / read;
+    // P written; P V done; every product done
+    static constexpr int kFull = 0, kEmpty = kFull + kStages, kKReady = kEmpty + kStages,
+                         kVReady = kKReady + 2, kQReady = kVReady + 2, kSReady = kQReady + 1,
+                         kSFree = kSReady + 2, kPReady = kSFree + 2, kOReady = kPReady + 2,
+                         kDone = kOReady + 2, kNumBars = kDone + 1;
+    static constexpr uint32_t kMisc = kBar + kNumBars * 8;  // tmem, abort, scan [32], wg flags
+    static constexpr uint32_t kBytes = kMisc + 256;
+    static constexpr uint32_t kAlloc = kBytes + 1024;
+    static_assert(kBytes - kCum <= kMiscBytes && kStages >= 3, "shared-memory plan");
+    // tensor memory columns
+    static constexpr uint32_t kTS = 0;                       // S^T x 2
+    static constexpr uint32_t kTO = 2 * R;                   // O^T, hi sums then lo sums
+    static constexpr uint32_t kOWidth = NP == 1 ? (R < 64 ? 64 : R) : NP == 3 && R == 32 ? 96 : 2 * R;
+    static constexpr uint32_t kTK = kTO + kOWidth;           // K x 2
+    static constexpr uint32_t kTV = kTK + D;                 // V^T x 2
+    static_assert(kTV + 128 <= kTmemCols, "tensor memory plan");
+};
+
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort) {
+    if (ptx::mbar_test_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!ptx::mbar_try_wait(bar, parity, 20000)) {
+        if (*abort || clock64() - t0 > kWaitLimit) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float warp_max_f32(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Column sums of v[0..31] over a warp: lane c returns column c's.
+__device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    for (int s = 16; s > 0; s >>= 1) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int i = 0; i < s; ++i) {
+            const float send = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+        }
+    }
+    return v[0];
+}
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// bf16 bits of the scale with byte b.
+__device__ __forceinline__ uint32_t scale_bf16(uint32_t b) {
+    return b == qc::kScaleNaN ? 0x7FC0u : (b << 4) + 0x3480u;
+}
+
+// -136 s for a pair of scales (bf16 -136 = 0xC308; the product is exact).
+__device__ __forceinline__ uint32_t minus_136(uint32_t s2) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(s2), "r"(0xC308C308u));
+    return d;
+}
+
+// Codes 2p and 2p + 1 of a word as the bf16 pair (128 + c0, 128 + c1).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int p) {
+    return ((w >> (4 * p)) & 0x000F000Fu) | 0x43004300u;
+}
+
+// The bf16 parts of two weights, element 0 in the low half.  One part: rounded to nearest.
+// More: each earlier part keeps the upper 16 bits of what is left (exactly), the last is
+// rounded: two leave a relative 2^-16 at most, three 2^-24.
+template <int NP>
+__device__ __forceinline__ void split_weights(float p0, float p1, uint32_t (&out)[NP]) {
+    if constexpr (NP == 1) {
+        out[0] = tcc::pack_bf16(p0, p1);
+    } else if constexpr (NP == 2) {
+        tcc::split_pair(p0, p1, out[0], out[1]);
+    } else {
+        const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+        out[0] = __byte_perm(b0, b1, 0x7632);
+        tcc::split_pair(p0 - __uint_as_float(b0 & 0xFFFF0000u),
+                        p1 - __uint_as_float(b1 & 0xFFFF0000u), out[1], out[2]);
+    }
+}
+
+// Workspace: 8 ints per piece (valid, b, kvh, mt, first tile of the unit past its own
+// tiles, all tiles, bad), then per piece O [R][D], m [R] (as -m), l [R].  Piece 2 i is the
+// continuation CTA i begins with, piece 2 i + 1 the unit it begins and does not end.
+template <int D, int R>
+__device__ __forceinline__ float *piece_data(const QParams &P, int piece) {
+    return P.a.ws + (size_t)2 * P.grid * 8 + (size_t)piece * R * (D + 2);
+}
+
+template <int D, int R, int NP>
+__global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
+    qcache_attention_kernel(const QParams P) {
+    using L = Lay<D, R, NP>;
+    using Rc = qc::Rec<D>;
+    constexpr int SW = L::kSW, NS = L::kStages;
+    constexpr int kWarpK = 4 * SW, kWarpV = kWarpK + 4, kWarpCopy = kWarpV + 4,
+                  kWarpMma = kWarpCopy + 1;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const QAttnArgs &a = P.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3;
+    const uint32_t sbase = ptx::smem_addr(sm);
+    auto bar = [&](int i) { return sbase + L::kBar + 8u * (uint32_t)i; };
+    int *s_cum = reinterpret_cast<int *>(sm + L::kCum);
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(sm + L::kMisc);
+    volatile int *abort = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
+    int *s_scan = reinterpret_cast<int *>(sm + L::kMisc + 16);
+    int *s_wg = reinterpret_cast<int *>(sm + L::kMisc + 16 + 128);  // [SW][2]: bad, stop
+
+    if (tid == 0) {
+        *abort = 0;
+        for (int i = 0; i < L::kNumBars; ++i) {
+            uint32_t count = 1;
+            if (i >= L::kEmpty && i < L::kKReady) count = 8;                 // K and V warps
+            if (i >= L::kKReady && i < L::kQReady) count = 128;
+            if (i == L::kQReady || (i >= L::kSFree && i < L::kOReady)) count = 128 * SW;
+            ptx::mbar_init(bar(i), count);
+        }
+        ptx::fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        ptx::tmem_alloc(ptx::smem_addr(s_tmem), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_launch_next();
+
+    // ---- prefix sums of the requests' tiles
+    {
+        constexpr int per = (kChunkB + L::kThreads - 1) / L::kThreads;
+        int w[per], sum = 0;
+#pragma unroll
+        for (int k = 0; k < per; ++k) {
+            const int i = tid * per + k;
+            w[k] = 0;
+            if (i < P.nb) {
+                const Req r = request<R>(P, P.b0 + i);
+                w[k] = a.Hkv * r.mts * r.nt;
+                if (blockIdx.x == 0 && !r.range) report(a.status, TV_ERR_TREE);
+            }
+            sum += w[k];
+        }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        int before = 0;
+        for (int k = 0; k < warp; ++k) before += s_scan[k];
+        int at = before + inc - sum;
+#pragma unroll
+        for (int k = 0; k < per; ++k) {
+            const int i = tid * per + k;
+            if (i < P.nb) s_cum[i] = at;
+            at += w[k];
+            if (i == P.nb - 1) s_cum[P.nb] = at;
+        }
+    }
+    ptx::tc_fence_before_sync();
     __syncthreads();
-    if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = x;
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *s_tmem;
+    const int total = s_cum[P.nb];
+    const int shares = min(P.grid, total), me = min((int)blockIdx.x, shares);
+    const int first = shares > 0 ? (int)((long long)total * me / shares) : 0;
+    Walk<R> walk{first, me < shares ? (int)((long long)total * (me + 1) / shares) : first};
+    const int ntiles = walk.t1 - first;
+    Seg s;
+
+    if (warp == kWarpCopy) {
+        // ------------------------------------------------ producer: one bulk copy per page;
+        // the lanes hold the next 32 pages' records
+        int rc = 0;  // context tiles so far
+        bool ok = true;
+        while (ok && walk.next(P, s_cum, s)) {
+            const int end = min(s.j1, s.r.nct);
+            const uint8_t *rec = nullptr;
+            for (int j = s.j0; j < end; ++j) {
+                const int k = (j - s.j0) % 16;
+                if (k == 0) {
+                    const int i = 2 * j + lane;
+                    int page = 0;
+                    if (i < s.r.np) {
+                        page = a.table[(size_t)s.b * a.max_pages + page_of(s.r, i)];
+                        if (page < 0 || page >= a.num_pages) page = 0;  // the unit is bad
+                    }
+                    rec = a.cache + ((size_t)page * a.Hkv + s.kvh) * L::kRec;
+                }
+                const int st = rc % NS;
+                ok = __all_sync(0xffffffffu,
+                                rc < NS || wait_phase(bar(L::kEmpty + st), ((rc / NS) - 1) & 1,
+                                                      abort));
+                if (!ok) break;
+                const bool two = 2 * j + 1 < s.r.np;
+                const uint32_t dst = sbase + L::kRing + (uint32_t)st * 2 * L::kRec;
+                if (lane == 2 * k) {
+                    ptx::mbar_arrive_expect_tx(bar(L::kFull + st), (two ? 2 : 1) * L::kRec);
+                    ptx::bulk_g2s(dst, rec, L::kRec, bar(L::kFull + st));
+                }
+                __syncwarp();
+                if (lane == 2 * k + 1 && two)
+                    ptx::bulk_g2s(dst + L::kRec, rec, L::kRec, bar(L::kFull + st));
+                ++rc;
+            }
+        }
+        __syncwarp();
+        // no copy may still be landing when the CTA ends
+        if (lane == 0)
+            for (int j = max(0, rc - NS); j < rc; ++j)
+                ptx::mbar_wait(bar(L::kFull + j % NS), (j / NS) & 1, kWaitLimit);
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // ------------------------------------------------ product issuer: whichever of the
+        // next S and the next P V is ready
+        if (lane == 0 && ntiles > 0) {
+            constexpr uint32_t idS = ptx::idesc_bf16_f32(128, R);
+            constexpr uint32_t nPV = NP == 1 ? L::kOWidth : 2 * R;
+            constexpr uint32_t idPV = ptx::idesc_bf16_f32_bmn(128, nPV);
+            constexpr uint32_t id3 = ptx::idesc_bf16_f32_bmn(128, 64);
+            const uint32_t sQ = sbase + L::kQ;
+            Walk<R> wp = walk;
+            int js = 0, jp = 0, s_end = 0, p_first = 0, p_end = 0, seg = -1;
+            bool ok = true;
+            long long t_last = clock64();
+            while (ok && jp < ntiles) {
+                bool progressed = false;
+                if (js < ntiles) {
+                    if (js == s_end) {
+                        walk.next(P, s_cum, s);
+                        s_end = js + s.j1 - s.j0;
+                        ++seg;
+                    }
+                    const int x = js & 1;
+                    // (Q's phase of this unit stays complete until the next unit's, which
+                    // needs this unit's last S first)
+                    if (ptx::mbar_test_wait(bar(L::kKReady + x), (js >> 1) & 1) &&
+                        (js < 2 || ptx::mbar_test_wait(bar(L::kSFree + x), ((js >> 1) - 1) & 1)) &&
+                        ptx::mbar_test_wait(bar(L::kQReady), seg & 1)) {
+                        ptx::tc_fence_after_sync();
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            ptx::mma_bf16_ts(
+                                tmem + L::kTS + R * x, tmem + L::kTK + (D / 2) * x + 8u * kk,
+                                ptx::desc_kmajor_sw128(sQ + (kk >> 2) * (R * 128) + (kk & 3) * 32,
+                                                       1024),
+                                idS, kk > 0);
+                        ptx::mma_commit(bar(L::kSReady + x));
+                        ++js;
+                        progressed = true;
+                    }
+                }
+                if (jp < js) {
+                    if (jp == p_end) {
+                        wp.next(P, s_cum, s);
+                        p_first = jp;
+                        p_end = jp + s.j1 - s.j0;
+                    }
+                    const int x = jp & 1;
+                    if (ptx::mbar_test_wait(bar(L::kVReady + x), (jp >> 1) & 1) &&
+                        ptx::mbar_test_wait(bar(L::kPReady + x), (jp >> 1) & 1)) {
+                        ptx::tc_fence_after_sync();
+                        const uint32_t sP = sbase + L::kP + (uint32_t)x * L::kPSlabs * kSlab;
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint32_t av = tmem + L::kTV + 64u * x + 8u * kk;
+                            const uint32_t acc = jp > p_first || kk > 0;
+                            ptx::mma_bf16_ts(
+                                tmem + L::kTO, av,
+                                ptx::desc_mnmajor_sw128(sP + kk * 2048u, nPV > 64 ? kSlab : 0u,
+                                                        1024),
+                                idPV, acc);
+                            // the third part adds to the second's sums (at R = 32 its row
+                            // has 32 idle columns, which go to idle columns)
+                            if constexpr (NP == 3)
+                                ptx::mma_bf16_ts(
+                                    tmem + L::kTO + R, av,
+                                    ptx::desc_mnmajor_sw128(
+                                        sP + (R == 64 ? 2 : 1) * kSlab + kk * 2048u, 0u, 1024),
+                                    id3, 1u);
+                        }
+                        ptx::mma_commit(bar(L::kOReady + x));
+                        ++jp;
+                        progressed = true;
+                    }
+                }
+                if (progressed) {
+                    t_last = clock64();
+                } else {
+                    // sleep on the event most likely next
+                    if (jp < js)
+                        ptx::mbar_try_wait(bar(L::kPReady + (jp & 1)), (jp >> 1) & 1, 500);
+                    else
+                        ptx::mbar_try_wait(bar(L::kKReady + (js & 1)), (js >> 1) & 1, 500);
+                    if (*abort || clock64() - t_last > kWaitLimit) {
+                        *abort = 1;
+                        ok = false;
+                    }
+                }
+            }
+            ptx::mma_commit(bar(L::kDone));
+            ptx::mbar_wait(bar(L::kDone), 0, kWaitLimit);
+        }
+        __syncwarp();
+    } else if (warp >= kWarpV) {
+        // ------------------------------------------------ V^T operand: thread = channel
+        const int c = 32 * quad + lane;
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTV;
+        uint2 *s_vs = reinterpret_cast<uint2 *>(sm + L::kVs) + quad * 64;
+        const bool live = 32 * quad < D;
+        int it = 0, rc = 0;
+        bool ok = true;
+        while (ok && walk.next(P, s_cum, s)) {
+            const long long vis = a.window > 0 ? (long long)s.r.ctx + 1 - a.window : 0;
+            const int sinks = a.window > 0 ? a.sinks : 0;
+            for (int j = s.j0; j < s.j1; ++j, ++it) {
+                const uint32_t dst = tl + 64u * (it & 1);
+                if (it >= 2)
+                    ok = wait_phase(bar(L::kOReady + (it & 1)), ((it >> 1) - 1) & 1, abort);
+                if (j < s.r.nct) {
+                    const int st = rc % NS;
+                    ok = ok && wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    ptx::tc_fence_after_sync();
+                    const uint8_t *rec = sm + L::kRing + (uint32_t)st * 2 * L::kRec;
+                    if (live) {
+                        // the group's scales (a warp's 32 channels), two positions per lane;
+                        // a position that no node sees gets 0, whatever the cache holds there
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t b2 = *reinterpret_cast<const uint16_t *>(
+                                rec + h * L::kRec + Rc::kVScales + quad * kQPage + 2 * lane);
+                            uint32_t s0 = scale_bf16(b2 & 0xFFu), s1 = scale_bf16(b2 >> 8);
+                            const int i = 2 * j + h;
+                            const int pos = page_of(s.r, i) * kQPage + 2 * lane;
+                            if (i >= s.r.np || pos >= s.r.ctx || (pos < vis && pos >= sinks))
+                                s0 = 0;
+                            if (i >= s.r.np || pos + 1 >= s.r.ctx ||
+                                (pos + 1 < vis && pos + 1 >= sinks))
+                                s1 = 0;
+                            const uint32_t s2 = s0 | (s1 << 16);
+                            s_vs[h * 32 + lane] = make_uint2(s2, minus_136(s2));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t out[32];
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const uint4 w4 = *reinterpret_cast<const uint4 *>(
+                                    rec + h * L::kRec + Rc::kVCodes + (q * D + c) * 16);
+                                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const uint4 sc = *reinterpret_cast<const uint4 *>(
+                                        s_vs + h * 32 + q * 16 + 2 * e);
+                                    out[16 * q + 2 * e] =
+                                        fma_bf16x2(code_pair(w[e / 2], 2 * (e & 1)), sc.x, sc.y);
+                                    out[16 * q + 2 * e + 1] = fma_bf16x2(
+                                        code_pair(w[e / 2], 2 * (e & 1) + 1), sc.z, sc.w);
+                                }
+                            }
+                            ptx::tmem_st_x32(dst + 32u * h, out);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(L::kEmpty + st));
+                    ++rc;
+                } else {
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    ptx::tc_fence_after_sync();
+                    if (live) {
+                        const int n0 = (j - s.r.nct) * kKeys;
+                        const uint16_t *v = static_cast<const uint16_t *>(a.v_tree) +
+                                            (size_t)s.r.off * a.kv_stride + s.kvh * D + c;
+#pragma unroll 1
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t out[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const int n = n0 + 32 * h + 2 * e;
+                                const uint32_t x0 = n < s.r.n ? v[(size_t)n * a.kv_stride] : 0;
+                                const uint32_t x1 =
+                                    n + 1 < s.r.n ? v[(size_t)(n + 1) * a.kv_stride] : 0;
+                                out[e] = x0 | (x1 << 16);
+                            }
+                            ptx::tmem_st_x16(dst + 16u * h, out);
+                        }
+                    }
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(bar(L::kVReady + (it & 1)));
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kWarpK) {
+        // ------------------------------------------------ K operand: thread = key
+        const int key = 32 * quad + lane;
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTK;
+        int it = 0, rc = 0;
+        bool ok = true;
+        while (ok && walk.next(P, s_cum, s)) {
+            for (int j = s.j0; j < s.j1; ++j, ++it) {
+                const uint32_t dst = tl + (D / 2) * (it & 1);
+                // S of two tiles ago has read this buffer
+                if (it >= 2)
+                    ok = wait_phase(bar(L::kSReady + (it & 1)), ((it >> 1) - 1) & 1, abort);
+                if (j < s.r.nct) {
+                    const int st = rc % NS;
+                    ok = ok && wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    ptx::tc_fence_after_sync();
+                    const uint8_t *rec =
+                        sm + L::kRing + ((uint32_t)st * 2 + key / kQPage) * L::kRec;
+                    const int p = key % kQPage;
+                    uint32_t sc;
+                    if constexpr (D == 128)
+                        sc = *reinterpret_cast<const uint32_t *>(rec + Rc::kKScales + p * 4);
+                    else
+                        sc = *reinterpret_cast<const uint16_t *>(rec + Rc::kKScales + p * 2);
+#pragma unroll
+                    for (int g2 = 0; g2 < D / 64; ++g2) {
+                        uint32_t out[32];
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const uint32_t s1 = scale_bf16((sc >> (8 * (2 * g2 + g))) & 0xFFu);
+                            const uint32_t s2 = s1 | (s1 << 16), ms = minus_136(s2);
+                            const uint4 w4 = *reinterpret_cast<const uint4 *>(
+                                rec + Rc::kKCodes + ((2 * g2 + g) * kQPage + p) * 16);
+                            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                out[16 * g + e] = fma_bf16x2(code_pair(w[e / 4], e & 3), s2, ms);
+                        }
+                        ptx::tmem_st_x32(dst + 32u * g2, out);
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(L::kEmpty + st));
+                    ++rc;
+                } else {
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    ptx::tc_fence_after_sync();
+                    const int n = (j - s.r.nct) * kKeys + key;
+                    const uint4 *k = reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(a.k_tree) +
+                        (size_t)(s.r.off + (n < s.r.n ? n : 0)) * a.kv_stride + s.kvh * D);
+#pragma unroll
+                    for (int g2 = 0; g2 < D / 64; ++g2) {
+                        uint32_t out[32];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint4 x = n < s.r.n ? k[8 * g2 + e] : make_uint4(0, 0, 0, 0);
+                            out[4 * e] = x.x;
+                            out[4 * e + 1] = x.y;
+                            out[4 * e + 2] = x.z;
+                            out[4 * e + 3] = x.w;
+                        }
+                        ptx::tmem_st_x32(dst + 32u * g2, out);
+                    }
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(bar(L::kKReady + (it & 1)));
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ softmax: 32 query rows per group,
+        // thread = key
+        const int sw = warp / 4, key = 32 * quad + lane, t128 = tid - 128 * sw;
+        const int bid = 1 + sw;  // the group's named barrier
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
+        int16_t *s_par = reinterpret_cast<int16_t *>(sm + L::kPar) + sw * kMaxNodes;
+        uint32_t *s_anc = reinterpret_cast<uint32_t *>(sm + L::kAnc) + sw * 32 * 8;
+        int *s_lo = reinterpret_cast<int *>(sm + L::kLo) + sw * 32;
+        float *s_nm = reinterpret_cast<float *>(sm + L::kNm) + sw * 32;
+        float *s_al = reinterpret_cast<float *>(sm + L::kAl) + sw * 32;
+        float *s_red = reinterpret_cast<float *>(sm + L::kRed) + sw * 128;
+        volatile int *s_bad = s_wg + 2 * sw, *s_stop = s_wg + 2 * sw + 1;
+        int *hdr = reinterpret_cast<int *>(a.ws) + (size_t)2 * blockIdx.x * 8;
+        if (tid == 0) hdr[0] = hdr[8] = 0;
+        if (t128 == 0) *s_stop = 0;
+
+        // the unit's query rows, K-major with 128-byte swizzle; rows past the last keep
+        // what they held: their columns of S and O are never used
+        auto load_q = [&](const Seg &u) {
+            const int rows = min((int)min((long long)u.r.n * P.grp - (long long)u.mt * R, (long long)R) -
+                                     32 * sw, 32);
+            for (int e = t128; e < 32 * (D / 8); e += 128) {
+                const int rr = e / (D / 8), ch = e % (D / 8), r = 32 * sw + rr;
+                if (rr >= rows) continue;
+                const int row = u.mt * R + r, node = row / P.grp;
+                const uint4 x = *reinterpret_cast<const uint4 *>(
+                    static_cast<const __nv_bfloat16 *>(a.q) +
+                    (size_t)(u.r.off + node) * a.q_stride +
+                    (size_t)(u.kvh * P.grp + row % P.grp) * D + ch * 8);
+                *reinterpret_cast<uint4 *>(sm + L::kQ + (ch / 8) * (R * 128) + r * 128 +
+                                           ((ch % 8) ^ (r & 7)) * 16) = x;
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(bar(L::kQReady));
+        };
+
+        int it = 0;
+        bool ok = true, more = walk.next(P, s_cum, s);
+        if (more) load_q(s);
+        while (more) {
+            const Req &r = s.r;
+            const int nrows = (int)min((long long)r.n * P.grp - (long long)s.mt * R, (long long)R);
+            const int live = min(max(nrows - 32 * sw, 0), 32);  // this group's rows
+            // ---- the tree, the pages, and each row's view of them
+            tcc::named_barrier(bid, 128);  // the previous unit's reads are done
+            if (t128 == 0) *s_bad = r.bad ? TV_ERR_SHAPE : 0;
+            if (t128 < 32) s_nm[t128] = kNoMax;
+            tcc::named_barrier(bid, 128);
+            for (int i = t128; i < r.n; i += 128) {
+                const int p = a.parent[r.off + i];
+                s_par[i] = (int16_t)p;
+                if (p < -1 || p >= i) *s_bad = TV_ERR_TREE;
+            }
+            for (int i = t128; i < r.np; i += 128) {
+                const int page = a.table[(size_t)s.b * a.max_pages + page_of(r, i)];
+                if (page < 0 || page >= a.num_pages) *s_bad = TV_ERR_SHAPE;
+            }
+            tcc::named_barrier(bid, 128);
+            const int bad = *s_bad;
+            if (bad && t128 == 0 && sw == 0) report(a.status, bad);
+            if (t128 < 32) {
+                uint32_t anc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                int lo = 0;
+                if (t128 < live && !bad) {
+                    const int node = (s.mt * R + 32 * sw + t128) / P.grp;
+                    int depth = 0;
+                    for (int q = node; q >= 0; q = s_par[q]) ++depth;
+                    if (a.window > 0)
+                        lo = (int)min(max((long long)r.ctx + depth - a.window, 0LL), 0x7fffffffLL);
+                    int up = 0;  // steps above the node
+                    for (int q = node; q >= 0; q = s_par[q], ++up) {
+                        const bool see = a.window == 0 || up < a.window ||
+                                         (long long)r.ctx + depth - up - 1 < a.sinks;
+#pragma unroll
+                        for (int w = 0; w < 8; ++w)
+                            anc[w] |= see && (q >> 5) == w ? 1u << (q & 31) : 0u;
+                    }
+                }
+                s_lo[t128] = lo;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) s_anc[t128 * 8 + w] = anc[w];
+            }
+            tcc::named_barrier(bid, 128);
+            // the first position that every row sees by its window
+            const int lo_all = a.window > 0 ? (int)min((long long)r.ctx + r.n - a.window, 0x7fffffffLL)
+                                            : 0;
+            const int sinks = a.window > 0 ? a.sinks : 0;
+
+            float l[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) l[c] = 0.f;
+            for (int j = s.j0; j < s.j1; ++j, ++it) {
+                const int x2 = it & 1;
+                if (ok) ok = wait_phase(bar(L::kSReady + x2), (it >> 1) & 1, abort);
+                if (ok && it >= 2)  // P V of two tiles ago has read this P buffer
+                    ok = wait_phase(bar(L::kOReady + x2), ((it >> 1) - 1) & 1, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                ptx::tc_fence_after_sync();
+                float x[32];
+                {
+                    uint32_t u[32];
+                    ptx::tmem_ld_x32_nowait(tl + L::kTS + R * x2 + 32 * sw, u);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(u[c]);
+                }
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(bar(L::kSFree + x2));
+                // masks
+                if (j < r.nct) {
+                    const int i = 2 * j + key / kQPage;
+                    const int pos = page_of(r, i) * kQPage + key % kQPage;
+                    const bool in = i < r.np && pos < r.ctx;
+                    if (!in || (pos < lo_all && pos >= sinks)) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            x[c] = in && pos >= s_lo[c] ? x[c] : neg_inf();
+                    }
+                } else {
+                    const int w = (j - r.nct) * 4 + quad;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        x[c] = (s_anc[c * 8 + w] >> lane) & 1u ? x[c] : neg_inf();
+                }
+                float top = neg_inf();
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (4 * q < live) {
+                        const float4 nm = *reinterpret_cast<const float4 *>(s_nm + 4 * q);
+                        top = fmaxf(top, fmaxf(fmaxf(fmaf(x[4 * q], P.sl2, nm.x),
+                                                     fmaf(x[4 * q + 1], P.sl2, nm.y)),
+                                               fmaxf(fmaf(x[4 * q + 2], P.sl2, nm.z),
+                                                     fmaf(x[4 * q + 3], P.sl2, nm.w))));
+                    }
+                }
+                if (!ok) *s_stop = 1;
+                if (!tcc::named_barrier_and(bid, 128, ok && !(top > kHeadroom))) {
+                    // ---- raise the reference maxima that need it (or stop, all together:
+                    // s_stop is not written between this barrier and the next)
+                    const bool stop = *s_stop != 0;
+                    float mine = neg_inf();  // column `lane`'s maximum over the warp's keys
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float m = warp_max_f32(x[c]);
+                        if (lane == c) mine = m;
+                    }
+                    s_red[quad * 32 + lane] = mine;
+                    tcc::named_barrier(bid, 128);
+                    if (stop) {
+                        ok = false;
+                        more = false;
+                        break;
+                    }
+                    const float m4 = fmaxf(fmaxf(s_red[lane], s_red[32 + lane]),
+                                           fmaxf(s_red[64 + lane], s_red[96 + lane])) * P.sl2;
+                    const float old = s_nm[lane];
+                    const bool need = m4 + old > kHeadroom;
+                    const float nm = need ? -m4 : old;
+                    const float al = need ? ex2(nm - old) : 1.f;  // 2^(m_old - m_new)
+                    tcc::named_barrier(bid, 128);
+                    if (quad == 0) {
+                        s_nm[lane] = nm;
+                        s_al[lane] = al;
+                    }
+                    tcc::named_barrier(bid, 128);
+                    if (j > s.j0) {
+                        // O and l of the earlier tiles, once the last P V is done
+                        ok = wait_phase(bar(L::kOReady + (x2 ^ 1)), ((it - 1) >> 1) & 1, abort);
+                        ok = __all_sync(0xffffffffu, ok);
+                        ptx::tc_fence_after_sync();
+#pragma unroll 1
+                        for (int part = 0; part < (NP > 1 ? 2 : 1); ++part) {
+#pragma unroll 1
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t o[16];
+                                const uint32_t at = tl + L::kTO + R * part + 32 * sw + 16 * q;
+                                ptx::tmem_ld_x16_nowait(at, o);
+                                ptx::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) *
+                                                           s_al[16 * q + e]);
+                                ptx::tmem_st_x16(at, o);
+                            }
+                        }
+                        ptx::tmem_wait_st();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) l[c] *= s_al[c];
+                    }
+                }
+                // ---- weights: P[key][row], a row of 128 bytes per key
+                uint8_t *prow = sm + L::kP + (uint32_t)x2 * L::kPSlabs * kSlab + key * 128;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (8 * q < live) {
+                        uint32_t w[NP][4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int c = 8 * q + 2 * e;
+                            const float2 nm = *reinterpret_cast<const float2 *>(s_nm + c);
+                            const float p0 = ex2(fmaf(x[c], P.sl2, nm.x));
+                            const float p1 = ex2(fmaf(x[c + 1], P.sl2, nm.y));
+                            l[c] += p0;
+                            l[c + 1] += p1;
+                            uint32_t part[NP];
+                            split_weights<NP>(p0, p1, part);
+#pragma unroll
+                            for (int k = 0; k < NP; ++k) w[k][e] = part[k];
+                        }
+#pragma unroll
+                        for (int k = 0; k < NP; ++k) {
+                            // R = 64: part k is slab k, this group's half of its rows;
+                            // R = 32: parts 0 and 1 share slab 0, part 2 starts slab 1
+                            const int slab = R == 64 ? k : k / 2;
+                            const int ch = (R == 64 ? 4 * sw : 4 * (k & 1)) + q;
+                            *reinterpret_cast<uint4 *>(prow + slab * kSlab +
+                                                       ((ch ^ (key & 7)) << 4)) =
+                                make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+                        }
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(bar(L::kPReady + x2));
+            }
+            if (!more) break;
+
+            // ---- the next unit's queries (every S of this one is done), then this one's
+            // results
+            Seg u = s;
+            more = walk.next(P, s_cum, s);
+            if (more) load_q(s);
+            const float part = column_sums(l, lane);
+            s_red[quad * 32 + lane] = part;
+            tcc::named_barrier(bid, 128);
+            float *s_l = s_al;  // 1 / l
+            const float sum = s_red[lane] + s_red[32 + lane] + s_red[64 + lane] + s_red[96 + lane];
+            const bool whole = u.j0 == 0 && u.j1 == u.r.nt;
+            const int piece = 2 * blockIdx.x + (u.j0 == 0 ? 1 : 0);
+            if (quad == 0) s_l[lane] = bad ? 0.f : whole ? 1.f / sum : 1.f;
+            tcc::named_barrier(bid, 128);
+            if (ok) ok = wait_phase(bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            ptx::tc_fence_after_sync();
+            float *pd = piece_data<D, R>(P, piece);
+            const int c = 32 * quad + lane;  // this thread's channel
+            if (32 * quad < D) {
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    if (8 * q >= live) break;
+                    uint32_t hi[8], lo[8];
+                    ptx::tmem_ld_x8_nowait(tl + L::kTO + 32 * sw + 8 * q, hi);
+                    if (NP > 1) ptx::tmem_ld_x8_nowait(tl + L::kTO + R + 32 * sw + 8 * q, lo);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int rr = 8 * q + e;
+                        if (rr >= live || !ok) continue;
+                        float o = __uint_as_float(hi[e]);
+                        if (NP > 1) o += __uint_as_float(lo[e]);
+                        o = bad ? 0.f : o * s_l[rr];
+                        const int r = 32 * sw + rr, row = u.mt * R + r;
+                        if (whole) {
+                            const size_t at = ((size_t)(u.r.off + row / P.grp) * a.H +
+                                               u.kvh * P.grp + row % P.grp) * D + c;
+                            if (a.out_f32)
+                                static_cast<float *>(a.out)[at] = o;
+                            else
+                                static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(o);
+                        } else {
+                            pd[r * D + c] = o;
+                        }
+                    }
+                }
+            }
+            if (!whole) {
+                if (quad == 0) {
+                    pd[R * D + 32 * sw + lane] = s_nm[lane];
+                    pd[R * D + R + 32 * sw + lane] = sum;
+                }
+                if (tid == 0) {
+                    int *h = hdr + (u.j0 == 0 ? 8 : 0);
+                    h[1] = u.b;
+                    h[2] = u.kvh;
+                    h[3] = u.mt;
+                    h[4] = first + it - (u.j1 - u.j0) - u.j0 + u.r.nt;  // end of the unit
+                    h[5] = total;
+                    h[6] = bad;
+                    h[0] = 1;
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before_sync();
     __syncthreads();
-    return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+    if (tid == 0 && *abort) report(a.status, TV_ERR_TIMEOUT);
+    if (warp == kWarpMma) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the pieces of the units that were cut: CTA (i, y) takes 8 rows of the unit that
+// main CTA i began and did not end, one warp per row:
+//   out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p.
+template <int D, int R>
+__global__ void __launch_bounds__(256) qcache_attention_join_kernel(const QParams P) {
+    const QAttnArgs &a = P.a;
+    const int i = blockIdx.x, lane = threadIdx.x % 32;
+    const int r = blockIdx.y * 8 + threadIdx.x / 32;
+    pdl_wait();
+    pdl_launch_next();
+    const int *hdr = reinterpret_cast<const int *>(a.ws) + ((size_t)2 * i + 1) * 8;
+    if (!hdr[0]) return;
+    const int b = hdr[1], kvh = hdr[2], mt = hdr[3], end = hdr[4], total = hdr[5], bad = hdr[6];
+    const int off = a.node_offsets[b], n = a.node_offsets[b + 1] - off;
+    const long long row = (long long)mt * R + r;
+    if (row >= (long long)n * P.grp) return;
+    // the CTA whose share holds the unit's last tile
+    const int last = (int)(((long long)end * min(P.grid, total) - 1) / total);
+    const int pieces = last - i + 1;
+    auto data = [&](int p) { return piece_data<D, R>(P, p == 0 ? 2 * i + 1 : 2 * (i + p)); };
+    float nm = kNoMax;
+    for (int p = lane; p < pieces; p += 32) nm = fminf(nm, data(p)[R * D + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) nm = fminf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
+    float o[D / 32], den = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < pieces; ++p) {
+        const float *d = data(p);
+        const float w = ex2(nm - d[R * D + r]);
+        den += w * d[R * D + R + r];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) o[c] += w * d[r * D + 32 * c + lane];
+    }
+    const float inv = bad ? 0.f : 1.f / den;
+    const size_t at = ((size_t)(off + row / P.grp) * a.H + kvh * P.grp + row % P.grp) * D + lane;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        const float y = bad ? 0.f : o[c] * inv;
+        if (a.out_f32)
+            static_cast<float *>(a.out)[at + 32 * c] = y;
+        else
+            static_cast<__nv_bfloat16 *>(a.out)[at + 32 * c] = __float2bfloat16_rn(y);
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    return n > 0 ? n : 152;
+}
+
+// Rows per unit: 32 when no request has more, else 64.
+int rows_per_unit(const QAttnArgs &a) { return a.max_nodes * (a.H / a.Hkv) <= 32 ? 32 : 64; }
+
+// One CTA per SM, or one per tile when a batch cannot have as many.
+int grid_size(const QAttnArgs &a) {
+    const int R = rows_per_unit(a);
+    const long long mts = ((long long)a.max_nodes * (a.H / a.Hkv) + R - 1) / R;
+    const long long tiles = (long long)a.B * a.Hkv * mts *
+                            ((a.max_pages + 1) / 2 + (a.max_nodes + kKeys - 1) / kKeys);
+    return (int)std::min<long long>(sm_count(), tiles);
+}
+
+template <int D, int R, int NP>
+cudaError_t launch_parts(const QAttnArgs &a, cudaStream_t s) {
+    using L = Lay<D, R, NP>;
+    static_assert(L::kAlloc <= tcc::kSmemLimit, "shared-memory plan exceeds the limit");
+    const cudaError_t attr = configure_smem_once(qcache_attention_kernel<D, R, NP>, false);
+    if (attr != cudaSuccess) return attr;
+    QParams P;
+    P.a = a;
+    P.grp = a.H / a.Hkv;
+    P.grid = grid_size(a);
+    P.sl2 = a.scale * 1.4426950408889634f;
+    for (P.b0 = 0; P.b0 < a.B; P.b0 += kChunkB) {
+        P.nb = std::min(kChunkB, a.B - P.b0);
+        cudaError_t e = launch_pdl(qcache_attention_kernel<D, R, NP>, dim3(P.grid),
+                                   dim3(L::kThreads), (size_t)L::kAlloc, s, P);
+        if (e != cudaSuccess) return e;
+        if (P.grid > 1) {
+            e = launch_pdl(qcache_attention_join_kernel<D, R>, dim3(P.grid, R / 8), dim3(256), 0,
+                           s, P);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    return cudaSuccess;
 }
 
 template <int D>
-__global__ void __launch_bounds__(128) qcache_attention_kernel(const QAttnArgs a) {
-    using R = qc::Rec<D>;
-    __shared__ float s_q[D], s_p[64], s_red[4];
-    __shared__ int s_path[kMaxNodes];
-    __shared__ int s_len, s_bad;
-    const int tid = threadIdx.x;
-    const int b = blockIdx.x / a.max_nodes, i = blockIdx.x % a.max_nodes, h = blockIdx.y;
-    const int kvh = h / (a.H / a.Hkv);
-    pdl_wait();
-    pdl_launch_next();
-    int off, n;
-    const bool range = request_range(a.node_offsets, b, a.T, a.max_nodes, off, n);
-    if (!range && tid == 0) report(a.status, TV_ERR_TREE);
-    if (!range || i >= n) return;
-    if (tid == 0) s_bad = 0;
-    __syncthreads();
-    for (int t = tid; t < n; t += 128) {
-        const int p = a.parent[off + t];
-        if (p < -1 || p >= t) s_bad = TV_ERR_TREE;
-    }
-    __syncthreads();
-    const int ctx = a.ctx_len[b];
-    if (tid == 0 && !s_bad && (ctx < 0 || ctx > (long long)a.max_pages * kQPage))
-        s_bad = TV_ERR_SHAPE;
-    if (tid == 0 && !s_bad) {
-        int len = 0;
-        for (int t = i; t >= 0; t = a.parent[off + t]) s_path[len++] = t;
-        s_len = len;
-    }
-    __syncthreads();
-    const int sinks = a.window > 0 ? min(a.sinks, max(ctx, 0)) : 0;
-    const int depth = s_len;
-    // the window's first position for this node, and for any node of the request
-    const long long lo = a.window > 0 ? max(0LL, (long long)ctx + depth - a.window) : 0;
-    const long long lo1 = a.window > 0 ? max(0LL, (long long)ctx + 1 - a.window) : 0;
-    if (!s_bad)
-        for (int p = tid; p * kQPage < ctx; p += 128) {
-            if (p * kQPage >= sinks && (p + 1LL) * kQPage <= lo1) continue;
-            const int page = a.table[(size_t)b * a.max_pages + p];
-            if (page < 0 || page >= a.num_pages) s_bad = TV_ERR_SHAPE;
-        }
-    __syncthreads();
-    const size_t row = (size_t)(off + i) * a.H + h;
-    float *of = static_cast<float *>(a.out) + row * D;
-    __nv_bfloat16 *oh = static_cast<__nv_bfloat16 *>(a.out) + row * D;
-    if (s_bad) {
-        if (tid == 0) report(a.status, s_bad);
-        if (tid < D) {
-            if (a.out_f32)
-                of[tid] = 0.f;
-            else
-                oh[tid] = __float2bfloat16_rn(0.f);
-        }
-        return;
-    }
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
-    if (tid < D) s_q[tid] = __bfloat162float(q[(size_t)(off + i) * a.q_stride + h * D + tid]);
-    __syncthreads();
-    const float ninf = __uint_as_float(0xff800000u);
-    float m = ninf, l = 0.f, o = 0.f;
-    const int pages = (ctx + kQPage - 1) / kQPage, tiles = pages + (depth + 63) / 64;
-    for (int t = 0; t < tiles; ++t) {
-        if (t < pages && t * kQPage >= sinks && (t + 1LL) * kQPage <= lo) continue;
-        const uint8_t *rec = nullptr;
-        if (t < pages)
-            rec = a.cache +
-                  ((size_t)a.table[(size_t)b * a.max_pages + t] * a.Hkv + kvh) * R::kBytes;
-        float x = ninf;
-        if (tid < 64 && t < pages) {
-            const int pos = t * kQPage + tid;
-            if (pos < ctx && (pos >= lo || pos < sinks)) {
-                x = 0.f;
-                for (int g = 0; g < (int)R::kGroups; ++g) {
-                    const float s = qc::scale_value(rec[R::kKScales + tid * R::kGroups + g]);
-                    float acc = 0.f;
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t word = *reinterpret_cast<const uint32_t *>(
-                            rec + R::kKCodes + (g * kQPage + tid) * 16 + w * 4);
-                        for (int e = 0; e < 8; ++e)
-                            acc += s_q[g * 32 + w * 8 + e] *
-                                   (float)((int)(word >> qc::code_shift(e) & 15u) - 8);
-                    }
-                    x += s * acc;
-                }
-                x *= a.scale;
-            }
-        } else if (tid < 64) {
-            const int r = (t - pages) * 64 + tid;  // r steps above node i
-            if (r < depth && (a.window <= 0 || r < a.window ||
-                              ctx + (long long)depth - r - 1 < a.sinks)) {
-                const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k_tree) +
-                                         (size_t)(off + s_path[r]) * a.kv_stride + kvh * D;
-                x = 0.f;
-                for (int c = 0; c < D; ++c) x += s_q[c] * __bfloat162float(k[c]);
-                x *= a.scale;
-            }
-        }
-        const float top = block_max(x, s_red);
-        const float mn = fmaxf(m, top), ref = mn == ninf ? 0.f : mn;
-        const float f = m == ninf ? 0.f : expf(m - ref);
-        if (tid < 64) s_p[tid] = x == ninf ? 0.f : expf(x - ref);
-        __syncthreads();
-        m = mn;
-        l *= f;
-        o *= f;
-        for (int j = 0; j < 64; ++j) {
-            const float p = s_p[j];
-            l += p;
-            if (p == 0.f || tid >= D) continue;
-            if (t < pages) {
-                const uint32_t word = *reinterpret_cast<const uint32_t *>(
-                    rec + R::kVCodes + ((j / 32) * D + tid) * 16 + ((j % 32) / 8) * 4);
-                o += p * qc::scale_value(rec[R::kVScales + (tid / 32) * kQPage + j]) *
-                     (float)((int)(word >> qc::code_shift(j & 7) & 15u) - 8);
-            } else {
-                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_tree) +
-                                         (size_t)(off + s_path[(t - pages) * 64 + j]) *
-                                             a.kv_stride + kvh * D;
-                o += p * __bfloat162float(v[tid]);
-            }
-        }
-        __syncthreads();
-    }
-    if (tid < D) {
-        if (a.out_f32)
-            of[tid] = o / l;
-        else
-            oh[tid] = __float2bfloat16_rn(o / l);
-    }
+cudaError_t launch_rows(const QAttnArgs &a, cudaStream_t s) {
+    if (rows_per_unit(a) == 32)
+        return a.out_f32 ? launch_parts<D, 32, 3>(a, s) : launch_parts<D, 32, 2>(a, s);
+    return a.out_f32 ? launch_parts<D, 64, 3>(a, s) : launch_parts<D, 64, 2>(a, s);
 }
 
 }  // namespace
 
 size_t qcache_attention_workspace_bytes(const QAttnArgs &a) {
-    (void)a;
-    return 0;
+    const size_t R = rows_per_unit(a);
+    return (size_t)2 * grid_size(a) * (8 + R * (a.d + 2)) * sizeof(float);
 }
 
 cudaError_t launch_qcache_attention(const QAttnArgs &a, cudaStream_t s) {
-    const dim3 grid(a.B * a.max_nodes, a.H);
-    return a.d == 64 ? launch_pdl(qcache_attention_kernel<64>, grid, dim3(128), 0, s, a)
-                     : launch_pdl(qcache_attention_kernel<128>, grid, dim3(128), 0, s, a);
+    return a.d == 64 ? launch_rows<64>(a, s) : launch_rows<128>(a, s);
 }
 
 }  // namespace tv
