@@ -22,8 +22,8 @@
 // in the workspace, joined by a second kernel.
 //
 // Warp roles: NSW = R / 32 softmax groups of 4 warps (32 rows each, lane = key), one group
-// that dequantises K, one for V, a producer warp (page table, bulk copies), a warp that
-// issues the products.  The reference maximum m of a row is raised only when a score
+// that dequantises K, one for V, a copy warp (segments, page table, bulk copies), one warp
+// each that issues S and P V, and one that prepares the next unit's rows.  The reference maximum m of a row is raised only when a score
 // exceeds it by more than 8 (log2 units); all 128 threads of a group vote per tile.  Weights
 // enter the value product as NP bf16 parts; sums l are kept in fp32 from the same weights.
 // Every mbarrier wait is bounded, as in tree_attention.cu.
@@ -83,93 +83,120 @@ __device__ __forceinline__ Req request(const QParams &P, int b) {
     return r;
 }
 
-__device__ __forceinline__ int page_of(const Req &r, int i) { return i < r.sp ? i : i - r.sp + r.lp; }
-
-// A run of tiles [j0, j1) of one unit.
+// A run of tiles [j0, j1) of one unit, as the copy warp hands it to the other roles.
 struct Seg {
-    Req r;
-    int b, kvh, mt, j0, j1;
+    int b, kvh, mt, j0, j1;              // j1 = 0: no more
+    int off, n, ctx, bad;                // as in Req
+    int sp, lp, np, nct, nt;
 };
+constexpr int kSegInts = 16, kSegs = 4;  // ring of segments in shared memory
+static_assert(sizeof(Seg) <= kSegInts * 4, "");
+
+__device__ __forceinline__ int page_of(const Seg &s, int i) {
+    return i < s.sp ? i : i - s.sp + s.lp;
+}
 
 // Walks this CTA's share [t, t1) of the tiles.
 template <int R>
-struct Walk {
-    int t, t1;
-    __device__ bool next(const QParams &P, const int *cum, Seg &s) {
-        if (t >= t1) return false;
-        int lo = 0, hi = P.nb - 1;  // the last request whose tiles begin at or before t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cum[mid] <= t)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        s.b = P.b0 + lo;
-        s.r = request<R>(P, s.b);
-        const int rem = t - cum[lo], unit = rem / s.r.nt;
-        s.j0 = rem % s.r.nt;
-        s.j1 = min(s.r.nt, s.j0 + (t1 - t));
-        s.kvh = unit / s.r.mts;
-        s.mt = unit % s.r.mts;
-        t += s.j1 - s.j0;
-        return true;
+__device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, int t, int t1) {
+    Seg s{};
+    if (t >= t1) return s;
+    int lo = 0, hi = P.nb - 1;  // the last request whose tiles begin at or before t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
     }
-};
+    const Req r = request<R>(P, P.b0 + lo);
+    const int rem = t - cum[lo], unit = rem / r.nt;
+    s.b = P.b0 + lo;
+    s.j0 = rem % r.nt;
+    s.j1 = min(r.nt, s.j0 + (t1 - t));
+    s.kvh = unit / r.mts;
+    s.mt = unit % r.mts;
+    s.off = r.off;
+    s.n = r.n;
+    s.ctx = r.ctx;
+    s.bad = r.bad;
+    s.sp = r.sp;
+    s.lp = r.lp;
+    s.np = r.np;
+    s.nct = r.nct;
+    s.nt = r.nt;
+    return s;
+}
 
 // Shared memory.  P: two buffers of NP parts; at R = 64 a part fills a 128-byte row, at
-// R = 32 two parts share one.
+// R = 32 two parts share one.  Q and the rows' masks come in two buffers, one per unit.
 template <int D, int R, int NP>
 struct Lay {
     static constexpr int kSW = R / 32;                     // softmax groups
-    static constexpr int kWarps = 4 * kSW + 8 + 2;
+    static constexpr int kWarps = 4 * kSW + 16 + 4;
     static constexpr int kThreads = kWarps * 32;
+    // registers: at launch (all that fit), and after the split; the control warps keep theirs
+    static constexpr int kRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kRegsOperand = 48;
+    static constexpr int kRegsSoftmax = kSW == 2 ? 120 : 168;
+    static_assert(kThreads * kRegs >=
+                      128 * (kSW * kRegsSoftmax + 4 * kRegsOperand + kRegs), "register split");
     static constexpr uint32_t kRec = qrec_bytes(D);
     static constexpr uint32_t kPSlabs = (NP * R + 63) / 64;
+    static constexpr uint32_t kQBytes = R * D * 2;
     static constexpr uint32_t kQ = 0;
-    static constexpr uint32_t kP = kQ + R * D * 2;
+    static constexpr uint32_t kP = kQ + 2 * kQBytes;
     static constexpr uint32_t kRing = kP + 2 * kPSlabs * kSlab;
-    static constexpr uint32_t kMiscBytes = 18 * 1024;
+    static constexpr uint32_t kMiscBytes = 20 * 1024;
     static constexpr int kStages =
         (int)std::min<uint32_t>(16, (227 * 1024 - 1024 - kMiscBytes - kRing) / (2 * kRec));
     static constexpr uint32_t kCum = kRing + kStages * 2 * kRec;       // int [kChunkB + 1]
-    static constexpr uint32_t kPar = kCum + (kChunkB + 4) * 4;         // int16 [kSW][256]
-    static constexpr uint32_t kAnc = kPar + kSW * kMaxNodes * 2;       // u32 [kSW][32][8]
-    static constexpr uint32_t kLo = kAnc + kSW * 32 * 8 * 4;           // int [kSW][32]
-    static constexpr uint32_t kNm = kLo + kSW * 128;                   // float [kSW][32]
-    static constexpr uint32_t kAl = kNm + kSW * 128;                   // float [kSW][32]
-    static constexpr uint32_t kRed = kAl + kSW * 128;                  // float [kSW][4][32]
-    static constexpr uint32_t kVs = kRed + kSW * 512;                  // uint2 [4][2][32]
-    static constexpr uint32_t kBar = kVs + 4 * 2 * 32 * 8;
-    // mbarriers: ring full / empty; K and V operands written; Q loaded; S ready / read;
-    // P written; P V done; every product done
+    static constexpr uint32_t kPar = kCum + (kChunkB + 4) * 4;         // int16 [256]
+    static constexpr uint32_t kSee = kPar + kMaxNodes * 2;             // u32 [2][kSW][256]
+    static constexpr uint32_t kLo = kSee + 2 * kSW * kMaxNodes * 4;    // int [2][R]
+    static constexpr uint32_t kRow = kLo + 2 * R * 4;                  // int [2][R]
+    static constexpr uint32_t kNm = kRow + 2 * R * 4;                  // float [R]
+    static constexpr uint32_t kAl = kNm + R * 4;                       // float [R]
+    static constexpr uint32_t kRed = kAl + R * 4;                      // float [kSW][4][32]
+    static constexpr uint32_t kVs = kRed + kSW * 512;                  // uint2 [2][4][32]
+    static constexpr uint32_t kSeg = kVs + 2 * 4 * 32 * 8;             // int [kSegs][16]
+    static constexpr uint32_t kBar = kSeg + kSegs * kSegInts * 4;
+    // mbarriers: ring full / empty; K and V operands written; a unit's rows prepared /
+    // done with; S ready / read; P written; P V done; segments written / taken; all done
     static constexpr int kFull = 0, kEmpty = kFull + kStages, kKReady = kEmpty + kStages,
-                         kVReady = kKReady + 2, kQReady = kVReady + 2, kSReady = kQReady + 1,
-                         kSFree = kSReady + 2, kPReady = kSFree + 2, kOReady = kPReady + 2,
-                         kDone = kOReady + 2, kNumBars = kDone + 1;
-    static constexpr uint32_t kMisc = kBar + kNumBars * 8;  // tmem, abort, scan [32], wg flags
+                         kVReady = kKReady + 2, kPrep = kVReady + 2, kPrepFree = kPrep + 2,
+                         kSReady = kPrepFree + 2, kSFree = kSReady + 2, kPReady = kSFree + 2,
+                         kOReady = kPReady + 2, kSegFull = kOReady + 2,
+                         kSegFree = kSegFull + kSegs, kDone = kSegFree + kSegs,
+                         kNumBars = kDone + 2;
+    static constexpr uint32_t kMisc = kBar + kNumBars * 8;  // tmem, abort, scan, stop, bad
     static constexpr uint32_t kBytes = kMisc + 256;
     static constexpr uint32_t kAlloc = kBytes + 1024;
     static_assert(kBytes - kCum <= kMiscBytes && kStages >= 3, "shared-memory plan");
     // tensor memory columns
     static constexpr uint32_t kTS = 0;                       // S^T x 2
     static constexpr uint32_t kTO = 2 * R;                   // O^T, hi sums then lo sums
-    static constexpr uint32_t kOWidth = NP == 1 ? (R < 64 ? 64 : R) : NP == 3 && R == 32 ? 96 : 2 * R;
+    static constexpr uint32_t kOWidth = NP == 1 ? 64 : NP == 3 && R == 32 ? 96 : 2 * R;
     static constexpr uint32_t kTK = kTO + kOWidth;           // K x 2
     static constexpr uint32_t kTV = kTK + D;                 // V^T x 2
     static_assert(kTV + 128 <= kTmemCols, "tensor memory plan");
 };
 
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort) {
-    if (ptx::mbar_test_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!ptx::mbar_try_wait(bar, parity, 20000)) {
-        if (*abort || clock64() - t0 > kWaitLimit) {
-            *abort = 1;
-            return false;
-        }
+// Wait for a phase, giving up when the CTA's abort flag is raised or after 2^24 tries (of
+// some 100 cycles each).  Two dozen warps wait here most of the time and a try returns
+// after a fraction of a microsecond, so the loop is kept to a few instructions: with a
+// clock read and the flag in every round the waits took more issue slots than the work.
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort) {
+    for (int k = 0; k < 1 << 14 && !*abort; ++k) {
+#pragma unroll 1
+        for (int n = 0; n < 1 << 10; ++n)
+            if (ptx::mbar_try_wait_hw(bar, parity)) return true;
     }
-    return true;
+    *abort = 1;
+    return false;
+}
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return ptx::mbar_try_wait_hw(bar, parity) || wait_slow(bar, parity, abort);
 }
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -198,6 +225,22 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
         }
     }
     return v[0];
+}
+
+// (x0, x1) * s + (a0, a1), and (x0, x1) + (a0, a1), two lanes per instruction.
+__device__ __forceinline__ void fma2(float &x0, float &x1, float s, float a0, float a1) {
+    asm("{\n\t.reg .b64 x, s, a;\n\t"
+        "mov.b64 x, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 a, {%3, %4};\n\t"
+        "fma.rn.f32x2 x, x, s, a;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(x0), "+f"(x1)
+        : "f"(s), "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ void add2(float &x0, float &x1, float a0, float a1) {
+    asm("{\n\t.reg .b64 x, a;\n\t"
+        "mov.b64 x, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\t"
+        "add.rn.f32x2 x, x, a;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(x0), "+f"(x1)
+        : "f"(a0), "f"(a1));
 }
 
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
@@ -254,28 +297,33 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     using L = Lay<D, R, NP>;
     using Rc = qc::Rec<D>;
     constexpr int SW = L::kSW, NS = L::kStages;
-    constexpr int kWarpK = 4 * SW, kWarpV = kWarpK + 4, kWarpCopy = kWarpV + 4,
-                  kWarpMma = kWarpCopy + 1;
+    constexpr int kWarpK = 4 * SW, kWarpV = kWarpK + 8, kWarpCopy = kWarpV + 8,
+                  kWarpMma = kWarpCopy + 1, kWarpPv = kWarpMma + 1, kWarpPrep = kWarpPv + 1;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // aligned by an offset, not through an integer: the compiler still sees shared memory
+    uint8_t *sm = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
     const QAttnArgs &a = P.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3;
     const uint32_t sbase = ptx::smem_addr(sm);
     auto bar = [&](int i) { return sbase + L::kBar + 8u * (uint32_t)i; };
     int *s_cum = reinterpret_cast<int *>(sm + L::kCum);
+    int *s_seg = reinterpret_cast<int *>(sm + L::kSeg);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(sm + L::kMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
     int *s_scan = reinterpret_cast<int *>(sm + L::kMisc + 16);
-    int *s_wg = reinterpret_cast<int *>(sm + L::kMisc + 16 + 128);  // [SW][2]: bad, stop
+    volatile int *s_stop = reinterpret_cast<volatile int *>(sm + L::kMisc + 16 + 128);  // [SW]
+    volatile int *s_bad = s_stop + 4;                                                   // [2]
 
     if (tid == 0) {
         *abort = 0;
+        for (int i = 0; i < SW; ++i) s_stop[i] = 0;
         for (int i = 0; i < L::kNumBars; ++i) {
             uint32_t count = 1;
-            if (i >= L::kEmpty && i < L::kKReady) count = 8;                 // K and V warps
-            if (i >= L::kKReady && i < L::kQReady) count = 128;
-            if (i == L::kQReady || (i >= L::kSFree && i < L::kOReady)) count = 128 * SW;
+            if (i >= L::kEmpty && i < L::kKReady) count = 16;            // K and V warps
+            if (i >= L::kKReady && i < L::kPrep) count = 256;
+            if (i >= L::kPrepFree && i < L::kSReady) count = 4 * SW;     // softmax warps
+            if (i >= L::kSFree && i < L::kOReady) count = 128 * SW;
+            if (i >= L::kSegFree && i < L::kDone) count = 4 * SW + 16 + 3;
             ptx::mbar_init(bar(i), count);
         }
         ptx::fence_mbar_init();
@@ -328,25 +376,44 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     const int total = s_cum[P.nb];
     const int shares = min(P.grid, total), me = min((int)blockIdx.x, shares);
     const int first = shares > 0 ? (int)((long long)total * me / shares) : 0;
-    Walk<R> walk{first, me < shares ? (int)((long long)total * (me + 1) / shares) : first};
-    const int ntiles = walk.t1 - first;
-    Seg s;
+    const int t1 = me < shares ? (int)((long long)total * (me + 1) / shares) : first;
+
+    // Segment `i` of this CTA, from the ring; false at the end (or when a wait expired).
+    auto take = [&](int i, Seg &s) {
+        const bool got = __all_sync(
+            0xffffffffu, wait_phase(bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, abort));
+        if (!got) return false;
+        s = *reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(L::kSegFree + i % kSegs));
+        return s.j1 > 0;
+    };
 
     if (warp == kWarpCopy) {
-        // ------------------------------------------------ producer: one bulk copy per page;
-        // the lanes hold the next 32 pages' records
-        int rc = 0;  // context tiles so far
+        // ------------------------------------------------ segments, and one bulk copy per
+        // page; the lanes hold the next 32 pages' records
+        int rc = 0, t = first;  // context tiles so far, next tile
         bool ok = true;
-        while (ok && walk.next(P, s_cum, s)) {
-            const int end = min(s.j1, s.r.nct);
+        for (int i = 0; ok; ++i) {
+            const Seg s = next_segment<R>(P, s_cum, t, t1);
+            ok = __all_sync(0xffffffffu, i < kSegs || wait_phase(bar(L::kSegFree + i % kSegs),
+                                                                 (i / kSegs - 1) & 1, abort));
+            if (!ok) break;
+            if (lane == 0) {
+                *reinterpret_cast<Seg *>(s_seg + (i % kSegs) * kSegInts) = s;
+                ptx::mbar_arrive(bar(L::kSegFull + i % kSegs));
+            }
+            if (s.j1 == 0) break;
+            t += s.j1 - s.j0;
+            const int end = min(s.j1, s.nct);
             const uint8_t *rec = nullptr;
             for (int j = s.j0; j < end; ++j) {
                 const int k = (j - s.j0) % 16;
                 if (k == 0) {
-                    const int i = 2 * j + lane;
+                    const int i2 = 2 * j + lane;
                     int page = 0;
-                    if (i < s.r.np) {
-                        page = a.table[(size_t)s.b * a.max_pages + page_of(s.r, i)];
+                    if (i2 < s.np) {
+                        page = a.table[(size_t)s.b * a.max_pages + page_of(s, i2)];
                         if (page < 0 || page >= a.num_pages) page = 0;  // the unit is bad
                     }
                     rec = a.cache + ((size_t)page * a.Hkv + s.kvh) * L::kRec;
@@ -356,7 +423,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                                 rc < NS || wait_phase(bar(L::kEmpty + st), ((rc / NS) - 1) & 1,
                                                       abort));
                 if (!ok) break;
-                const bool two = 2 * j + 1 < s.r.np;
+                const bool two = 2 * j + 1 < s.np;
                 const uint32_t dst = sbase + L::kRing + (uint32_t)st * 2 * L::kRec;
                 if (lane == 2 * k) {
                     ptx::mbar_arrive_expect_tx(bar(L::kFull + st), (two ? 2 : 1) * L::kRec);
@@ -375,156 +442,191 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 ptx::mbar_wait(bar(L::kFull + j % NS), (j / NS) & 1, kWaitLimit);
         __syncwarp();
     } else if (warp == kWarpMma) {
-        // ------------------------------------------------ product issuer: whichever of the
-        // next S and the next P V is ready
-        if (lane == 0 && ntiles > 0) {
-            constexpr uint32_t idS = ptx::idesc_bf16_f32(128, R);
-            constexpr uint32_t nPV = NP == 1 ? L::kOWidth : 2 * R;
-            constexpr uint32_t idPV = ptx::idesc_bf16_f32_bmn(128, nPV);
-            constexpr uint32_t id3 = ptx::idesc_bf16_f32_bmn(128, 64);
-            const uint32_t sQ = sbase + L::kQ;
-            Walk<R> wp = walk;
-            int js = 0, jp = 0, s_end = 0, p_first = 0, p_end = 0, seg = -1;
-            bool ok = true;
-            long long t_last = clock64();
-            while (ok && jp < ntiles) {
-                bool progressed = false;
-                if (js < ntiles) {
-                    if (js == s_end) {
-                        walk.next(P, s_cum, s);
-                        s_end = js + s.j1 - s.j0;
-                        ++seg;
-                    }
-                    const int x = js & 1;
-                    // (Q's phase of this unit stays complete until the next unit's, which
-                    // needs this unit's last S first)
-                    if (ptx::mbar_test_wait(bar(L::kKReady + x), (js >> 1) & 1) &&
-                        (js < 2 || ptx::mbar_test_wait(bar(L::kSFree + x), ((js >> 1) - 1) & 1)) &&
-                        ptx::mbar_test_wait(bar(L::kQReady), seg & 1)) {
-                        ptx::tc_fence_after_sync();
+        // ------------------------------------------------ S^T = K Q^T of every tile
+        constexpr uint32_t idS = ptx::idesc_bf16_f32(128, R);
+        const uint32_t lead = ptx::elect_one();
+        int it = 0;
+        bool ok = true;
+        Seg s;
+        for (int i = 0; ok && take(i, s); ++i) {
+            const uint32_t sQ = sbase + L::kQ + (i & 1) * L::kQBytes;
+            ok = wait_phase(bar(L::kPrep + (i & 1)), (i >> 1) & 1, abort);
+            for (int j = s.j0; j < s.j1; ++j, ++it) {
+                const int x = it & 1;
+                ok = ok && wait_phase(bar(L::kKReady + x), (it >> 1) & 1, abort) &&
+                     (it < 2 || wait_phase(bar(L::kSFree + x), ((it >> 1) - 1) & 1, abort));
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                ptx::tc_fence_after_sync();
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            ptx::mma_bf16_ts(
-                                tmem + L::kTS + R * x, tmem + L::kTK + (D / 2) * x + 8u * kk,
-                                ptx::desc_kmajor_sw128(sQ + (kk >> 2) * (R * 128) + (kk & 3) * 32,
-                                                       1024),
-                                idS, kk > 0);
-                        ptx::mma_commit(bar(L::kSReady + x));
-                        ++js;
-                        progressed = true;
-                    }
-                }
-                if (jp < js) {
-                    if (jp == p_end) {
-                        wp.next(P, s_cum, s);
-                        p_first = jp;
-                        p_end = jp + s.j1 - s.j0;
-                    }
-                    const int x = jp & 1;
-                    if (ptx::mbar_test_wait(bar(L::kVReady + x), (jp >> 1) & 1) &&
-                        ptx::mbar_test_wait(bar(L::kPReady + x), (jp >> 1) & 1)) {
-                        ptx::tc_fence_after_sync();
-                        const uint32_t sP = sbase + L::kP + (uint32_t)x * L::kPSlabs * kSlab;
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const uint32_t av = tmem + L::kTV + 64u * x + 8u * kk;
-                            const uint32_t acc = jp > p_first || kk > 0;
-                            ptx::mma_bf16_ts(
-                                tmem + L::kTO, av,
-                                ptx::desc_mnmajor_sw128(sP + kk * 2048u, nPV > 64 ? kSlab : 0u,
-                                                        1024),
-                                idPV, acc);
-                            // the third part adds to the second's sums (at R = 32 its row
-                            // has 32 idle columns, which go to idle columns)
-                            if constexpr (NP == 3)
-                                ptx::mma_bf16_ts(
-                                    tmem + L::kTO + R, av,
-                                    ptx::desc_mnmajor_sw128(
-                                        sP + (R == 64 ? 2 : 1) * kSlab + kk * 2048u, 0u, 1024),
-                                    id3, 1u);
-                        }
-                        ptx::mma_commit(bar(L::kOReady + x));
-                        ++jp;
-                        progressed = true;
-                    }
-                }
-                if (progressed) {
-                    t_last = clock64();
-                } else {
-                    // sleep on the event most likely next
-                    if (jp < js)
-                        ptx::mbar_try_wait(bar(L::kPReady + (jp & 1)), (jp >> 1) & 1, 500);
-                    else
-                        ptx::mbar_try_wait(bar(L::kKReady + (js & 1)), (js >> 1) & 1, 500);
-                    if (*abort || clock64() - t_last > kWaitLimit) {
-                        *abort = 1;
-                        ok = false;
-                    }
-                }
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ptx::mma_bf16_ts_lead(
+                        tmem + L::kTS + R * x, tmem + L::kTK + (D / 2) * x + 8u * kk,
+                        ptx::desc_kmajor_sw128(sQ + (kk >> 2) * (R * 128) + (kk & 3) * 32, 1024),
+                        idS, kk > 0, lead);
+                ptx::mma_commit_lead(bar(L::kSReady + x), lead);
             }
-            ptx::mma_commit(bar(L::kDone));
-            ptx::mbar_wait(bar(L::kDone), 0, kWaitLimit);
+        }
+        __syncwarp();
+        ptx::mma_commit_lead(bar(L::kDone), lead);
+        ptx::mbar_wait(bar(L::kDone), 0, kWaitLimit);
+    } else if (warp == kWarpPv) {
+        // ------------------------------------------------ O^T += V^T P^T of every tile
+        constexpr uint32_t nPV = NP == 1 ? 64 : 2 * R;
+        constexpr uint32_t idPV = ptx::idesc_bf16_f32_bmn(128, nPV);
+        constexpr uint32_t id3 = ptx::idesc_bf16_f32_bmn(128, 64);
+        const uint32_t lead = ptx::elect_one();
+        int it = 0;
+        bool ok = true;
+        Seg s;
+        for (int i = 0; ok && take(i, s); ++i) {
+            for (int j = s.j0; j < s.j1; ++j, ++it) {
+                const int x = it & 1;
+                ok = wait_phase(bar(L::kVReady + x), (it >> 1) & 1, abort) &&
+                     wait_phase(bar(L::kPReady + x), (it >> 1) & 1, abort);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                ptx::tc_fence_after_sync();
+                const uint32_t sP = sbase + L::kP + (uint32_t)x * L::kPSlabs * kSlab;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t av = tmem + L::kTV + 64u * x + 8u * kk;
+                    ptx::mma_bf16_ts_lead(
+                        tmem + L::kTO, av,
+                        ptx::desc_mnmajor_sw128(sP + kk * 2048u, nPV > 64 ? kSlab : 0u, 1024),
+                        idPV, kk > 0 || j > s.j0, lead);
+                    // the third part adds to the second's sums (at R = 32 its row has 32
+                    // idle columns, which go to idle columns)
+                    if constexpr (NP == 3)
+                        ptx::mma_bf16_ts_lead(
+                            tmem + L::kTO + R, av,
+                            ptx::desc_mnmajor_sw128(sP + (R == 64 ? 2 : 1) * kSlab + kk * 2048u,
+                                                    0u, 1024),
+                            id3, 1u, lead);
+                }
+                ptx::mma_commit_lead(bar(L::kOReady + x), lead);
+            }
+        }
+        __syncwarp();
+        ptx::mma_commit_lead(bar(L::kDone + 1), lead);
+        ptx::mbar_wait(bar(L::kDone + 1), 0, kWaitLimit);
+    } else if (warp == kWarpPrep) {
+        // ------------------------------------------------ a unit's rows, one unit ahead:
+        // queries, root-path masks, windows, output rows; the tree's and the pages' checks
+        int16_t *s_par = reinterpret_cast<int16_t *>(sm + L::kPar);
+        Seg s;
+        for (int i = 0; take(i, s); ++i) {
+            const int x = i & 1;
+            if (!__all_sync(0xffffffffu, i < 2 || wait_phase(bar(L::kPrepFree + x),
+                                                             ((i >> 1) - 1) & 1, abort)))
+                break;
+            // per softmax group and tree node: the group's rows that see the node
+            uint32_t *s_see = reinterpret_cast<uint32_t *>(sm + L::kSee) + x * SW * kMaxNodes;
+            int *s_lo = reinterpret_cast<int *>(sm + L::kLo) + x * R;
+            int *s_row = reinterpret_cast<int *>(sm + L::kRow) + x * R;
+            const int nrows = (int)min((long long)s.n * P.grp - (long long)s.mt * R, (long long)R);
+            // rows past the last keep what they held: their columns are never used
+            constexpr int CH = D / 8;  // 16-byte pieces of a row, a row per CH lanes
+            for (int r = lane / CH; r < nrows; r += 32 / CH) {
+                const int row = s.mt * R + r, node = row / P.grp, ch = lane % CH;
+                ptx::cp_async_16(sbase + L::kQ + x * L::kQBytes + (ch / 8) * (R * 128) + r * 128 +
+                                     ((ch % 8) ^ (r & 7)) * 16,
+                                 static_cast<const __nv_bfloat16 *>(a.q) +
+                                     (size_t)(s.off + node) * a.q_stride +
+                                     (size_t)(s.kvh * P.grp + row % P.grp) * D + ch * 8);
+            }
+            int bad = s.bad ? TV_ERR_SHAPE : 0;
+            for (int k = lane; k < s.np; k += 32) {
+                const int page = a.table[(size_t)s.b * a.max_pages + page_of(s, k)];
+                if (page < 0 || page >= a.num_pages) bad = TV_ERR_SHAPE;
+            }
+            for (int k = lane; k < s.n; k += 32) {
+                const int p = a.parent[s.off + k];
+                s_par[k] = (int16_t)p;
+                if (p < -1 || p >= k) bad = TV_ERR_TREE;
+            }
+            for (int k = lane; k < SW * kMaxNodes; k += 32) s_see[k] = 0;
+            bad = __reduce_max_sync(0xffffffffu, bad);
+            __syncwarp();
+            for (int r = lane; r < R; r += 32) {
+                int lo = 0;
+                const int row = s.mt * R + r, node = row / P.grp;
+                if (r < nrows && !bad) {
+                    int depth = 0;
+                    for (int q = node; q >= 0; q = s_par[q]) ++depth;
+                    if (a.window > 0)
+                        lo = (int)min(max((long long)s.ctx + depth - a.window, 0LL), 0x7fffffffLL);
+                    int up = 0;  // steps above the node
+                    for (int q = node; q >= 0; q = s_par[q], ++up) {
+                        if (a.window == 0 || up < a.window ||
+                            (long long)s.ctx + depth - up - 1 < a.sinks)
+                            atomicOr(s_see + (r / 32) * kMaxNodes + q, 1u << lane);
+                    }
+                }
+                s_lo[r] = lo;
+                s_row[r] = (s.off + node) * a.H + s.kvh * P.grp + row % P.grp;
+            }
+            if (lane == 0) {
+                s_bad[x] = bad;
+                if (bad) report(a.status, bad);
+            }
+            ptx::cp_async_wait_all();
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(L::kPrep + x));
         }
         __syncwarp();
     } else if (warp >= kWarpV) {
-        // ------------------------------------------------ V^T operand: thread = channel
-        const int c = 32 * quad + lane;
-        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTV;
-        uint2 *s_vs = reinterpret_cast<uint2 *>(sm + L::kVs) + quad * 64;
+        // ------------------------------------------------ V^T operand: thread = channel, a
+        // warpgroup per half of the tile's keys
+        ptx::regs_dec<L::kRegsOperand>();
+        const int c = 32 * quad + lane, h = (warp - kWarpV) / 4;
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTV + 32u * h;
+        uint2 *s_vs = reinterpret_cast<uint2 *>(sm + L::kVs) + (warp - kWarpV) * 32;
         const bool live = 32 * quad < D;
         int it = 0, rc = 0;
         bool ok = true;
-        while (ok && walk.next(P, s_cum, s)) {
-            const long long vis = a.window > 0 ? (long long)s.r.ctx + 1 - a.window : 0;
+        Seg s;
+        for (int i = 0; ok && take(i, s); ++i) {
+            const long long vis = a.window > 0 ? (long long)s.ctx + 1 - a.window : 0;
             const int sinks = a.window > 0 ? a.sinks : 0;
             for (int j = s.j0; j < s.j1; ++j, ++it) {
                 const uint32_t dst = tl + 64u * (it & 1);
                 if (it >= 2)
                     ok = wait_phase(bar(L::kOReady + (it & 1)), ((it >> 1) - 1) & 1, abort);
-                if (j < s.r.nct) {
+                if (j < s.nct) {
                     const int st = rc % NS;
                     ok = ok && wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     ptx::tc_fence_after_sync();
-                    const uint8_t *rec = sm + L::kRing + (uint32_t)st * 2 * L::kRec;
+                    const uint8_t *rec = sm + L::kRing + ((uint32_t)st * 2 + h) * L::kRec;
                     if (live) {
                         // the group's scales (a warp's 32 channels), two positions per lane;
                         // a position that no node sees gets 0, whatever the cache holds there
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t b2 = *reinterpret_cast<const uint16_t *>(
-                                rec + h * L::kRec + Rc::kVScales + quad * kQPage + 2 * lane);
-                            uint32_t s0 = scale_bf16(b2 & 0xFFu), s1 = scale_bf16(b2 >> 8);
-                            const int i = 2 * j + h;
-                            const int pos = page_of(s.r, i) * kQPage + 2 * lane;
-                            if (i >= s.r.np || pos >= s.r.ctx || (pos < vis && pos >= sinks))
-                                s0 = 0;
-                            if (i >= s.r.np || pos + 1 >= s.r.ctx ||
-                                (pos + 1 < vis && pos + 1 >= sinks))
-                                s1 = 0;
-                            const uint32_t s2 = s0 | (s1 << 16);
-                            s_vs[h * 32 + lane] = make_uint2(s2, minus_136(s2));
-                        }
+                        const uint32_t b2 = *reinterpret_cast<const uint16_t *>(
+                            rec + Rc::kVScales + quad * kQPage + 2 * lane);
+                        uint32_t s0 = scale_bf16(b2 & 0xFFu), s1 = scale_bf16(b2 >> 8);
+                        const int i2 = 2 * j + h, pos = page_of(s, i2) * kQPage + 2 * lane;
+                        if (i2 >= s.np || pos >= s.ctx || (pos < vis && pos >= sinks)) s0 = 0;
+                        if (i2 >= s.np || pos + 1 >= s.ctx || (pos + 1 < vis && pos + 1 >= sinks))
+                            s1 = 0;
+                        const uint32_t s2 = s0 | (s1 << 16);
+                        s_vs[lane] = make_uint2(s2, minus_136(s2));
                         __syncwarp();
+#pragma unroll 1
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t out[16];
+                            const uint4 w4 = *reinterpret_cast<const uint4 *>(
+                                rec + Rc::kVCodes + (q * D + c) * 16);
+                            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t out[32];
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const uint4 w4 = *reinterpret_cast<const uint4 *>(
-                                    rec + h * L::kRec + Rc::kVCodes + (q * D + c) * 16);
-                                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const uint4 sc = *reinterpret_cast<const uint4 *>(
-                                        s_vs + h * 32 + q * 16 + 2 * e);
-                                    out[16 * q + 2 * e] =
-                                        fma_bf16x2(code_pair(w[e / 2], 2 * (e & 1)), sc.x, sc.y);
-                                    out[16 * q + 2 * e + 1] = fma_bf16x2(
-                                        code_pair(w[e / 2], 2 * (e & 1) + 1), sc.z, sc.w);
-                                }
+                            for (int e = 0; e < 8; ++e) {
+                                const uint4 sc =
+                                    *reinterpret_cast<const uint4 *>(s_vs + q * 16 + 2 * e);
+                                out[2 * e] =
+                                    fma_bf16x2(code_pair(w[e / 2], 2 * (e & 1)), sc.x, sc.y);
+                                out[2 * e + 1] =
+                                    fma_bf16x2(code_pair(w[e / 2], 2 * (e & 1) + 1), sc.z, sc.w);
                             }
-                            ptx::tmem_st_x32(dst + 32u * h, out);
+                            ptx::tmem_st_x16(dst + 16u * q, out);
                         }
                     }
                     __syncwarp();
@@ -534,21 +636,21 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     ptx::tc_fence_after_sync();
                     if (live) {
-                        const int n0 = (j - s.r.nct) * kKeys;
+                        const int n0 = (j - s.nct) * kKeys + 64 * h;
                         const uint16_t *v = static_cast<const uint16_t *>(a.v_tree) +
-                                            (size_t)s.r.off * a.kv_stride + s.kvh * D + c;
+                                            (size_t)s.off * a.kv_stride + s.kvh * D + c;
 #pragma unroll 1
-                        for (int h = 0; h < 4; ++h) {
+                        for (int q = 0; q < 2; ++q) {
                             uint32_t out[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                const int n = n0 + 32 * h + 2 * e;
-                                const uint32_t x0 = n < s.r.n ? v[(size_t)n * a.kv_stride] : 0;
+                                const int n = n0 + 32 * q + 2 * e;
+                                const uint32_t x0 = n < s.n ? v[(size_t)n * a.kv_stride] : 0;
                                 const uint32_t x1 =
-                                    n + 1 < s.r.n ? v[(size_t)(n + 1) * a.kv_stride] : 0;
+                                    n + 1 < s.n ? v[(size_t)(n + 1) * a.kv_stride] : 0;
                                 out[e] = x0 | (x1 << 16);
                             }
-                            ptx::tmem_st_x16(dst + 16u * h, out);
+                            ptx::tmem_st_x16(dst + 16u * q, out);
                         }
                     }
                 }
@@ -559,18 +661,21 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp >= kWarpK) {
-        // ------------------------------------------------ K operand: thread = key
-        const int key = 32 * quad + lane;
-        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTK;
+        // ------------------------------------------------ K operand: thread = key, a
+        // warpgroup per half of the channels
+        ptx::regs_dec<L::kRegsOperand>();
+        const int key = 32 * quad + lane, g0 = (warp - kWarpK) / 4 * (D / 64);
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTK + 16u * g0;
         int it = 0, rc = 0;
         bool ok = true;
-        while (ok && walk.next(P, s_cum, s)) {
+        Seg s;
+        for (int i = 0; ok && take(i, s); ++i) {
             for (int j = s.j0; j < s.j1; ++j, ++it) {
                 const uint32_t dst = tl + (D / 2) * (it & 1);
                 // S of two tiles ago has read this buffer
                 if (it >= 2)
                     ok = wait_phase(bar(L::kSReady + (it & 1)), ((it >> 1) - 1) & 1, abort);
-                if (j < s.r.nct) {
+                if (j < s.nct) {
                     const int st = rc % NS;
                     ok = ok && wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -580,24 +685,21 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     const int p = key % kQPage;
                     uint32_t sc;
                     if constexpr (D == 128)
-                        sc = *reinterpret_cast<const uint32_t *>(rec + Rc::kKScales + p * 4);
+                        sc = *reinterpret_cast<const uint16_t *>(rec + Rc::kKScales + p * 4 + g0);
                     else
-                        sc = *reinterpret_cast<const uint16_t *>(rec + Rc::kKScales + p * 2);
+                        sc = rec[Rc::kKScales + p * 2 + g0];
+#pragma unroll 1
+                    for (int g = 0; g < D / 64; ++g, sc >>= 8) {
+                        uint32_t out[16];
+                        const uint32_t s1 = scale_bf16(sc & 0xFFu);
+                        const uint32_t s2 = s1 | (s1 << 16), ms = minus_136(s2);
+                        const uint4 w4 = *reinterpret_cast<const uint4 *>(
+                            rec + Rc::kKCodes + ((g0 + g) * kQPage + p) * 16);
+                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                    for (int g2 = 0; g2 < D / 64; ++g2) {
-                        uint32_t out[32];
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const uint32_t s1 = scale_bf16((sc >> (8 * (2 * g2 + g))) & 0xFFu);
-                            const uint32_t s2 = s1 | (s1 << 16), ms = minus_136(s2);
-                            const uint4 w4 = *reinterpret_cast<const uint4 *>(
-                                rec + Rc::kKCodes + ((2 * g2 + g) * kQPage + p) * 16);
-                            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                out[16 * g + e] = fma_bf16x2(code_pair(w[e / 4], e & 3), s2, ms);
-                        }
-                        ptx::tmem_st_x32(dst + 32u * g2, out);
+                        for (int e = 0; e < 16; ++e)
+                            out[e] = fma_bf16x2(code_pair(w[e / 4], e & 3), s2, ms);
+                        ptx::tmem_st_x16(dst + 16u * g, out);
                     }
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(bar(L::kEmpty + st));
@@ -605,22 +707,22 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 } else {
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     ptx::tc_fence_after_sync();
-                    const int n = (j - s.r.nct) * kKeys + key;
+                    const int n = (j - s.nct) * kKeys + key;
                     const uint4 *k = reinterpret_cast<const uint4 *>(
                         static_cast<const __nv_bfloat16 *>(a.k_tree) +
-                        (size_t)(s.r.off + (n < s.r.n ? n : 0)) * a.kv_stride + s.kvh * D);
+                        (size_t)(s.off + (n < s.n ? n : 0)) * a.kv_stride + s.kvh * D) + 4 * g0;
+#pragma unroll 1
+                    for (int g = 0; g < D / 64; ++g) {
+                        uint32_t out[16];
 #pragma unroll
-                    for (int g2 = 0; g2 < D / 64; ++g2) {
-                        uint32_t out[32];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint4 x = n < s.r.n ? k[8 * g2 + e] : make_uint4(0, 0, 0, 0);
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 x = n < s.n ? k[4 * g + e] : make_uint4(0, 0, 0, 0);
                             out[4 * e] = x.x;
                             out[4 * e + 1] = x.y;
                             out[4 * e + 2] = x.z;
                             out[4 * e + 3] = x.w;
                         }
-                        ptx::tmem_st_x32(dst + 32u * g2, out);
+                        ptx::tmem_st_x16(dst + 16u * g, out);
                     }
                 }
                 ptx::tmem_wait_st();
@@ -632,96 +734,44 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     } else {
         // ------------------------------------------------ softmax: 32 query rows per group,
         // thread = key
-        const int sw = warp / 4, key = 32 * quad + lane, t128 = tid - 128 * sw;
+        ptx::regs_inc<L::kRegsSoftmax>();
+        const int sw = warp / 4, key = 32 * quad + lane;
         const int bid = 1 + sw;  // the group's named barrier
-        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
-        int16_t *s_par = reinterpret_cast<int16_t *>(sm + L::kPar) + sw * kMaxNodes;
-        uint32_t *s_anc = reinterpret_cast<uint32_t *>(sm + L::kAnc) + sw * 32 * 8;
-        int *s_lo = reinterpret_cast<int *>(sm + L::kLo) + sw * 32;
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 32 * sw;
         float *s_nm = reinterpret_cast<float *>(sm + L::kNm) + sw * 32;
         float *s_al = reinterpret_cast<float *>(sm + L::kAl) + sw * 32;
         float *s_red = reinterpret_cast<float *>(sm + L::kRed) + sw * 128;
-        volatile int *s_bad = s_wg + 2 * sw, *s_stop = s_wg + 2 * sw + 1;
         int *hdr = reinterpret_cast<int *>(a.ws) + (size_t)2 * blockIdx.x * 8;
         if (tid == 0) hdr[0] = hdr[8] = 0;
-        if (t128 == 0) *s_stop = 0;
-
-        // the unit's query rows, K-major with 128-byte swizzle; rows past the last keep
-        // what they held: their columns of S and O are never used
-        auto load_q = [&](const Seg &u) {
-            const int rows = min((int)min((long long)u.r.n * P.grp - (long long)u.mt * R, (long long)R) -
-                                     32 * sw, 32);
-            for (int e = t128; e < 32 * (D / 8); e += 128) {
-                const int rr = e / (D / 8), ch = e % (D / 8), r = 32 * sw + rr;
-                if (rr >= rows) continue;
-                const int row = u.mt * R + r, node = row / P.grp;
-                const uint4 x = *reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(a.q) +
-                    (size_t)(u.r.off + node) * a.q_stride +
-                    (size_t)(u.kvh * P.grp + row % P.grp) * D + ch * 8);
-                *reinterpret_cast<uint4 *>(sm + L::kQ + (ch / 8) * (R * 128) + r * 128 +
-                                           ((ch % 8) ^ (r & 7)) * 16) = x;
-            }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(bar(L::kQReady));
-        };
 
         int it = 0;
-        bool ok = true, more = walk.next(P, s_cum, s);
-        if (more) load_q(s);
-        while (more) {
-            const Req &r = s.r;
-            const int nrows = (int)min((long long)r.n * P.grp - (long long)s.mt * R, (long long)R);
-            const int live = min(max(nrows - 32 * sw, 0), 32);  // this group's rows
-            // ---- the tree, the pages, and each row's view of them
-            tcc::named_barrier(bid, 128);  // the previous unit's reads are done
-            if (t128 == 0) *s_bad = r.bad ? TV_ERR_SHAPE : 0;
-            if (t128 < 32) s_nm[t128] = kNoMax;
-            tcc::named_barrier(bid, 128);
-            for (int i = t128; i < r.n; i += 128) {
-                const int p = a.parent[r.off + i];
-                s_par[i] = (int16_t)p;
-                if (p < -1 || p >= i) *s_bad = TV_ERR_TREE;
-            }
-            for (int i = t128; i < r.np; i += 128) {
-                const int page = a.table[(size_t)s.b * a.max_pages + page_of(r, i)];
-                if (page < 0 || page >= a.num_pages) *s_bad = TV_ERR_SHAPE;
-            }
-            tcc::named_barrier(bid, 128);
-            const int bad = *s_bad;
-            if (bad && t128 == 0 && sw == 0) report(a.status, bad);
-            if (t128 < 32) {
-                uint32_t anc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                int lo = 0;
-                if (t128 < live && !bad) {
-                    const int node = (s.mt * R + 32 * sw + t128) / P.grp;
-                    int depth = 0;
-                    for (int q = node; q >= 0; q = s_par[q]) ++depth;
-                    if (a.window > 0)
-                        lo = (int)min(max((long long)r.ctx + depth - a.window, 0LL), 0x7fffffffLL);
-                    int up = 0;  // steps above the node
-                    for (int q = node; q >= 0; q = s_par[q], ++up) {
-                        const bool see = a.window == 0 || up < a.window ||
-                                         (long long)r.ctx + depth - up - 1 < a.sinks;
-#pragma unroll
-                        for (int w = 0; w < 8; ++w)
-                            anc[w] |= see && (q >> 5) == w ? 1u << (q & 31) : 0u;
-                    }
-                }
-                s_lo[t128] = lo;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) s_anc[t128 * 8 + w] = anc[w];
-            }
-            tcc::named_barrier(bid, 128);
+        bool ok = true, go = true;
+        for (int i = 0; go; ++i) {
+            // (the segment stays in its ring slot until the results are out)
+            if (!__all_sync(0xffffffffu, wait_phase(bar(L::kSegFull + i % kSegs),
+                                                    (i / kSegs) & 1, abort)))
+                break;
+            const Seg &s = *reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
+            const int j1 = s.j1, nct = s.nct;
+            if (j1 == 0) break;
+            const int xu = i & 1;
+            const int live = (int)min(max((long long)s.n * P.grp - (long long)s.mt * R - 32 * sw,
+                                          0LL), 32LL);  // this group's rows
+            const uint32_t *s_see =
+                reinterpret_cast<const uint32_t *>(sm + L::kSee) + (xu * SW + sw) * kMaxNodes;
+            const int *s_lo = reinterpret_cast<const int *>(sm + L::kLo) + xu * R + 32 * sw;
             // the first position that every row sees by its window
-            const int lo_all = a.window > 0 ? (int)min((long long)r.ctx + r.n - a.window, 0x7fffffffLL)
-                                            : 0;
+            const int lo_all =
+                a.window > 0 ? (int)min((long long)s.ctx + s.n - a.window, 0x7fffffffLL) : 0;
             const int sinks = a.window > 0 ? a.sinks : 0;
+            if (quad == 0) s_nm[lane] = kNoMax;
+            if (ok) ok = wait_phase(bar(L::kPrep + xu), (i >> 1) & 1, abort);
+            tcc::named_barrier(bid, 128);
 
             float l[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) l[c] = 0.f;
-            for (int j = s.j0; j < s.j1; ++j, ++it) {
+            for (int j = s.j0; j < j1; ++j, ++it) {
                 const int x2 = it & 1;
                 if (ok) ok = wait_phase(bar(L::kSReady + x2), (it >> 1) & 1, abort);
                 if (ok && it >= 2)  // P V of two tiles ago has read this P buffer
@@ -729,97 +779,103 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 ptx::tc_fence_after_sync();
                 float x[32];
-                {
-                    uint32_t u[32];
-                    ptx::tmem_ld_x32_nowait(tl + L::kTS + R * x2 + 32 * sw, u);
-                    ptx::tmem_wait_ld();
+                for (bool raise = false;; raise = true) {
+                    {
+                        uint32_t u[32];
+                        ptx::tmem_ld_x32_nowait(tl + L::kTS + R * x2, u);
+                        ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(u[c]);
-                }
-                ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(bar(L::kSFree + x2));
-                // masks
-                if (j < r.nct) {
-                    const int i = 2 * j + key / kQPage;
-                    const int pos = page_of(r, i) * kQPage + key % kQPage;
-                    const bool in = i < r.np && pos < r.ctx;
-                    if (!in || (pos < lo_all && pos >= sinks)) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            x[c] = in && pos >= s_lo[c] ? x[c] : neg_inf();
+                        for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(u[c]);
                     }
-                } else {
-                    const int w = (j - r.nct) * 4 + quad;
+                    // masks
+                    if (j < nct) {
+                        const int i2 = 2 * j + key / kQPage;
+                        const int pos = page_of(s, i2) * kQPage + key % kQPage;
+                        const bool in = i2 < s.np && pos < s.ctx;
+                        if (!in || (pos < lo_all && pos >= sinks)) {
+                            // (eight loads at a time: more would spill)
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        x[c] = (s_anc[c * 8 + w] >> lane) & 1u ? x[c] : neg_inf();
-                }
-                float top = neg_inf();
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    if (4 * q < live) {
-                        const float4 nm = *reinterpret_cast<const float4 *>(s_nm + 4 * q);
-                        top = fmaxf(top, fmaxf(fmaxf(fmaf(x[4 * q], P.sl2, nm.x),
-                                                     fmaf(x[4 * q + 1], P.sl2, nm.y)),
-                                               fmaxf(fmaf(x[4 * q + 2], P.sl2, nm.z),
-                                                     fmaf(x[4 * q + 3], P.sl2, nm.w))));
-                    }
-                }
-                if (!ok) *s_stop = 1;
-                if (!tcc::named_barrier_and(bid, 128, ok && !(top > kHeadroom))) {
-                    // ---- raise the reference maxima that need it (or stop, all together:
-                    // s_stop is not written between this barrier and the next)
-                    const bool stop = *s_stop != 0;
-                    float mine = neg_inf();  // column `lane`'s maximum over the warp's keys
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float m = warp_max_f32(x[c]);
-                        if (lane == c) mine = m;
-                    }
-                    s_red[quad * 32 + lane] = mine;
-                    tcc::named_barrier(bid, 128);
-                    if (stop) {
-                        ok = false;
-                        more = false;
-                        break;
-                    }
-                    const float m4 = fmaxf(fmaxf(s_red[lane], s_red[32 + lane]),
-                                           fmaxf(s_red[64 + lane], s_red[96 + lane])) * P.sl2;
-                    const float old = s_nm[lane];
-                    const bool need = m4 + old > kHeadroom;
-                    const float nm = need ? -m4 : old;
-                    const float al = need ? ex2(nm - old) : 1.f;  // 2^(m_old - m_new)
-                    tcc::named_barrier(bid, 128);
-                    if (quad == 0) {
-                        s_nm[lane] = nm;
-                        s_al[lane] = al;
-                    }
-                    tcc::named_barrier(bid, 128);
-                    if (j > s.j0) {
-                        // O and l of the earlier tiles, once the last P V is done
-                        ok = wait_phase(bar(L::kOReady + (x2 ^ 1)), ((it - 1) >> 1) & 1, abort);
-                        ok = __all_sync(0xffffffffu, ok);
-                        ptx::tc_fence_after_sync();
-#pragma unroll 1
-                        for (int part = 0; part < (NP > 1 ? 2 : 1); ++part) {
-#pragma unroll 1
-                            for (int q = 0; q < 2; ++q) {
-                                uint32_t o[16];
-                                const uint32_t at = tl + L::kTO + R * part + 32 * sw + 16 * q;
-                                ptx::tmem_ld_x16_nowait(at, o);
-                                ptx::tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) *
-                                                           s_al[16 * q + e]);
-                                ptx::tmem_st_x16(at, o);
+                            for (int c = 0; c < 32; ++c) {
+                                x[c] = in && pos >= s_lo[c] ? x[c] : neg_inf();
+                                if (c % 8 == 7) asm volatile("" ::: "memory");
                             }
                         }
-                        ptx::tmem_wait_st();
+                    } else {
+                        const uint32_t see = s_see[(j - nct) * kKeys + key];
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) l[c] *= s_al[c];
+                        for (int c = 0; c < 32; ++c)
+                            x[c] = (see >> c) & 1u ? x[c] : neg_inf();
                     }
+                    if (raise) {
+                        // ---- raise the reference maxima that need it (or stop, all
+                        // together: s_stop is not written between the vote and the barrier)
+                        const bool stop = s_stop[sw] != 0;
+                        float mine = neg_inf();  // column `lane`'s maximum over the warp's keys
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float m = warp_max_f32(x[c]);
+                            if (lane == c) mine = m;
+                        }
+                        s_red[quad * 32 + lane] = mine;
+                        tcc::named_barrier(bid, 128);
+                        if (stop) {
+                            go = false;
+                            break;
+                        }
+                        const float m4 = fmaxf(fmaxf(s_red[lane], s_red[32 + lane]),
+                                               fmaxf(s_red[64 + lane], s_red[96 + lane])) * P.sl2;
+                        const float old = s_nm[lane];
+                        const bool need = m4 + old > kHeadroom;
+                        tcc::named_barrier(bid, 128);
+                        if (quad == 0) {
+                            s_nm[lane] = need ? -m4 : old;
+                            s_al[lane] = need ? ex2(-m4 - old) : 1.f;  // 2^(m_old - m_new)
+                        }
+                        tcc::named_barrier(bid, 128);
+                        if (j > s.j0) {
+                            // O and l of the earlier tiles, once the last P V is done
+                            ok = wait_phase(bar(L::kOReady + (x2 ^ 1)), ((it - 1) >> 1) & 1, abort);
+                            ok = __all_sync(0xffffffffu, ok);
+                            ptx::tc_fence_after_sync();
+#pragma unroll 1
+                            for (int q = 0; q < (NP > 1 ? 8 : 4); ++q) {
+                                uint32_t o[8];
+                                const uint32_t at = tl + L::kTO + R * (q / 4) + 8 * (q % 4);
+                                ptx::tmem_ld_x8_nowait(at, o);
+                                ptx::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) *
+                                                           s_al[8 * (q % 4) + e]);
+                                ptx::tmem_st_x8(at, o);
+                            }
+                            ptx::tmem_wait_st();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                l[c] *= s_al[c];
+                                if (c % 8 == 7) asm volatile("" ::: "memory");
+                            }
+                        }
+                    }
+                    // exponents, and whether any is too large for the reference
+                    float top = neg_inf();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        if (4 * (q & ~1) < live) {
+                            const float4 nm = *reinterpret_cast<const float4 *>(s_nm + 4 * q);
+                            fma2(x[4 * q], x[4 * q + 1], P.sl2, nm.x, nm.y);
+                            fma2(x[4 * q + 2], x[4 * q + 3], P.sl2, nm.z, nm.w);
+                            top = fmaxf(fmaxf(top, x[4 * q]), x[4 * q + 1]);
+                            top = fmaxf(fmaxf(top, x[4 * q + 2]), x[4 * q + 3]);
+                        }
+                    }
+                    if (raise) break;
+                    if (!ok) s_stop[sw] = 1;
+                    if (tcc::named_barrier_and(bid, 128, ok && !(top > kHeadroom))) break;
                 }
+                if (!go) break;
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(bar(L::kSFree + x2));
                 // ---- weights: P[key][row], a row of 128 bytes per key
                 uint8_t *prow = sm + L::kP + (uint32_t)x2 * L::kPSlabs * kSlab + key * 128;
 #pragma unroll
@@ -829,11 +885,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int c = 8 * q + 2 * e;
-                            const float2 nm = *reinterpret_cast<const float2 *>(s_nm + c);
-                            const float p0 = ex2(fmaf(x[c], P.sl2, nm.x));
-                            const float p1 = ex2(fmaf(x[c + 1], P.sl2, nm.y));
-                            l[c] += p0;
-                            l[c + 1] += p1;
+                            const float p0 = ex2(x[c]), p1 = ex2(x[c + 1]);
+                            add2(l[c], l[c + 1], p0, p1);
                             uint32_t part[NP];
                             split_weights<NP>(p0, p1, part);
 #pragma unroll
@@ -855,52 +908,45 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 ptx::tc_fence_before_sync();
                 ptx::mbar_arrive(bar(L::kPReady + x2));
             }
-            if (!more) break;
+            if (!go) break;
 
-            // ---- the next unit's queries (every S of this one is done), then this one's
-            // results
-            Seg u = s;
-            more = walk.next(P, s_cum, s);
-            if (more) load_q(s);
-            const float part = column_sums(l, lane);
-            s_red[quad * 32 + lane] = part;
+            // ---- results
+            s_red[quad * 32 + lane] = column_sums(l, lane);
             tcc::named_barrier(bid, 128);
+            const int bad = s_bad[xu];
             float *s_l = s_al;  // 1 / l
             const float sum = s_red[lane] + s_red[32 + lane] + s_red[64 + lane] + s_red[96 + lane];
-            const bool whole = u.j0 == 0 && u.j1 == u.r.nt;
-            const int piece = 2 * blockIdx.x + (u.j0 == 0 ? 1 : 0);
-            if (quad == 0) s_l[lane] = bad ? 0.f : whole ? 1.f / sum : 1.f;
+            const bool whole = s.j0 == 0 && s.j1 == s.nt;
+            if (quad == 0) s_l[lane] = whole ? 1.f / sum : 1.f;
             tcc::named_barrier(bid, 128);
             if (ok) ok = wait_phase(bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1, abort);
             ok = __all_sync(0xffffffffu, ok);
             ptx::tc_fence_after_sync();
-            float *pd = piece_data<D, R>(P, piece);
-            const int c = 32 * quad + lane;  // this thread's channel
-            if (32 * quad < D) {
+            const int *s_row = reinterpret_cast<const int *>(sm + L::kRow) + xu * R + 32 * sw;
+            float *pd = piece_data<D, R>(P, 2 * blockIdx.x + (s.j0 == 0 ? 1 : 0));
+            if (32 * quad < D && ok) {
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     if (8 * q >= live) break;
                     uint32_t hi[8], lo[8];
-                    ptx::tmem_ld_x8_nowait(tl + L::kTO + 32 * sw + 8 * q, hi);
-                    if (NP > 1) ptx::tmem_ld_x8_nowait(tl + L::kTO + R + 32 * sw + 8 * q, lo);
+                    ptx::tmem_ld_x8_nowait(tl + L::kTO + 8 * q, hi);
+                    if (NP > 1) ptx::tmem_ld_x8_nowait(tl + L::kTO + R + 8 * q, lo);
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int rr = 8 * q + e;
-                        if (rr >= live || !ok) continue;
+                        if (rr >= live) continue;
                         float o = __uint_as_float(hi[e]);
                         if (NP > 1) o += __uint_as_float(lo[e]);
                         o = bad ? 0.f : o * s_l[rr];
-                        const int r = 32 * sw + rr, row = u.mt * R + r;
                         if (whole) {
-                            const size_t at = ((size_t)(u.r.off + row / P.grp) * a.H +
-                                               u.kvh * P.grp + row % P.grp) * D + c;
+                            const size_t at = (size_t)s_row[rr] * D + key;  // key: the channel
                             if (a.out_f32)
                                 static_cast<float *>(a.out)[at] = o;
                             else
                                 static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(o);
                         } else {
-                            pd[r * D + c] = o;
+                            pd[(32 * sw + rr) * D + key] = o;
                         }
                     }
                 }
@@ -911,16 +957,22 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     pd[R * D + R + 32 * sw + lane] = sum;
                 }
                 if (tid == 0) {
-                    int *h = hdr + (u.j0 == 0 ? 8 : 0);
-                    h[1] = u.b;
-                    h[2] = u.kvh;
-                    h[3] = u.mt;
-                    h[4] = first + it - (u.j1 - u.j0) - u.j0 + u.r.nt;  // end of the unit
+                    int *h = hdr + (s.j0 == 0 ? 8 : 0);
+                    h[1] = s.b;
+                    h[2] = s.kvh;
+                    h[3] = s.mt;
+                    h[4] = first + it - (s.j1 - s.j0) - s.j0 + s.nt;  // end of the unit
                     h[5] = total;
                     h[6] = bad;
                     h[0] = 1;
                 }
             }
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(bar(L::kPrepFree + xu));
+                ptx::mbar_arrive(bar(L::kSegFree + i % kSegs));
+            }
+            tcc::named_barrier(bid, 128);  // s_nm and s_al may be written again
         }
     }
 
@@ -1005,6 +1057,11 @@ cudaError_t launch_parts(const QAttnArgs &a, cudaStream_t s) {
     static_assert(L::kAlloc <= tcc::kSmemLimit, "shared-memory plan exceeds the limit");
     const cudaError_t attr = configure_smem_once(qcache_attention_kernel<D, R, NP>, false);
     if (attr != cudaSuccess) return attr;
+    // the register split counts on what the block is launched with
+    cudaFuncAttributes fa;
+    const cudaError_t got = cudaFuncGetAttributes(&fa, qcache_attention_kernel<D, R, NP>);
+    if (got != cudaSuccess) return got;
+    if (fa.numRegs != L::kRegs) return cudaErrorInvalidConfiguration;
     QParams P;
     P.a = a;
     P.grp = a.H / a.Hkv;
