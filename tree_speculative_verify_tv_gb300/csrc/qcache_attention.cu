@@ -17,16 +17,22 @@
 //   two codes at once: ((word >> 4 p) & 0x000F000F) | 0x43004300 is the bf16 pair
 //   (128 + c0, 128 + c1), and one packed fma with s and -136 s gives s (c - 8), exactly
 //   (at most 7 significant bits; 136 s has at most 8).
-// Work: the tiles of all (request, KV head, tile of R rows) units are laid end to end and
-// every CTA (one per SM) takes an equal share; a unit that is cut leaves (O, m, l) pieces
-// in the workspace, joined by a second kernel.
+// Work: the tiles of all (request, KV head, tile of R rows) units are laid end to end,
+// with a constant cost per unit, and every CTA takes an equal share; a unit that is cut leaves (O, m, l) pieces in the
+// workspace, joined by a second kernel.
 //
-// Warp roles: NSW = R / 32 softmax groups of 4 warps (32 rows each, lane = key), one group
-// that dequantises K, one for V, a copy warp (segments, page table, bulk copies), one warp
-// each that issues S and P V, and one that prepares the next unit's rows.  The reference maximum m of a row is raised only when a score
-// exceeds it by more than 8 (log2 units); all 128 threads of a group vote per tile.  Weights
-// enter the value product as NP bf16 parts; sums l are kept in fp32 from the same weights.
-// Every mbarrier wait is bounded, as in tree_attention.cu.
+// One CTA per SM; S, P, K and V in two buffers each.  Warpgroups: R / 32 for the softmax (32
+// query rows each, lane = key), two that dequantise K (half of the channels each), two for V
+// (half of the keys each), and four control warps: copies (segments, page table, bulk
+// copies), S products, P V products, and the next unit's rows.  The reference maximum m of
+// a row is raised only when a score exceeds it by more than 32 (log2 units; nothing
+// overflows before 2^127); the softmax warps vote per tile.  Weights enter the value product
+// as NP bf16 parts; sums l are kept in fp32 from the same weights.  Every mbarrier wait is
+// bounded, as in tree_attention.cu.
+//
+// Two things bound the roles: latency, since a tile passes through four of them and each
+// wait costs a hundred cycles or more, and the instruction cache, so loops are kept rolled
+// and waits short.
 #include <algorithm>
 
 #include "qcache.cuh"
@@ -35,13 +41,12 @@
 namespace tv {
 namespace {
 
-using tcc::kWaitLimit;
-
 constexpr int kKeys = 128;             // keys per tile
-constexpr int kChunkB = 2048;          // requests per launch (their tile counts are in smem)
+constexpr int kChunkB = 1024;          // requests per launch (their tile counts are in smem)
 constexpr uint32_t kSlab = kKeys * 128;  // 128 keys x 128 bytes
-constexpr float kHeadroom = 8.f;
+constexpr float kHeadroom = 32.f;
 constexpr float kNoMax = 1e30f;        // -m of a row that has seen no key
+constexpr int kUnitCost = 3;           // what a unit costs beside its tiles, in tiles
 constexpr uint32_t kTmemCols = 512;
 
 struct QParams {
@@ -88,6 +93,7 @@ struct Seg {
     int b, kvh, mt, j0, j1;              // j1 = 0: no more
     int off, n, ctx, bad;                // as in Req
     int sp, lp, np, nct, nt;
+    int end;                             // end of the unit's tiles among all costs
 };
 constexpr int kSegInts = 16, kSegs = 4;  // ring of segments in shared memory
 static_assert(sizeof(Seg) <= kSegInts * 4, "");
@@ -98,22 +104,33 @@ __device__ __forceinline__ int page_of(const Seg &s, int i) {
 
 // Walks this CTA's share [t, t1) of the tiles.
 template <int R>
-__device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, int t, int t1) {
+__device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, int &t, int t1) {
     Seg s{};
-    if (t >= t1) return s;
-    int lo = 0, hi = P.nb - 1;  // the last request whose tiles begin at or before t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cum[mid] <= t)
-            lo = mid;
-        else
-            hi = mid - 1;
+    Req r;
+    int lo, unit;
+    for (;;) {
+        if (t >= t1) return s;
+        int hi = P.nb - 1;  // the last request whose costs begin at or before t
+        lo = 0;
+#pragma unroll 1
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cum[mid] <= t)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        r = request<R>(P, P.b0 + lo);
+        const int rem = t - cum[lo];
+        unit = rem / (r.nt + kUnitCost);
+        s.j0 = rem % (r.nt + kUnitCost);
+        if (s.j0 < r.nt) break;
+        t = cum[lo] + (unit + 1) * (r.nt + kUnitCost);  // past the unit's tiles
     }
-    const Req r = request<R>(P, P.b0 + lo);
-    const int rem = t - cum[lo], unit = rem / r.nt;
     s.b = P.b0 + lo;
-    s.j0 = rem % r.nt;
     s.j1 = min(r.nt, s.j0 + (t1 - t));
+    s.end = cum[lo] + unit * (r.nt + kUnitCost) + r.nt;
+    t += s.j1 - s.j0;
     s.kvh = unit / r.mts;
     s.mt = unit % r.mts;
     s.off = r.off;
@@ -128,26 +145,26 @@ __device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, in
     return s;
 }
 
-// Shared memory.  P: two buffers of NP parts; at R = 64 a part fills a 128-byte row, at
-// R = 32 two parts share one.  Q and the rows' masks come in two buffers, one per unit.
+// Shared memory.  P: two buffers; at R = 64 a part fills the 128-byte row of a key, at R = 32
+// two parts share one.  Q and the rows' masks come in two buffers, one per unit.
 template <int D, int R, int NP>
 struct Lay {
-    static constexpr int kSW = R / 32;                     // softmax groups
-    static constexpr int kWarps = 4 * kSW + 16 + 4;
-    static constexpr int kThreads = kWarps * 32;
-    // registers: at launch (all that fit), and after the split; the control warps keep theirs
+    static constexpr int kSW = R / 32;  // softmax warpgroups
+    static constexpr int kWarps = 4 * kSW + 20, kThreads = kWarps * 32;
+    // registers: at launch (all that fit), and after the split
     static constexpr int kRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kRegsOperand = 48;
-    static constexpr int kRegsSoftmax = kSW == 2 ? 120 : 168;
+    static constexpr int kRegsSoftmax = kSW == 2 ? 112 : 128, kRegsK = kSW == 2 ? 48 : 56,
+                         kRegsV = kSW == 2 ? 56 : 64, kRegsControl = kSW == 2 ? 64 : 80;
     static_assert(kThreads * kRegs >=
-                      128 * (kSW * kRegsSoftmax + 4 * kRegsOperand + kRegs), "register split");
+                      128 * (kSW * kRegsSoftmax + 2 * kRegsK + 2 * kRegsV + kRegsControl),
+                  "register split");
     static constexpr uint32_t kRec = qrec_bytes(D);
     static constexpr uint32_t kPSlabs = (NP * R + 63) / 64;
     static constexpr uint32_t kQBytes = R * D * 2;
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kP = kQ + 2 * kQBytes;
     static constexpr uint32_t kRing = kP + 2 * kPSlabs * kSlab;
-    static constexpr uint32_t kMiscBytes = 20 * 1024;
+    static constexpr uint32_t kMiscBytes = 16 * 1024;
     static constexpr int kStages =
         (int)std::min<uint32_t>(16, (227 * 1024 - 1024 - kMiscBytes - kRing) / (2 * kRec));
     static constexpr uint32_t kCum = kRing + kStages * 2 * kRec;       // int [kChunkB + 1]
@@ -158,8 +175,8 @@ struct Lay {
     static constexpr uint32_t kNm = kRow + 2 * R * 4;                  // float [R]
     static constexpr uint32_t kAl = kNm + R * 4;                       // float [R]
     static constexpr uint32_t kRed = kAl + R * 4;                      // float [kSW][4][32]
-    static constexpr uint32_t kVs = kRed + kSW * 512;                  // uint2 [2][4][32]
-    static constexpr uint32_t kSeg = kVs + 2 * 4 * 32 * 8;             // int [kSegs][16]
+    static constexpr uint32_t kVs = kRed + kSW * 512;                  // u32 [8][32]
+    static constexpr uint32_t kSeg = kVs + 8 * 32 * 4;                 // int [kSegs][16]
     static constexpr uint32_t kBar = kSeg + kSegs * kSegInts * 4;
     // mbarriers: ring full / empty; K and V operands written; a unit's rows prepared /
     // done with; S ready / read; P written; P V done; segments written / taken; all done
@@ -169,34 +186,44 @@ struct Lay {
                          kOReady = kPReady + 2, kSegFull = kOReady + 2,
                          kSegFree = kSegFull + kSegs, kDone = kSegFree + kSegs,
                          kNumBars = kDone + 2;
-    static constexpr uint32_t kMisc = kBar + kNumBars * 8;  // tmem, abort, scan, stop, bad
-    static constexpr uint32_t kBytes = kMisc + 256;
+    static constexpr uint32_t kMisc = kBar + kNumBars * 8;  // tmem, abort, bad, scan
+    static constexpr uint32_t kBytes = kMisc + 192;
     static constexpr uint32_t kAlloc = kBytes + 1024;
-    static_assert(kBytes - kCum <= kMiscBytes && kStages >= 3, "shared-memory plan");
+    static_assert(kBytes - kCum <= kMiscBytes && kStages >= 3 && kAlloc <= 227 * 1024,
+                  "shared-memory plan");
     // tensor memory columns
     static constexpr uint32_t kTS = 0;                       // S^T x 2
-    static constexpr uint32_t kTO = 2 * R;                   // O^T, hi sums then lo sums
+    static constexpr uint32_t kTO = 2 * R;                   // O^T, sums of part 0, then 1
     static constexpr uint32_t kOWidth = NP == 1 ? 64 : NP == 3 && R == 32 ? 96 : 2 * R;
     static constexpr uint32_t kTK = kTO + kOWidth;           // K x 2
     static constexpr uint32_t kTV = kTK + D;                 // V^T x 2
     static_assert(kTV + 128 <= kTmemCols, "tensor memory plan");
 };
 
-// Wait for a phase, giving up when the CTA's abort flag is raised or after 2^24 tries (of
-// some 100 cycles each).  Two dozen warps wait here most of the time and a try returns
-// after a fraction of a microsecond, so the loop is kept to a few instructions: with a
-// clock read and the flag in every round the waits took more issue slots than the work.
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort) {
-    for (int k = 0; k < 1 << 14 && !*abort; ++k) {
-#pragma unroll 1
-        for (int n = 0; n < 1 << 10; ++n)
-            if (ptx::mbar_try_wait_hw(bar, parity)) return true;
-    }
-    *abort = 1;
-    return false;
-}
+// Wait for a phase, giving up (and raising the CTA's abort flag) after 2^24 tries, of some
+// 50 cycles each.  The whole wait is one short loop: with clock reads and the flag in it the
+// dozen places that wait made the kernel several times larger than the instruction cache.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return ptx::mbar_try_wait_hw(bar, parity) || wait_slow(bar, parity, abort);
+    const bool ok = ptx::mbar_wait_tries(bar, parity, 1u << 24);
+    if (!ok) *abort = 1;
+    return ok;
+}
+
+// The same for a warpgroup on named barrier `bid`, for up to two phases: true in all 128
+// threads or in none.
+__device__ __forceinline__ bool group_wait(int bid, int quad, uint32_t bar0, uint32_t parity0,
+                                           bool both, uint32_t bar1, uint32_t parity1,
+                                           volatile int *abort) {
+    bool ok = true;
+    if (quad == 0)
+        ok = wait_phase(bar0, parity0, abort) && (!both || wait_phase(bar1, parity1, abort));
+    return tcc::named_barrier_and(bid, 128, ok);
+}
+
+// One arrival of a converged warp, after what its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar);
 }
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -261,9 +288,26 @@ __device__ __forceinline__ uint32_t minus_136(uint32_t s2) {
     return d;
 }
 
-// Codes 2p and 2p + 1 of a word as the bf16 pair (128 + c0, 128 + c1).
+// Codes 2p and 2p + 1 of a word as the bf16 pair (128 + c0, 128 + c1).  The mask and the
+// exponent go in by one lop3 (the compiler makes two of the C expression, and these
+// operations bound the dequantising: two cycles each per warp).
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int p) {
-    return ((w >> (4 * p)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(d)
+        : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
+    return d;
+}
+
+// (x - 136) s, both steps exact: without a second operand per pair of scales to load.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t x, uint32_t s2) {
+    uint32_t d;
+    asm("{\n\t.reg .b32 t;\n\t"
+        "add.rn.bf16x2 t, %1, %2;\n\t"
+        "mul.rn.bf16x2 %0, t, %3;\n\t}"
+        : "=r"(d)
+        : "r"(x), "r"(0xC308C308u), "r"(s2));
+    return d;
 }
 
 // The bf16 parts of two weights, element 0 in the low half.  One part: rounded to nearest.
@@ -296,9 +340,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     qcache_attention_kernel(const QParams P) {
     using L = Lay<D, R, NP>;
     using Rc = qc::Rec<D>;
-    constexpr int SW = L::kSW, NS = L::kStages;
+    constexpr int SW = L::kSW, NS = L::kStages, kWarps = L::kWarps;
     constexpr int kWarpK = 4 * SW, kWarpV = kWarpK + 8, kWarpCopy = kWarpV + 8,
-                  kWarpMma = kWarpCopy + 1, kWarpPv = kWarpMma + 1, kWarpPrep = kWarpPv + 1;
+                  kWarpS = kWarpCopy + 1, kWarpPv = kWarpS + 1, kWarpPrep = kWarpPv + 1;
     extern __shared__ uint8_t smem_raw[];
     // aligned by an offset, not through an integer: the compiler still sees shared memory
     uint8_t *sm = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -310,32 +354,31 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     int *s_seg = reinterpret_cast<int *>(sm + L::kSeg);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(sm + L::kMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
-    int *s_scan = reinterpret_cast<int *>(sm + L::kMisc + 16);
-    volatile int *s_stop = reinterpret_cast<volatile int *>(sm + L::kMisc + 16 + 128);  // [SW]
-    volatile int *s_bad = s_stop + 4;                                                   // [2]
+    volatile int *s_bad = reinterpret_cast<volatile int *>(sm + L::kMisc + 16);  // [2]
+    int *s_scan = reinterpret_cast<int *>(sm + L::kMisc + 32);                   // [28]
 
     if (tid == 0) {
         *abort = 0;
-        for (int i = 0; i < SW; ++i) s_stop[i] = 0;
+#pragma unroll 1
         for (int i = 0; i < L::kNumBars; ++i) {
-            uint32_t count = 1;
-            if (i >= L::kEmpty && i < L::kKReady) count = 16;            // K and V warps
-            if (i >= L::kKReady && i < L::kPrep) count = 256;
-            if (i >= L::kPrepFree && i < L::kSReady) count = 4 * SW;     // softmax warps
-            if (i >= L::kSFree && i < L::kOReady) count = 128 * SW;
-            if (i >= L::kSegFree && i < L::kDone) count = 4 * SW + 16 + 3;
+            uint32_t count = 1;  // arriving warps
+            if (i >= L::kEmpty && i < L::kKReady) count = 16;  // K and V
+            if (i >= L::kKReady && i < L::kPrep) count = 8;    // K or V
+            if (i >= L::kPrepFree && i < L::kSReady) count = 4 * SW;
+            if (i >= L::kSFree && i < L::kOReady) count = 4 * SW;
+            if (i >= L::kSegFree && i < L::kDone) count = kWarps - 1;
             ptx::mbar_init(bar(i), count);
         }
         ptx::fence_mbar_init();
     }
-    if (warp == kWarpMma) {
+    if (warp == kWarpS) {
         ptx::tmem_alloc(ptx::smem_addr(s_tmem), kTmemCols);
         ptx::tmem_relinquish();
     }
     pdl_wait();
     pdl_launch_next();
 
-    // ---- prefix sums of the requests' tiles
+    // ---- prefix sums of the requests' costs: their tiles, and a constant per unit
     {
         constexpr int per = (kChunkB + L::kThreads - 1) / L::kThreads;
         int w[per], sum = 0;
@@ -345,7 +388,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             w[k] = 0;
             if (i < P.nb) {
                 const Req r = request<R>(P, P.b0 + i);
-                w[k] = a.Hkv * r.mts * r.nt;
+                w[k] = r.nt > 0 ? a.Hkv * r.mts * (r.nt + kUnitCost) : 0;
                 if (blockIdx.x == 0 && !r.range) report(a.status, TV_ERR_TREE);
             }
             sum += w[k];
@@ -359,6 +402,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         if (lane == 31) s_scan[warp] = inc;
         __syncthreads();
         int before = 0;
+#pragma unroll 1
         for (int k = 0; k < warp; ++k) before += s_scan[k];
         int at = before + inc - sum;
 #pragma unroll
@@ -378,22 +422,24 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     const int first = shares > 0 ? (int)((long long)total * me / shares) : 0;
     const int t1 = me < shares ? (int)((long long)total * (me + 1) / shares) : first;
 
-    // Segment `i` of this CTA, from the ring; false at the end (or when a wait expired).
-    auto take = [&](int i, Seg &s) {
+    // Segment `i` of this CTA, in the ring until leave(i): null at the end, or when a wait
+    // expired.  (A reference: the fields are read where they are used, which keeps the
+    // operand warps within their registers.)
+    auto enter = [&](int i) -> const Seg * {
         const bool got = __all_sync(
             0xffffffffu, wait_phase(bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, abort));
-        if (!got) return false;
-        s = *reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(L::kSegFree + i % kSegs));
-        return s.j1 > 0;
+        const Seg *s = reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
+        return got && s->j1 > 0 ? s : nullptr;
     };
+    auto leave = [&](int i) { warp_arrive(bar(L::kSegFree + i % kSegs), lane); };
 
+    if (warp >= kWarpCopy) ptx::regs_dec<L::kRegsControl>();
     if (warp == kWarpCopy) {
         // ------------------------------------------------ segments, and one bulk copy per
         // page; the lanes hold the next 32 pages' records
         int rc = 0, t = first;  // context tiles so far, next tile
         bool ok = true;
+#pragma unroll 1
         for (int i = 0; ok; ++i) {
             const Seg s = next_segment<R>(P, s_cum, t, t1);
             ok = __all_sync(0xffffffffu, i < kSegs || wait_phase(bar(L::kSegFree + i % kSegs),
@@ -404,9 +450,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 ptx::mbar_arrive(bar(L::kSegFull + i % kSegs));
             }
             if (s.j1 == 0) break;
-            t += s.j1 - s.j0;
             const int end = min(s.j1, s.nct);
             const uint8_t *rec = nullptr;
+#pragma unroll 1
             for (int j = s.j0; j < end; ++j) {
                 const int k = (j - s.j0) % 16;
                 if (k == 0) {
@@ -438,23 +484,29 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         __syncwarp();
         // no copy may still be landing when the CTA ends
         if (lane == 0)
+#pragma unroll 1
             for (int j = max(0, rc - NS); j < rc; ++j)
-                ptx::mbar_wait(bar(L::kFull + j % NS), (j / NS) & 1, kWaitLimit);
+                wait_phase(bar(L::kFull + j % NS), (j / NS) & 1, abort);
         __syncwarp();
-    } else if (warp == kWarpMma) {
+    } else if (warp == kWarpS) {
         // ------------------------------------------------ S^T = K Q^T of every tile
         constexpr uint32_t idS = ptx::idesc_bf16_f32(128, R);
         const uint32_t lead = ptx::elect_one();
         int it = 0;
         bool ok = true;
-        Seg s;
-        for (int i = 0; ok && take(i, s); ++i) {
+#pragma unroll 1
+        for (int i = 0; ok; ++i) {
+            const Seg *s = enter(i);
+            if (!s) break;
+            const int n = s->j1 - s->j0;
+            leave(i);
             const uint32_t sQ = sbase + L::kQ + (i & 1) * L::kQBytes;
             ok = wait_phase(bar(L::kPrep + (i & 1)), (i >> 1) & 1, abort);
-            for (int j = s.j0; j < s.j1; ++j, ++it) {
+#pragma unroll 1
+            for (int j = 0; j < n; ++j, ++it) {
                 const int x = it & 1;
                 ok = ok && wait_phase(bar(L::kKReady + x), (it >> 1) & 1, abort) &&
-                     (it < 2 || wait_phase(bar(L::kSFree + x), ((it >> 1) - 1) & 1, abort));
+                     wait_phase(bar(L::kSFree + x), ((it >> 1) + 1) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll
@@ -468,7 +520,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         }
         __syncwarp();
         ptx::mma_commit_lead(bar(L::kDone), lead);
-        ptx::mbar_wait(bar(L::kDone), 0, kWaitLimit);
+        wait_phase(bar(L::kDone), 0, abort);
     } else if (warp == kWarpPv) {
         // ------------------------------------------------ O^T += V^T P^T of every tile
         constexpr uint32_t nPV = NP == 1 ? 64 : 2 * R;
@@ -477,9 +529,14 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         const uint32_t lead = ptx::elect_one();
         int it = 0;
         bool ok = true;
-        Seg s;
-        for (int i = 0; ok && take(i, s); ++i) {
-            for (int j = s.j0; j < s.j1; ++j, ++it) {
+#pragma unroll 1
+        for (int i = 0; ok; ++i) {
+            const Seg *s = enter(i);
+            if (!s) break;
+            const int n = s->j1 - s->j0;
+            leave(i);
+#pragma unroll 1
+            for (int j = 0; j < n; ++j, ++it) {
                 const int x = it & 1;
                 ok = wait_phase(bar(L::kVReady + x), (it >> 1) & 1, abort) &&
                      wait_phase(bar(L::kPReady + x), (it >> 1) & 1, abort);
@@ -492,7 +549,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     ptx::mma_bf16_ts_lead(
                         tmem + L::kTO, av,
                         ptx::desc_mnmajor_sw128(sP + kk * 2048u, nPV > 64 ? kSlab : 0u, 1024),
-                        idPV, kk > 0 || j > s.j0, lead);
+                        idPV, kk > 0 || j > 0, lead);
                     // the third part adds to the second's sums (at R = 32 its row has 32
                     // idle columns, which go to idle columns)
                     if constexpr (NP == 3)
@@ -507,13 +564,17 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         }
         __syncwarp();
         ptx::mma_commit_lead(bar(L::kDone + 1), lead);
-        ptx::mbar_wait(bar(L::kDone + 1), 0, kWaitLimit);
+        wait_phase(bar(L::kDone + 1), 0, abort);
     } else if (warp == kWarpPrep) {
         // ------------------------------------------------ a unit's rows, one unit ahead:
         // queries, root-path masks, windows, output rows; the tree's and the pages' checks
         int16_t *s_par = reinterpret_cast<int16_t *>(sm + L::kPar);
-        Seg s;
-        for (int i = 0; take(i, s); ++i) {
+#pragma unroll 1
+        for (int i = 0;; ++i) {
+            const Seg *sp = enter(i);
+            if (!sp) break;
+            const Seg s = *sp;
+            leave(i);
             const int x = i & 1;
             if (!__all_sync(0xffffffffu, i < 2 || wait_phase(bar(L::kPrepFree + x),
                                                              ((i >> 1) - 1) & 1, abort)))
@@ -525,6 +586,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             const int nrows = (int)min((long long)s.n * P.grp - (long long)s.mt * R, (long long)R);
             // rows past the last keep what they held: their columns are never used
             constexpr int CH = D / 8;  // 16-byte pieces of a row, a row per CH lanes
+#pragma unroll 1
             for (int r = lane / CH; r < nrows; r += 32 / CH) {
                 const int row = s.mt * R + r, node = row / P.grp, ch = lane % CH;
                 ptx::cp_async_16(sbase + L::kQ + x * L::kQBytes + (ch / 8) * (R * 128) + r * 128 +
@@ -534,27 +596,33 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                                      (size_t)(s.kvh * P.grp + row % P.grp) * D + ch * 8);
             }
             int bad = s.bad ? TV_ERR_SHAPE : 0;
+#pragma unroll 1
             for (int k = lane; k < s.np; k += 32) {
                 const int page = a.table[(size_t)s.b * a.max_pages + page_of(s, k)];
                 if (page < 0 || page >= a.num_pages) bad = TV_ERR_SHAPE;
             }
+#pragma unroll 1
             for (int k = lane; k < s.n; k += 32) {
                 const int p = a.parent[s.off + k];
                 s_par[k] = (int16_t)p;
                 if (p < -1 || p >= k) bad = TV_ERR_TREE;
             }
+#pragma unroll 1
             for (int k = lane; k < SW * kMaxNodes; k += 32) s_see[k] = 0;
             bad = __reduce_max_sync(0xffffffffu, bad);
             __syncwarp();
+#pragma unroll 1
             for (int r = lane; r < R; r += 32) {
                 int lo = 0;
                 const int row = s.mt * R + r, node = row / P.grp;
                 if (r < nrows && !bad) {
                     int depth = 0;
+#pragma unroll 1
                     for (int q = node; q >= 0; q = s_par[q]) ++depth;
                     if (a.window > 0)
                         lo = (int)min(max((long long)s.ctx + depth - a.window, 0LL), 0x7fffffffLL);
                     int up = 0;  // steps above the node
+#pragma unroll 1
                     for (int q = node; q >= 0; q = s_par[q], ++up) {
                         if (a.window == 0 || up < a.window ||
                             (long long)s.ctx + depth - up - 1 < a.sinks)
@@ -576,40 +644,50 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         __syncwarp();
     } else if (warp >= kWarpV) {
         // ------------------------------------------------ V^T operand: thread = channel, a
-        // warpgroup per half of the tile's keys
-        ptx::regs_dec<L::kRegsOperand>();
+        // warpgroup per half of the keys
+        ptx::regs_dec<L::kRegsV>();
         const int c = 32 * quad + lane, h = (warp - kWarpV) / 4;
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTV + 32u * h;
-        uint2 *s_vs = reinterpret_cast<uint2 *>(sm + L::kVs) + (warp - kWarpV) * 32;
+        uint32_t *s_vs = reinterpret_cast<uint32_t *>(sm + L::kVs) + (warp - kWarpV) * 32;
         const bool live = 32 * quad < D;
         int it = 0, rc = 0;
         bool ok = true;
-        Seg s;
-        for (int i = 0; ok && take(i, s); ++i) {
+#pragma unroll 1
+        for (int i = 0; ok; ++i) {
+            const Seg *sp = enter(i);
+            if (!sp) break;
+            const Seg &s = *sp;
             const long long vis = a.window > 0 ? (long long)s.ctx + 1 - a.window : 0;
             const int sinks = a.window > 0 ? a.sinks : 0;
+#pragma unroll 1
             for (int j = s.j0; j < s.j1; ++j, ++it) {
-                const uint32_t dst = tl + 64u * (it & 1);
-                if (it >= 2)
-                    ok = wait_phase(bar(L::kOReady + (it & 1)), ((it >> 1) - 1) & 1, abort);
+                const int st = rc % NS;
+                // P V of two tiles ago has read the buffer; this tile's pages are here
+                const int x = it & 1;
+                const uint32_t dst = tl + 64u * x;
+                ok = group_wait(4 + h, quad, bar(L::kOReady + x), ((it >> 1) + 1) & 1, j < s.nct,
+                                bar(L::kFull + st), (rc / NS) & 1, abort);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
                 if (j < s.nct) {
-                    const int st = rc % NS;
-                    ok = ok && wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    ptx::tc_fence_after_sync();
                     const uint8_t *rec = sm + L::kRing + ((uint32_t)st * 2 + h) * L::kRec;
                     if (live) {
                         // the group's scales (a warp's 32 channels), two positions per lane;
                         // a position that no node sees gets 0, whatever the cache holds there
                         const uint32_t b2 = *reinterpret_cast<const uint16_t *>(
                             rec + Rc::kVScales + quad * kQPage + 2 * lane);
-                        uint32_t s0 = scale_bf16(b2 & 0xFFu), s1 = scale_bf16(b2 >> 8);
-                        const int i2 = 2 * j + h, pos = page_of(s, i2) * kQPage + 2 * lane;
-                        if (i2 >= s.np || pos >= s.ctx || (pos < vis && pos >= sinks)) s0 = 0;
-                        if (i2 >= s.np || pos + 1 >= s.ctx || (pos + 1 < vis && pos + 1 >= sinks))
-                            s1 = 0;
-                        const uint32_t s2 = s0 | (s1 << 16);
-                        s_vs[lane] = make_uint2(s2, minus_136(s2));
+                        uint32_t s2 = scale_bf16(b2 & 0xFFu) | (scale_bf16(b2 >> 8) << 16);
+                        const int i2 = 2 * j + h, p0 = page_of(s, i2) * kQPage;
+                        if (i2 >= s.np || p0 + kQPage > s.ctx ||
+                            (p0 < vis && p0 + kQPage > sinks)) {
+                            const int pos = p0 + 2 * lane;
+                            if (i2 >= s.np || pos >= s.ctx || (pos < vis && pos >= sinks))
+                                s2 &= 0xFFFF0000u;
+                            if (i2 >= s.np || pos + 1 >= s.ctx ||
+                                (pos + 1 < vis && pos + 1 >= sinks))
+                                s2 &= 0x0000FFFFu;
+                        }
+                        s_vs[lane] = s2;
                         __syncwarp();
 #pragma unroll 1
                         for (int q = 0; q < 2; ++q) {
@@ -618,13 +696,14 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                                 rec + Rc::kVCodes + (q * D + c) * 16);
                             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
+                            for (int e = 0; e < 4; ++e) {
+                                // the scales of four pairs of positions, for all lanes
                                 const uint4 sc =
-                                    *reinterpret_cast<const uint4 *>(s_vs + q * 16 + 2 * e);
-                                out[2 * e] =
-                                    fma_bf16x2(code_pair(w[e / 2], 2 * (e & 1)), sc.x, sc.y);
-                                out[2 * e + 1] =
-                                    fma_bf16x2(code_pair(w[e / 2], 2 * (e & 1) + 1), sc.z, sc.w);
+                                    *reinterpret_cast<const uint4 *>(s_vs + q * 16 + 4 * e);
+                                out[4 * e] = scaled_pair(code_pair(w[e], 0), sc.x);
+                                out[4 * e + 1] = scaled_pair(code_pair(w[e], 1), sc.y);
+                                out[4 * e + 2] = scaled_pair(code_pair(w[e], 2), sc.z);
+                                out[4 * e + 3] = scaled_pair(code_pair(w[e], 3), sc.w);
                             }
                             ptx::tmem_st_x16(dst + 16u * q, out);
                         }
@@ -633,8 +712,6 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     if (lane == 0) ptx::mbar_arrive(bar(L::kEmpty + st));
                     ++rc;
                 } else {
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    ptx::tc_fence_after_sync();
                     if (live) {
                         const int n0 = (j - s.nct) * kKeys + 64 * h;
                         const uint16_t *v = static_cast<const uint16_t *>(a.v_tree) +
@@ -656,30 +733,35 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(bar(L::kVReady + (it & 1)));
+                warp_arrive(bar(L::kVReady + x), lane);
             }
+            leave(i);
         }
         __syncwarp();
     } else if (warp >= kWarpK) {
         // ------------------------------------------------ K operand: thread = key, a
         // warpgroup per half of the channels
-        ptx::regs_dec<L::kRegsOperand>();
-        const int key = 32 * quad + lane, g0 = (warp - kWarpK) / 4 * (D / 64);
+        ptx::regs_dec<L::kRegsK>();
+        const int key = 32 * quad + lane, h = (warp - kWarpK) / 4, g0 = h * (D / 64);
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTK + 16u * g0;
         int it = 0, rc = 0;
         bool ok = true;
-        Seg s;
-        for (int i = 0; ok && take(i, s); ++i) {
+#pragma unroll 1
+        for (int i = 0; ok; ++i) {
+            const Seg *sp = enter(i);
+            if (!sp) break;
+            const Seg &s = *sp;
+#pragma unroll 1
             for (int j = s.j0; j < s.j1; ++j, ++it) {
-                const uint32_t dst = tl + (D / 2) * (it & 1);
-                // S of two tiles ago has read this buffer
-                if (it >= 2)
-                    ok = wait_phase(bar(L::kSReady + (it & 1)), ((it >> 1) - 1) & 1, abort);
+                const int st = rc % NS;
+                // S of two tiles ago has read the buffer; this tile's pages are here
+                const int x = it & 1;
+                const uint32_t dst = tl + (D / 2) * x;
+                ok = group_wait(6 + h, quad, bar(L::kSReady + x), ((it >> 1) + 1) & 1, j < s.nct,
+                                bar(L::kFull + st), (rc / NS) & 1, abort);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
                 if (j < s.nct) {
-                    const int st = rc % NS;
-                    ok = ok && wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    ptx::tc_fence_after_sync();
                     const uint8_t *rec =
                         sm + L::kRing + ((uint32_t)st * 2 + key / kQPage) * L::kRec;
                     const int p = key % kQPage;
@@ -705,8 +787,6 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     if (lane == 0) ptx::mbar_arrive(bar(L::kEmpty + st));
                     ++rc;
                 } else {
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    ptx::tc_fence_after_sync();
                     const int n = (j - s.nct) * kKeys + key;
                     const uint4 *k = reinterpret_cast<const uint4 *>(
                         static_cast<const __nv_bfloat16 *>(a.k_tree) +
@@ -727,8 +807,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(bar(L::kKReady + (it & 1)));
+                warp_arrive(bar(L::kKReady + x), lane);
             }
+            leave(i);
         }
         __syncwarp();
     } else {
@@ -738,25 +819,25 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         const int sw = warp / 4, key = 32 * quad + lane;
         const int bid = 1 + sw;  // the group's named barrier
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 32 * sw;
-        float *s_nm = reinterpret_cast<float *>(sm + L::kNm) + sw * 32;
-        float *s_al = reinterpret_cast<float *>(sm + L::kAl) + sw * 32;
-        float *s_red = reinterpret_cast<float *>(sm + L::kRed) + sw * 128;
+        float *s_nm = reinterpret_cast<float *>(sm + L::kNm) + 32 * sw;
+        float *s_al = reinterpret_cast<float *>(sm + L::kAl) + 32 * sw;
+        float *s_red = reinterpret_cast<float *>(sm + L::kRed) + 128 * sw;
         int *hdr = reinterpret_cast<int *>(a.ws) + (size_t)2 * blockIdx.x * 8;
         if (tid == 0) hdr[0] = hdr[8] = 0;
 
         int it = 0;
-        bool ok = true, go = true;
+        bool go = true;
+#pragma unroll 1
         for (int i = 0; go; ++i) {
             // (the segment stays in its ring slot until the results are out)
-            if (!__all_sync(0xffffffffu, wait_phase(bar(L::kSegFull + i % kSegs),
-                                                    (i / kSegs) & 1, abort)))
+            if (!group_wait(bid, quad, bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, false, 0, 0,
+                            abort))
                 break;
             const Seg &s = *reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
             const int j1 = s.j1, nct = s.nct;
             if (j1 == 0) break;
             const int xu = i & 1;
-            const int live = (int)min(max((long long)s.n * P.grp - (long long)s.mt * R - 32 * sw,
-                                          0LL), 32LL);  // this group's rows
+            const int live = min(max(s.n * P.grp - s.mt * R - 32 * sw, 0), 32);  // the group's rows
             const uint32_t *s_see =
                 reinterpret_cast<const uint32_t *>(sm + L::kSee) + (xu * SW + sw) * kMaxNodes;
             const int *s_lo = reinterpret_cast<const int *>(sm + L::kLo) + xu * R + 32 * sw;
@@ -765,21 +846,21 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 a.window > 0 ? (int)min((long long)s.ctx + s.n - a.window, 0x7fffffffLL) : 0;
             const int sinks = a.window > 0 ? a.sinks : 0;
             if (quad == 0) s_nm[lane] = kNoMax;
-            if (ok) ok = wait_phase(bar(L::kPrep + xu), (i >> 1) & 1, abort);
-            tcc::named_barrier(bid, 128);
+            if (!group_wait(bid, quad, bar(L::kPrep + xu), (i >> 1) & 1, false, 0, 0, abort)) break;
 
             float l[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) l[c] = 0.f;
+#pragma unroll 1
             for (int j = s.j0; j < j1; ++j, ++it) {
                 const int x2 = it & 1;
-                if (ok) ok = wait_phase(bar(L::kSReady + x2), (it >> 1) & 1, abort);
-                if (ok && it >= 2)  // P V of two tiles ago has read this P buffer
-                    ok = wait_phase(bar(L::kOReady + x2), ((it >> 1) - 1) & 1, abort);
-                ok = __all_sync(0xffffffffu, ok);
+                if (!(go = group_wait(bid, quad, bar(L::kSReady + x2), (it >> 1) & 1, false, 0, 0,
+                                      abort)))
+                    break;
                 ptx::tc_fence_after_sync();
                 float x[32];
-                for (bool raise = false;; raise = true) {
+#pragma unroll 1
+                for (bool raise = j == s.j0;; raise = true) {
                     {
                         uint32_t u[32];
                         ptx::tmem_ld_x32_nowait(tl + L::kTS + R * x2, u);
@@ -789,14 +870,16 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     }
                     // masks
                     if (j < nct) {
-                        const int i2 = 2 * j + key / kQPage;
-                        const int pos = page_of(s, i2) * kQPage + key % kQPage;
-                        const bool in = i2 < s.np && pos < s.ctx;
-                        if (!in || (pos < lo_all && pos >= sinks)) {
+                        const int i2 = 2 * j + key / kQPage, p0 = page_of(s, i2) * kQPage;
+                        if (i2 >= s.np || p0 + kQPage > s.ctx ||
+                            (p0 < lo_all && p0 + kQPage > sinks)) {
+                            const int pos = p0 + key % kQPage;
+                            const bool in = i2 < s.np && pos < s.ctx;
+                            const int least = pos < sinks ? 0x7fffffff : pos;
                             // (eight loads at a time: more would spill)
 #pragma unroll
                             for (int c = 0; c < 32; ++c) {
-                                x[c] = in && pos >= s_lo[c] ? x[c] : neg_inf();
+                                x[c] = in && least >= s_lo[c] ? x[c] : neg_inf();
                                 if (c % 8 == 7) asm volatile("" ::: "memory");
                             }
                         }
@@ -807,9 +890,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                             x[c] = (see >> c) & 1u ? x[c] : neg_inf();
                     }
                     if (raise) {
-                        // ---- raise the reference maxima that need it (or stop, all
-                        // together: s_stop is not written between the vote and the barrier)
-                        const bool stop = s_stop[sw] != 0;
+                        // ---- raise the reference maxima that need it
                         float mine = neg_inf();  // column `lane`'s maximum over the warp's keys
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
@@ -817,11 +898,11 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                             if (lane == c) mine = m;
                         }
                         s_red[quad * 32 + lane] = mine;
-                        tcc::named_barrier(bid, 128);
-                        if (stop) {
-                            go = false;
+                        // (P V of the previous tile is done, too: O may be rescaled)
+                        if (!(go = group_wait(bid, quad, bar(L::kOReady + (x2 ^ 1)),
+                                              ((it + 1) >> 1 & 1) ^ 1, false, 0, 0, abort)))
                             break;
-                        }
+                        ptx::tc_fence_after_sync();
                         const float m4 = fmaxf(fmaxf(s_red[lane], s_red[32 + lane]),
                                                fmaxf(s_red[64 + lane], s_red[96 + lane])) * P.sl2;
                         const float old = s_nm[lane];
@@ -833,10 +914,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         }
                         tcc::named_barrier(bid, 128);
                         if (j > s.j0) {
-                            // O and l of the earlier tiles, once the last P V is done
-                            ok = wait_phase(bar(L::kOReady + (x2 ^ 1)), ((it - 1) >> 1) & 1, abort);
-                            ok = __all_sync(0xffffffffu, ok);
-                            ptx::tc_fence_after_sync();
+                            // O and l of the earlier tiles
 #pragma unroll 1
                             for (int q = 0; q < (NP > 1 ? 8 : 4); ++q) {
                                 uint32_t o[8];
@@ -870,12 +948,13 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         }
                     }
                     if (raise) break;
-                    if (!ok) s_stop[sw] = 1;
-                    if (tcc::named_barrier_and(bid, 128, ok && !(top > kHeadroom))) break;
+                    // P V of two tiles ago has read this P buffer
+                    if (quad == 0) wait_phase(bar(L::kOReady + x2), ((it >> 1) + 1) & 1, abort);
+                    if (tcc::named_barrier_and(bid, 128, !(top > kHeadroom))) break;
                 }
                 if (!go) break;
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(bar(L::kSFree + x2));
+                warp_arrive(bar(L::kSFree + x2), lane);
                 // ---- weights: P[key][row], a row of 128 bytes per key
                 uint8_t *prow = sm + L::kP + (uint32_t)x2 * L::kPSlabs * kSlab + key * 128;
 #pragma unroll
@@ -906,25 +985,25 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(bar(L::kPReady + x2));
+                warp_arrive(bar(L::kPReady + x2), lane);
             }
             if (!go) break;
 
             // ---- results
             s_red[quad * 32 + lane] = column_sums(l, lane);
-            tcc::named_barrier(bid, 128);
+            if (!group_wait(bid, quad, bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1, false, 0, 0,
+                            abort))
+                break;
+            ptx::tc_fence_after_sync();
             const int bad = s_bad[xu];
             float *s_l = s_al;  // 1 / l
             const float sum = s_red[lane] + s_red[32 + lane] + s_red[64 + lane] + s_red[96 + lane];
             const bool whole = s.j0 == 0 && s.j1 == s.nt;
             if (quad == 0) s_l[lane] = whole ? 1.f / sum : 1.f;
             tcc::named_barrier(bid, 128);
-            if (ok) ok = wait_phase(bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1, abort);
-            ok = __all_sync(0xffffffffu, ok);
-            ptx::tc_fence_after_sync();
             const int *s_row = reinterpret_cast<const int *>(sm + L::kRow) + xu * R + 32 * sw;
             float *pd = piece_data<D, R>(P, 2 * blockIdx.x + (s.j0 == 0 ? 1 : 0));
-            if (32 * quad < D && ok) {
+            if (32 * quad < D) {
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     if (8 * q >= live) break;
@@ -961,7 +1040,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     h[1] = s.b;
                     h[2] = s.kvh;
                     h[3] = s.mt;
-                    h[4] = first + it - (s.j1 - s.j0) - s.j0 + s.nt;  // end of the unit
+                    h[4] = s.end;
                     h[5] = total;
                     h[6] = bad;
                     h[0] = 1;
@@ -979,7 +1058,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     ptx::tc_fence_before_sync();
     __syncthreads();
     if (tid == 0 && *abort) report(a.status, TV_ERR_TIMEOUT);
-    if (warp == kWarpMma) {
+    if (warp == kWarpS) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, kTmemCols);
     }
@@ -1047,14 +1126,13 @@ int grid_size(const QAttnArgs &a) {
     const int R = rows_per_unit(a);
     const long long mts = ((long long)a.max_nodes * (a.H / a.Hkv) + R - 1) / R;
     const long long tiles = (long long)a.B * a.Hkv * mts *
-                            ((a.max_pages + 1) / 2 + (a.max_nodes + kKeys - 1) / kKeys);
+                            ((a.max_pages + 1) / 2 + (a.max_nodes + kKeys - 1) / kKeys + kUnitCost);
     return (int)std::min<long long>(sm_count(), tiles);
 }
 
 template <int D, int R, int NP>
 cudaError_t launch_parts(const QAttnArgs &a, cudaStream_t s) {
     using L = Lay<D, R, NP>;
-    static_assert(L::kAlloc <= tcc::kSmemLimit, "shared-memory plan exceeds the limit");
     const cudaError_t attr = configure_smem_once(qcache_attention_kernel<D, R, NP>, false);
     if (attr != cudaSuccess) return attr;
     // the register split counts on what the block is launched with
@@ -1082,7 +1160,7 @@ cudaError_t launch_parts(const QAttnArgs &a, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t launch_rows(const QAttnArgs &a, cudaStream_t s) {
+cudaError_t launch_width(const QAttnArgs &a, cudaStream_t s) {
     if (rows_per_unit(a) == 32)
         return a.out_f32 ? launch_parts<D, 32, 3>(a, s) : launch_parts<D, 32, 2>(a, s);
     return a.out_f32 ? launch_parts<D, 64, 3>(a, s) : launch_parts<D, 64, 2>(a, s);
@@ -1096,7 +1174,7 @@ size_t qcache_attention_workspace_bytes(const QAttnArgs &a) {
 }
 
 cudaError_t launch_qcache_attention(const QAttnArgs &a, cudaStream_t s) {
-    return a.d == 64 ? launch_rows<64>(a, s) : launch_rows<128>(a, s);
+    return a.d == 64 ? launch_width<64>(a, s) : launch_width<128>(a, s);
 }
 
 }  // namespace tv
