@@ -73,18 +73,18 @@ __device__ __forceinline__ Req request(const QParams &P, int b) {
     r.range = request_range(a.node_offsets, b, a.T, a.max_nodes, r.off, r.n);
     if (!r.range) r.n = 0;
     r.ctx = a.ctx_len[b];
-    r.bad = r.ctx < 0 || r.ctx > (long long)a.max_pages * kQPage;
+    r.bad = r.ctx < 0 || r.ctx > a.max_pages * kQPage;
     if (r.bad) r.ctx = 0;
     const int cp = (r.ctx + kQPage - 1) / kQPage;
     if (a.window > 0) {
-        const long long lo = (long long)r.ctx + 1 - a.window;  // seen by a node at depth 1
-        r.lp = lo >= r.ctx ? cp : lo > 0 ? (int)lo / kQPage : 0;
+        const int lo = r.ctx + 1 - a.window;  // seen by a node at depth 1
+        r.lp = lo >= r.ctx ? cp : max(lo, 0) / kQPage;
         r.sp = min((min(a.sinks, r.ctx) + kQPage - 1) / kQPage, r.lp);
     }
     r.np = r.sp + cp - r.lp;
     r.nct = (r.np + 1) / 2;
     r.nt = r.n > 0 ? r.nct + (r.n + kKeys - 1) / kKeys : 0;
-    r.mts = (int)(((long long)r.n * P.grp + R - 1) / R);
+    r.mts = (r.n * P.grp + R - 1) / R;
     return r;
 }
 
@@ -94,8 +94,9 @@ struct Seg {
     int off, n, ctx, bad;                // as in Req
     int sp, lp, np, nct, nt;
     int end;                             // end of the unit's tiles among all costs
+    int c0, c1;                          // tiles whose keys are seen by every row
 };
-constexpr int kSegInts = 16, kSegs = 4;  // ring of segments in shared memory
+constexpr int kSegInts = 20, kSegs = 4;  // ring of segments in shared memory
 static_assert(sizeof(Seg) <= kSegInts * 4, "");
 
 __device__ __forceinline__ int page_of(const Seg &s, int i) {
@@ -107,7 +108,7 @@ template <int R>
 __device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, int &t, int t1) {
     Seg s{};
     Req r;
-    int lo, unit;
+    int lo, unit, first;
     for (;;) {
         if (t >= t1) return s;
         int hi = P.nb - 1;  // the last request whose costs begin at or before t
@@ -121,18 +122,18 @@ __device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, in
                 hi = mid - 1;
         }
         r = request<R>(P, P.b0 + lo);
-        const int rem = t - cum[lo];
-        unit = rem / (r.nt + kUnitCost);
-        s.j0 = rem % (r.nt + kUnitCost);
-        if (s.j0 < r.nt) break;
-        t = cum[lo] + (unit + 1) * (r.nt + kUnitCost);  // past the unit's tiles
+        unit = (t - cum[lo]) / (r.nt + kUnitCost);
+        first = cum[lo] + unit * (r.nt + kUnitCost);
+        if (t < first + r.nt) break;
+        t = first + r.nt + kUnitCost;  // past the unit's tiles
     }
     s.b = P.b0 + lo;
-    s.j1 = min(r.nt, s.j0 + (t1 - t));
-    s.end = cum[lo] + unit * (r.nt + kUnitCost) + r.nt;
-    t += s.j1 - s.j0;
+    s.j0 = t - first;
+    s.j1 = min(r.nt, t1 - first);
+    s.end = first + r.nt;
+    t = first + s.j1;
     s.kvh = unit / r.mts;
-    s.mt = unit % r.mts;
+    s.mt = unit - s.kvh * r.mts;
     s.off = r.off;
     s.n = r.n;
     s.ctx = r.ctx;
@@ -142,6 +143,14 @@ __device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, in
     s.np = r.np;
     s.nct = r.nct;
     s.nt = r.nt;
+    // whole pages below ctx, and past every node's window start
+    const int full = max(r.sp + r.ctx / kQPage - r.lp, 0);
+    s.c1 = min(full, r.np) / 2;
+    if (P.a.window > 0) {
+        const int all = r.ctx + r.n - P.a.window;  // the deepest node's, at most
+        const int page = max(all + kQPage - 1, 0) / kQPage;
+        s.c0 = (r.sp + max(page - r.lp, 0) + 1) / 2;
+    }
     return s;
 }
 
@@ -153,8 +162,8 @@ struct Lay {
     static constexpr int kWarps = 4 * kSW + 20, kThreads = kWarps * 32;
     // registers: at launch (all that fit), and after the split
     static constexpr int kRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kRegsSoftmax = kSW == 2 ? 112 : 128, kRegsK = kSW == 2 ? 48 : 56,
-                         kRegsV = kSW == 2 ? 56 : 64, kRegsControl = kSW == 2 ? 64 : 80;
+    static constexpr int kRegsSoftmax = kSW == 2 ? 128 : 144, kRegsK = 48,
+                         kRegsV = kSW == 2 ? 48 : 56, kRegsControl = kSW == 2 ? 56 : 80;
     static_assert(kThreads * kRegs >=
                       128 * (kSW * kRegsSoftmax + 2 * kRegsK + 2 * kRegsV + kRegsControl),
                   "register split");
@@ -164,7 +173,7 @@ struct Lay {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kP = kQ + 2 * kQBytes;
     static constexpr uint32_t kRing = kP + 2 * kPSlabs * kSlab;
-    static constexpr uint32_t kMiscBytes = 16 * 1024;
+    static constexpr uint32_t kMiscBytes = 23 * 1024;
     static constexpr int kStages =
         (int)std::min<uint32_t>(16, (227 * 1024 - 1024 - kMiscBytes - kRing) / (2 * kRec));
     static constexpr uint32_t kCum = kRing + kStages * 2 * kRec;       // int [kChunkB + 1]
@@ -175,7 +184,8 @@ struct Lay {
     static constexpr uint32_t kNm = kRow + 2 * R * 4;                  // float [R]
     static constexpr uint32_t kAl = kNm + R * 4;                       // float [R]
     static constexpr uint32_t kRed = kAl + R * 4;                      // float [kSW][4][32]
-    static constexpr uint32_t kVs = kRed + kSW * 512;                  // u32 [8][32]
+    static constexpr uint32_t kScratch = kRed + kSW * 512;             // float [4 kSW][32][9]
+    static constexpr uint32_t kVs = kScratch + kSW * 4 * 32 * 9 * 4;   // u32 [8][32]
     static constexpr uint32_t kSeg = kVs + 8 * 32 * 4;                 // int [kSegs][16]
     static constexpr uint32_t kBar = kSeg + kSegs * kSegInts * 4;
     // mbarriers: ring full / empty; K and V operands written; a unit's rows prepared /
@@ -203,8 +213,9 @@ struct Lay {
 // Wait for a phase, giving up (and raising the CTA's abort flag) after 2^24 tries, of some
 // 50 cycles each.  The whole wait is one short loop: with clock reads and the flag in it the
 // dozen places that wait made the kernel several times larger than the instruction cache.
+template <int kSleep = 0>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort) {
-    const bool ok = ptx::mbar_wait_tries(bar, parity, 1u << 24);
+    const bool ok = ptx::mbar_wait_tries<kSleep>(bar, parity, 1u << (kSleep ? 22 : 24));
     if (!ok) *abort = 1;
     return ok;
 }
@@ -234,24 +245,30 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ float warp_max_f32(float x) {
-    float y;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Column sums of v[0..31] over a warp: lane c returns column c's.
-__device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
+// Sums or maxima of v[0..31] over a warp, column c to out[c], by way of `buf` (32 rows of
+// 9): a butterfly of shuffles takes several times the instructions.
+template <bool kMax>
+__device__ __forceinline__ void warp_columns(float *buf, float *out, int lane,
+                                             const float (&v)[32]) {
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-        const bool up = lane & s;
+    for (int q = 0; q < 4; ++q) {
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < s; ++i) {
-            const float send = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+        for (int e = 0; e < 8; ++e) buf[lane * 9 + e] = v[8 * q + e];
+        __syncwarp();
+        float y = buf[(lane / 8) * 9 + lane % 8];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            const float z = buf[(lane / 8 + 4 * k) * 9 + lane % 8];
+            y = kMax ? fmaxf(y, z) : y + z;
         }
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+            const float z = __shfl_xor_sync(0xffffffffu, y, o);
+            y = kMax ? fmaxf(y, z) : y + z;
+        }
+        if (lane < 8) out[8 * q + lane] = y;
     }
-    return v[0];
 }
 
 // (x0, x1) * s + (a0, a1), and (x0, x1) + (a0, a1), two lanes per instruction.
@@ -381,17 +398,13 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     // ---- prefix sums of the requests' costs: their tiles, and a constant per unit
     {
         constexpr int per = (kChunkB + L::kThreads - 1) / L::kThreads;
-        int w[per], sum = 0;
-#pragma unroll
-        for (int k = 0; k < per; ++k) {
-            const int i = tid * per + k;
-            w[k] = 0;
-            if (i < P.nb) {
-                const Req r = request<R>(P, P.b0 + i);
-                w[k] = r.nt > 0 ? a.Hkv * r.mts * (r.nt + kUnitCost) : 0;
-                if (blockIdx.x == 0 && !r.range) report(a.status, TV_ERR_TREE);
-            }
-            sum += w[k];
+        int sum = 0;
+#pragma unroll 1
+        for (int i = tid * per; i < min(tid * per + per, P.nb); ++i) {
+            const Req r = request<R>(P, P.b0 + i);
+            if (blockIdx.x == 0 && !r.range) report(a.status, TV_ERR_TREE);
+            s_cum[i] = sum;  // within the thread, for now
+            sum += r.nt > 0 ? a.Hkv * r.mts * (r.nt + kUnitCost) : 0;
         }
         int inc = sum;
 #pragma unroll
@@ -404,14 +417,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         int before = 0;
 #pragma unroll 1
         for (int k = 0; k < warp; ++k) before += s_scan[k];
-        int at = before + inc - sum;
-#pragma unroll
-        for (int k = 0; k < per; ++k) {
-            const int i = tid * per + k;
-            if (i < P.nb) s_cum[i] = at;
-            at += w[k];
-            if (i == P.nb - 1) s_cum[P.nb] = at;
-        }
+#pragma unroll 1
+        for (int i = tid * per; i < min(tid * per + per, P.nb); ++i) s_cum[i] += before + inc - sum;
+        if (tid == L::kThreads - 1) s_cum[P.nb] = before + inc;
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     // operand warps within their registers.)
     auto enter = [&](int i) -> const Seg * {
         const bool got = __all_sync(
-            0xffffffffu, wait_phase(bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, abort));
+            0xffffffffu, wait_phase<100>(bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, abort));
         const Seg *s = reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
         return got && s->j1 > 0 ? s : nullptr;
     };
@@ -442,8 +450,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
         for (int i = 0; ok; ++i) {
             const Seg s = next_segment<R>(P, s_cum, t, t1);
-            ok = __all_sync(0xffffffffu, i < kSegs || wait_phase(bar(L::kSegFree + i % kSegs),
-                                                                 (i / kSegs - 1) & 1, abort));
+            ok = __all_sync(0xffffffffu, i < kSegs || wait_phase<100>(bar(L::kSegFree + i % kSegs),
+                                                                      (i / kSegs - 1) & 1, abort));
             if (!ok) break;
             if (lane == 0) {
                 *reinterpret_cast<Seg *>(s_seg + (i % kSegs) * kSegInts) = s;
@@ -466,8 +474,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 }
                 const int st = rc % NS;
                 ok = __all_sync(0xffffffffu,
-                                rc < NS || wait_phase(bar(L::kEmpty + st), ((rc / NS) - 1) & 1,
-                                                      abort));
+                                rc < NS || wait_phase<100>(bar(L::kEmpty + st), ((rc / NS) - 1) & 1,
+                                                           abort));
                 if (!ok) break;
                 const bool two = 2 * j + 1 < s.np;
                 const uint32_t dst = sbase + L::kRing + (uint32_t)st * 2 * L::kRec;
@@ -576,24 +584,28 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             const Seg s = *sp;
             leave(i);
             const int x = i & 1;
-            if (!__all_sync(0xffffffffu, i < 2 || wait_phase(bar(L::kPrepFree + x),
-                                                             ((i >> 1) - 1) & 1, abort)))
+            if (!__all_sync(0xffffffffu, i < 2 || wait_phase<200>(bar(L::kPrepFree + x),
+                                                                  ((i >> 1) - 1) & 1, abort)))
                 break;
             // per softmax group and tree node: the group's rows that see the node
             uint32_t *s_see = reinterpret_cast<uint32_t *>(sm + L::kSee) + x * SW * kMaxNodes;
             int *s_lo = reinterpret_cast<int *>(sm + L::kLo) + x * R;
             int *s_row = reinterpret_cast<int *>(sm + L::kRow) + x * R;
-            const int nrows = (int)min((long long)s.n * P.grp - (long long)s.mt * R, (long long)R);
+            const int nrows = min(s.n * P.grp - s.mt * R, R);
             // rows past the last keep what they held: their columns are never used
-            constexpr int CH = D / 8;  // 16-byte pieces of a row, a row per CH lanes
-#pragma unroll 1
-            for (int r = lane / CH; r < nrows; r += 32 / CH) {
-                const int row = s.mt * R + r, node = row / P.grp, ch = lane % CH;
-                ptx::cp_async_16(sbase + L::kQ + x * L::kQBytes + (ch / 8) * (R * 128) + r * 128 +
-                                     ((ch % 8) ^ (r & 7)) * 16,
-                                 static_cast<const __nv_bfloat16 *>(a.q) +
+            constexpr int CH = D / 8, kStep = 32 / CH;  // a row per CH lanes, 16 bytes each
+            const int ch = lane % CH;
+            int node = (s.mt * R + lane / CH) / P.grp, head = s.mt * R + lane / CH - node * P.grp;
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
                                      (size_t)(s.off + node) * a.q_stride +
-                                     (size_t)(s.kvh * P.grp + row % P.grp) * D + ch * 8);
+                                     (size_t)(s.kvh * P.grp + head) * D + ch * 8;
+            uint32_t to = sbase + L::kQ + x * L::kQBytes + (ch / 8) * (R * 128);
+#pragma unroll 1
+            for (int r = lane / CH; r < nrows; r += kStep) {
+                ptx::cp_async_16(to + r * 128 + ((ch % 8) ^ (r & 7)) * 16, q);
+                head += kStep;
+                q += kStep * D;
+                for (; head >= P.grp; head -= P.grp) q += a.q_stride - (int64_t)P.grp * D;
             }
             int bad = s.bad ? TV_ERR_SHAPE : 0;
 #pragma unroll 1
@@ -619,13 +631,12 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     int depth = 0;
 #pragma unroll 1
                     for (int q = node; q >= 0; q = s_par[q]) ++depth;
-                    if (a.window > 0)
-                        lo = (int)min(max((long long)s.ctx + depth - a.window, 0LL), 0x7fffffffLL);
+                    if (a.window > 0) lo = max(s.ctx + depth - a.window, 0);
                     int up = 0;  // steps above the node
 #pragma unroll 1
                     for (int q = node; q >= 0; q = s_par[q], ++up) {
                         if (a.window == 0 || up < a.window ||
-                            (long long)s.ctx + depth - up - 1 < a.sinks)
+                            s.ctx + depth - up - 1 < a.sinks)
                             atomicOr(s_see + (r / 32) * kMaxNodes + q, 1u << lane);
                     }
                 }
@@ -657,7 +668,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             const Seg *sp = enter(i);
             if (!sp) break;
             const Seg &s = *sp;
-            const long long vis = a.window > 0 ? (long long)s.ctx + 1 - a.window : 0;
+            const int vis = a.window > 0 ? s.ctx + 1 - a.window : 0;
             const int sinks = a.window > 0 ? a.sinks : 0;
 #pragma unroll 1
             for (int j = s.j0; j < s.j1; ++j, ++it) {
@@ -677,10 +688,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         const uint32_t b2 = *reinterpret_cast<const uint16_t *>(
                             rec + Rc::kVScales + quad * kQPage + 2 * lane);
                         uint32_t s2 = scale_bf16(b2 & 0xFFu) | (scale_bf16(b2 >> 8) << 16);
-                        const int i2 = 2 * j + h, p0 = page_of(s, i2) * kQPage;
-                        if (i2 >= s.np || p0 + kQPage > s.ctx ||
-                            (p0 < vis && p0 + kQPage > sinks)) {
-                            const int pos = p0 + 2 * lane;
+                        if (j < s.c0 || j >= s.c1) {
+                            const int i2 = 2 * j + h;
+                            const int pos = page_of(s, i2) * kQPage + 2 * lane;
                             if (i2 >= s.np || pos >= s.ctx || (pos < vis && pos >= sinks))
                                 s2 &= 0xFFFF0000u;
                             if (i2 >= s.np || pos + 1 >= s.ctx ||
@@ -713,19 +723,25 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     ++rc;
                 } else {
                     if (live) {
-                        const int n0 = (j - s.nct) * kKeys + 64 * h;
-                        const uint16_t *v = static_cast<const uint16_t *>(a.v_tree) +
-                                            (size_t)s.off * a.kv_stride + s.kvh * D + c;
+                        // 32 nodes at a time, their loads in flight together
 #pragma unroll 1
                         for (int q = 0; q < 2; ++q) {
+                            const int n0 = (j - s.nct) * kKeys + 64 * h + 32 * q;
                             uint32_t out[16];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int n = n0 + 32 * q + 2 * e;
-                                const uint32_t x0 = n < s.n ? v[(size_t)n * a.kv_stride] : 0;
-                                const uint32_t x1 =
-                                    n + 1 < s.n ? v[(size_t)(n + 1) * a.kv_stride] : 0;
-                                out[e] = x0 | (x1 << 16);
+                            for (int e = 0; e < 16; ++e) out[e] = 0;
+                            if (n0 < s.n) {
+                                const uint16_t *v = static_cast<const uint16_t *>(a.v_tree) +
+                                                    (size_t)(s.off + n0) * a.kv_stride +
+                                                    s.kvh * D + c;
+                                const int most = s.n - n0;
+                                uint16_t y[32];
+#pragma unroll
+                                for (int e = 0; e < 32; ++e, v += a.kv_stride)
+                                    y[e] = e < most ? *v : (uint16_t)0;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    out[e] = y[2 * e] | ((uint32_t)y[2 * e + 1] << 16);
                             }
                             ptx::tmem_st_x16(dst + 16u * q, out);
                         }
@@ -788,22 +804,26 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     ++rc;
                 } else {
                     const int n = (j - s.nct) * kKeys + key;
-                    const uint4 *k = reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(a.k_tree) +
-                        (size_t)(s.off + (n < s.n ? n : 0)) * a.kv_stride + s.kvh * D) + 4 * g0;
-#pragma unroll 1
-                    for (int g = 0; g < D / 64; ++g) {
-                        uint32_t out[16];
+                    uint32_t out[D / 4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint4 x = n < s.n ? k[4 * g + e] : make_uint4(0, 0, 0, 0);
-                            out[4 * e] = x.x;
-                            out[4 * e + 1] = x.y;
-                            out[4 * e + 2] = x.z;
-                            out[4 * e + 3] = x.w;
+                    for (int e = 0; e < D / 4; ++e) out[e] = 0;
+                    if (n < s.n) {
+                        const uint4 *k = reinterpret_cast<const uint4 *>(
+                            static_cast<const __nv_bfloat16 *>(a.k_tree) +
+                            (size_t)(s.off + n) * a.kv_stride + s.kvh * D) + 4 * g0;
+#pragma unroll
+                        for (int e = 0; e < D / 16; ++e) {
+                            const uint4 y = k[e];
+                            out[4 * e] = y.x;
+                            out[4 * e + 1] = y.y;
+                            out[4 * e + 2] = y.z;
+                            out[4 * e + 3] = y.w;
                         }
-                        ptx::tmem_st_x16(dst + 16u * g, out);
                     }
+                    if constexpr (D == 128)
+                        ptx::tmem_st_x32(dst, out);
+                    else
+                        ptx::tmem_st_x16(dst, out);
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before_sync();
@@ -822,6 +842,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         float *s_nm = reinterpret_cast<float *>(sm + L::kNm) + 32 * sw;
         float *s_al = reinterpret_cast<float *>(sm + L::kAl) + 32 * sw;
         float *s_red = reinterpret_cast<float *>(sm + L::kRed) + 128 * sw;
+        float *scratch = reinterpret_cast<float *>(sm + L::kScratch) + warp * 32 * 9;
         int *hdr = reinterpret_cast<int *>(a.ws) + (size_t)2 * blockIdx.x * 8;
         if (tid == 0) hdr[0] = hdr[8] = 0;
 
@@ -834,23 +855,35 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                             abort))
                 break;
             const Seg &s = *reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
-            const int j1 = s.j1, nct = s.nct;
+            const int j1 = s.j1;
             if (j1 == 0) break;
             const int xu = i & 1;
             const int live = min(max(s.n * P.grp - s.mt * R - 32 * sw, 0), 32);  // the group's rows
             const uint32_t *s_see =
                 reinterpret_cast<const uint32_t *>(sm + L::kSee) + (xu * SW + sw) * kMaxNodes;
             const int *s_lo = reinterpret_cast<const int *>(sm + L::kLo) + xu * R + 32 * sw;
-            // the first position that every row sees by its window
-            const int lo_all =
-                a.window > 0 ? (int)min((long long)s.ctx + s.n - a.window, 0x7fffffffLL) : 0;
-            const int sinks = a.window > 0 ? a.sinks : 0;
+            const int c0 = s.c0, c1 = s.c1;
+            // bit c: row c of the group sees this thread's key in tile j
+            auto seen = [&](int j) -> uint32_t {
+                if (j >= s.nct) return s_see[(j - s.nct) * kKeys + key];
+                const int i2 = 2 * j + key / kQPage;
+                const int pos = page_of(s, i2) * kQPage + key % kQPage;
+                if (i2 >= s.np || pos >= s.ctx) return 0;
+                if (a.window == 0 || pos < a.sinks) return 0xffffffffu;
+                uint32_t see = 0;
+#pragma unroll 4
+                for (int c = 0; c < 32; ++c) see |= pos >= s_lo[c] ? 1u << c : 0u;
+                return see;
+            };
             if (quad == 0) s_nm[lane] = kNoMax;
             if (!group_wait(bid, quad, bar(L::kPrep + xu), (i >> 1) & 1, false, 0, 0, abort)) break;
 
-            float l[32];
+            float l[32], nm[32];  // sums, and -m of every row
 #pragma unroll
-            for (int c = 0; c < 32; ++c) l[c] = 0.f;
+            for (int c = 0; c < 32; ++c) {
+                l[c] = 0.f;
+                nm[c] = kNoMax;
+            }
 #pragma unroll 1
             for (int j = s.j0; j < j1; ++j, ++it) {
                 const int x2 = it & 1;
@@ -868,37 +901,15 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(u[c]);
                     }
-                    // masks
-                    if (j < nct) {
-                        const int i2 = 2 * j + key / kQPage, p0 = page_of(s, i2) * kQPage;
-                        if (i2 >= s.np || p0 + kQPage > s.ctx ||
-                            (p0 < lo_all && p0 + kQPage > sinks)) {
-                            const int pos = p0 + key % kQPage;
-                            const bool in = i2 < s.np && pos < s.ctx;
-                            const int least = pos < sinks ? 0x7fffffff : pos;
-                            // (eight loads at a time: more would spill)
+                    if (j < c0 || j >= c1) {
+                        const uint32_t see = seen(j);
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                x[c] = in && least >= s_lo[c] ? x[c] : neg_inf();
-                                if (c % 8 == 7) asm volatile("" ::: "memory");
-                            }
-                        }
-                    } else {
-                        const uint32_t see = s_see[(j - nct) * kKeys + key];
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            x[c] = (see >> c) & 1u ? x[c] : neg_inf();
+                        for (int c = 0; c < 32; ++c) x[c] = (see >> c) & 1u ? x[c] : neg_inf();
                     }
                     if (raise) {
-                        // ---- raise the reference maxima that need it
-                        float mine = neg_inf();  // column `lane`'s maximum over the warp's keys
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float m = warp_max_f32(x[c]);
-                            if (lane == c) mine = m;
-                        }
-                        s_red[quad * 32 + lane] = mine;
-                        // (P V of the previous tile is done, too: O may be rescaled)
+                        // ---- raise the reference maxima that need it; P V of the previous
+                        // tile is done, so that O may be rescaled
+                        warp_columns<true>(scratch, s_red + quad * 32, lane, x);
                         if (!(go = group_wait(bid, quad, bar(L::kOReady + (x2 ^ 1)),
                                               ((it + 1) >> 1 & 1) ^ 1, false, 0, 0, abort)))
                             break;
@@ -934,23 +945,26 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                                 if (c % 8 == 7) asm volatile("" ::: "memory");
                             }
                         }
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) nm[c] = s_nm[c];
                     }
                     // exponents, and whether any is too large for the reference
-                    float top = neg_inf();
+                    float top[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        if (4 * (q & ~1) < live) {
-                            const float4 nm = *reinterpret_cast<const float4 *>(s_nm + 4 * q);
-                            fma2(x[4 * q], x[4 * q + 1], P.sl2, nm.x, nm.y);
-                            fma2(x[4 * q + 2], x[4 * q + 3], P.sl2, nm.z, nm.w);
-                            top = fmaxf(fmaxf(top, x[4 * q]), x[4 * q + 1]);
-                            top = fmaxf(fmaxf(top, x[4 * q + 2]), x[4 * q + 3]);
+                    for (int q = 0; q < 4; ++q) {
+                        if (8 * q < live) {
+#pragma unroll
+                            for (int c = 8 * q; c < 8 * q + 8; c += 2) {
+                                fma2(x[c], x[c + 1], P.sl2, nm[c], nm[c + 1]);
+                                top[c / 2 % 4] = fmaxf(fmaxf(top[c / 2 % 4], x[c]), x[c + 1]);
+                            }
                         }
                     }
+                    const bool fits = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= kHeadroom;
                     if (raise) break;
                     // P V of two tiles ago has read this P buffer
                     if (quad == 0) wait_phase(bar(L::kOReady + x2), ((it >> 1) + 1) & 1, abort);
-                    if (tcc::named_barrier_and(bid, 128, !(top > kHeadroom))) break;
+                    if (tcc::named_barrier_and(bid, 128, fits)) break;
                 }
                 if (!go) break;
                 ptx::tc_fence_before_sync();
@@ -990,7 +1004,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             if (!go) break;
 
             // ---- results
-            s_red[quad * 32 + lane] = column_sums(l, lane);
+            warp_columns<false>(scratch, s_red + quad * 32, lane, l);
             if (!group_wait(bid, quad, bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1, false, 0, 0,
                             abort))
                 break;
@@ -1003,29 +1017,27 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             tcc::named_barrier(bid, 128);
             const int *s_row = reinterpret_cast<const int *>(sm + L::kRow) + xu * R + 32 * sw;
             float *pd = piece_data<D, R>(P, 2 * blockIdx.x + (s.j0 == 0 ? 1 : 0));
-            if (32 * quad < D) {
+            float *of = whole ? static_cast<float *>(a.out) : pd;
+            const bool half = whole && !a.out_f32;
+            if (32 * quad < D) {  // (key: the channel)
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    if (8 * q >= live) break;
-                    uint32_t hi[8], lo[8];
-                    ptx::tmem_ld_x8_nowait(tl + L::kTO + 8 * q, hi);
-                    if (NP > 1) ptx::tmem_ld_x8_nowait(tl + L::kTO + R + 8 * q, lo);
+                for (int q = 0; 4 * q < live; ++q) {
+                    uint32_t hi[4], lo[4];
+                    ptx::tmem_ld_x4_nowait(tl + L::kTO + 4 * q, hi);
+                    if (NP > 1) ptx::tmem_ld_x4_nowait(tl + L::kTO + R + 4 * q, lo);
                     ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int rr = 8 * q + e;
-                        if (rr >= live) continue;
+                    for (int e = 0; e < 4; ++e) {
+                        const int rr = 4 * q + e;
                         float o = __uint_as_float(hi[e]);
                         if (NP > 1) o += __uint_as_float(lo[e]);
                         o = bad ? 0.f : o * s_l[rr];
-                        if (whole) {
-                            const size_t at = (size_t)s_row[rr] * D + key;  // key: the channel
-                            if (a.out_f32)
-                                static_cast<float *>(a.out)[at] = o;
-                            else
+                        const size_t at = (size_t)(whole ? s_row[rr] : 32 * sw + rr) * D + key;
+                        if (rr < live) {
+                            if (half)
                                 static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(o);
-                        } else {
-                            pd[(32 * sw + rr) * D + key] = o;
+                            else
+                                of[at] = o;
                         }
                     }
                 }

@@ -57,23 +57,42 @@ __device__ __forceinline__ bool mbar_try_wait_hw(uint32_t bar, uint32_t parity) 
     return ok != 0;
 }
 
-// Up to `tries` of those in a row (a loop of five instructions, whatever the caller).
+// Up to `tries` of those in a row (a loop of a few instructions, whatever the caller), with
+// `kSleep` nanoseconds between them when the wait is not on a critical path.
+template <int kSleep = 0>
 __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity, uint32_t tries) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, %3;\n\t"
-        "TV_WAIT_%=:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra TV_DONE_%=;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
-        "@q bra TV_WAIT_%=;\n\t"
-        "TV_DONE_%=:\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(tries)
-        : "memory");
+    if constexpr (kSleep == 0)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+            "mov.u32 n, %3;\n\t"
+            "TV_WAIT_%=:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "@p bra TV_DONE_%=;\n\t"
+            "sub.u32 n, n, 1;\n\t"
+            "setp.ne.u32 q, n, 0;\n\t"
+            "@q bra TV_WAIT_%=;\n\t"
+            "TV_DONE_%=:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(tries)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+            "mov.u32 n, %3;\n\t"
+            "TV_WAIT_%=:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "@p bra TV_DONE_%=;\n\t"
+            "nanosleep.u32 %4;\n\t"
+            "sub.u32 n, n, 1;\n\t"
+            "setp.ne.u32 q, n, 0;\n\t"
+            "@q bra TV_WAIT_%=;\n\t"
+            "TV_DONE_%=:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(tries), "n"(kSleep)
+            : "memory");
     return ok != 0;
 }
 
@@ -374,6 +393,20 @@ __device__ __forceinline__ void tmem_ld_x8_nowait(uint32_t taddr, uint32_t (&r)[
           "=r"(r[7])
         : "r"(taddr)
         : "memory");
+}
+
+// The same with 4 columns.
+__device__ __forceinline__ void tmem_ld_x4_nowait(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {

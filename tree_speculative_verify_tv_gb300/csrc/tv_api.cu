@@ -572,8 +572,8 @@ tv_status qcache_dims(int32_t B, int32_t rows, int32_t Hkv, int32_t d, int32_t n
     if (B < 0 || rows < 0 || Hkv < 1 || d < 1 || num_pages < 1 || max_pages < 1)
         return TV_ERR_SHAPE;
     if (d != 64 && d != 128) return TV_ERR_UNSUPPORTED;
-    // positions and work items are counted in 32 bits
-    if (max_pages > 0x7fffffff / tv::kQPage) return TV_ERR_UNSUPPORTED;
+    // positions (a tree's past the context, too) and work items are counted in 32 bits
+    if (max_pages > 0x7fff0000 / tv::kQPage) return TV_ERR_UNSUPPORTED;
     if (((int64_t)rows / tv::kQPage + 2LL * B) * Hkv * (d / tv::kQGroup) > 0x7fffffffLL)
         return TV_ERR_UNSUPPORTED;
     return TV_OK;
