@@ -9,7 +9,7 @@
 namespace tv {
 namespace {
 
-constexpr int kThreadsQ = 256;
+constexpr int kThreadsQ = 128;
 
 // Row blocks: request b's rows are cut where its positions enter a new page.  Block ids
 // are handed out by base(b) = row_offsets[b] / 64 + 2 b, which leaves every request at
@@ -71,112 +71,291 @@ __device__ __forceinline__ uint8_t *record(const int32_t *table, int max_pages, 
     return cache + ((size_t)page * Hkv + h) * qc::Rec<D>::kBytes;
 }
 
-// Rows src(0..cnt-1) of one group (lane = channel) into places off, off + 1, .. of a
-// record.  V's words hold eight positions: a word that keeps some of its old codes is
-// read first (a page being written has one writer per word, this warp).
+// What a lane holds of a row: 8 channels (one word of K's codes), D / 8 lanes to a row.
+// Scale byte of the 32-channel group of four neighbouring lanes, from their pieces.
+__device__ __forceinline__ uint32_t group_scale(const uint4 &x) {
+    const uint32_t m = 0x7FFF7FFFu;
+    uint32_t y = qc::max2(qc::max2(x.x & m, x.y & m), qc::max2(x.z & m, x.w & m));
+    y = qc::max2(y, __shfl_xor_sync(0xffffffffu, y, 1));
+    y = qc::max2(y, __shfl_xor_sync(0xffffffffu, y, 2));
+    return qc::scale_byte(max(y & 0xFFFFu, y >> 16));
+}
+
+__device__ __forceinline__ float low_half(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float high_half(uint32_t x) {
+    return __uint_as_float(x & 0xFFFF0000u);
+}
+
+// K rows [off, off + cnt) of a record: a warp takes 32 / (D / 8) rows at a time, kBatch
+// loads in flight per lane.  Bound by the reads of the bf16 rows.
 template <int D, typename Row>
-__device__ __forceinline__ void put_rows(uint8_t *rec, int g, int lane, int off, int cnt,
-                                         const __nv_bfloat16 *k, const __nv_bfloat16 *v,
-                                         Row row) {
+__device__ __forceinline__ void put_k(uint8_t *rec, int lane, int off, int cnt,
+                                      const __nv_bfloat16 *k, Row row) {
     using R = qc::Rec<D>;
-    const int c = g * kQGroup + lane;
-    uint32_t word = 0, mask = 0;
-    for (int m = 0; m < cnt; ++m) {
-        const size_t at = row(m) + c;
-        const uint32_t xk = __bfloat16_as_ushort(k[at]), xv = __bfloat16_as_ushort(v[at]);
-        const uint32_t bk = qc::scale_byte(__reduce_max_sync(0xffffffffu, xk & 0x7FFFu));
-        const uint32_t bv = qc::scale_byte(__reduce_max_sync(0xffffffffu, xv & 0x7FFFu));
-        const int p = off + m;
-        uint32_t w = qc::code(xk, qc::scale_inverse(bk)) << qc::code_shift(lane & 7);
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 4;
+    const int w = lane % kLanes, g = w / 4;
+    for (int m0 = lane / kLanes; m0 < cnt + lane / kLanes; m0 += kRows * kBatch) {
+        uint4 x[kBatch];
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
-        if ((lane & 7) == 0)
-            *reinterpret_cast<uint32_t *>(rec + R::kKCodes + (g * kQPage + p) * 16 + lane / 2) = w;
-        if (lane == 0) {
-            rec[R::kKScales + p * R::kGroups + g] = (uint8_t)bk;
-            rec[R::kVScales + g * kQPage + p] = (uint8_t)bv;
+        for (int u = 0; u < kBatch; ++u) {
+            const int m = m0 + u * kRows;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (m < cnt) x[u] = *reinterpret_cast<const uint4 *>(k + row(m) + w * 8);
         }
-        const int sh = qc::code_shift(p & 7);
-        word |= qc::code(xv, qc::scale_inverse(bv)) << sh;
-        mask |= 15u << sh;
-        if ((p & 7) == 7 || m == cnt - 1) {
-            uint32_t *dst = reinterpret_cast<uint32_t *>(
-                rec + R::kVCodes + ((p / 32) * D + c) * 16 + ((p % 32) / 8) * 4);
-            if (mask != 0xffffffffu) word |= *dst & ~mask;
-            *dst = word;
-            word = mask = 0;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int m = m0 + u * kRows, p = off + m;
+            const uint32_t b = group_scale(x[u]);
+            const float inv = qc::scale_inverse(b);
+            const bool far = b == 254;
+            const uint32_t h[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            uint32_t word = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                word |= (qc::code(low_half(h[e]), inv, far) & 15u) << qc::code_shift(2 * e);
+                word |= (qc::code(high_half(h[e]), inv, far) & 15u) << qc::code_shift(2 * e + 1);
+            }
+            // the row's scale bytes in its first lane
+            uint32_t sc = w % 4 == 0 ? b << (8 * g) : 0;
+            sc |= __shfl_xor_sync(0xffffffffu, sc, 4);
+            if (D == 128) sc |= __shfl_xor_sync(0xffffffffu, sc, 8);
+            if (m < cnt) {
+                *reinterpret_cast<uint32_t *>(rec + R::kKCodes + (g * kQPage + p) * 16 +
+                                              w % 4 * 4) = word;
+                if (w == 0) {
+                    if (D == 128)
+                        *reinterpret_cast<uint32_t *>(rec + R::kKScales + p * 4) = sc;
+                    else
+                        *reinterpret_cast<uint16_t *>(rec + R::kKScales + p * 2) = (uint16_t)sc;
+                }
+            }
         }
     }
 }
 
+// V rows [off, off + cnt) of a record: a lane takes its 8 channels at kPos consecutive
+// positions (half a page at D = 128, a quarter at D = 64), so that it ends with whole
+// words, of 8 positions each.  Words that keep some of their old codes are read first (a
+// page being written has one writer, this warp).
+template <int D, typename Row>
+__device__ __forceinline__ void put_v(uint8_t *rec, int lane, int off, int cnt,
+                                      const __nv_bfloat16 *v, Row row) {
+    using R = qc::Rec<D>;
+    constexpr int kLanes = D / 8, kPos = kQPage * kLanes / 32, kBatch = 8;
+    const int o = lane % kLanes, p0 = lane / kLanes * kPos, g = o / 4;
+    const int lo = max(off - p0, 0), hi = min(off + cnt - p0, kPos);  // of this lane's places
+    uint32_t word[kPos / 8][8];
+#pragma unroll
+    for (int q = 0; q < kPos / 8; ++q) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = 8 * q + u;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (i >= lo && i < hi)
+                x[u] = *reinterpret_cast<const uint4 *>(v + row(p0 + i - off) + o * 8);
+        }
+        uint32_t bytes[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) word[q][c] = 0;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const uint32_t b = group_scale(x[u]);
+            const float inv = qc::scale_inverse(b);
+            const bool far = b == 254;
+            const uint32_t h[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            bytes[u / 4] |= b << (8 * (u % 4));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                word[q][2 * e] |= (qc::code(low_half(h[e]), inv, far) & 15u) << qc::code_shift(u);
+                word[q][2 * e + 1] |= (qc::code(high_half(h[e]), inv, far) & 15u)
+                                      << qc::code_shift(u);
+            }
+        }
+        // the group's scale bytes, by its first lane
+        if (o % 4 == 0) {
+            uint8_t *sc = rec + R::kVScales + g * kQPage + p0 + 8 * q;
+            if (lo <= 8 * q && hi >= 8 * q + 8) {
+                *reinterpret_cast<uint2 *>(sc) = make_uint2(bytes[0], bytes[1]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (8 * q + u >= lo && 8 * q + u < hi)
+                        sc[u] = (uint8_t)(bytes[u / 4] >> (8 * (u % 4)));
+            }
+        }
+    }
+    if (lo >= hi) return;
+    // words of positions [8 q, 8 q + 8): which codes are new
+    uint32_t mask[kPos / 8];
+    bool all = true;
+#pragma unroll
+    for (int q = 0; q < kPos / 8; ++q) {
+        mask[q] = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (8 * q + u >= lo && 8 * q + u < hi) mask[q] |= 15u << qc::code_shift(u);
+        all = all && mask[q] == 0xffffffffu;
+    }
+    uint32_t *dst = reinterpret_cast<uint32_t *>(rec + R::kVCodes + ((p0 / 32) * D + 8 * o) * 16 +
+                                                 p0 % 32 / 8 * 4);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint32_t *d = dst + 4 * c;
+        if (!all) {
+#pragma unroll
+            for (int q = 0; q < kPos / 8; ++q)
+                if (mask[q] != 0xffffffffu)
+                    word[q][c] = (word[q][c] & mask[q]) | (d[q] & ~mask[q]);
+        }
+        if constexpr (kPos == 32)
+            *reinterpret_cast<uint4 *>(d) =
+                make_uint4(word[0][c], word[1][c], word[2][c], word[3][c]);
+        else
+            *reinterpret_cast<uint2 *>(d) = make_uint2(word[0][c], word[1][c]);
+    }
+}
+
+// One warp per K or V of a (block, head).
 template <int D>
 __global__ void __launch_bounds__(kThreadsQ) qcache_write_kernel(const QRowsArgs a) {
-    constexpr int G = D / kQGroup;
-    const int lane = threadIdx.x % 32;
-    const long long unit = (long long)blockIdx.x * (kThreadsQ / 32) + threadIdx.x / 32;
-    const int g = (int)(unit % G), h = (int)(unit / G % a.Hkv);
-    const long long blk = unit / G / a.Hkv;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const long long unit = (long long)blockIdx.x * (kThreadsQ / 64) + warp / 2;
+    const int h = (int)(unit % a.Hkv);
+    const long long blk = unit / a.Hkv;
     pdl_wait();
     pdl_launch_next();
     if (blk >= a.T / kQPage + 2LL * a.B) return;
-    const RowBlock r = row_block(a, (int)blk, lane == 0 && g == 0 && h == 0);
+    const RowBlock r = row_block(a, (int)blk, lane == 0 && warp % 2 == 0 && h == 0);
     if (r.cnt == 0 || !r.fits) return;
     uint8_t *rec = record<D>(a.table, a.max_pages, a.num_pages, a.Hkv, a.cache, r.b, r.pos, h,
                              a.status);
     if (!rec) return;
     const size_t first = (size_t)r.row * a.stride + (size_t)h * D;
-    put_rows<D>(rec, g, lane, r.pos % kQPage, r.cnt, static_cast<const __nv_bfloat16 *>(a.k),
-                static_cast<const __nv_bfloat16 *>(a.v),
-                [&](int m) { return first + (size_t)m * a.stride; });
+    auto row = [&](int m) { return first + (size_t)m * a.stride; };
+    if (warp % 2 == 0)
+        put_k<D>(rec, lane, r.pos % kQPage, r.cnt, static_cast<const __nv_bfloat16 *>(a.k), row);
+    else
+        put_v<D>(rec, lane, r.pos % kQPage, r.cnt, static_cast<const __nv_bfloat16 *>(a.v), row);
 }
 
+// One warp per K or V of a (block, head): a lane gives 8 channels of a row, 16 bytes.
 template <int D>
 __global__ void __launch_bounds__(kThreadsQ) qcache_read_kernel(const QRowsArgs a) {
     using R = qc::Rec<D>;
-    constexpr int G = D / kQGroup;
-    const int lane = threadIdx.x % 32;
-    const long long unit = (long long)blockIdx.x * (kThreadsQ / 32) + threadIdx.x / 32;
-    const int g = (int)(unit % G), h = (int)(unit / G % a.Hkv);
-    const long long blk = unit / G / a.Hkv;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kPos = kQPage * kLanes / 32, kBatch = 8;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const long long unit = (long long)blockIdx.x * (kThreadsQ / 64) + warp / 2;
+    const int h = (int)(unit % a.Hkv);
+    const long long blk = unit / a.Hkv;
     pdl_wait();
     pdl_launch_next();
     if (blk >= a.T / kQPage + 2LL * a.B) return;
-    const bool tell = lane == 0 && g == 0 && h == 0;
+    const bool tell = lane == 0 && warp % 2 == 0 && h == 0;
     const RowBlock r = row_block(a, (int)blk, tell);
     if (r.cnt == 0) return;
     const int len = a.len[r.b];
     const bool len_ok = len >= 0 && len <= (long long)a.max_pages * kQPage;
     if (tell && !len_ok) report(a.status, TV_ERR_SHAPE);
-    const int live = r.fits && len_ok ? min(max(len - r.pos, 0), r.cnt) : 0;
+    int live = r.fits && len_ok ? min(max(len - r.pos, 0), r.cnt) : 0;
     const uint8_t *rec = live > 0 ? record<D>(a.table, a.max_pages, a.num_pages, a.Hkv, a.cache,
                                               r.b, r.pos, h, a.status)
                                   : nullptr;
-    const int c = g * kQGroup + lane, sh = qc::code_shift(lane & 7);
-    __nv_bfloat16 *k = static_cast<__nv_bfloat16 *>(a.k), *v = static_cast<__nv_bfloat16 *>(a.v);
-    for (int m = 0; m < r.cnt; ++m) {
-        const size_t at = (size_t)(r.row + m) * a.stride + (size_t)h * D + c;
-        float xk = 0.f, xv = 0.f;
-        if (rec && m < live) {
-            const int p = r.pos % kQPage + m;
-            const uint32_t wk = *reinterpret_cast<const uint32_t *>(
-                rec + R::kKCodes + (g * kQPage + p) * 16 + lane / 8 * 4);
-            const uint32_t wv = *reinterpret_cast<const uint32_t *>(
-                rec + R::kVCodes + ((p / 32) * D + c) * 16 + ((p % 32) / 8) * 4);
-            xk = qc::scale_value(rec[R::kKScales + p * R::kGroups + g]) *
-                 (float)((int)(wk >> sh & 15u) - 8);
-            xv = qc::scale_value(rec[R::kVScales + g * kQPage + p]) *
-                 (float)((int)(wv >> qc::code_shift(p & 7) & 15u) - 8);
+    if (!rec) live = 0;
+    const int off = r.pos % kQPage, w = lane % kLanes, g = w / 4;
+    const size_t first = (size_t)r.row * a.stride + (size_t)h * D + w * 8;
+    if (warp % 2 == 0) {
+        __nv_bfloat16 *k = static_cast<__nv_bfloat16 *>(a.k) + first;
+        for (int m0 = lane / kLanes; m0 < r.cnt; m0 += kRows * kBatch) {
+            uint32_t word[kBatch], b[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int m = m0 + u * kRows, p = off + m;
+                word[u] = 0x88888888u;  // zeros
+                b[u] = 0;
+                if (m < live) {
+                    word[u] = *reinterpret_cast<const uint32_t *>(
+                        rec + R::kKCodes + (g * kQPage + p) * 16 + w % 4 * 4);
+                    b[u] = rec[R::kKScales + p * R::kGroups + g];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int m = m0 + u * kRows;
+                const uint32_t s2 = qc::scale_pair(b[u]), ms = qc::minus_136(s2);
+                if (m < r.cnt)
+                    *reinterpret_cast<uint4 *>(k + (size_t)m * a.stride) = make_uint4(
+                        qc::value_pair(word[u], 0, s2, ms), qc::value_pair(word[u], 1, s2, ms),
+                        qc::value_pair(word[u], 2, s2, ms), qc::value_pair(word[u], 3, s2, ms));
+            }
         }
-        k[at] = __float2bfloat16_rn(xk);  // exact: at most 7 significant bits
-        v[at] = __float2bfloat16_rn(xv);
+        return;
+    }
+    // V: this lane's 8 channels at kPos positions, words of 8 positions per channel
+    const int p0 = lane / kLanes * kPos;
+    __nv_bfloat16 *v = static_cast<__nv_bfloat16 *>(a.v) + first;
+    const int lo = max(off - p0, 0), hi = min(off + r.cnt - p0, kPos);
+    const int end = min(off + live - p0, kPos);  // rows from here on are zeros
+    if (lo >= hi) return;
+    uint32_t word[8][kPos / 8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint8_t *src = rec + R::kVCodes + ((p0 / 32) * D + 8 * w + c) * 16 + p0 % 32 / 8 * 4;
+#pragma unroll
+        for (int q = 0; q < kPos / 8; ++q) word[c][q] = 0x88888888u;
+        if (end > lo) {
+            if constexpr (kPos == 32) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                word[c][0] = x.x;
+                word[c][1] = x.y;
+                word[c][2] = x.z;
+                word[c][3] = x.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                word[c][0] = x.x;
+                word[c][1] = x.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kPos / 8; ++q) {
+        if (8 * q >= hi || 8 * q + 8 <= lo) continue;
+        uint32_t bytes[2] = {0, 0};
+        if (end > lo) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(rec + R::kVScales + g * kQPage + p0 + 8 * q);
+            bytes[0] = x.x;
+            bytes[1] = x.y;
+        }
+        // even positions have their nibbles in the words' low halves, odd ones in the high
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {
+            uint32_t pair[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                pair[e] = __byte_perm(word[2 * e][q], word[2 * e + 1][q], odd ? 0x7632 : 0x5410);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int u = 2 * p + odd, i = 8 * q + u;
+                const uint32_t b = (bytes[u / 4] >> (8 * (u % 4))) & 0xFFu;
+                const uint32_t s2 = qc::scale_pair(b), ms = qc::minus_136(s2);
+                uint4 y = make_uint4(qc::value_pair(pair[0], p, s2, ms),
+                                     qc::value_pair(pair[1], p, s2, ms),
+                                     qc::value_pair(pair[2], p, s2, ms),
+                                     qc::value_pair(pair[3], p, s2, ms));
+                if (i >= end) y = make_uint4(0, 0, 0, 0);
+                if (i >= lo && i < hi)
+                    *reinterpret_cast<uint4 *>(v + (size_t)(p0 + i - off) * a.stride) = y;
+            }
+        }
     }
 }
 
 // One CTA per request, so that the lengths may advance in place: everything that reads
-// ctx_len has read it before the barrier.
+// ctx_len has read it before the barrier.  A warp per K or V of a head.
+constexpr int kThreadsCommit = 512;
+
 template <int D>
-__global__ void __launch_bounds__(kThreadsQ) qcache_commit_kernel(const QCommitArgs a) {
-    constexpr int G = D / kQGroup;
+__global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCommitArgs a) {
     __shared__ int s_node[kMaxDepth];
     __shared__ int s_bad;
     const int b = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -204,16 +383,19 @@ __global__ void __launch_bounds__(kThreadsQ) qcache_commit_kernel(const QCommitA
         if (bad) report(a.status, bad);
     }
     if (bad) return;
-    for (int u = warp; u < a.Hkv * G; u += kThreadsQ / 32) {
-        const int g = u % G, h = u / G;
+    for (int u = warp; u < a.Hkv * 2; u += kThreadsCommit / 32) {
+        const int h = u / 2;
         for (int m0 = 0; m0 < L;) {  // the pages that the path touches: one or two
             const int pos = ctx + m0, cnt = min(L - m0, kQPage - pos % kQPage);
             const int page = a.table[(size_t)b * a.max_pages + pos / kQPage];
             uint8_t *rec = a.cache + ((size_t)page * a.Hkv + h) * qc::Rec<D>::kBytes;
-            put_rows<D>(rec, g, lane, pos % kQPage, cnt, static_cast<const __nv_bfloat16 *>(a.k),
-                        static_cast<const __nv_bfloat16 *>(a.v), [&](int m) {
-                            return (size_t)s_node[m0 + m] * a.stride + (size_t)h * D;
-                        });
+            auto row = [&](int m) { return (size_t)s_node[m0 + m] * a.stride + (size_t)h * D; };
+            if (u % 2 == 0)
+                put_k<D>(rec, lane, pos % kQPage, cnt, static_cast<const __nv_bfloat16 *>(a.k),
+                         row);
+            else
+                put_v<D>(rec, lane, pos % kQPage, cnt, static_cast<const __nv_bfloat16 *>(a.v),
+                         row);
             m0 += cnt;
         }
     }
@@ -221,8 +403,8 @@ __global__ void __launch_bounds__(kThreadsQ) qcache_commit_kernel(const QCommitA
 
 template <typename Kern>
 cudaError_t launch_rows(Kern kern, const QRowsArgs &a, cudaStream_t s) {
-    const long long units = (a.T / kQPage + 2LL * a.B) * a.Hkv * (a.d / kQGroup);
-    const unsigned grid = (unsigned)((units + kThreadsQ / 32 - 1) / (kThreadsQ / 32));
+    const long long units = (a.T / kQPage + 2LL * a.B) * a.Hkv;
+    const unsigned grid = (unsigned)((units + kThreadsQ / 64 - 1) / (kThreadsQ / 64));
     return launch_pdl(kern, dim3(grid), dim3(kThreadsQ), 0, s, a);
 }
 
@@ -239,8 +421,8 @@ cudaError_t launch_qcache_read(const QRowsArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_qcache_commit(const QCommitArgs &a, cudaStream_t s) {
-    return a.d == 64 ? launch_pdl(qcache_commit_kernel<64>, dim3(a.B), dim3(kThreadsQ), 0, s, a)
-                     : launch_pdl(qcache_commit_kernel<128>, dim3(a.B), dim3(kThreadsQ), 0, s, a);
+    return a.d == 64 ? launch_pdl(qcache_commit_kernel<64>, dim3(a.B), dim3(kThreadsCommit), 0, s, a)
+                     : launch_pdl(qcache_commit_kernel<128>, dim3(a.B), dim3(kThreadsCommit), 0, s, a);
 }
 
 }  // namespace tv

@@ -25,13 +25,17 @@ constexpr uint32_t kScaleNaN = 255;
 __device__ __forceinline__ int code_shift(int e) { return ((e >> 1) + 4 * (e & 1)) * 4; }
 
 // Scale byte of a group whose largest |x| has the bf16 bits `amax` (sign clear): amax / 7
-// rounded to four significant bits, ties to even.  amax / 7 needs no more care than one
-// correctly rounded fp32 division: 7 times a tie has at most 8 significant bits, so a
-// quotient that is a tie is exact, and any other is a relative 2^-12 or more away.
+// rounded to four significant bits, ties to even.  The quotient is the reciprocal's product
+// corrected by its residual, exact wherever amax is a multiple of 7: a tie (7 times a tie has
+// at most 8 significant bits) is exact, and any other quotient is a relative 2^-12 or more
+// away from one.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
-    const uint32_t r = __float_as_uint(__fdiv_rn(__uint_as_float(amax << 16), 7.f));
+    const float x = __uint_as_float(amax << 16), c = 1.f / 7.f;
+    const float q = x * c;
+    const uint32_t r = __float_as_uint(fmaf(fmaf(-7.f, q, x), c, q));
     const int b = (int)((r + 0x7FFFFu + ((r >> 20) & 1u)) >> 20) - 840;  // 2^-22 -> 0
-    return amax > 0x7F80u ? kScaleNaN : (uint32_t)min(max(b, 0), 254);
+    // (an infinity's residual is NaN; its byte is the largest, as any beyond the range)
+    return amax > 0x7F80u ? kScaleNaN : amax == 0x7F80u ? 254u : (uint32_t)min(max(b, 0), 254);
 }
 
 // s = (8 + b % 8) 2^(b / 8 - 25) as fp32; NaN for b = 255.
@@ -41,17 +45,47 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
 
 // 1 / s, raised by a relative 2^-18: |x| times this, rounded to nearest, is |x| / s
 // rounded with halves away from zero.  x has 8 and s 4 significant bits, so a quotient
-// that is not a half is a relative 2^-9 or more away from one, far beyond the raise.
+// that is not a half is a relative 2^-9 or more away from one, far beyond the raise, and
+// the raise is far beyond the error of the approximate reciprocal (2^-22).
 __device__ __forceinline__ float scale_inverse(uint32_t b) {
-    return b == kScaleNaN ? 0.f
-                          : __fdiv_rn(1.f + 1.f / 262144.f, __uint_as_float((b + 840u) << 20));
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__uint_as_float((b + 840u) << 20)));
+    return b == kScaleNaN ? 0.f : y * (1.f + 1.f / 262144.f);
 }
 
-// Code 1..15 of the bf16 value with bits `x` (any code for a NaN: its scale says NaN).
-__device__ __forceinline__ uint32_t code(uint32_t x, float inv) {
-    const float a = fminf(__uint_as_float((x & 0x7FFFu) << 16) * inv, 7.f);
-    const int q = __float2int_rn(a);
-    return (uint32_t)(8 + ((x & 0x8000u) ? -q : q));
+// Code 1..15 of x in the low four bits (the others are not clear); any code for a NaN, whose
+// scale says so.  Adding 1.5 2^23 + 8 rounds to an integer; only a group at the end of the
+// range (b = 254) can leave it.
+__device__ __forceinline__ uint32_t code(float x, float inv, bool far) {
+    float t = fmaf(x, inv, 12582920.f);
+    if (far) t = fminf(fmaxf(t, 12582913.f), 12582927.f);
+    return __float_as_uint(t);
+}
+
+// The larger of two packed pairs of bf16 bits without sign (as integers: NaN wins).
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// Two values (the even one in the low half) s (c - 8) of word w's nibbles p and p + 4: the
+// magic exponent makes 128 + c of a nibble, and one packed fma with s and -136 s the value,
+// exactly.
+__device__ __forceinline__ uint32_t value_pair(uint32_t w, int p, uint32_t s2, uint32_t ms2) {
+    uint32_t x, d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(x)
+        : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(s2), "r"(ms2));
+    return d;
+}
+
+// bf16 bits of the scale with byte b, in both halves, and -136 times it.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t b) {
+    const uint32_t s = b == kScaleNaN ? 0x7FC0u : (b << 4) + 0x3480u;
+    return s | (s << 16);
+}
+__device__ __forceinline__ uint32_t minus_136(uint32_t s2) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(s2), "r"(0xC308C308u));  // exact
+    return d;
 }
 
 }  // namespace qc
