@@ -72,6 +72,8 @@ _lib = None
 def load(path: Optional[str] = None):
     """Load libtreeverify.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -134,17 +136,32 @@ def load(path: Optional[str] = None):
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:  # None or an address
         return x
-    return x.data_ptr()
+
+
+_current_stream = None
+
+
+def _find_current_stream():
+    """The current stream's handle by the quickest way this torch has: a call of a small
+    kernel takes less time on the GPU than torch.cuda.current_stream() on the host."""
+    import torch
+    raw, dev = (getattr(torch._C, f, None) for f in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    torch.cuda.init()
+    if raw is None or dev is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(dev())
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

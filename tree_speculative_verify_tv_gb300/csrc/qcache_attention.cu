@@ -34,6 +34,7 @@
 // wait costs a hundred cycles or more, and the instruction cache, so loops are kept rolled
 // and waits short.
 #include <algorithm>
+#include <atomic>
 
 #include "qcache.cuh"
 #include "tc_common.cuh"
@@ -1123,11 +1124,16 @@ __global__ void __launch_bounds__(256) qcache_attention_join_kernel(const QParam
     }
 }
 
+// SMs of the current device, asked once per device.
 int sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
-    return n > 0 ? n : 152;
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+        return 152;
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 // Rows per unit: 32 when no request has more, else 64.
@@ -1147,11 +1153,14 @@ cudaError_t launch_parts(const QAttnArgs &a, cudaStream_t s) {
     using L = Lay<D, R, NP>;
     const cudaError_t attr = configure_smem_once(qcache_attention_kernel<D, R, NP>, false);
     if (attr != cudaSuccess) return attr;
-    // the register split counts on what the block is launched with
-    cudaFuncAttributes fa;
-    const cudaError_t got = cudaFuncGetAttributes(&fa, qcache_attention_kernel<D, R, NP>);
-    if (got != cudaSuccess) return got;
-    if (fa.numRegs != L::kRegs) return cudaErrorInvalidConfiguration;
+    // the register split counts on what the block is launched with (a fact of the build)
+    static const cudaError_t regs = [] {
+        cudaFuncAttributes fa;
+        const cudaError_t got = cudaFuncGetAttributes(&fa, qcache_attention_kernel<D, R, NP>);
+        if (got != cudaSuccess) return got;
+        return fa.numRegs == L::kRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+    }();
+    if (regs != cudaSuccess) return regs;
     QParams P;
     P.a = a;
     P.grp = a.H / a.Hkv;
