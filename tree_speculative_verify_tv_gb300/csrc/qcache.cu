@@ -10,6 +10,7 @@ namespace tv {
 namespace {
 
 constexpr int kThreadsQ = 128;
+constexpr int kWriteCtas = 8;  // writing CTAs per SM that registers leave room for
 
 // Row blocks: request b's rows are cut where its positions enter a new page.  Block ids
 // are handed out by base(b) = row_offsets[b] / 64 + 2 b, which leaves every request at
@@ -86,15 +87,25 @@ __device__ __forceinline__ float high_half(uint32_t x) {
     return __uint_as_float(x & 0xFFFF0000u);
 }
 
-// K rows [off, off + cnt) of a record: a warp takes 32 / (D / 8) rows at a time, kBatch
+// The piece with values beyond the range of the largest step clamped (a rare branch).
+__device__ __forceinline__ uint4 in_range(uint4 x, uint32_t b) {
+    if (__any_sync(0xffffffffu, b == 254)) {
+        if (b == 254)
+            x = make_uint4(qc::clamp_pair(x.x), qc::clamp_pair(x.y), qc::clamp_pair(x.z),
+                           qc::clamp_pair(x.w));
+    }
+    return x;
+}
+
+// K rows from .. cnt - 1 of those that go to places off + row: a warp takes 32 / (D / 8) rows at a time, kBatch
 // loads in flight per lane.  Bound by the reads of the bf16 rows.
 template <int D, typename Row>
-__device__ __forceinline__ void put_k(uint8_t *rec, int lane, int off, int cnt,
+__device__ __forceinline__ void put_k(uint8_t *rec, int lane, int off, int from, int cnt,
                                       const __nv_bfloat16 *k, Row row) {
     using R = qc::Rec<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 4;
     const int w = lane % kLanes, g = w / 4;
-    for (int m0 = lane / kLanes; m0 < cnt + lane / kLanes; m0 += kRows * kBatch) {
+    for (int m0 = from + lane / kLanes; m0 < cnt + lane / kLanes; m0 += kRows * kBatch) {
         uint4 x[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -107,13 +118,13 @@ __device__ __forceinline__ void put_k(uint8_t *rec, int lane, int off, int cnt,
             const int m = m0 + u * kRows, p = off + m;
             const uint32_t b = group_scale(x[u]);
             const float inv = qc::scale_inverse(b);
-            const bool far = b == 254;
-            const uint32_t h[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            const uint4 y = in_range(x[u], b);
+            const uint32_t h[4] = {y.x, y.y, y.z, y.w};
             uint32_t word = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                word |= (qc::code(low_half(h[e]), inv, far) & 15u) << qc::code_shift(2 * e);
-                word |= (qc::code(high_half(h[e]), inv, far) & 15u) << qc::code_shift(2 * e + 1);
+                word = qc::put_code(word, low_half(h[e]), inv, qc::code_shift(2 * e));
+                word = qc::put_code(word, high_half(h[e]), inv, qc::code_shift(2 * e + 1));
             }
             // the row's scale bytes in its first lane
             uint32_t sc = w % 4 == 0 ? b << (8 * g) : 0;
@@ -133,20 +144,23 @@ __device__ __forceinline__ void put_k(uint8_t *rec, int lane, int off, int cnt,
     }
 }
 
-// V rows [off, off + cnt) of a record: a lane takes its 8 channels at kPos consecutive
-// positions (half a page at D = 128, a quarter at D = 64), so that it ends with whole
-// words, of 8 positions each.  Words that keep some of their old codes are read first (a
+// V rows [off, off + cnt) of a record, as far as they fall into part `part` of its places
+// (half a page at D = 128, all of it at D = 64): a lane takes its 8 channels at 16
+// consecutive positions, so that it ends with whole words, of 8 positions each.  Words that keep some of their old codes are read first (a
 // page being written has one writer, this warp).
 template <int D, typename Row>
-__device__ __forceinline__ void put_v(uint8_t *rec, int lane, int off, int cnt,
+__device__ __forceinline__ void put_v(uint8_t *rec, int lane, int part, int off, int cnt,
                                       const __nv_bfloat16 *v, Row row) {
     using R = qc::Rec<D>;
-    constexpr int kLanes = D / 8, kPos = kQPage * kLanes / 32, kBatch = 8;
-    const int o = lane % kLanes, p0 = lane / kLanes * kPos, g = o / 4;
+    constexpr int kLanes = D / 8, kPos = 16, kBatch = 8;
+    const int o = lane % kLanes, p0 = part * kPos * (32 / kLanes) + lane / kLanes * kPos, g = o / 4;
     const int lo = max(off - p0, 0), hi = min(off + cnt - p0, kPos);  // of this lane's places
     uint32_t word[kPos / 8][8];
 #pragma unroll
     for (int q = 0; q < kPos / 8; ++q) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) word[q][c] = 0;
+        if (!__any_sync(0xffffffffu, 8 * q < hi && 8 * q + 8 > lo)) continue;
         uint4 x[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -157,19 +171,18 @@ __device__ __forceinline__ void put_v(uint8_t *rec, int lane, int off, int cnt,
         }
         uint32_t bytes[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 8; ++c) word[q][c] = 0;
-#pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const uint32_t b = group_scale(x[u]);
             const float inv = qc::scale_inverse(b);
-            const bool far = b == 254;
-            const uint32_t h[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            const uint4 y = in_range(x[u], b);
+            const uint32_t h[4] = {y.x, y.y, y.z, y.w};
             bytes[u / 4] |= b << (8 * (u % 4));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                word[q][2 * e] |= (qc::code(low_half(h[e]), inv, far) & 15u) << qc::code_shift(u);
-                word[q][2 * e + 1] |= (qc::code(high_half(h[e]), inv, far) & 15u)
-                                      << qc::code_shift(u);
+                word[q][2 * e] = qc::put_code(word[q][2 * e], low_half(h[e]), inv,
+                                              qc::code_shift(u));
+                word[q][2 * e + 1] = qc::put_code(word[q][2 * e + 1], high_half(h[e]), inv,
+                                                  qc::code_shift(u));
             }
         }
         // the group's scale bytes, by its first lane
@@ -208,35 +221,34 @@ __device__ __forceinline__ void put_v(uint8_t *rec, int lane, int off, int cnt,
                 if (mask[q] != 0xffffffffu)
                     word[q][c] = (word[q][c] & mask[q]) | (d[q] & ~mask[q]);
         }
-        if constexpr (kPos == 32)
-            *reinterpret_cast<uint4 *>(d) =
-                make_uint4(word[0][c], word[1][c], word[2][c], word[3][c]);
-        else
-            *reinterpret_cast<uint2 *>(d) = make_uint2(word[0][c], word[1][c]);
+        *reinterpret_cast<uint2 *>(d) = make_uint2(word[0][c], word[1][c]);
     }
 }
 
-// One warp per K or V of a (block, head).
+// One warp per part of K or V of a (block, head): half a page (of V at D = 64: all of it).
 template <int D>
-__global__ void __launch_bounds__(kThreadsQ) qcache_write_kernel(const QRowsArgs a) {
+__global__ void __launch_bounds__(kThreadsQ, kWriteCtas) qcache_write_kernel(const QRowsArgs a) {
+    constexpr int kParts = 2, kVParts = D / 64;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const long long unit = (long long)blockIdx.x * (kThreadsQ / 64) + warp / 2;
-    const int h = (int)(unit % a.Hkv);
-    const long long blk = unit / a.Hkv;
+    const int h = blockIdx.x % a.Hkv, blk = blockIdx.x / a.Hkv;
     pdl_wait();
     pdl_launch_next();
-    if (blk >= a.T / kQPage + 2LL * a.B) return;
-    const RowBlock r = row_block(a, (int)blk, lane == 0 && warp % 2 == 0 && h == 0);
+    const RowBlock r = row_block(a, blk, threadIdx.x == 0 && h == 0);
     if (r.cnt == 0 || !r.fits) return;
     uint8_t *rec = record<D>(a.table, a.max_pages, a.num_pages, a.Hkv, a.cache, r.b, r.pos, h,
                              a.status);
     if (!rec) return;
     const size_t first = (size_t)r.row * a.stride + (size_t)h * D;
     auto row = [&](int m) { return first + (size_t)m * a.stride; };
-    if (warp % 2 == 0)
-        put_k<D>(rec, lane, r.pos % kQPage, r.cnt, static_cast<const __nv_bfloat16 *>(a.k), row);
-    else
-        put_v<D>(rec, lane, r.pos % kQPage, r.cnt, static_cast<const __nv_bfloat16 *>(a.v), row);
+    const int off = r.pos % kQPage;
+    if (warp < kParts) {
+        const int half = (r.cnt + kParts - 1) / kParts;
+        put_k<D>(rec, lane, off, warp * half, min(r.cnt, (warp + 1) * half),
+                 static_cast<const __nv_bfloat16 *>(a.k), row);
+    } else if (warp < kParts + kVParts) {
+        put_v<D>(rec, lane, warp - kParts, off, r.cnt, static_cast<const __nv_bfloat16 *>(a.v),
+                 row);
+    }
 }
 
 // One warp per K or V of a (block, head): a lane gives 8 channels of a row, 16 bytes.
@@ -356,7 +368,7 @@ constexpr int kThreadsCommit = 512;
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCommitArgs a) {
-    __shared__ int s_node[kMaxDepth];
+    __shared__ int s_node[kMaxDepth], s_page[2];
     __shared__ int s_bad;
     const int b = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     pdl_wait();
@@ -375,6 +387,7 @@ __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCo
         if (node < 0 || node >= n) s_bad = TV_ERR_TREE;
         const int page = a.table[(size_t)b * a.max_pages + (ctx + m) / kQPage];
         if (page < 0 || page >= a.num_pages) atomicCAS(&s_bad, 0, TV_ERR_SHAPE);
+        s_page[(ctx + m) / kQPage - ctx / kQPage] = page;
     }
     __syncthreads();
     const int bad = s_bad;
@@ -383,46 +396,45 @@ __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCo
         if (bad) report(a.status, bad);
     }
     if (bad) return;
-    for (int u = warp; u < a.Hkv * 2; u += kThreadsCommit / 32) {
-        const int h = u / 2;
+    constexpr int kTasks = 1 + D / 64;  // K, and the parts of V
+    for (int u = warp; u < a.Hkv * kTasks; u += kThreadsCommit / 32) {
+        const int h = u / kTasks, part = u % kTasks - 1;
         for (int m0 = 0; m0 < L;) {  // the pages that the path touches: one or two
             const int pos = ctx + m0, cnt = min(L - m0, kQPage - pos % kQPage);
-            const int page = a.table[(size_t)b * a.max_pages + pos / kQPage];
-            uint8_t *rec = a.cache + ((size_t)page * a.Hkv + h) * qc::Rec<D>::kBytes;
+            uint8_t *rec = a.cache +
+                           ((size_t)s_page[pos / kQPage - ctx / kQPage] * a.Hkv + h) *
+                               qc::Rec<D>::kBytes;
             auto row = [&](int m) { return (size_t)s_node[m0 + m] * a.stride + (size_t)h * D; };
-            if (u % 2 == 0)
-                put_k<D>(rec, lane, pos % kQPage, cnt, static_cast<const __nv_bfloat16 *>(a.k),
+            if (part < 0)
+                put_k<D>(rec, lane, pos % kQPage, 0, cnt, static_cast<const __nv_bfloat16 *>(a.k),
                          row);
             else
-                put_v<D>(rec, lane, pos % kQPage, cnt, static_cast<const __nv_bfloat16 *>(a.v),
-                         row);
+                put_v<D>(rec, lane, part, pos % kQPage, cnt,
+                         static_cast<const __nv_bfloat16 *>(a.v), row);
             m0 += cnt;
         }
     }
 }
 
-template <typename Kern>
-cudaError_t launch_rows(Kern kern, const QRowsArgs &a, cudaStream_t s) {
-    const long long units = (a.T / kQPage + 2LL * a.B) * a.Hkv;
-    const unsigned grid = (unsigned)((units + kThreadsQ / 64 - 1) / (kThreadsQ / 64));
-    return launch_pdl(kern, dim3(grid), dim3(kThreadsQ), 0, s, a);
-}
-
 }  // namespace
 
 cudaError_t launch_qcache_write(const QRowsArgs &a, cudaStream_t s) {
-    return a.d == 64 ? launch_rows(qcache_write_kernel<64>, a, s)
-                     : launch_rows(qcache_write_kernel<128>, a, s);
+    const dim3 grid((unsigned)((a.T / kQPage + 2LL * a.B) * a.Hkv));
+    return a.d == 64 ? launch_pdl(qcache_write_kernel<64>, grid, dim3(kThreadsQ), 0, s, a)
+                     : launch_pdl(qcache_write_kernel<128>, grid, dim3(kThreadsQ), 0, s, a);
 }
 
 cudaError_t launch_qcache_read(const QRowsArgs &a, cudaStream_t s) {
-    return a.d == 64 ? launch_rows(qcache_read_kernel<64>, a, s)
-                     : launch_rows(qcache_read_kernel<128>, a, s);
+    const long long units = (a.T / kQPage + 2LL * a.B) * a.Hkv;
+    const dim3 grid((unsigned)((units + kThreadsQ / 64 - 1) / (kThreadsQ / 64)));
+    return a.d == 64 ? launch_pdl(qcache_read_kernel<64>, grid, dim3(kThreadsQ), 0, s, a)
+                     : launch_pdl(qcache_read_kernel<128>, grid, dim3(kThreadsQ), 0, s, a);
 }
 
 cudaError_t launch_qcache_commit(const QCommitArgs &a, cudaStream_t s) {
-    return a.d == 64 ? launch_pdl(qcache_commit_kernel<64>, dim3(a.B), dim3(kThreadsCommit), 0, s, a)
-                     : launch_pdl(qcache_commit_kernel<128>, dim3(a.B), dim3(kThreadsCommit), 0, s, a);
+    return a.d == 64
+               ? launch_pdl(qcache_commit_kernel<64>, dim3(a.B), dim3(kThreadsCommit), 0, s, a)
+               : launch_pdl(qcache_commit_kernel<128>, dim3(a.B), dim3(kThreadsCommit), 0, s, a);
 }
 
 }  // namespace tv

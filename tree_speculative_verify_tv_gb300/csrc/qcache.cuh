@@ -53,13 +53,20 @@ __device__ __forceinline__ float scale_inverse(uint32_t b) {
     return b == kScaleNaN ? 0.f : y * (1.f + 1.f / 262144.f);
 }
 
-// Code 1..15 of x in the low four bits (the others are not clear); any code for a NaN, whose
-// scale says so.  Adding 1.5 2^23 + 8 rounds to an integer; only a group at the end of the
-// range (b = 254) can leave it.
-__device__ __forceinline__ uint32_t code(float x, float inv, bool far) {
-    float t = fmaf(x, inv, 12582920.f);
-    if (far) t = fminf(fmaxf(t, 12582913.f), 12582927.f);
-    return __float_as_uint(t);
+// `word` with code 1..15 of x at bit `sh` (any code for a NaN, whose scale says so).  Adding
+// 1.5 2^23 + 8 rounds to an integer in the low bits; only a group at the end of the range
+// (b = 254) could leave 1..15, and has its values clamped before.
+__device__ __forceinline__ uint32_t put_code(uint32_t word, float x, float inv, int sh) {
+    const uint32_t t = __float_as_uint(fmaf(x, inv, 12582920.f));
+    asm("lop3.b32 %0, %1, %2, %0, 0xEA;" : "+r"(word) : "r"(t << sh), "r"(15u << sh));
+    return word;
+}
+
+// A pair of bf16 within +-6272, what b = 254 reaches (as packed values: a NaN becomes one).
+__device__ __forceinline__ uint32_t clamp_pair(uint32_t x) {
+    asm("min.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0x45C445C4u));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xC5C4C5C4u));
+    return x;
 }
 
 // The larger of two packed pairs of bf16 bits without sign (as integers: NaN wins).
