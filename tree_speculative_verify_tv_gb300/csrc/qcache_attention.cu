@@ -178,8 +178,8 @@ struct Lay {
     static constexpr int kStages =
         (int)std::min<uint32_t>(16, (227 * 1024 - 1024 - kMiscBytes - kRing) / (2 * kRec));
     static constexpr uint32_t kCum = kRing + kStages * 2 * kRec;       // int [kChunkB + 1]
-    static constexpr uint32_t kPar = kCum + (kChunkB + 4) * 4;         // int16 [256]
-    static constexpr uint32_t kSee = kPar + kMaxNodes * 2;             // u32 [2][kSW][256]
+    static constexpr uint32_t kPar = kCum + (kChunkB + 4) * 4;         // int [256]
+    static constexpr uint32_t kSee = kPar + kMaxNodes * 4;             // u32 [2][kSW][256]
     static constexpr uint32_t kLo = kSee + 2 * kSW * kMaxNodes * 4;    // int [2][R]
     static constexpr uint32_t kRow = kLo + 2 * R * 4;                  // int [2][R]
     static constexpr uint32_t kNm = kRow + 2 * R * 4;                  // float [R]
@@ -221,15 +221,10 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     return ok;
 }
 
-// The same for a warpgroup on named barrier `bid`, for up to two phases: true in all 128
-// threads or in none.
-__device__ __forceinline__ bool group_wait(int bid, int quad, uint32_t bar0, uint32_t parity0,
-                                           bool both, uint32_t bar1, uint32_t parity1,
+// The same for a warpgroup on named barrier `bid`: true in all 128 threads or in none.
+__device__ __forceinline__ bool group_wait(int bid, int quad, uint32_t bar, uint32_t parity,
                                            volatile int *abort) {
-    bool ok = true;
-    if (quad == 0)
-        ok = wait_phase(bar0, parity0, abort) && (!both || wait_phase(bar1, parity1, abort));
-    return tcc::named_barrier_and(bid, 128, ok);
+    return tcc::named_barrier_and(bid, 128, quad != 0 || wait_phase(bar, parity, abort));
 }
 
 // One arrival of a converged warp, after what its lanes did before.
@@ -345,6 +340,13 @@ __device__ __forceinline__ void split_weights(float p0, float p1, uint32_t (&out
     }
 }
 
+// Adds rows (bits 0..31 the first softmax group's) to those that see a node.
+template <int SW>
+__device__ __forceinline__ void see_rows(uint32_t *see, uint64_t rows) {
+    if ((uint32_t)rows) atomicOr(see, (uint32_t)rows);
+    if (SW == 2 && (uint32_t)(rows >> 32)) atomicOr(see + kMaxNodes, (uint32_t)(rows >> 32));
+}
+
 // Workspace: 8 ints per piece (valid, b, kvh, mt, first tile of the unit past its own
 // tiles, all tiles, bad), then per piece O [R][D], m [R] (as -m), l [R].  Piece 2 i is the
 // continuation CTA i begins with, piece 2 i + 1 the unit it begins and does not end.
@@ -372,7 +374,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     int *s_seg = reinterpret_cast<int *>(sm + L::kSeg);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(sm + L::kMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
-    volatile int *s_bad = reinterpret_cast<volatile int *>(sm + L::kMisc + 16);  // [2]
+    volatile int *s_bad = reinterpret_cast<volatile int *>(sm + L::kMisc + 8);     // [2]
+    volatile int *s_stray = reinterpret_cast<volatile int *>(sm + L::kMisc + 16);  // [kSegs]
     int *s_scan = reinterpret_cast<int *>(sm + L::kMisc + 32);                   // [28]
 
     if (tid == 0) {
@@ -456,6 +459,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             if (!ok) break;
             if (lane == 0) {
                 *reinterpret_cast<Seg *>(s_seg + (i % kSegs) * kSegInts) = s;
+                s_stray[i % kSegs] = 0;
                 ptx::mbar_arrive(bar(L::kSegFull + i % kSegs));
             }
             if (s.j1 == 0) break;
@@ -469,8 +473,13 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     int page = 0;
                     if (i2 < s.np) {
                         page = a.table[(size_t)s.b * a.max_pages + page_of(s, i2)];
-                        if (page < 0 || page >= a.num_pages) page = 0;  // the unit is bad
+                        if (page < 0 || page >= a.num_pages) {
+                            page = 0;
+                            s_stray[i % kSegs] = 1;  // the unit is bad
+                            report(a.status, TV_ERR_SHAPE);
+                        }
                     }
+                    __syncwarp();  // (before the arrival below)
                     rec = a.cache + ((size_t)page * a.Hkv + s.kvh) * L::kRec;
                 }
                 const int st = rc % NS;
@@ -514,8 +523,11 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < n; ++j, ++it) {
                 const int x = it & 1;
+                // (P V of two tiles ago has read its weights, too: the softmax warps take
+                // that from S being ready)
                 ok = ok && wait_phase(bar(L::kKReady + x), (it >> 1) & 1, abort) &&
-                     wait_phase(bar(L::kSFree + x), ((it >> 1) + 1) & 1, abort);
+                     wait_phase(bar(L::kSFree + x), ((it >> 1) + 1) & 1, abort) &&
+                     wait_phase(bar(L::kOReady + x), ((it >> 1) + 1) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll
@@ -577,7 +589,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     } else if (warp == kWarpPrep) {
         // ------------------------------------------------ a unit's rows, one unit ahead:
         // queries, root-path masks, windows, output rows; the tree's and the pages' checks
-        int16_t *s_par = reinterpret_cast<int16_t *>(sm + L::kPar);
+        int *s_par = reinterpret_cast<int *>(sm + L::kPar);
 #pragma unroll 1
         for (int i = 0;; ++i) {
             const Seg *sp = enter(i);
@@ -588,10 +600,10 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             if (!__all_sync(0xffffffffu, i < 2 || wait_phase<200>(bar(L::kPrepFree + x),
                                                                   ((i >> 1) - 1) & 1, abort)))
                 break;
-            // per softmax group and tree node: the group's rows that see the node
-            uint32_t *s_see = reinterpret_cast<uint32_t *>(sm + L::kSee) + x * SW * kMaxNodes;
-            int *s_lo = reinterpret_cast<int *>(sm + L::kLo) + x * R;
-            int *s_row = reinterpret_cast<int *>(sm + L::kRow) + x * R;
+            // the nodes' parents and the queries, all in flight together
+#pragma unroll 1
+            for (int k = lane; k < s.n; k += 32)
+                ptx::cp_async_4(ptx::smem_addr(s_par + k), a.parent + s.off + k);
             const int nrows = min(s.n * P.grp - s.mt * R, R);
             // rows past the last keep what they held: their columns are never used
             constexpr int CH = D / 8, kStep = 32 / CH;  // a row per CH lanes, 16 bytes each
@@ -608,47 +620,49 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 q += kStep * D;
                 for (; head >= P.grp; head -= P.grp) q += a.q_stride - (int64_t)P.grp * D;
             }
-            int bad = s.bad ? TV_ERR_SHAPE : 0;
+            // per softmax group and tree node: the group's rows that see the node
+            uint32_t *s_see = reinterpret_cast<uint32_t *>(sm + L::kSee) + x * SW * kMaxNodes;
+            int *s_lo = reinterpret_cast<int *>(sm + L::kLo) + x * R;
+            int *s_row = reinterpret_cast<int *>(sm + L::kRow) + x * R;
 #pragma unroll 1
-            for (int k = lane; k < s.np; k += 32) {
-                const int page = a.table[(size_t)s.b * a.max_pages + page_of(s, k)];
-                if (page < 0 || page >= a.num_pages) bad = TV_ERR_SHAPE;
-            }
-#pragma unroll 1
-            for (int k = lane; k < s.n; k += 32) {
-                const int p = a.parent[s.off + k];
-                s_par[k] = (int16_t)p;
-                if (p < -1 || p >= k) bad = TV_ERR_TREE;
-            }
-#pragma unroll 1
-            for (int k = lane; k < SW * kMaxNodes; k += 32) s_see[k] = 0;
-            bad = __reduce_max_sync(0xffffffffu, bad);
+            for (int k = lane; k < SW * kMaxNodes / 4; k += 32)
+                reinterpret_cast<uint4 *>(s_see)[k] = make_uint4(0, 0, 0, 0);
+            ptx::cp_async_wait_all();
             __syncwarp();
+            bool tree = true;
 #pragma unroll 1
-            for (int r = lane; r < R; r += 32) {
+            for (int k = lane; k < s.n; k += 32) tree = tree && s_par[k] >= -1 && s_par[k] < k;
+            tree = __all_sync(0xffffffffu, tree);
+            const int bad = !tree ? TV_ERR_TREE : s.bad ? TV_ERR_SHAPE : 0;
+            // a lane per node that has rows here, up its root path
+            const int row0 = s.mt * R, node1 = (row0 + nrows - 1) / P.grp;
+#pragma unroll 1
+            for (int k = row0 / P.grp + lane; k <= node1; k += 32) {
+                const int r0 = max(k * P.grp - row0, 0), r1 = min((k + 1) * P.grp - row0, R);
+                const uint64_t rows = (~0ull >> (64 - (r1 - r0))) << r0;
                 int lo = 0;
-                const int row = s.mt * R + r, node = row / P.grp;
-                if (r < nrows && !bad) {
+                if (a.window > 0) {
                     int depth = 0;
 #pragma unroll 1
-                    for (int q = node; q >= 0; q = s_par[q]) ++depth;
-                    if (a.window > 0) lo = max(s.ctx + depth - a.window, 0);
-                    int up = 0;  // steps above the node
+                    for (int y = k; tree && y >= 0; y = s_par[y]) ++depth;
+                    lo = max(s.ctx + depth - a.window, 0);
 #pragma unroll 1
-                    for (int q = node; q >= 0; q = s_par[q], ++up) {
-                        if (a.window == 0 || up < a.window ||
-                            s.ctx + depth - up - 1 < a.sinks)
-                            atomicOr(s_see + (r / 32) * kMaxNodes + q, 1u << lane);
-                    }
+                    for (int y = k, at = s.ctx + depth - 1; tree && y >= 0; y = s_par[y], --at)
+                        if (at >= lo || at < a.sinks) see_rows<SW>(s_see + y, rows);
+                } else {
+#pragma unroll 1
+                    for (int y = k; tree && y >= 0; y = s_par[y]) see_rows<SW>(s_see + y, rows);
                 }
-                s_lo[r] = lo;
-                s_row[r] = (s.off + node) * a.H + s.kvh * P.grp + row % P.grp;
+#pragma unroll 1
+                for (int r = r0; r < r1; ++r) {
+                    s_lo[r] = lo;
+                    s_row[r] = (s.off + k) * a.H + s.kvh * P.grp + row0 + r - k * P.grp;
+                }
             }
             if (lane == 0) {
                 s_bad[x] = bad;
                 if (bad) report(a.status, bad);
             }
-            ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(L::kPrep + x));
@@ -677,9 +691,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 // P V of two tiles ago has read the buffer; this tile's pages are here
                 const int x = it & 1;
                 const uint32_t dst = tl + 64u * x;
-                ok = group_wait(4 + h, quad, bar(L::kOReady + x), ((it >> 1) + 1) & 1, j < s.nct,
-                                bar(L::kFull + st), (rc / NS) & 1, abort);
-                if (!ok) break;
+                ok = wait_phase(bar(L::kOReady + x), ((it >> 1) + 1) & 1, abort) &&
+                     (j >= s.nct || wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort));
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
                 if (j < s.nct) {
                     const uint8_t *rec = sm + L::kRing + ((uint32_t)st * 2 + h) * L::kRec;
@@ -724,7 +738,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     ++rc;
                 } else {
                     if (live) {
-                        // 32 nodes at a time, their loads in flight together
+                        // 32 nodes at a time, 16 loads in flight: a lane takes its channel
+                        // and its neighbour's for half of the nodes, and they exchange
 #pragma unroll 1
                         for (int q = 0; q < 2; ++q) {
                             const int n0 = (j - s.nct) * kKeys + 64 * h + 32 * q;
@@ -732,17 +747,25 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 16; ++e) out[e] = 0;
                             if (n0 < s.n) {
+                                const int odd = lane & 1, n1 = n0 + 16 * odd;
                                 const uint16_t *v = static_cast<const uint16_t *>(a.v_tree) +
-                                                    (size_t)(s.off + n0) * a.kv_stride +
-                                                    s.kvh * D + c;
-                                const int most = s.n - n0;
-                                uint16_t y[32];
+                                                    (size_t)(s.off + n1) * a.kv_stride +
+                                                    s.kvh * D + (c & ~1);
+                                const int most = s.n - n1;
+                                uint32_t y[16];
 #pragma unroll
-                                for (int e = 0; e < 32; ++e, v += a.kv_stride)
-                                    y[e] = e < most ? *v : (uint16_t)0;
+                                for (int e = 0; e < 16; ++e, v += a.kv_stride)
+                                    y[e] = e < most ? *reinterpret_cast<const uint32_t *>(v) : 0u;
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    out[e] = y[2 * e] | ((uint32_t)y[2 * e + 1] << 16);
+                                for (int e = 0; e < 8; ++e) {
+                                    // the even channel's halves, and the odd one's
+                                    const uint32_t c0 = __byte_perm(y[2 * e], y[2 * e + 1], 0x5410);
+                                    const uint32_t c1 = __byte_perm(y[2 * e], y[2 * e + 1], 0x7632);
+                                    const uint32_t got =
+                                        __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1);
+                                    out[e] = odd ? got : c0;
+                                    out[8 + e] = odd ? c1 : got;
+                                }
                             }
                             ptx::tmem_st_x16(dst + 16u * q, out);
                         }
@@ -774,9 +797,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 // S of two tiles ago has read the buffer; this tile's pages are here
                 const int x = it & 1;
                 const uint32_t dst = tl + (D / 2) * x;
-                ok = group_wait(6 + h, quad, bar(L::kSReady + x), ((it >> 1) + 1) & 1, j < s.nct,
-                                bar(L::kFull + st), (rc / NS) & 1, abort);
-                if (!ok) break;
+                ok = wait_phase(bar(L::kSReady + x), ((it >> 1) + 1) & 1, abort) &&
+                     (j >= s.nct || wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort));
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
                 if (j < s.nct) {
                     const uint8_t *rec =
@@ -852,8 +875,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
         for (int i = 0; go; ++i) {
             // (the segment stays in its ring slot until the results are out)
-            if (!group_wait(bid, quad, bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, false, 0, 0,
-                            abort))
+            if (!group_wait(bid, quad, bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, abort))
                 break;
             const Seg &s = *reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
             const int j1 = s.j1;
@@ -877,7 +899,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 return see;
             };
             if (quad == 0) s_nm[lane] = kNoMax;
-            if (!group_wait(bid, quad, bar(L::kPrep + xu), (i >> 1) & 1, false, 0, 0, abort)) break;
+            if (!group_wait(bid, quad, bar(L::kPrep + xu), (i >> 1) & 1, abort)) break;
 
             float l[32], nm[32];  // sums, and -m of every row
 #pragma unroll
@@ -888,9 +910,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
             for (int j = s.j0; j < j1; ++j, ++it) {
                 const int x2 = it & 1;
-                if (!(go = group_wait(bid, quad, bar(L::kSReady + x2), (it >> 1) & 1, false, 0, 0,
-                                      abort)))
-                    break;
+                // each warp for itself; the vote below brings the group together
+                const bool here = wait_phase(bar(L::kSReady + x2), (it >> 1) & 1, abort);
                 ptx::tc_fence_after_sync();
                 float x[32];
 #pragma unroll 1
@@ -911,9 +932,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         // ---- raise the reference maxima that need it; P V of the previous
                         // tile is done, so that O may be rescaled
                         warp_columns<true>(scratch, s_red + quad * 32, lane, x);
-                        if (!(go = group_wait(bid, quad, bar(L::kOReady + (x2 ^ 1)),
-                                              ((it + 1) >> 1 & 1) ^ 1, false, 0, 0, abort)))
-                            break;
+                        go = here && wait_phase(bar(L::kOReady + (x2 ^ 1)),
+                                                ((it + 1) >> 1 & 1) ^ 1, abort);
+                        if (!(go = tcc::named_barrier_and(bid, 128, go))) break;
                         ptx::tc_fence_after_sync();
                         const float m4 = fmaxf(fmaxf(s_red[lane], s_red[32 + lane]),
                                                fmaxf(s_red[64 + lane], s_red[96 + lane])) * P.sl2;
@@ -962,10 +983,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         }
                     }
                     const bool fits = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= kHeadroom;
-                    if (raise) break;
-                    // P V of two tiles ago has read this P buffer
-                    if (quad == 0) wait_phase(bar(L::kOReady + x2), ((it >> 1) + 1) & 1, abort);
-                    if (tcc::named_barrier_and(bid, 128, fits)) break;
+                    if (raise || tcc::named_barrier_and(bid, 128, fits && here)) break;
                 }
                 if (!go) break;
                 ptx::tc_fence_before_sync();
@@ -1006,11 +1024,11 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 
             // ---- results
             warp_columns<false>(scratch, s_red + quad * 32, lane, l);
-            if (!group_wait(bid, quad, bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1, false, 0, 0,
+            if (!group_wait(bid, quad, bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1,
                             abort))
                 break;
             ptx::tc_fence_after_sync();
-            const int bad = s_bad[xu];
+            const int bad = s_bad[xu] | s_stray[i % kSegs];
             float *s_l = s_al;  // 1 / l
             const float sum = s_red[lane] + s_red[32 + lane] + s_red[64 + lane] + s_red[96 + lane];
             const bool whole = s.j0 == 0 && s.j1 == s.nt;
@@ -1089,7 +1107,7 @@ __global__ void __launch_bounds__(256) qcache_attention_join_kernel(const QParam
     pdl_launch_next();
     const int *hdr = reinterpret_cast<const int *>(a.ws) + ((size_t)2 * i + 1) * 8;
     if (!hdr[0]) return;
-    const int b = hdr[1], kvh = hdr[2], mt = hdr[3], end = hdr[4], total = hdr[5], bad = hdr[6];
+    const int b = hdr[1], kvh = hdr[2], mt = hdr[3], end = hdr[4], total = hdr[5];
     const int off = a.node_offsets[b], n = a.node_offsets[b + 1] - off;
     const long long row = (long long)mt * R + r;
     if (row >= (long long)n * P.grp) return;
@@ -1098,7 +1116,12 @@ __global__ void __launch_bounds__(256) qcache_attention_join_kernel(const QParam
     const int pieces = last - i + 1;
     auto data = [&](int p) { return piece_data<D, R>(P, p == 0 ? 2 * i + 1 : 2 * (i + p)); };
     float nm = kNoMax;
-    for (int p = lane; p < pieces; p += 32) nm = fminf(nm, data(p)[R * D + r]);
+    int bad = 0;
+    for (int p = lane; p < pieces; p += 32) {
+        nm = fminf(nm, data(p)[R * D + r]);
+        bad |= hdr[p == 0 ? 6 : 16 * p - 2];  // (the header of piece 2 (i + p))
+    }
+    bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) nm = fminf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
     float o[D / 32], den = 0.f;
