@@ -241,13 +241,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Sums or maxima of v[0..31] over a warp, column c to out[c], by way of `buf` (32 rows of
+// Sums or maxima of v[0..live - 1] over a warp, column c to out[c] (in
+// blocks of 8, 8 and 16), by way of `buf` (32 rows of
 // 9): a butterfly of shuffles takes several times the instructions.
 template <bool kMax>
-__device__ __forceinline__ void warp_columns(float *buf, float *out, int lane,
+__device__ __forceinline__ void warp_columns(float *buf, float *out, int lane, int live,
                                              const float (&v)[32]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
+        if (min(8 * q, 16) >= live) continue;
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 8; ++e) buf[lane * 9 + e] = v[8 * q + e];
@@ -378,19 +380,16 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     volatile int *s_stray = reinterpret_cast<volatile int *>(sm + L::kMisc + 16);  // [kSegs]
     int *s_scan = reinterpret_cast<int *>(sm + L::kMisc + 32);                   // [28]
 
-    if (tid == 0) {
-        *abort = 0;
-#pragma unroll 1
-        for (int i = 0; i < L::kNumBars; ++i) {
-            uint32_t count = 1;  // arriving warps
-            if (i >= L::kEmpty && i < L::kKReady) count = 16;  // K and V
-            if (i >= L::kKReady && i < L::kPrep) count = 8;    // K or V
-            if (i >= L::kPrepFree && i < L::kSReady) count = 4 * SW;
-            if (i >= L::kSFree && i < L::kOReady) count = 4 * SW;
-            if (i >= L::kSegFree && i < L::kDone) count = kWarps - 1;
-            ptx::mbar_init(bar(i), count);
-        }
+    if (tid < L::kNumBars) {
+        uint32_t count = 1;  // arriving warps
+        if (tid >= L::kEmpty && tid < L::kKReady) count = 16;  // K and V
+        if (tid >= L::kKReady && tid < L::kPrep) count = 8;    // K or V
+        if (tid >= L::kPrepFree && tid < L::kSReady) count = 4 * SW;
+        if (tid >= L::kSFree && tid < L::kOReady) count = 4 * SW;
+        if (tid >= L::kSegFree && tid < L::kDone) count = kWarps - 1;
+        ptx::mbar_init(bar(tid), count);
         ptx::fence_mbar_init();
+        if (tid == 0) *abort = 0;
     }
     if (warp == kWarpS) {
         ptx::tmem_alloc(ptx::smem_addr(s_tmem), kTmemCols);
@@ -401,7 +400,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 
     // ---- prefix sums of the requests' costs: their tiles, and a constant per unit
     {
-        constexpr int per = (kChunkB + L::kThreads - 1) / L::kThreads;
+        const int per = P.nb > L::kThreads ? 2 : 1;
+        static_assert(kChunkB <= 2 * L::kThreads, "requests per thread");
         int sum = 0;
 #pragma unroll 1
         for (int i = tid * per; i < min(tid * per + per, P.nb); ++i) {
@@ -418,9 +418,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         }
         if (lane == 31) s_scan[warp] = inc;
         __syncthreads();
-        int before = 0;
-#pragma unroll 1
-        for (int k = 0; k < warp; ++k) before += s_scan[k];
+        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? s_scan[lane] : 0);
 #pragma unroll 1
         for (int i = tid * per; i < min(tid * per + per, P.nb); ++i) s_cum[i] += before + inc - sum;
         if (tid == L::kThreads - 1) s_cum[P.nb] = before + inc;
@@ -608,17 +606,21 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             // rows past the last keep what they held: their columns are never used
             constexpr int CH = D / 8, kStep = 32 / CH;  // a row per CH lanes, 16 bytes each
             const int ch = lane % CH;
-            int node = (s.mt * R + lane / CH) / P.grp, head = s.mt * R + lane / CH - node * P.grp;
+            const uint32_t to = sbase + L::kQ + x * L::kQBytes + (ch / 8) * (R * 128);
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
-                                     (size_t)(s.off + node) * a.q_stride +
-                                     (size_t)(s.kvh * P.grp + head) * D + ch * 8;
-            uint32_t to = sbase + L::kQ + x * L::kQBytes + (ch / 8) * (R * 128);
+                                     (size_t)s.off * a.q_stride + (size_t)s.kvh * P.grp * D + ch * 8;
 #pragma unroll 1
-            for (int r = lane / CH; r < nrows; r += kStep) {
-                ptx::cp_async_16(to + r * 128 + ((ch % 8) ^ (r & 7)) * 16, q);
-                head += kStep;
-                q += kStep * D;
-                for (; head >= P.grp; head -= P.grp) q += a.q_stride - (int64_t)P.grp * D;
+            for (int half = 0; half < nrows; half += 32) {
+                // a lane knows where row half + lane begins
+                const int row = s.mt * R + half + lane, node = row / P.grp;
+                const int64_t at = node * a.q_stride + (row - node * P.grp) * D;
+#pragma unroll 4
+                for (int k = 0; k < 32; k += kStep) {
+                    const int64_t from = __shfl_sync(0xffffffffu, at, k + lane / CH);
+                    const int r = half + k + lane / CH;
+                    if (r < nrows)
+                        ptx::cp_async_16(to + r * 128 + ((ch % 8) ^ (r & 7)) * 16, q + from);
+                }
             }
             // per softmax group and tree node: the group's rows that see the node
             uint32_t *s_see = reinterpret_cast<uint32_t *>(sm + L::kSee) + x * SW * kMaxNodes;
@@ -698,6 +700,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 if (j < s.nct) {
                     const uint8_t *rec = sm + L::kRing + ((uint32_t)st * 2 + h) * L::kRec;
                     if (live) {
+                        const uint8_t *codes = rec + Rc::kVCodes + c * 16;
+                        uint4 w4 = *reinterpret_cast<const uint4 *>(codes);
                         // the group's scales (a warp's 32 channels), two positions per lane;
                         // a position that no node sees gets 0, whatever the cache holds there
                         const uint32_t b2 = *reinterpret_cast<const uint16_t *>(
@@ -717,9 +721,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
                         for (int q = 0; q < 2; ++q) {
                             uint32_t out[16];
-                            const uint4 w4 = *reinterpret_cast<const uint4 *>(
-                                rec + Rc::kVCodes + (q * D + c) * 16);
                             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                            if (q == 0) w4 = *reinterpret_cast<const uint4 *>(codes + D * 16);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 // the scales of four pairs of positions, for all lanes
@@ -931,7 +934,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     if (raise) {
                         // ---- raise the reference maxima that need it; P V of the previous
                         // tile is done, so that O may be rescaled
-                        warp_columns<true>(scratch, s_red + quad * 32, lane, x);
+                        warp_columns<true>(scratch, s_red + quad * 32, lane, live, x);
                         go = here && wait_phase(bar(L::kOReady + (x2 ^ 1)),
                                                 ((it + 1) >> 1 & 1) ^ 1, abort);
                         if (!(go = tcc::named_barrier_and(bid, 128, go))) break;
@@ -973,10 +976,10 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     // exponents, and whether any is too large for the reference
                     float top[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (8 * q < live) {
+                    for (int k = 0; k < 3; ++k) {
+                        if (8 * k < live) {
 #pragma unroll
-                            for (int c = 8 * q; c < 8 * q + 8; c += 2) {
+                            for (int c = 8 * k; c < (k == 2 ? 32 : 8 * k + 8); c += 2) {
                                 fma2(x[c], x[c + 1], P.sl2, nm[c], nm[c + 1]);
                                 top[c / 2 % 4] = fmaxf(fmaxf(top[c / 2 % 4], x[c]), x[c + 1]);
                             }
@@ -991,8 +994,10 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 // ---- weights: P[key][row], a row of 128 bytes per key
                 uint8_t *prow = sm + L::kP + (uint32_t)x2 * L::kPSlabs * kSlab + key * 128;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (8 * q < live) {
+                for (int b = 0; b < 3; ++b) {
+                    if (8 * b >= live) continue;
+#pragma unroll
+                    for (int q = b; q < (b == 2 ? 4 : b + 1); ++q) {
                         uint32_t w[NP][4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -1023,7 +1028,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             if (!go) break;
 
             // ---- results
-            warp_columns<false>(scratch, s_red + quad * 32, lane, l);
+            warp_columns<false>(scratch, s_red + quad * 32, lane, live, l);
             if (!group_wait(bid, quad, bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1,
                             abort))
                 break;

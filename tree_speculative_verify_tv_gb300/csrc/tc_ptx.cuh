@@ -43,22 +43,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity,
     return ok != 0;
 }
 
-// The same with the hardware's own time limit.  (A limit given in the instruction makes
-// the compiler wrap it in a loop of sleeps and clock reads, which takes issue slots.)
-__device__ __forceinline__ bool mbar_try_wait_hw(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Up to `tries` of those in a row (a loop of a few instructions, whatever the caller), with
-// `kSleep` nanoseconds between them when the wait is not on a critical path.
+// Up to `tries` tests in a row, each with the hardware's own time limit (one given in the
+// instruction makes the compiler wrap it in a loop of sleeps and clock reads, which takes
+// issue slots): a loop of a few instructions, whatever the caller, with `kSleep`
+// nanoseconds between them when the wait is not on a critical path.
 template <int kSleep = 0>
 __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity, uint32_t tries) {
     uint32_t ok;
