@@ -104,6 +104,17 @@ __device__ __forceinline__ int page_of(const Seg &s, int i) {
     return i < s.sp ? i : i - s.sp + s.lp;
 }
 
+// The costs [0, total) in `shares` parts, the first `rest` of them one longer.
+struct Shares {
+    int each, rest;
+    __device__ Shares(int total, int shares) : each(total / shares) { rest = total - each * shares; }
+    __device__ int begin(int i) const { return i * each + min(i, rest); }
+    __device__ int of(int t) const {
+        const int longer = rest * (each + 1);
+        return t < longer ? t / (each + 1) : rest + (t - longer) / each;
+    }
+};
+
 // Walks this CTA's share [t, t1) of the tiles.
 template <int R>
 __device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, int &t, int t1) {
@@ -160,13 +171,15 @@ __device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, in
 template <int D, int R, int NP>
 struct Lay {
     static constexpr int kSW = R / 32;  // softmax warpgroups
-    static constexpr int kWarps = 4 * kSW + 20, kThreads = kWarps * 32;
+    static constexpr int kVG = 2;  // V warpgroups: as many as fit
+    static constexpr int kWarps = 4 * (kSW + 2 + kVG + 1), kThreads = kWarps * 32;
     // registers: at launch (all that fit), and after the split
     static constexpr int kRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kRegsSoftmax = kSW == 2 ? 128 : 144, kRegsK = 48,
-                         kRegsV = kSW == 2 ? 48 : 56, kRegsControl = kSW == 2 ? 56 : 80;
-    static_assert(kThreads * kRegs >=
-                      128 * (kSW * kRegsSoftmax + 2 * kRegsK + 2 * kRegsV + kRegsControl),
+    static constexpr int kRegsSoftmax = kSW == 2 ? 128 : 144, kRegsOperand = 48,
+                         kRegsControl = 56;
+    static_assert(kRegsSoftmax >= kRegs && kRegsOperand <= kRegs && kRegsControl <= kRegs &&
+                      kThreads * kRegs >=
+                          128 * (kSW * kRegsSoftmax + (2 + kVG) * kRegsOperand + kRegsControl),
                   "register split");
     static constexpr uint32_t kRec = qrec_bytes(D);
     static constexpr uint32_t kPSlabs = (NP * R + 63) / 64;
@@ -205,7 +218,7 @@ struct Lay {
     // tensor memory columns
     static constexpr uint32_t kTS = 0;                       // S^T x 2
     static constexpr uint32_t kTO = 2 * R;                   // O^T, sums of part 0, then 1
-    static constexpr uint32_t kOWidth = NP == 1 ? 64 : NP == 3 && R == 32 ? 96 : 2 * R;
+    static constexpr uint32_t kOWidth = NP == 3 && R == 32 ? 96 : 2 * R;
     static constexpr uint32_t kTK = kTO + kOWidth;           // K x 2
     static constexpr uint32_t kTV = kTK + D;                 // V^T x 2
     static_assert(kTV + 128 <= kTmemCols, "tensor memory plan");
@@ -325,14 +338,12 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t x, uint32_t s2) {
     return d;
 }
 
-// The bf16 parts of two weights, element 0 in the low half.  One part: rounded to nearest.
-// More: each earlier part keeps the upper 16 bits of what is left (exactly), the last is
-// rounded: two leave a relative 2^-16 at most, three 2^-24.
+// The bf16 parts of two weights, element 0 in the low half.  Each earlier part keeps the
+// upper 16 bits of what is left (exactly), the last is rounded: two leave a relative 2^-16
+// at most, three 2^-24.
 template <int NP>
 __device__ __forceinline__ void split_weights(float p0, float p1, uint32_t (&out)[NP]) {
-    if constexpr (NP == 1) {
-        out[0] = tcc::pack_bf16(p0, p1);
-    } else if constexpr (NP == 2) {
+    if constexpr (NP == 2) {
         tcc::split_pair(p0, p1, out[0], out[1]);
     } else {
         const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
@@ -349,8 +360,8 @@ __device__ __forceinline__ void see_rows(uint32_t *see, uint64_t rows) {
     if (SW == 2 && (uint32_t)(rows >> 32)) atomicOr(see + kMaxNodes, (uint32_t)(rows >> 32));
 }
 
-// Workspace: 8 ints per piece (valid, b, kvh, mt, first tile of the unit past its own
-// tiles, all tiles, bad), then per piece O [R][D], m [R] (as -m), l [R].  Piece 2 i is the
+// Workspace: 8 ints per piece (valid, pieces of its unit, the unit's first row among the
+// rows of its KV head's heads, its rows, first node, KV head, bad), then per piece O [R][D], m [R] (as -m), l [R].  Piece 2 i is the
 // continuation CTA i begins with, piece 2 i + 1 the unit it begins and does not end.
 template <int D, int R>
 __device__ __forceinline__ float *piece_data(const QParams &P, int piece) {
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     using L = Lay<D, R, NP>;
     using Rc = qc::Rec<D>;
     constexpr int SW = L::kSW, NS = L::kStages, kWarps = L::kWarps;
-    constexpr int kWarpK = 4 * SW, kWarpV = kWarpK + 8, kWarpCopy = kWarpV + 8,
+    constexpr int kWarpK = 4 * SW, kWarpV = kWarpK + 8, kWarpCopy = kWarpV + 4 * L::kVG,
                   kWarpS = kWarpCopy + 1, kWarpPv = kWarpS + 1, kWarpPrep = kWarpPv + 1;
     extern __shared__ uint8_t smem_raw[];
     // aligned by an offset, not through an integer: the compiler still sees shared memory
@@ -382,8 +393,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 
     if (tid < L::kNumBars) {
         uint32_t count = 1;  // arriving warps
-        if (tid >= L::kEmpty && tid < L::kKReady) count = 16;  // K and V
-        if (tid >= L::kKReady && tid < L::kPrep) count = 8;    // K or V
+        if (tid >= L::kEmpty && tid < L::kKReady) count = 8 + 4 * L::kVG;  // K and V
+        if (tid >= L::kKReady && tid < L::kVReady) count = 8;
+        if (tid >= L::kVReady && tid < L::kPrep) count = 4 * L::kVG;
         if (tid >= L::kPrepFree && tid < L::kSReady) count = 4 * SW;
         if (tid >= L::kSFree && tid < L::kOReady) count = 4 * SW;
         if (tid >= L::kSegFree && tid < L::kDone) count = kWarps - 1;
@@ -429,15 +441,15 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     const uint32_t tmem = *s_tmem;
     const int total = s_cum[P.nb];
     const int shares = min(P.grid, total), me = min((int)blockIdx.x, shares);
-    const int first = shares > 0 ? (int)((long long)total * me / shares) : 0;
-    const int t1 = me < shares ? (int)((long long)total * (me + 1) / shares) : first;
+    const Shares share(total, max(shares, 1));
+    const int first = share.begin(me), t1 = me < shares ? share.begin(me + 1) : first;
 
     // Segment `i` of this CTA, in the ring until leave(i): null at the end, or when a wait
     // expired.  (A reference: the fields are read where they are used, which keeps the
     // operand warps within their registers.)
     auto enter = [&](int i) -> const Seg * {
         const bool got = __all_sync(
-            0xffffffffu, wait_phase<100>(bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, abort));
+            0xffffffffu, wait_phase<20>(bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, abort));
         const Seg *s = reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
         return got && s->j1 > 0 ? s : nullptr;
     };
@@ -542,7 +554,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         wait_phase(bar(L::kDone), 0, abort);
     } else if (warp == kWarpPv) {
         // ------------------------------------------------ O^T += V^T P^T of every tile
-        constexpr uint32_t nPV = NP == 1 ? 64 : 2 * R;
+        constexpr uint32_t nPV = 2 * R;
         constexpr uint32_t idPV = ptx::idesc_bf16_f32_bmn(128, nPV);
         constexpr uint32_t id3 = ptx::idesc_bf16_f32_bmn(128, 64);
         const uint32_t lead = ptx::elect_one();
@@ -672,11 +684,12 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         __syncwarp();
     } else if (warp >= kWarpV) {
         // ------------------------------------------------ V^T operand: thread = channel, a
-        // warpgroup per half of the keys
-        ptx::regs_dec<L::kRegsV>();
-        const int c = 32 * quad + lane, h = (warp - kWarpV) / 4;
-        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTV + 32u * h;
-        uint32_t *s_vs = reinterpret_cast<uint32_t *>(sm + L::kVs) + (warp - kWarpV) * 32;
+        // warpgroup per half or quarter of the keys (kN blocks of 32)
+        ptx::regs_dec<L::kRegsOperand>();
+        constexpr int kN = 4 / L::kVG;
+        const int c = 32 * quad + lane, k0 = (warp - kWarpV) / 4 * kN, h = k0 / 2;
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTV + 16u * k0;
+        uint32_t *s_vs = reinterpret_cast<uint32_t *>(sm + L::kVs) + (warp - kWarpV) * 16 * kN;
         const bool live = 32 * quad < D;
         int it = 0, rc = 0;
         bool ok = true;
@@ -700,29 +713,38 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 if (j < s.nct) {
                     const uint8_t *rec = sm + L::kRing + ((uint32_t)st * 2 + h) * L::kRec;
                     if (live) {
-                        const uint8_t *codes = rec + Rc::kVCodes + c * 16;
-                        uint4 w4 = *reinterpret_cast<const uint4 *>(codes);
-                        // the group's scales (a warp's 32 channels), two positions per lane;
+                        // the group's scales (a warp's 32 channels), kN positions per lane;
                         // a position that no node sees gets 0, whatever the cache holds there
-                        const uint32_t b2 = *reinterpret_cast<const uint16_t *>(
-                            rec + Rc::kVScales + quad * kQPage + 2 * lane);
-                        uint32_t s2 = scale_bf16(b2 & 0xFFu) | (scale_bf16(b2 >> 8) << 16);
+                        const int p0 = 32 * (k0 % 2);
+                        const uint8_t *codes = rec + Rc::kVCodes + ((k0 % 2) * D + c) * 16;
+                        uint4 w4 = *reinterpret_cast<const uint4 *>(codes);
+                        const uint8_t *from = rec + Rc::kVScales + quad * kQPage + p0 + kN * lane;
+                        uint32_t s2;
+                        if constexpr (kN == 2) {
+                            const uint32_t b2 = *reinterpret_cast<const uint16_t *>(from);
+                            s2 = scale_bf16(b2 & 0xFFu) | (scale_bf16(b2 >> 8) << 16);
+                        } else {
+                            s2 = scale_bf16(*from);
+                        }
                         if (j < s.c0 || j >= s.c1) {
                             const int i2 = 2 * j + h;
-                            const int pos = page_of(s, i2) * kQPage + 2 * lane;
-                            if (i2 >= s.np || pos >= s.ctx || (pos < vis && pos >= sinks))
-                                s2 &= 0xFFFF0000u;
-                            if (i2 >= s.np || pos + 1 >= s.ctx ||
-                                (pos + 1 < vis && pos + 1 >= sinks))
-                                s2 &= 0x0000FFFFu;
+                            const int pos = page_of(s, i2) * kQPage + p0 + kN * lane;
+#pragma unroll
+                            for (int e = 0; e < kN; ++e)
+                                if (i2 >= s.np || pos + e >= s.ctx ||
+                                    (pos + e < vis && pos + e >= sinks))
+                                    s2 &= 0xFFFF0000u >> (16 * e);
                         }
-                        s_vs[lane] = s2;
+                        if constexpr (kN == 2)
+                            s_vs[lane] = s2;
+                        else
+                            reinterpret_cast<uint16_t *>(s_vs)[lane] = (uint16_t)s2;
                         __syncwarp();
 #pragma unroll 1
-                        for (int q = 0; q < 2; ++q) {
+                        for (int q = 0; q < kN; ++q) {
                             uint32_t out[16];
                             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                            if (q == 0) w4 = *reinterpret_cast<const uint4 *>(codes + D * 16);
+                            if (q + 1 < kN) w4 = *reinterpret_cast<const uint4 *>(codes + D * 16);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 // the scales of four pairs of positions, for all lanes
@@ -744,8 +766,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         // 32 nodes at a time, 16 loads in flight: a lane takes its channel
                         // and its neighbour's for half of the nodes, and they exchange
 #pragma unroll 1
-                        for (int q = 0; q < 2; ++q) {
-                            const int n0 = (j - s.nct) * kKeys + 64 * h + 32 * q;
+                        for (int q = 0; q < kN; ++q) {
+                            const int n0 = (j - s.nct) * kKeys + 32 * (k0 + q);
                             uint32_t out[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) out[e] = 0;
@@ -784,7 +806,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     } else if (warp >= kWarpK) {
         // ------------------------------------------------ K operand: thread = key, a
         // warpgroup per half of the channels
-        ptx::regs_dec<L::kRegsK>();
+        ptx::regs_dec<L::kRegsOperand>();
         const int key = 32 * quad + lane, h = (warp - kWarpK) / 4, g0 = h * (D / 64);
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTK + 16u * g0;
         int it = 0, rc = 0;
@@ -952,7 +974,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         if (j > s.j0) {
                             // O and l of the earlier tiles
 #pragma unroll 1
-                            for (int q = 0; q < (NP > 1 ? 8 : 4); ++q) {
+                            for (int q = 0; q < 8; ++q) {
                                 uint32_t o[8];
                                 const uint32_t at = tl + L::kTO + R * (q / 4) + 8 * (q % 4);
                                 ptx::tmem_ld_x8_nowait(at, o);
@@ -1045,16 +1067,15 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             const bool half = whole && !a.out_f32;
             if (32 * quad < D) {  // (key: the channel)
 #pragma unroll 1
-                for (int q = 0; 4 * q < live; ++q) {
-                    uint32_t hi[4], lo[4];
-                    ptx::tmem_ld_x4_nowait(tl + L::kTO + 4 * q, hi);
-                    if (NP > 1) ptx::tmem_ld_x4_nowait(tl + L::kTO + R + 4 * q, lo);
+                for (int q = 0; 8 * q < live; ++q) {
+                    uint32_t hi[8], lo[8];
+                    ptx::tmem_ld_x8_nowait(tl + L::kTO + 8 * q, hi);
+                    ptx::tmem_ld_x8_nowait(tl + L::kTO + R + 8 * q, lo);
                     ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int rr = 4 * q + e;
-                        float o = __uint_as_float(hi[e]);
-                        if (NP > 1) o += __uint_as_float(lo[e]);
+                    for (int e = 0; e < 8; ++e) {
+                        const int rr = 8 * q + e;
+                        float o = __uint_as_float(hi[e]) + __uint_as_float(lo[e]);
                         o = bad ? 0.f : o * s_l[rr];
                         const size_t at = (size_t)(whole ? s_row[rr] : 32 * sw + rr) * D + key;
                         if (rr < live) {
@@ -1073,11 +1094,12 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 }
                 if (tid == 0) {
                     int *h = hdr + (s.j0 == 0 ? 8 : 0);
-                    h[1] = s.b;
-                    h[2] = s.kvh;
-                    h[3] = s.mt;
-                    h[4] = s.end;
-                    h[5] = total;
+                    // (the unit ends in the share of its last tile)
+                    h[1] = share.of(s.end - 1) - (int)blockIdx.x + 1;
+                    h[2] = s.mt * R;
+                    h[3] = s.n * P.grp;
+                    h[4] = s.off;
+                    h[5] = s.kvh;
                     h[6] = bad;
                     h[0] = 1;
                 }
@@ -1110,45 +1132,58 @@ __global__ void __launch_bounds__(256) qcache_attention_join_kernel(const QParam
     const int r = blockIdx.y * 8 + threadIdx.x / 32;
     pdl_wait();
     pdl_launch_next();
-    const int *hdr = reinterpret_cast<const int *>(a.ws) + ((size_t)2 * i + 1) * 8;
-    if (!hdr[0]) return;
-    const int b = hdr[1], kvh = hdr[2], mt = hdr[3], end = hdr[4], total = hdr[5];
-    const int off = a.node_offsets[b], n = a.node_offsets[b + 1] - off;
-    const long long row = (long long)mt * R + r;
-    if (row >= (long long)n * P.grp) return;
-    // the CTA whose share holds the unit's last tile
-    const int last = (int)(((long long)end * min(P.grid, total) - 1) / total);
-    const int pieces = last - i + 1;
-    auto data = [&](int p) { return piece_data<D, R>(P, p == 0 ? 2 * i + 1 : 2 * (i + p)); };
-    float nm = kNoMax;
+    const int4 *hdr = reinterpret_cast<const int4 *>(a.ws) + ((size_t)2 * i + 1) * 2;
+    const int4 h0 = hdr[0], h1 = hdr[1];
+    if (!h0.x) return;
+    const int pieces = h0.y, row = h0.z + r;
+    if (row >= h0.w) return;
+    // kBatch pieces at a time, all their loads in flight together
+    constexpr int kBatch = 8;
+    float nm = kNoMax, o[D / 32], den = 0.f;
     int bad = 0;
-    for (int p = lane; p < pieces; p += 32) {
-        nm = fminf(nm, data(p)[R * D + r]);
-        bad |= hdr[p == 0 ? 6 : 16 * p - 2];  // (the header of piece 2 (i + p))
-    }
-    bad = __any_sync(0xffffffffu, bad);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) nm = fminf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
-    float o[D / 32], den = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < pieces; ++p) {
-        const float *d = data(p);
-        const float w = ex2(nm - d[R * D + r]);
-        den += w * d[R * D + R + r];
+#pragma unroll 1
+    for (int p0 = 0; p0 < pieces; p0 += kBatch) {
+        float m[kBatch], l[kBatch], y[kBatch][D / 32];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) o[c] += w * d[r * D + 32 * c + lane];
+        for (int k = 0; k < kBatch; ++k) {
+            // piece 2 i + 1, then the continuations 2 (i + 1), 2 (i + 2), ...
+            const int p = p0 + k, at = p == 0 ? 2 * i + 1 : 2 * (i + p);
+            const float *d = piece_data<D, R>(P, at);
+            const bool have = p < pieces;
+            m[k] = have ? d[R * D + r] : kNoMax;
+            l[k] = have ? d[R * D + R + r] : 0.f;
+            if (have) bad |= reinterpret_cast<const int *>(a.ws)[8 * at + 6];
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) y[k][c] = have ? d[r * D + 32 * c + lane] : 0.f;
+        }
+        float now = nm;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) now = fminf(now, m[k]);
+        const float keep = ex2(now - nm);
+        den *= keep;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) o[c] *= keep;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float w = ex2(now - m[k]);
+            den += w * l[k];
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) o[c] += w * y[k][c];
+        }
+        nm = now;
     }
     const float inv = bad ? 0.f : 1.f / den;
-    const size_t at = ((size_t)(off + row / P.grp) * a.H + kvh * P.grp + row % P.grp) * D + lane;
+    const size_t at =
+        ((size_t)(h1.x + row / P.grp) * a.H + h1.y * P.grp + row % P.grp) * D + lane;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
-        const float y = bad ? 0.f : o[c] * inv;
+        const float v = bad ? 0.f : o[c] * inv;
         if (a.out_f32)
-            static_cast<float *>(a.out)[at + 32 * c] = y;
+            static_cast<float *>(a.out)[at + 32 * c] = v;
         else
-            static_cast<__nv_bfloat16 *>(a.out)[at + 32 * c] = __float2bfloat16_rn(y);
+            static_cast<__nv_bfloat16 *>(a.out)[at + 32 * c] = __float2bfloat16_rn(v);
     }
 }
 
