@@ -363,8 +363,9 @@ __global__ void __launch_bounds__(kThreadsQ) qcache_read_kernel(const QRowsArgs 
 }
 
 // One CTA per request, so that the lengths may advance in place: everything that reads
-// ctx_len has read it before the barrier.  A warp per K or V of a head.
-constexpr int kThreadsCommit = 512;
+// ctx_len has read it before the barrier.  A warp per K, or part of V, of a head: 24 of them
+// at 8 heads of 128 channels (16 warps, and two rounds, took 1.6 us longer per call).
+constexpr int kThreadsCommit = 768;
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCommitArgs a) {
