@@ -187,7 +187,7 @@ struct Lay {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kP = kQ + 2 * kQBytes;
     static constexpr uint32_t kRing = kP + 2 * kPSlabs * kSlab;
-    static constexpr uint32_t kMiscBytes = 23 * 1024;
+    static constexpr uint32_t kMiscBytes = 14 * 1024;
     static constexpr int kStages =
         (int)std::min<uint32_t>(16, (227 * 1024 - 1024 - kMiscBytes - kRing) / (2 * kRec));
     static constexpr uint32_t kCum = kRing + kStages * 2 * kRec;       // int [kChunkB + 1]
@@ -198,8 +198,7 @@ struct Lay {
     static constexpr uint32_t kNm = kRow + 2 * R * 4;                  // float [R]
     static constexpr uint32_t kAl = kNm + R * 4;                       // float [R]
     static constexpr uint32_t kRed = kAl + R * 4;                      // float [kSW][4][32]
-    static constexpr uint32_t kScratch = kRed + kSW * 512;             // float [4 kSW][32][9]
-    static constexpr uint32_t kVs = kScratch + kSW * 4 * 32 * 9 * 4;   // u32 [8][32]
+    static constexpr uint32_t kVs = kRed + kSW * 512;   // u32 [8][32]
     static constexpr uint32_t kSeg = kVs + 8 * 32 * 4;                 // int [kSegs][16]
     static constexpr uint32_t kBar = kSeg + kSegs * kSegInts * 4;
     // mbarriers: ring full / empty; K and V operands written; a unit's rows prepared /
@@ -254,31 +253,31 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Sums or maxima of v[0..live - 1] over a warp, column c to out[c] (in
-// blocks of 8, 8 and 16), by way of `buf` (32 rows of
-// 9): a butterfly of shuffles takes several times the instructions.
+// Sums or maxima of v[0..live - 1] over a warp, column c to out[c] (in blocks of 8, 8 and
+// 16).  At each of three steps a lane hands half of a block's columns to its neighbour, and
+// two more add up what lanes of one column hold.
 template <bool kMax>
-__device__ __forceinline__ void warp_columns(float *buf, float *out, int lane, int live,
+__device__ __forceinline__ void warp_columns(float *out, int lane, int live,
                                              const float (&v)[32]) {
+    auto join = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
+    const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         if (min(8 * q, 16) >= live) continue;
-        __syncwarp();
+        float y[4], z[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) buf[lane * 9 + e] = v[8 * q + e];
-        __syncwarp();
-        float y = buf[(lane / 8) * 9 + lane % 8];
-#pragma unroll
-        for (int k = 1; k < 8; ++k) {
-            const float z = buf[(lane / 8 + 4 * k) * 9 + lane % 8];
-            y = kMax ? fmaxf(y, z) : y + z;
+        for (int c = 0; c < 4; ++c) {
+            const float x0 = v[8 * q + 2 * c], x1 = v[8 * q + 2 * c + 1];
+            y[c] = join(b0 ? x1 : x0, __shfl_xor_sync(0xffffffffu, b0 ? x0 : x1, 1));
         }
 #pragma unroll
-        for (int o = 8; o < 32; o <<= 1) {
-            const float z = __shfl_xor_sync(0xffffffffu, y, o);
-            y = kMax ? fmaxf(y, z) : y + z;
-        }
-        if (lane < 8) out[8 * q + lane] = y;
+        for (int c = 0; c < 2; ++c)
+            z[c] = join(b1 ? y[2 * c + 1] : y[2 * c],
+                        __shfl_xor_sync(0xffffffffu, b1 ? y[2 * c] : y[2 * c + 1], 2));
+        float w = join(b2 ? z[1] : z[0], __shfl_xor_sync(0xffffffffu, b2 ? z[0] : z[1], 4));
+        w = join(w, __shfl_xor_sync(0xffffffffu, w, 8));
+        w = join(w, __shfl_xor_sync(0xffffffffu, w, 16));
+        if (lane < 8) out[8 * q + lane] = w;
     }
 }
 
@@ -603,17 +602,21 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
         for (int i = 0;; ++i) {
             const Seg *sp = enter(i);
-            if (!sp) break;
-            const Seg s = *sp;
-            leave(i);
             const int x = i & 1;
             if (!__all_sync(0xffffffffu, i < 2 || wait_phase<200>(bar(L::kPrepFree + x),
                                                                   ((i >> 1) - 1) & 1, abort)))
                 break;
+            if (!sp) {  // (the softmax warps wait for rows before they look at the segment)
+                if (lane == 0 && !*abort) ptx::mbar_arrive(bar(L::kPrep + x));
+                break;
+            }
+            const Seg s = *sp;
+            leave(i);
             // the nodes' parents and the queries, all in flight together
 #pragma unroll 1
             for (int k = lane; k < s.n; k += 32)
                 ptx::cp_async_4(ptx::smem_addr(s_par + k), a.parent + s.off + k);
+            ptx::cp_async_commit();
             const int nrows = min(s.n * P.grp - s.mt * R, R);
             // rows past the last keep what they held: their columns are never used
             constexpr int CH = D / 8, kStep = 32 / CH;  // a row per CH lanes, 16 bytes each
@@ -634,6 +637,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         ptx::cp_async_16(to + r * 128 + ((ch % 8) ^ (r & 7)) * 16, q + from);
                 }
             }
+            ptx::cp_async_commit();
             // per softmax group and tree node: the group's rows that see the node
             uint32_t *s_see = reinterpret_cast<uint32_t *>(sm + L::kSee) + x * SW * kMaxNodes;
             int *s_lo = reinterpret_cast<int *>(sm + L::kLo) + x * R;
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
             for (int k = lane; k < SW * kMaxNodes / 4; k += 32)
                 reinterpret_cast<uint4 *>(s_see)[k] = make_uint4(0, 0, 0, 0);
-            ptx::cp_async_wait_all();
+            ptx::cp_async_wait_group<1>();  // the parents; the queries under the masks
             __syncwarp();
             bool tree = true;
 #pragma unroll 1
@@ -677,6 +681,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 s_bad[x] = bad;
                 if (bad) report(a.status, bad);
             }
+            ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(L::kPrep + x));
@@ -891,7 +896,6 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         float *s_nm = reinterpret_cast<float *>(sm + L::kNm) + 32 * sw;
         float *s_al = reinterpret_cast<float *>(sm + L::kAl) + 32 * sw;
         float *s_red = reinterpret_cast<float *>(sm + L::kRed) + 128 * sw;
-        float *scratch = reinterpret_cast<float *>(sm + L::kScratch) + warp * 32 * 9;
         int *hdr = reinterpret_cast<int *>(a.ws) + (size_t)2 * blockIdx.x * 8;
         if (tid == 0) hdr[0] = hdr[8] = 0;
 
@@ -900,8 +904,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
         for (int i = 0; go; ++i) {
             // (the segment stays in its ring slot until the results are out)
-            if (!group_wait(bid, quad, bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, abort))
-                break;
+            if (quad == 0) s_nm[lane] = kNoMax;
+            if (!group_wait(bid, quad, bar(L::kPrep + (i & 1)), (i >> 1) & 1, abort)) break;
             const Seg &s = *reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
             const int j1 = s.j1;
             if (j1 == 0) break;
@@ -923,8 +927,6 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 for (int c = 0; c < 32; ++c) see |= pos >= s_lo[c] ? 1u << c : 0u;
                 return see;
             };
-            if (quad == 0) s_nm[lane] = kNoMax;
-            if (!group_wait(bid, quad, bar(L::kPrep + xu), (i >> 1) & 1, abort)) break;
 
             float l[32], nm[32];  // sums, and -m of every row
 #pragma unroll
@@ -956,7 +958,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     if (raise) {
                         // ---- raise the reference maxima that need it; P V of the previous
                         // tile is done, so that O may be rescaled
-                        warp_columns<true>(scratch, s_red + quad * 32, lane, live, x);
+                        warp_columns<true>(s_red + quad * 32, lane, live, x);
                         go = here && wait_phase(bar(L::kOReady + (x2 ^ 1)),
                                                 ((it + 1) >> 1 & 1) ^ 1, abort);
                         if (!(go = tcc::named_barrier_and(bid, 128, go))) break;
@@ -1050,7 +1052,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             if (!go) break;
 
             // ---- results
-            warp_columns<false>(scratch, s_red + quad * 32, lane, live, l);
+            warp_columns<false>(s_red + quad * 32, lane, live, l);
             if (!group_wait(bid, quad, bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1,
                             abort))
                 break;
@@ -1063,7 +1065,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             tcc::named_barrier(bid, 128);
             const int *s_row = reinterpret_cast<const int *>(sm + L::kRow) + xu * R + 32 * sw;
             float *pd = piece_data<D, R>(P, 2 * blockIdx.x + (s.j0 == 0 ? 1 : 0));
-            float *of = whole ? static_cast<float *>(a.out) : pd;
+            float *of = (whole ? static_cast<float *>(a.out) : pd) + key;
             const bool half = whole && !a.out_f32;
             if (32 * quad < D) {  // (key: the channel)
 #pragma unroll 1
@@ -1071,19 +1073,27 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     uint32_t hi[8], lo[8];
                     ptx::tmem_ld_x8_nowait(tl + L::kTO + 8 * q, hi);
                     ptx::tmem_ld_x8_nowait(tl + L::kTO + R + 8 * q, lo);
-                    ptx::tmem_wait_ld();
+                    int row[8];
+                    float f[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int rr = 8 * q + e;
-                        float o = __uint_as_float(hi[e]) + __uint_as_float(lo[e]);
-                        o = bad ? 0.f : o * s_l[rr];
-                        const size_t at = (size_t)(whole ? s_row[rr] : 32 * sw + rr) * D + key;
-                        if (rr < live) {
-                            if (half)
-                                static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(o);
-                            else
-                                of[at] = o;
-                        }
+                        row[e] = whole ? s_row[8 * q + e] : 32 * sw + 8 * q + e;
+                        f[e] = s_l[8 * q + e];
+                    }
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        f[e] = bad ? 0.f
+                                   : (__uint_as_float(hi[e]) + __uint_as_float(lo[e])) * f[e];
+                    if (half) {
+                        __nv_bfloat16 *oh = static_cast<__nv_bfloat16 *>(a.out) + key;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (8 * q + e < live) oh[(size_t)row[e] * D] = __float2bfloat16_rn(f[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (8 * q + e < live) of[(size_t)row[e] * D] = f[e];
                     }
                 }
             }
