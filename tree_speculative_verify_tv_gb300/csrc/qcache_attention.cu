@@ -175,8 +175,8 @@ struct Lay {
     static constexpr int kWarps = 4 * (kSW + 2 + kVG + 1), kThreads = kWarps * 32;
     // registers: at launch (all that fit), and after the split
     static constexpr int kRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kRegsSoftmax = kSW == 2 ? 128 : 144, kRegsOperand = 48,
-                         kRegsControl = 56;
+    static constexpr int kRegsSoftmax = kSW == 2 ? 128 : 144,
+                         kRegsOperand = kSW == 2 ? 48 : 64, kRegsControl = kSW == 2 ? 56 : 80;
     static_assert(kRegsSoftmax >= kRegs && kRegsOperand <= kRegs && kRegsControl <= kRegs &&
                       kThreads * kRegs >=
                           128 * (kSW * kRegsSoftmax + (2 + kVG) * kRegsOperand + kRegsControl),
@@ -253,8 +253,7 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Sums or maxima of v[0..live - 1] over a warp, column c to out[c] (in blocks of 8, 8 and
-// 16).  At each of three steps a lane hands half of a block's columns to its neighbour, and
+// Sums or maxima of v[0..live - 1] over a warp, column c to out[c] (in blocks of 8 and 24).  At each of three steps a lane hands half of a block's columns to its neighbour, and
 // two more add up what lanes of one column hold.
 template <bool kMax>
 __device__ __forceinline__ void warp_columns(float *out, int lane, int live,
@@ -263,7 +262,7 @@ __device__ __forceinline__ void warp_columns(float *out, int lane, int live,
     const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        if (min(8 * q, 16) >= live) continue;
+        if (min(8 * q, 8) >= live) continue;
         float y[4], z[2];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -745,7 +744,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         else
                             reinterpret_cast<uint16_t *>(s_vs)[lane] = (uint16_t)s2;
                         __syncwarp();
-#pragma unroll 1
+#pragma unroll (3 - SW)
                         for (int q = 0; q < kN; ++q) {
                             uint32_t out[16];
                             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -840,7 +839,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         sc = *reinterpret_cast<const uint16_t *>(rec + Rc::kKScales + p * 4 + g0);
                     else
                         sc = rec[Rc::kKScales + p * 2 + g0];
-#pragma unroll 1
+#pragma unroll (3 - SW)
                     for (int g = 0; g < D / 64; ++g, sc >>= 8) {
                         uint32_t out[16];
                         const uint32_t s1 = scale_bf16(sc & 0xFFu);
@@ -1000,10 +999,10 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     // exponents, and whether any is too large for the reference
                     float top[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         if (8 * k < live) {
 #pragma unroll
-                            for (int c = 8 * k; c < (k == 2 ? 32 : 8 * k + 8); c += 2) {
+                            for (int c = 8 * k; c < (k == 1 ? 32 : 8); c += 2) {
                                 fma2(x[c], x[c + 1], P.sl2, nm[c], nm[c + 1]);
                                 top[c / 2 % 4] = fmaxf(fmaxf(top[c / 2 % 4], x[c]), x[c + 1]);
                             }
@@ -1018,10 +1017,10 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 // ---- weights: P[key][row], a row of 128 bytes per key
                 uint8_t *prow = sm + L::kP + (uint32_t)x2 * L::kPSlabs * kSlab + key * 128;
 #pragma unroll
-                for (int b = 0; b < 3; ++b) {
+                for (int b = 0; b < 2; ++b) {
                     if (8 * b >= live) continue;
 #pragma unroll
-                    for (int q = b; q < (b == 2 ? 4 : b + 1); ++q) {
+                    for (int q = b; q < (b == 1 ? 4 : 1); ++q) {
                         uint32_t w[NP][4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
