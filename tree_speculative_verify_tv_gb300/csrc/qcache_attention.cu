@@ -171,15 +171,14 @@ __device__ __forceinline__ Seg next_segment(const QParams &P, const int *cum, in
 template <int D, int R, int NP>
 struct Lay {
     static constexpr int kSW = R / 32;  // softmax warpgroups
-    static constexpr int kVG = 2;  // V warpgroups: as many as fit
-    static constexpr int kWarps = 4 * (kSW + 2 + kVG + 1), kThreads = kWarps * 32;
+    static constexpr int kWarps = 4 * (kSW + 5), kThreads = kWarps * 32;
     // registers: at launch (all that fit), and after the split
     static constexpr int kRegs = 65536 / kThreads / 8 * 8;
     static constexpr int kRegsSoftmax = kSW == 2 ? 128 : 144,
                          kRegsOperand = kSW == 2 ? 48 : 64, kRegsControl = kSW == 2 ? 56 : 80;
     static_assert(kRegsSoftmax >= kRegs && kRegsOperand <= kRegs && kRegsControl <= kRegs &&
                       kThreads * kRegs >=
-                          128 * (kSW * kRegsSoftmax + (2 + kVG) * kRegsOperand + kRegsControl),
+                          128 * (kSW * kRegsSoftmax + 4 * kRegsOperand + kRegsControl),
                   "register split");
     static constexpr uint32_t kRec = qrec_bytes(D);
     static constexpr uint32_t kPSlabs = (NP * R + 63) / 64;
@@ -223,12 +222,21 @@ struct Lay {
     static_assert(kTV + 128 <= kTmemCols, "tensor memory plan");
 };
 
-// Wait for a phase, giving up (and raising the CTA's abort flag) after 2^24 tries, of some
-// 50 cycles each.  The whole wait is one short loop: with clock reads and the flag in it the
-// dozen places that wait made the kernel several times larger than the instruction cache.
-template <int kSleep = 0>
+// Wait for a phase, giving up (and raising the CTA's abort flag) after 2^20 tries: 30 ms at
+// least, 5 s at most, where the next step of a neighbour takes microseconds.  The whole wait
+// is one short loop: with clock reads and the flag in it the dozen places that wait made the
+// kernel several times larger than the instruction cache.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort) {
-    const bool ok = ptx::mbar_wait_tries<kSleep>(bar, parity, 1u << (kSleep ? 22 : 24));
+    const bool ok = ptx::mbar_wait_tries(bar, parity, 1u << 20);
+    if (!ok) *abort = 1;
+    return ok;
+}
+
+// The same for waits that may take as long as a unit does, and may see its end late: up to
+// 2^33 cycles, some four seconds.
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t ns,
+                                          volatile int *abort) {
+    const bool ok = ptx::mbar_wait_asleep(bar, parity, ns, 1ll << 33);
     if (!ok) *abort = 1;
     return ok;
 }
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     using L = Lay<D, R, NP>;
     using Rc = qc::Rec<D>;
     constexpr int SW = L::kSW, NS = L::kStages, kWarps = L::kWarps;
-    constexpr int kWarpK = 4 * SW, kWarpV = kWarpK + 8, kWarpCopy = kWarpV + 4 * L::kVG,
+    constexpr int kWarpK = 4 * SW, kWarpV = kWarpK + 8, kWarpCopy = kWarpV + 8,
                   kWarpS = kWarpCopy + 1, kWarpPv = kWarpS + 1, kWarpPrep = kWarpPv + 1;
     extern __shared__ uint8_t smem_raw[];
     // aligned by an offset, not through an integer: the compiler still sees shared memory
@@ -391,9 +399,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 
     if (tid < L::kNumBars) {
         uint32_t count = 1;  // arriving warps
-        if (tid >= L::kEmpty && tid < L::kKReady) count = 8 + 4 * L::kVG;  // K and V
-        if (tid >= L::kKReady && tid < L::kVReady) count = 8;
-        if (tid >= L::kVReady && tid < L::kPrep) count = 4 * L::kVG;
+        if (tid >= L::kEmpty && tid < L::kKReady) count = 16;  // K and V
+        if (tid >= L::kKReady && tid < L::kPrep) count = 8;     // K or V
         if (tid >= L::kPrepFree && tid < L::kSReady) count = 4 * SW;
         if (tid >= L::kSFree && tid < L::kOReady) count = 4 * SW;
         if (tid >= L::kSegFree && tid < L::kDone) count = kWarps - 1;
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     // operand warps within their registers.)
     auto enter = [&](int i) -> const Seg * {
         const bool got = __all_sync(
-            0xffffffffu, wait_phase<20>(bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, abort));
+            0xffffffffu, wait_long(bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, 20, abort));
         const Seg *s = reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
         return got && s->j1 > 0 ? s : nullptr;
     };
@@ -462,8 +469,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
         for (int i = 0; ok; ++i) {
             const Seg s = next_segment<R>(P, s_cum, t, t1);
-            ok = __all_sync(0xffffffffu, i < kSegs || wait_phase<100>(bar(L::kSegFree + i % kSegs),
-                                                                      (i / kSegs - 1) & 1, abort));
+            ok = __all_sync(0xffffffffu, i < kSegs || wait_long(bar(L::kSegFree + i % kSegs),
+                                                                (i / kSegs - 1) & 1, 100, abort));
             if (!ok) break;
             if (lane == 0) {
                 *reinterpret_cast<Seg *>(s_seg + (i % kSegs) * kSegInts) = s;
@@ -492,8 +499,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 }
                 const int st = rc % NS;
                 ok = __all_sync(0xffffffffu,
-                                rc < NS || wait_phase<100>(bar(L::kEmpty + st), ((rc / NS) - 1) & 1,
-                                                           abort));
+                                rc < NS || wait_long(bar(L::kEmpty + st), ((rc / NS) - 1) & 1,
+                                                     100, abort));
                 if (!ok) break;
                 const bool two = 2 * j + 1 < s.np;
                 const uint32_t dst = sbase + L::kRing + (uint32_t)st * 2 * L::kRec;
@@ -602,8 +609,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         for (int i = 0;; ++i) {
             const Seg *sp = enter(i);
             const int x = i & 1;
-            if (!__all_sync(0xffffffffu, i < 2 || wait_phase<200>(bar(L::kPrepFree + x),
-                                                                  ((i >> 1) - 1) & 1, abort)))
+            if (!__all_sync(0xffffffffu, i < 2 || wait_long(bar(L::kPrepFree + x),
+                                                            ((i >> 1) - 1) & 1, 200, abort)))
                 break;
             if (!sp) {  // (the softmax warps wait for rows before they look at the segment)
                 if (lane == 0 && !*abort) ptx::mbar_arrive(bar(L::kPrep + x));
@@ -688,12 +695,11 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         __syncwarp();
     } else if (warp >= kWarpV) {
         // ------------------------------------------------ V^T operand: thread = channel, a
-        // warpgroup per half or quarter of the keys (kN blocks of 32)
+        // warpgroup per half of the keys (a page, or 64 nodes)
         ptx::regs_dec<L::kRegsOperand>();
-        constexpr int kN = 4 / L::kVG;
-        const int c = 32 * quad + lane, k0 = (warp - kWarpV) / 4 * kN, h = k0 / 2;
-        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTV + 16u * k0;
-        uint32_t *s_vs = reinterpret_cast<uint32_t *>(sm + L::kVs) + (warp - kWarpV) * 16 * kN;
+        const int c = 32 * quad + lane, h = (warp - kWarpV) / 4;
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTV + 32u * h;
+        uint32_t *s_vs = reinterpret_cast<uint32_t *>(sm + L::kVs) + (warp - kWarpV) * 32;
         const bool live = 32 * quad < D;
         int it = 0, rc = 0;
         bool ok = true;
@@ -717,38 +723,31 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 if (j < s.nct) {
                     const uint8_t *rec = sm + L::kRing + ((uint32_t)st * 2 + h) * L::kRec;
                     if (live) {
-                        // the group's scales (a warp's 32 channels), kN positions per lane;
+                        // the group's scales (a warp's 32 channels), two positions per lane;
                         // a position that no node sees gets 0, whatever the cache holds there
-                        const int p0 = 32 * (k0 % 2);
-                        const uint8_t *codes = rec + Rc::kVCodes + ((k0 % 2) * D + c) * 16;
+                        const uint8_t *codes = rec + Rc::kVCodes + c * 16;
                         uint4 w4 = *reinterpret_cast<const uint4 *>(codes);
-                        const uint8_t *from = rec + Rc::kVScales + quad * kQPage + p0 + kN * lane;
-                        uint32_t s2;
-                        if constexpr (kN == 2) {
-                            const uint32_t b2 = *reinterpret_cast<const uint16_t *>(from);
-                            s2 = scale_bf16(b2 & 0xFFu) | (scale_bf16(b2 >> 8) << 16);
-                        } else {
-                            s2 = scale_bf16(*from);
-                        }
+                        const uint32_t b2 = *reinterpret_cast<const uint16_t *>(
+                            rec + Rc::kVScales + quad * kQPage + 2 * lane);
+                        uint32_t s2 = scale_bf16(b2 & 0xFFu) | (scale_bf16(b2 >> 8) << 16);
                         if (j < s.c0 || j >= s.c1) {
                             const int i2 = 2 * j + h;
-                            const int pos = page_of(s, i2) * kQPage + p0 + kN * lane;
+                            const int pos = page_of(s, i2) * kQPage + 2 * lane;
 #pragma unroll
-                            for (int e = 0; e < kN; ++e)
+                            for (int e = 0; e < 2; ++e)
                                 if (i2 >= s.np || pos + e >= s.ctx ||
                                     (pos + e < vis && pos + e >= sinks))
                                     s2 &= 0xFFFF0000u >> (16 * e);
                         }
-                        if constexpr (kN == 2)
-                            s_vs[lane] = s2;
-                        else
-                            reinterpret_cast<uint16_t *>(s_vs)[lane] = (uint16_t)s2;
+                        s_vs[lane] = s2;
                         __syncwarp();
+                        // (side by side where the registers suffice: 64 single tokens 125.1
+                        // to 122.2 us)
 #pragma unroll (3 - SW)
-                        for (int q = 0; q < kN; ++q) {
+                        for (int q = 0; q < 2; ++q) {
                             uint32_t out[16];
                             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                            if (q + 1 < kN) w4 = *reinterpret_cast<const uint4 *>(codes + D * 16);
+                            if (q == 0) w4 = *reinterpret_cast<const uint4 *>(codes + D * 16);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 // the scales of four pairs of positions, for all lanes
@@ -770,8 +769,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         // 32 nodes at a time, 16 loads in flight: a lane takes its channel
                         // and its neighbour's for half of the nodes, and they exchange
 #pragma unroll 1
-                        for (int q = 0; q < kN; ++q) {
-                            const int n0 = (j - s.nct) * kKeys + 32 * (k0 + q);
+                        for (int q = 0; q < 2; ++q) {
+                            const int n0 = (j - s.nct) * kKeys + 64 * h + 32 * q;
                             uint32_t out[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) out[e] = 0;

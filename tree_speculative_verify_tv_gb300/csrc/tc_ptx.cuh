@@ -43,44 +43,26 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity,
     return ok != 0;
 }
 
-// Up to `tries` tests in a row, each with the hardware's own time limit (one given in the
-// instruction makes the compiler wrap it in a loop of sleeps and clock reads, which takes
-// issue slots): a loop of a few instructions, whatever the caller, with `kSleep`
-// nanoseconds between them when the wait is not on a critical path.
-template <int kSleep = 0>
+// Up to `tries` tests in a row, each with the hardware's own time limit (some 7800 cycles
+// when nothing happens, 54 when the phase is complete; a limit given in the instruction makes
+// the compiler wrap it in a loop of sleeps and clock reads, which takes issue slots): a loop
+// of a few instructions, whatever the caller.
 __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity, uint32_t tries) {
     uint32_t ok;
-    if constexpr (kSleep == 0)
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-            "mov.u32 n, %3;\n\t"
-            "TV_WAIT_%=:\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "@p bra TV_DONE_%=;\n\t"
-            "sub.u32 n, n, 1;\n\t"
-            "setp.ne.u32 q, n, 0;\n\t"
-            "@q bra TV_WAIT_%=;\n\t"
-            "TV_DONE_%=:\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(tries)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-            "mov.u32 n, %3;\n\t"
-            "TV_WAIT_%=:\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "@p bra TV_DONE_%=;\n\t"
-            "nanosleep.u32 %4;\n\t"
-            "sub.u32 n, n, 1;\n\t"
-            "setp.ne.u32 q, n, 0;\n\t"
-            "@q bra TV_WAIT_%=;\n\t"
-            "TV_DONE_%=:\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(tries), "n"(kSleep)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n\t"
+        "TV_WAIT_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra TV_DONE_%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra TV_WAIT_%=;\n\t"
+        "TV_DONE_%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(tries)
+        : "memory");
     return ok != 0;
 }
 
@@ -95,6 +77,18 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+// Tests with sleeps of `ns` between them, for waits that are not on a critical path: false
+// once `limit` clock cycles pass.
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, uint32_t ns,
+                                                 long long limit) {
+    const long long t0 = clock64();
+    while (!mbar_test_wait(bar, parity)) {
+        if (clock64() - t0 > limit) return false;
+        __nanosleep(ns);
+    }
+    return true;
 }
 
 // Plain arrival (release semantics for the thread's earlier shared-memory writes).
