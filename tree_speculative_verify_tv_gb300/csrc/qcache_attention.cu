@@ -201,10 +201,10 @@ struct Lay {
     static constexpr uint32_t kSeg = kVs + 8 * 32 * 4;                 // int [kSegs][16]
     static constexpr uint32_t kBar = kSeg + kSegs * kSegInts * 4;
     // mbarriers: ring full / empty; K and V operands written; a unit's rows prepared /
-    // done with; S ready / read; P written; P V done; segments written / taken; all done
+    // done with; S ready; P written; P V done; segments written / taken; all done
     static constexpr int kFull = 0, kEmpty = kFull + kStages, kKReady = kEmpty + kStages,
                          kVReady = kKReady + 2, kPrep = kVReady + 2, kPrepFree = kPrep + 2,
-                         kSReady = kPrepFree + 2, kSFree = kSReady + 2, kPReady = kSFree + 2,
+                         kSReady = kPrepFree + 2, kPReady = kSReady + 2,
                          kOReady = kPReady + 2, kSegFull = kOReady + 2,
                          kSegFree = kSegFull + kSegs, kDone = kSegFree + kSegs,
                          kNumBars = kDone + 2;
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         if (tid >= L::kEmpty && tid < L::kKReady) count = 16;  // K and V
         if (tid >= L::kKReady && tid < L::kPrep) count = 8;     // K or V
         if (tid >= L::kPrepFree && tid < L::kSReady) count = 4 * SW;
-        if (tid >= L::kSFree && tid < L::kOReady) count = 4 * SW;
+        if (tid >= L::kPReady && tid < L::kOReady) count = 4 * SW;
         if (tid >= L::kSegFree && tid < L::kDone) count = kWarps - 1;
         ptx::mbar_init(bar(tid), count);
         ptx::fence_mbar_init();
@@ -538,10 +538,9 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < n; ++j, ++it) {
                 const int x = it & 1;
-                // (P V of two tiles ago has read its weights, too: the softmax warps take
-                // that from S being ready)
+                // P V of two tiles ago is done: so is the softmax with that S, and S being
+                // ready tells the softmax warps that its weights have been read
                 ok = ok && wait_phase(bar(L::kKReady + x), (it >> 1) & 1, abort) &&
-                     wait_phase(bar(L::kSFree + x), ((it >> 1) + 1) & 1, abort) &&
                      wait_phase(bar(L::kOReady + x), ((it >> 1) + 1) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
@@ -1011,8 +1010,6 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     if (raise || tcc::named_barrier_and(bid, 128, fits && here)) break;
                 }
                 if (!go) break;
-                ptx::tc_fence_before_sync();
-                warp_arrive(bar(L::kSFree + x2), lane);
                 // ---- weights: P[key][row], a row of 128 bytes per key
                 uint8_t *prow = sm + L::kP + (uint32_t)x2 * L::kPSlabs * kSlab + key * 128;
 #pragma unroll
