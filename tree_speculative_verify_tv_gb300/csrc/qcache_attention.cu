@@ -700,7 +700,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTV + 32u * h;
         uint32_t *s_vs = reinterpret_cast<uint32_t *>(sm + L::kVs) + (warp - kWarpV) * 32;
         const bool live = 32 * quad < D;
-        int it = 0, rc = 0;
+        int it = 0, st = 0;  // tiles so far, ring stage
+        uint32_t full = 0;   // and the parity of its phase
         bool ok = true;
 #pragma unroll 1
         for (int i = 0; ok; ++i) {
@@ -711,12 +712,11 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             const int sinks = a.window > 0 ? a.sinks : 0;
 #pragma unroll 1
             for (int j = s.j0; j < s.j1; ++j, ++it) {
-                const int st = rc % NS;
                 // P V of two tiles ago has read the buffer; this tile's pages are here
                 const int x = it & 1;
                 const uint32_t dst = tl + 64u * x;
                 ok = wait_phase(bar(L::kOReady + x), ((it >> 1) + 1) & 1, abort) &&
-                     (j >= s.nct || wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort));
+                     (j >= s.nct || wait_phase(bar(L::kFull + st), full, abort));
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
                 if (j < s.nct) {
@@ -762,7 +762,10 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     }
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(bar(L::kEmpty + st));
-                    ++rc;
+                    if (++st == NS) {
+                        st = 0;
+                        full ^= 1;
+                    }
                 } else {
                     if (live) {
                         // 32 nodes at a time, 16 loads in flight: a lane takes its channel
@@ -811,7 +814,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         ptx::regs_dec<L::kRegsOperand>();
         const int key = 32 * quad + lane, h = (warp - kWarpK) / 4, g0 = h * (D / 64);
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + L::kTK + 16u * g0;
-        int it = 0, rc = 0;
+        int it = 0, st = 0;  // tiles so far, ring stage
+        uint32_t full = 0;   // and the parity of its phase
         bool ok = true;
 #pragma unroll 1
         for (int i = 0; ok; ++i) {
@@ -820,12 +824,11 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             const Seg &s = *sp;
 #pragma unroll 1
             for (int j = s.j0; j < s.j1; ++j, ++it) {
-                const int st = rc % NS;
                 // S of two tiles ago has read the buffer; this tile's pages are here
                 const int x = it & 1;
                 const uint32_t dst = tl + (D / 2) * x;
                 ok = wait_phase(bar(L::kSReady + x), ((it >> 1) + 1) & 1, abort) &&
-                     (j >= s.nct || wait_phase(bar(L::kFull + st), (rc / NS) & 1, abort));
+                     (j >= s.nct || wait_phase(bar(L::kFull + st), full, abort));
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
                 if (j < s.nct) {
@@ -852,7 +855,10 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                     }
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(bar(L::kEmpty + st));
-                    ++rc;
+                    if (++st == NS) {
+                        st = 0;
+                        full ^= 1;
+                    }
                 } else {
                     const int n = (j - s.nct) * kKeys + key;
                     uint32_t out[D / 4];
