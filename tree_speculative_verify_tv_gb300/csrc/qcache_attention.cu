@@ -444,10 +444,6 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *s_tmem;
-    const int total = s_cum[P.nb];
-    const int shares = min(P.grid, total), me = min((int)blockIdx.x, shares);
-    const Shares share(total, max(shares, 1));
-    const int first = share.begin(me), t1 = me < shares ? share.begin(me + 1) : first;
 
     // Segment `i` of this CTA, in the ring until leave(i): null at the end, or when a wait
     // expired.  (A reference: the fields are read where they are used, which keeps the
@@ -464,7 +460,11 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     if (warp == kWarpCopy) {
         // ------------------------------------------------ segments, and one bulk copy per
         // page; the lanes hold the next 32 pages' records
-        int rc = 0, t = first;  // context tiles so far, next tile
+        const int total = s_cum[P.nb], shares = min(P.grid, total),
+                  me = min((int)blockIdx.x, shares);
+        const Shares share(total, max(shares, 1));
+        const int t1 = me < shares ? share.begin(me + 1) : share.begin(me);
+        int rc = 0, t = share.begin(me);  // context tiles so far, next tile
         bool ok = true;
 #pragma unroll 1
         for (int i = 0; ok; ++i) {
@@ -917,7 +917,13 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             const uint32_t *s_see =
                 reinterpret_cast<const uint32_t *>(sm + L::kSee) + (xu * SW + sw) * kMaxNodes;
             const int *s_lo = reinterpret_cast<const int *>(sm + L::kLo) + xu * R + 32 * sw;
+            // tiles that every row sees whole: in registers where there are enough (with 128,
+            // 256-node trees 121.4 to 118.8 us without; with 144, 64 single tokens 125.9 to
+            // 118.9 with them)
             const int c0 = s.c0, c1 = s.c1;
+            auto clear = [&](int j) {
+                return SW == 1 ? j >= c0 && j < c1 : j >= s.c0 && j < s.c1;
+            };
             // bit c: row c of the group sees this thread's key in tile j
             auto seen = [&](int j) -> uint32_t {
                 if (j >= s.nct) return s_see[(j - s.nct) * kKeys + key];
@@ -953,7 +959,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(u[c]);
                     }
-                    if (j < c0 || j >= c1) {
+                    if (!clear(j)) {
                         const uint32_t see = seen(j);
 #pragma unroll
                         for (int c = 0; c < 32; ++c) x[c] = (see >> c) & 1u ? x[c] : neg_inf();
@@ -1106,6 +1112,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 if (tid == 0) {
                     int *h = hdr + (s.j0 == 0 ? 8 : 0);
                     // (the unit ends in the share of its last tile)
+                    const int total = s_cum[P.nb];
+                    const Shares share(total, min(P.grid, total));
                     h[1] = share.of(s.end - 1) - (int)blockIdx.x + 1;
                     h[2] = s.mt * R;
                     h[3] = s.n * P.grp;
