@@ -38,11 +38,7 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
     return amax > 0x7F80u ? kScaleNaN : amax == 0x7F80u ? 254u : (uint32_t)min(max(b, 0), 254);
 }
 
-// s = (8 + b % 8) 2^(b / 8 - 25) as fp32; NaN for b = 255.
-__device__ __forceinline__ float scale_value(uint32_t b) {
-    return b == kScaleNaN ? __uint_as_float(0x7FC00000u) : __uint_as_float((b + 840u) << 20);
-}
-
+// With s = (8 + b % 8) 2^(b / 8 - 25), whose fp32 bits are (b + 840) << 20:
 // 1 / s, raised by a relative 2^-18: |x| times this, rounded to nearest, is |x| / s
 // rounded with halves away from zero.  x has 8 and s 4 significant bits, so a quotient
 // that is not a half is a relative 2^-9 or more away from one, far beyond the raise, and
@@ -72,21 +68,31 @@ __device__ __forceinline__ uint32_t clamp_pair(uint32_t x) {
 // The larger of two packed pairs of bf16 bits without sign (as integers: NaN wins).
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
-// Two values (the even one in the low half) s (c - 8) of word w's nibbles p and p + 4: the
-// magic exponent makes 128 + c of a nibble, and one packed fma with s and -136 s the value,
-// exactly.
-__device__ __forceinline__ uint32_t value_pair(uint32_t w, int p, uint32_t s2, uint32_t ms2) {
-    uint32_t x, d;
+// Codes 2p and 2p + 1 of a word as the bf16 pair (128 + c0, 128 + c1).  The mask and the
+// exponent go in by one lop3 (the compiler makes two of the C expression, and these
+// operations bound the dequantising: two cycles each per warp).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int p) {
+    uint32_t d;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
-        : "=r"(x)
+        : "=r"(d)
         : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(s2), "r"(ms2));
     return d;
 }
 
-// bf16 bits of the scale with byte b, in both halves, and -136 times it.
+// Two values (the even one in the low half) s (c - 8) of word w's nibbles p and p + 4: one
+// packed fma of 128 + c with s and -136 s, exactly.
+__device__ __forceinline__ uint32_t value_pair(uint32_t w, int p, uint32_t s2, uint32_t ms2) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(code_pair(w, p)), "r"(s2), "r"(ms2));
+    return d;
+}
+
+// bf16 bits of the scale with byte b; in both halves; and -136 times it.
+__device__ __forceinline__ uint32_t scale_bf16(uint32_t b) {
+    return b == kScaleNaN ? 0x7FC0u : (b << 4) + 0x3480u;
+}
 __device__ __forceinline__ uint32_t scale_pair(uint32_t b) {
-    const uint32_t s = b == kScaleNaN ? 0x7FC0u : (b << 4) + 0x3480u;
+    const uint32_t s = scale_bf16(b);
     return s | (s << 16);
 }
 __device__ __forceinline__ uint32_t minus_136(uint32_t s2) {

@@ -17,9 +17,9 @@
 //   two codes at once: ((word >> 4 p) & 0x000F000F) | 0x43004300 is the bf16 pair
 //   (128 + c0, 128 + c1), and one packed fma with s and -136 s gives s (c - 8), exactly
 //   (at most 7 significant bits; 136 s has at most 8).
-// Work: the tiles of all (request, KV head, tile of R rows) units are laid end to end,
-// with a constant cost per unit, and every CTA takes an equal share; a unit that is cut leaves (O, m, l) pieces in the
-// workspace, joined by a second kernel.
+// Work: the tiles of all (request, KV head, tile of R rows) units are laid end to end, with
+// a constant cost per unit, and every CTA takes an equal share; a unit that is cut leaves
+// (O, m, l) pieces in the workspace, joined by a second kernel.
 //
 // One CTA per SM; S, P, K and V in two buffers each.  Warpgroups: R / 32 for the softmax (32
 // query rows each, lane = key), two that dequantise K (half of the channels each), two for V
@@ -27,12 +27,24 @@
 // copies), S products, P V products, and the next unit's rows.  The reference maximum m of
 // a row is raised only when a score exceeds it by more than 32 (log2 units; nothing
 // overflows before 2^127); the softmax warps vote per tile.  Weights enter the value product
-// as NP bf16 parts; sums l are kept in fp32 from the same weights.  Every mbarrier wait is
-// bounded, as in tree_attention.cu.
+// as NP bf16 parts: two leave a relative 2^-16 for bf16 outputs, three 2^-24 for fp32 (one
+// alone, 2^-9, would double a bf16 output's rounding); sums l are kept in fp32 from the same
+// weights.  Every mbarrier wait is bounded.
 //
-// Two things bound the roles: latency, since a tile passes through four of them and each
-// wait costs a hundred cycles or more, and the instruction cache, so loops are kept rolled
-// and waits short.
+// Measured (32 query heads over 8, d = 128): 16 trees of 16 nodes over 4096 positions 51.5 us
+// (1.5 TB/s of cache, 22 % of the copy bandwidth; the bf16 cache's pass takes 57.5 us for 3.8
+// times the bytes), 64 single tokens over 1..8191 positions (64 heads) 119 us (3.0 TB/s,
+// 45 %), one token over 500 positions 9.5 us.  A tile costs a CTA some 1500 cycles at 8 live
+// rows and 2300 at 64.  What bounds it: instructions.  The dequantising warps, the softmax
+// and the waits fill 64 to 70 % of the issue slots over the whole run, the arithmetic pipe
+// 50 to 56 %, the tensor pipe 23 %, DRAM 22 to 45 %; without V's dequantising the same runs
+// take 46 and 102 us, without the weights 43 and 115, and without either, K's and the vote
+// 37 and 81, which is the chain of signals from role to role.  The rest is per unit (a first
+// reference, results: 6000 cycles) and per launch (15000 cycles to the first product with
+// cold caches, 5 us for the second kernel and the launches).
+//
+// The instruction cache counts, too (32 KB per SM, 8 KB per scheduler): loops are kept
+// rolled and waits short.
 #include <algorithm>
 #include <atomic>
 
@@ -47,7 +59,9 @@ constexpr int kChunkB = 1024;          // requests per launch (their tile counts
 constexpr uint32_t kSlab = kKeys * 128;  // 128 keys x 128 bytes
 constexpr float kHeadroom = 32.f;
 constexpr float kNoMax = 1e30f;        // -m of a row that has seen no key
-constexpr int kUnitCost = 3;           // what a unit costs beside its tiles, in tiles
+// What a unit costs beside its tiles, in tiles: 64 ragged single tokens 126.7, 122.4, 123.1,
+// 125.2 us at 2, 3, 4, 6; 256-node trees 122.9, 122.2, 121.4, 119.4.
+constexpr int kUnitCost = 3;
 constexpr uint32_t kTmemCols = 512;
 
 struct QParams {
@@ -261,8 +275,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Sums or maxima of v[0..live - 1] over a warp, column c to out[c] (in blocks of 8 and 24).  At each of three steps a lane hands half of a block's columns to its neighbour, and
-// two more add up what lanes of one column hold.
+// Sums or maxima of v[0..live - 1] over a warp, column c to out[c] (in blocks of 8 and 24).
+// At each of three steps a lane hands half of eight columns to its neighbour, and two more
+// add up what the lanes of one column hold.
 template <bool kMax>
 __device__ __forceinline__ void warp_columns(float *out, int lane, int live,
                                              const float (&v)[32]) {
@@ -304,36 +319,8 @@ __device__ __forceinline__ void add2(float &x0, float &x1, float a0, float a1) {
         : "f"(a0), "f"(a1));
 }
 
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-
-// bf16 bits of the scale with byte b.
-__device__ __forceinline__ uint32_t scale_bf16(uint32_t b) {
-    return b == qc::kScaleNaN ? 0x7FC0u : (b << 4) + 0x3480u;
-}
-
-// -136 s for a pair of scales (bf16 -136 = 0xC308; the product is exact).
-__device__ __forceinline__ uint32_t minus_136(uint32_t s2) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(s2), "r"(0xC308C308u));
-    return d;
-}
-
-// Codes 2p and 2p + 1 of a word as the bf16 pair (128 + c0, 128 + c1).  The mask and the
-// exponent go in by one lop3 (the compiler makes two of the C expression, and these
-// operations bound the dequantising: two cycles each per warp).
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int p) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
-        : "=r"(d)
-        : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
-    return d;
-}
-
-// (x - 136) s, both steps exact: without a second operand per pair of scales to load.
+// (x - 136) s, both steps exact: what value_pair gives, without a second operand per pair
+// of scales to load.
 __device__ __forceinline__ uint32_t scaled_pair(uint32_t x, uint32_t s2) {
     uint32_t d;
     asm("{\n\t.reg .b32 t;\n\t"
@@ -395,7 +382,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     volatile int *abort = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
     volatile int *s_bad = reinterpret_cast<volatile int *>(sm + L::kMisc + 8);     // [2]
     volatile int *s_stray = reinterpret_cast<volatile int *>(sm + L::kMisc + 16);  // [kSegs]
-    int *s_scan = reinterpret_cast<int *>(sm + L::kMisc + 32);                   // [28]
+    int *s_scan = reinterpret_cast<int *>(sm + L::kMisc + 32);                      // a warp's
 
     if (tid < L::kNumBars) {
         uint32_t count = 1;  // arriving warps
@@ -728,7 +715,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         uint4 w4 = *reinterpret_cast<const uint4 *>(codes);
                         const uint32_t b2 = *reinterpret_cast<const uint16_t *>(
                             rec + Rc::kVScales + quad * kQPage + 2 * lane);
-                        uint32_t s2 = scale_bf16(b2 & 0xFFu) | (scale_bf16(b2 >> 8) << 16);
+                        uint32_t s2 =
+                            qc::scale_bf16(b2 & 0xFFu) | (qc::scale_bf16(b2 >> 8) << 16);
                         if (j < s.c0 || j >= s.c1) {
                             const int i2 = 2 * j + h;
                             const int pos = page_of(s, i2) * kQPage + 2 * lane;
@@ -752,10 +740,10 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                                 // the scales of four pairs of positions, for all lanes
                                 const uint4 sc =
                                     *reinterpret_cast<const uint4 *>(s_vs + q * 16 + 4 * e);
-                                out[4 * e] = scaled_pair(code_pair(w[e], 0), sc.x);
-                                out[4 * e + 1] = scaled_pair(code_pair(w[e], 1), sc.y);
-                                out[4 * e + 2] = scaled_pair(code_pair(w[e], 2), sc.z);
-                                out[4 * e + 3] = scaled_pair(code_pair(w[e], 3), sc.w);
+                                out[4 * e] = scaled_pair(qc::code_pair(w[e], 0), sc.x);
+                                out[4 * e + 1] = scaled_pair(qc::code_pair(w[e], 1), sc.y);
+                                out[4 * e + 2] = scaled_pair(qc::code_pair(w[e], 2), sc.z);
+                                out[4 * e + 3] = scaled_pair(qc::code_pair(w[e], 3), sc.w);
                             }
                             ptx::tmem_st_x16(dst + 16u * q, out);
                         }
@@ -843,14 +831,13 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll (3 - SW)
                     for (int g = 0; g < D / 64; ++g, sc >>= 8) {
                         uint32_t out[16];
-                        const uint32_t s1 = scale_bf16(sc & 0xFFu);
-                        const uint32_t s2 = s1 | (s1 << 16), ms = minus_136(s2);
+                        const uint32_t s2 = qc::scale_pair(sc & 0xFFu), ms = qc::minus_136(s2);
                         const uint4 w4 = *reinterpret_cast<const uint4 *>(
                             rec + Rc::kKCodes + ((g0 + g) * kQPage + p) * 16);
                         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            out[e] = fma_bf16x2(code_pair(w[e / 4], e & 3), s2, ms);
+                            out[e] = qc::value_pair(w[e / 4], e & 3, s2, ms);
                         ptx::tmem_st_x16(dst + 16u * g, out);
                     }
                     __syncwarp();
@@ -1144,6 +1131,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 // Joins the pieces of the units that were cut: CTA (i, y) takes 8 rows of the unit that
 // main CTA i began and did not end, one warp per row:
 //   out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p.
+// Bound by latency: a header, then everything of eight pieces at a time (m, l and O one after
+// the other, and the request's offsets: one token over 500 positions 11.2 us, not 9.6).
 template <int D, int R>
 __global__ void __launch_bounds__(256) qcache_attention_join_kernel(const QParams P) {
     const QAttnArgs &a = P.a;
@@ -1218,7 +1207,9 @@ int sm_count() {
     return n;
 }
 
-// Rows per unit: 32 when no request has more, else 64.
+// Rows per unit: 32 when no request has more, else 64.  (Units of 64 for 8 live rows, 64
+// single tokens of 64 heads: 138.7 us against 120.0; units of 32 for 64 rows, which dequantise
+// everything twice, 16 trees of 16 nodes: 69.0 against 51.8, 256-node trees 190 against 119.)
 int rows_per_unit(const QAttnArgs &a) { return a.max_nodes * (a.H / a.Hkv) <= 32 ? 32 : 64; }
 
 // One CTA per SM, or one per tile when a batch cannot have as many.

@@ -81,7 +81,7 @@ __host__ __device__ constexpr uint32_t qrec_bytes(int d) {
     return 2 * (qrec_codes(d) + qrec_scales(d));
 }
 
-// Rows of k and v are `stride` elements apart; `len` is read by commit and read only.
+// Rows of k and v are `stride` elements apart; `len` is read by the read back only.
 struct QRowsArgs {
     int32_t B, T, Hkv, d, num_pages, max_pages;
     const int32_t *offsets, *start, *len, *table;
