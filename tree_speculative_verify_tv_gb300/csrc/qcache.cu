@@ -5,12 +5,14 @@
 // techniques" §2, restores only the accepted path's state; the branches of an attention
 // layer differ only in their own keys and values).
 #include "qcache.cuh"
+#include "tc_ptx.cuh"
 
 namespace tv {
 namespace {
 
 constexpr int kThreadsQ = 128;
 constexpr int kWriteCtas = 8;  // writing CTAs per SM that registers leave room for
+constexpr int kWriteStage = 8;  // pieces of a lane in flight
 
 // Row blocks: request b's rows are cut where its positions enter a new page.  Block ids
 // are handed out by base(b) = row_offsets[b] / 64 + 2 b, which leaves every request at
@@ -87,61 +89,86 @@ __device__ __forceinline__ float high_half(uint32_t x) {
     return __uint_as_float(x & 0xFFFF0000u);
 }
 
-// The piece with values beyond the range of the largest step clamped (a rare branch).
+// The piece with values beyond the range of the largest step clamped, and zeros for that of a
+// group with a NaN (a rare branch; the others' values are within the range anyway).
 __device__ __forceinline__ uint4 in_range(uint4 x, uint32_t b) {
-    if (__any_sync(0xffffffffu, b == 254)) {
-        if (b == 254)
-            x = make_uint4(qc::clamp_pair(x.x), qc::clamp_pair(x.y), qc::clamp_pair(x.z),
-                           qc::clamp_pair(x.w));
+    if (__any_sync(0xffffffffu, b >= 254)) {
+        const uint32_t keep = b == 255 ? 0u : 0xffffffffu;
+        x = make_uint4(qc::clamp_pair(x.x) & keep, qc::clamp_pair(x.y) & keep,
+                       qc::clamp_pair(x.z) & keep, qc::clamp_pair(x.w) & keep);
     }
     return x;
 }
 
+// A lane's pieces on their way to the codes: asynchronous copies into shared memory of its
+// own, so that kStage loads are in flight from a short loop.  (Loads into registers needed
+// the loops around them unrolled: 52 KB of code, more than the instruction cache holds, and
+// 2 us more on a call of ragged chunks, 4 on 65536 rows.)
+template <int kStage>
+struct Staged {
+    uint4 *at;  // the warp's [kStage][32]
+    int lane;
+    __device__ void load(int i, const __nv_bfloat16 *from) const {
+        ptx::cp_async_16(ptx::smem_addr(at + i * 32 + lane), from);
+    }
+    __device__ uint4 operator[](int i) const { return at[i * 32 + lane]; }
+};
+
 // K rows from .. cnt - 1 of those that go to places off + row: a warp takes 32 / (D / 8)
-// rows at a time, kBatch loads in flight per lane.
-template <int D, typename Row>
-__device__ __forceinline__ void put_k(uint8_t *rec, int lane, int off, int from, int cnt,
-                                      const __nv_bfloat16 *k, Row row) {
+// rows at a time.
+template <int D, int kStage, typename Row>
+__device__ __forceinline__ void put_k(uint8_t *rec, const Staged<kStage> &stage, int off, int from,
+                                      int cnt, const __nv_bfloat16 *k, Row row) {
     using R = qc::Rec<D>;
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 4;
-    const int w = lane % kLanes, g = w / 4;
-    for (int m0 = from + lane / kLanes; m0 < cnt + lane / kLanes; m0 += kRows * kBatch) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int m = m0 + u * kRows;
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (m < cnt) x[u] = *reinterpret_cast<const uint4 *>(k + row(m) + w * 8);
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    const int lane = stage.lane, w = lane % kLanes, g = w / 4;
+#pragma unroll 1
+    for (int m0 = from; m0 < cnt; m0 += kRows * kStage) {
+        const int n = min(kStage, (cnt - m0 + kRows - 1) / kRows), first = m0 + lane / kLanes;
+#pragma unroll 2
+        for (int i = 0; i < n; ++i) {
+            const int m = first + i * kRows;
+            if (m < cnt) stage.load(i, k + row(m) + w * 8);
         }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int m = m0 + u * kRows, p = off + m;
-            const uint32_t b = group_scale(x[u]);
+        ptx::cp_async_wait_all();
+        uint8_t *codes = rec + R::kKCodes + (g * kQPage + off + first) * 16 + w % 4 * 4;
+        uint8_t *scales = rec + R::kKScales + (off + first) * R::kGroups;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const uint4 x = stage[i];
+            const uint32_t b = group_scale(x);
             const float inv = qc::scale_inverse(b);
-            const uint4 y = in_range(x[u], b);
+            const uint4 y = in_range(x, b);
             const uint32_t h[4] = {y.x, y.y, y.z, y.w};
-            uint32_t word = 0;
+            uint32_t word = qc::kNoCodes;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                word = qc::put_code(word, low_half(h[e]), inv, qc::code_shift(2 * e));
-                word = qc::put_code(word, high_half(h[e]), inv, qc::code_shift(2 * e + 1));
+                word = qc::put_code(word, low_half(h[e]), inv, 1u << qc::code_shift(2 * e));
+                word = qc::put_code(word, high_half(h[e]), inv, 1u << qc::code_shift(2 * e + 1));
             }
             // the row's scale bytes in its first lane
             uint32_t sc = w % 4 == 0 ? b << (8 * g) : 0;
             sc |= __shfl_xor_sync(0xffffffffu, sc, 4);
             if (D == 128) sc |= __shfl_xor_sync(0xffffffffu, sc, 8);
-            if (m < cnt) {
-                *reinterpret_cast<uint32_t *>(rec + R::kKCodes + (g * kQPage + p) * 16 +
-                                              w % 4 * 4) = word;
+            if (first + i * kRows < cnt) {
+                *reinterpret_cast<uint32_t *>(codes + i * kRows * 16) = word;
                 if (w == 0) {
                     if (D == 128)
-                        *reinterpret_cast<uint32_t *>(rec + R::kKScales + p * 4) = sc;
+                        *reinterpret_cast<uint32_t *>(scales + i * kRows * 4) = sc;
                     else
-                        *reinterpret_cast<uint16_t *>(rec + R::kKScales + p * 2) = (uint16_t)sc;
+                        *reinterpret_cast<uint16_t *>(scales + i * kRows * 2) = (uint16_t)sc;
                 }
             }
         }
     }
+}
+
+// The bits of elements [from, to) of a word of eight codes.
+__device__ __forceinline__ uint32_t code_mask(int from, int to) {
+    from = min(max(from, 0), 8), to = min(max(to, from), 8);
+    const uint32_t e = (1u << to) - (1u << from);  // a bit per element, then spread
+    const uint32_t s = (e & 3u) | (e & 12u) << 2 | (e & 48u) << 4 | (e & 192u) << 6;
+    return (s & 0x1111u) * 15u | ((s >> 1) & 0x1111u) * 0xF0000u;
 }
 
 // V rows [off, off + cnt) of a record, as far as they fall into part `part` of its places
@@ -149,42 +176,56 @@ __device__ __forceinline__ void put_k(uint8_t *rec, int lane, int off, int from,
 // consecutive positions, so that it ends with whole words, of 8 positions each.  Words that
 // keep some of their old codes are read first (a word being written has one writer, this
 // lane).
-template <int D, typename Row>
-__device__ __forceinline__ void put_v(uint8_t *rec, int lane, int part, int off, int cnt,
-                                      const __nv_bfloat16 *v, Row row) {
+template <int D, int kStage, typename Row>
+__device__ __forceinline__ void put_v(uint8_t *rec, const Staged<kStage> &stage, int part, int off,
+                                      int cnt, const __nv_bfloat16 *v, Row row) {
     using R = qc::Rec<D>;
-    constexpr int kLanes = D / 8, kPos = 16, kBatch = 8;
-    const int o = lane % kLanes, p0 = part * kPos * (32 / kLanes) + lane / kLanes * kPos, g = o / 4;
+    constexpr int kLanes = D / 8, kPos = 16;
+    static_assert(kStage == 8 || kStage == kPos, "a word or two of positions");
+    const int lane = stage.lane, o = lane % kLanes, g = o / 4;
+    const int p0 = part * kPos * (32 / kLanes) + lane / kLanes * kPos;
     const int lo = max(off - p0, 0), hi = min(off + cnt - p0, kPos);  // of this lane's places
-    uint32_t word[kPos / 8][8];
+    if (!__any_sync(0xffffffffu, lo < hi)) return;
+    uint32_t first[8], word[8];
 #pragma unroll
+    for (int c = 0; c < 8; ++c) word[c] = 0;
+#pragma unroll 1
     for (int q = 0; q < kPos / 8; ++q) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) word[q][c] = 0;
-        if (!__any_sync(0xffffffffu, 8 * q < hi && 8 * q + 8 > lo)) continue;
-        uint4 x[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int i = 8 * q + u;
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (i >= lo && i < hi)
-                x[u] = *reinterpret_cast<const uint4 *>(v + row(p0 + i - off) + o * 8);
-        }
-        uint32_t bytes[2] = {0, 0};
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const uint32_t b = group_scale(x[u]);
-            const float inv = qc::scale_inverse(b);
-            const uint4 y = in_range(x[u], b);
-            const uint32_t h[4] = {y.x, y.y, y.z, y.w};
-            bytes[u / 4] |= b << (8 * (u % 4));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                word[q][2 * e] = qc::put_code(word[q][2 * e], low_half(h[e]), inv,
-                                              qc::code_shift(u));
-                word[q][2 * e + 1] = qc::put_code(word[q][2 * e + 1], high_half(h[e]), inv,
-                                                  qc::code_shift(u));
+        if (kStage == 8 || q == 0) {
+#pragma unroll 2
+            for (int i = 0; i < kStage; ++i) {
+                const int p = 8 * q + i;
+                if (p >= lo && p < hi) stage.load(i, v + row(p0 + p - off) + o * 8);
             }
+            ptx::cp_async_wait_all();
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            first[c] = word[c];
+            word[c] = qc::kNoCodes;
+        }
+        if (!__any_sync(0xffffffffu, 8 * q < hi && 8 * q + 8 > lo)) continue;
+        uint32_t bytes[2] = {0, 0};  // eight scale bytes, moved down by two at a time
+#pragma unroll
+        for (int u = 0; u < 8; u += 2) {
+            uint32_t two[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                // (a place without a row has whatever is staged: it is not stored)
+                const uint4 x = stage[(kStage == 8 ? 0 : 8 * q) + u + s];
+                const uint32_t b = two[s] = group_scale(x);
+                const float inv = qc::scale_inverse(b);
+                const uint4 y = in_range(x, b);
+                const uint32_t h[4] = {y.x, y.y, y.z, y.w};
+                const uint32_t place = 1u << (2 * u + 16 * s);  // code_shift(u + s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    word[2 * e] = qc::put_code(word[2 * e], low_half(h[e]), inv, place);
+                    word[2 * e + 1] = qc::put_code(word[2 * e + 1], high_half(h[e]), inv, place);
+                }
+            }
+            bytes[0] = __byte_perm(bytes[0], bytes[1], 0x5432);
+            bytes[1] = __byte_perm(bytes[1], two[0] | two[1] << 8, 0x5432);
         }
         // the group's scale bytes, by its first lane
         if (o % 4 == 0) {
@@ -192,51 +233,43 @@ __device__ __forceinline__ void put_v(uint8_t *rec, int lane, int part, int off,
             if (lo <= 8 * q && hi >= 8 * q + 8) {
                 *reinterpret_cast<uint2 *>(sc) = make_uint2(bytes[0], bytes[1]);
             } else {
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (8 * q + u >= lo && 8 * q + u < hi)
-                        sc[u] = (uint8_t)(bytes[u / 4] >> (8 * (u % 4)));
+#pragma unroll 1
+                for (int u = max(lo - 8 * q, 0); u < min(hi - 8 * q, 8); ++u)
+                    sc[u] = (uint8_t)((u < 4 ? bytes[0] : bytes[1]) >> (8 * (u % 4)));
             }
         }
     }
     if (lo >= hi) return;
-    // words of positions [8 q, 8 q + 8): which codes are new
-    uint32_t mask[kPos / 8];
-    bool all = true;
-#pragma unroll
-    for (int q = 0; q < kPos / 8; ++q) {
-        mask[q] = 0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (8 * q + u >= lo && 8 * q + u < hi) mask[q] |= 15u << qc::code_shift(u);
-        all = all && mask[q] == 0xffffffffu;
-    }
+    const uint32_t mask0 = code_mask(lo, hi), mask1 = code_mask(lo - 8, hi - 8);
     uint32_t *dst = reinterpret_cast<uint32_t *>(rec + R::kVCodes + ((p0 / 32) * D + 8 * o) * 16 +
                                                  p0 % 32 / 8 * 4);
+    if ((mask0 & mask1) != 0xffffffffu) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        uint32_t *d = dst + 4 * c;
-        if (!all) {
-#pragma unroll
-            for (int q = 0; q < kPos / 8; ++q)
-                if (mask[q] != 0xffffffffu)
-                    word[q][c] = (word[q][c] & mask[q]) | (d[q] & ~mask[q]);
+        for (int c = 0; c < 8; ++c) {
+            const uint2 old = *reinterpret_cast<const uint2 *>(dst + 4 * c);
+            first[c] = (first[c] & mask0) | (old.x & ~mask0);
+            word[c] = (word[c] & mask1) | (old.y & ~mask1);
         }
-        *reinterpret_cast<uint2 *>(d) = make_uint2(word[0][c], word[1][c]);
     }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint2 *>(dst + 4 * c) = make_uint2(first[c], word[c]);
 }
 
 // One warp per part of K or V of a (block, head): half a page (of V at D = 64: all of it).
 //
-// 65536 rows of 8 heads x 128 channels: 81 us for the 268 MB read and the 71 MB written,
-// 4.2 TB/s, 63 % of the copy bandwidth.  The arithmetic pipe is the busiest unit (63 %; some
-// 20 of its operations per pair of values), with the loads' latency beside it: eight CTAs of
-// four warps per SM need 64 registers, and seven without the one spilled value took 84 us.  A
-// warp per whole page of K or V took 106 us, a thread per group of channels 330.
+// 65536 rows of 8 heads x 128 channels: 74.5 us for the 268 MB read and the 71 MB written,
+// 4.6 TB/s, 68 % of the copy bandwidth.  The arithmetic pipe is the busiest unit (60 %: some
+// 130 instructions per 8 channels of a row, of which 8 multiply-adds place codes; shift and
+// mask in their place, 79 us), with the copies' latency beside it: eight CTAs of four warps
+// per SM (nine 76 us, six 79; 16 pieces in flight per lane and six CTAs 85).  A warp per whole
+// page of K or V took 106 us, a thread per group of channels 330.
 template <int D>
 __global__ void __launch_bounds__(kThreadsQ, kWriteCtas) qcache_write_kernel(const QRowsArgs a) {
     constexpr int kParts = 2, kVParts = D / 64;
+    __shared__ uint4 s_stage[kThreadsQ / 32][kWriteStage][32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const Staged<kWriteStage> stage{s_stage[warp][0], lane};
     const int h = blockIdx.x % a.Hkv, blk = blockIdx.x / a.Hkv;
     pdl_wait();
     pdl_launch_next();
@@ -250,10 +283,10 @@ __global__ void __launch_bounds__(kThreadsQ, kWriteCtas) qcache_write_kernel(con
     const int off = r.pos % kQPage;
     if (warp < kParts) {
         const int half = (r.cnt + kParts - 1) / kParts;
-        put_k<D>(rec, lane, off, warp * half, min(r.cnt, (warp + 1) * half),
+        put_k<D>(rec, stage, off, warp * half, min(r.cnt, (warp + 1) * half),
                  static_cast<const __nv_bfloat16 *>(a.k), row);
     } else if (warp < kParts + kVParts) {
-        put_v<D>(rec, lane, warp - kParts, off, r.cnt, static_cast<const __nv_bfloat16 *>(a.v),
+        put_v<D>(rec, stage, warp - kParts, off, r.cnt, static_cast<const __nv_bfloat16 *>(a.v),
                  row);
     }
 }
@@ -372,14 +405,16 @@ __global__ void __launch_bounds__(kThreadsQ) qcache_read_kernel(const QRowsArgs 
 }
 
 // One CTA per request, so that the lengths may advance in place; latency bounds it (three
-// dependent loads, then the rows): with the positions read back 13.7 us for 16 requests, 47
+// dependent loads, then the rows): with the positions read back 12.6 us for 16 requests, 47
 // for 128 requests of 64-node trees.  Everything that reads
 // ctx_len has read it before the barrier.  A warp per K, or part of V, of a head: 24 of them
 // at 8 heads of 128 channels (16 warps, and two rounds, took 1.6 us longer per call).
-constexpr int kThreadsCommit = 768;
+constexpr int kThreadsCommit = 768, kCommitStage = 16;
+constexpr size_t kCommitShared = (size_t)kThreadsCommit * kCommitStage * sizeof(uint4);
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCommitArgs a) {
+    extern __shared__ uint4 s_stage[];  // [warps][kCommitStage][32]
     __shared__ int s_node[kMaxDepth], s_page[2];
     __shared__ int s_bad;
     const int b = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -408,6 +443,7 @@ __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCo
         if (bad) report(a.status, bad);
     }
     if (bad) return;
+    const Staged<kCommitStage> stage{s_stage + warp * kCommitStage * 32, lane};
     constexpr int kTasks = 1 + D / 64;  // K, and the parts of V
     for (int u = warp; u < a.Hkv * kTasks; u += kThreadsCommit / 32) {
         const int h = u / kTasks, part = u % kTasks - 1;
@@ -418,10 +454,10 @@ __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCo
                                qc::Rec<D>::kBytes;
             auto row = [&](int m) { return (size_t)s_node[m0 + m] * a.stride + (size_t)h * D; };
             if (part < 0)
-                put_k<D>(rec, lane, pos % kQPage, 0, cnt, static_cast<const __nv_bfloat16 *>(a.k),
+                put_k<D>(rec, stage, pos % kQPage, 0, cnt, static_cast<const __nv_bfloat16 *>(a.k),
                          row);
             else
-                put_v<D>(rec, lane, part, pos % kQPage, cnt,
+                put_v<D>(rec, stage, part, pos % kQPage, cnt,
                          static_cast<const __nv_bfloat16 *>(a.v), row);
             m0 += cnt;
         }
@@ -443,10 +479,16 @@ cudaError_t launch_qcache_read(const QRowsArgs &a, cudaStream_t s) {
                      : launch_pdl(qcache_read_kernel<128>, grid, dim3(kThreadsQ), 0, s, a);
 }
 
+template <int D>
+static cudaError_t launch_commit(const QCommitArgs &a, cudaStream_t s) {
+    const cudaError_t e = configure_smem_once(qcache_commit_kernel<D>, false);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(qcache_commit_kernel<D>, dim3(a.B), dim3(kThreadsCommit), kCommitShared, s,
+                      a);
+}
+
 cudaError_t launch_qcache_commit(const QCommitArgs &a, cudaStream_t s) {
-    return a.d == 64
-               ? launch_pdl(qcache_commit_kernel<64>, dim3(a.B), dim3(kThreadsCommit), 0, s, a)
-               : launch_pdl(qcache_commit_kernel<128>, dim3(a.B), dim3(kThreadsCommit), 0, s, a);
+    return a.d == 64 ? launch_commit<64>(a, s) : launch_commit<128>(a, s);
 }
 
 }  // namespace tv

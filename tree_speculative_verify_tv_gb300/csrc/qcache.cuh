@@ -49,16 +49,17 @@ __device__ __forceinline__ float scale_inverse(uint32_t b) {
     return b == kScaleNaN ? 0.f : y * (1.f + 1.f / 262144.f);
 }
 
-// `word` with code 1..15 of x at bit `sh` (any code for a NaN, whose scale says so).  Adding
-// 1.5 2^23 + 8 rounds to an integer in the low bits; only a group at the end of the range
-// (b = 254) could leave 1..15, and has its values clamped before.
-__device__ __forceinline__ uint32_t put_code(uint32_t word, float x, float inv, int sh) {
-    const uint32_t t = __float_as_uint(fmaf(x, inv, 12582920.f));
-    asm("lop3.b32 %0, %1, %2, %0, 0xEA;" : "+r"(word) : "r"(t << sh), "r"(15u << sh));
-    return word;
+// Adds code 1..15 of x, times `place` = 2^bit, to a word of eight: 1.5 2^23 + 8 + x / s rounds
+// to an integer in the low bits of an fp32, and what the eight exponents add is taken off by
+// kNoCodes, where a word starts.  One operation to place a code, on the multiplier's pipe,
+// where shift and mask take two on the one that bounds the quantiser.  Only groups with b =
+// 254 or 255 could leave 1..15; their values are made to fit before.
+constexpr uint32_t kNoCodes = 0u - 0x4B400000u * 0x11111111u;
+__device__ __forceinline__ uint32_t put_code(uint32_t word, float x, float inv, uint32_t place) {
+    return __float_as_uint(fmaf(x, inv, 12582920.f)) * place + word;
 }
 
-// A pair of bf16 within +-6272, what b = 254 reaches (as packed values: a NaN becomes one).
+// A pair of bf16 within +-6272, what b = 254 reaches (as packed values; a NaN becomes -6272).
 __device__ __forceinline__ uint32_t clamp_pair(uint32_t x) {
     asm("min.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0x45C445C4u));
     asm("max.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xC5C4C5C4u));
