@@ -654,12 +654,15 @@ tv_status tv_qcache_read(int32_t B, int32_t total_rows, int32_t Hkv, int32_t d,
  *              tv_qcache_attention_workspace_bytes bytes (scratch: partial results of
  *              contexts that are shared out over several CTAs)
  * Arithmetic: cache values are exact in bf16; scores, softmax sums and outputs
- * accumulate in fp32; softmax weights enter the value sums as a bf16 hi + lo pair.
+ * accumulate in fp32; softmax weights enter the value sums as two bf16 parts (2^-16
+ * relative) for bf16 outputs and three (2^-24) for fp32.
  * Positions that a request's nodes do not see may hold anything; a NaN or an infinity
  * in one that some of them see may reach the outputs of the request's other rows.
  * Host errors: as tv_tree_attention, plus TV_ERR_DTYPE for out_dtype, TV_ERR_NULL for a
  * missing and TV_ERR_SHAPE for a small workspace, TV_ERR_SHAPE for the strides, pages,
- * window and sinks.  Device-detected errors: as tv_tree_attention; a page outside
+ * window and sinks; TV_ERR_UNSUPPORTED for H / Hkv > 128 and where one request could
+ * have 2^31 or more tiles of 128 keys for 64 (or 32) of its rows over all KV heads.
+ * Device-detected errors: as tv_tree_attention; a page outside
  * [0, num_pages) gives TV_ERR_SHAPE and zero rows for that request.
  */
 size_t tv_qcache_attention_workspace_bytes(int32_t B, int32_t total_nodes, int32_t max_nodes,

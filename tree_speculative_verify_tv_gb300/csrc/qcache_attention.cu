@@ -56,6 +56,7 @@ namespace {
 
 constexpr int kKeys = 128;             // keys per tile
 constexpr int kChunkB = 1024;          // requests per launch (their tile counts are in smem)
+constexpr long long kMostCost = 0x7fffffff;  // of a launch's requests together
 constexpr uint32_t kSlab = kKeys * 128;  // 128 keys x 128 bytes
 constexpr float kHeadroom = 32.f;
 constexpr float kNoMax = 1e30f;        // -m of a row that has seen no key
@@ -1212,13 +1213,17 @@ int sm_count() {
 // everything twice, 16 trees of 16 nodes: 69.0 against 51.8, 256-node trees 190 against 119.)
 int rows_per_unit(const QAttnArgs &a) { return a.max_nodes * (a.H / a.Hkv) <= 32 ? 32 : 64; }
 
-// One CTA per SM, or one per tile when a batch cannot have as many.
-int grid_size(const QAttnArgs &a) {
+// The most that one request can cost.
+long long request_cost(const QAttnArgs &a) {
     const int R = rows_per_unit(a);
     const long long mts = ((long long)a.max_nodes * (a.H / a.Hkv) + R - 1) / R;
-    const long long tiles = (long long)a.B * a.Hkv * mts *
-                            ((a.max_pages + 1) / 2 + (a.max_nodes + kKeys - 1) / kKeys + kUnitCost);
-    return (int)std::min<long long>(sm_count(), tiles);
+    return a.Hkv * mts *
+           ((a.max_pages + 1) / 2 + (a.max_nodes + kKeys - 1) / kKeys + kUnitCost);
+}
+
+// One CTA per SM, or one per tile when a batch cannot have as many.
+int grid_size(const QAttnArgs &a) {
+    return (int)std::min<long long>(sm_count(), a.B * request_cost(a));
 }
 
 template <int D, int R, int NP>
@@ -1239,8 +1244,10 @@ cudaError_t launch_parts(const QAttnArgs &a, cudaStream_t s) {
     P.grp = a.H / a.Hkv;
     P.grid = grid_size(a);
     P.sl2 = a.scale * 1.4426950408889634f;
-    for (P.b0 = 0; P.b0 < a.B; P.b0 += kChunkB) {
-        P.nb = std::min(kChunkB, a.B - P.b0);
+    // as many requests per launch as the costs' 32-bit sums have room for
+    const int most = (int)std::min<long long>(kChunkB, kMostCost / request_cost(a));
+    for (P.b0 = 0; P.b0 < a.B; P.b0 += most) {
+        P.nb = std::min(most, a.B - P.b0);
         cudaError_t e = launch_pdl(qcache_attention_kernel<D, R, NP>, dim3(P.grid),
                                    dim3(L::kThreads), (size_t)L::kAlloc, s, P);
         if (e != cudaSuccess) return e;
@@ -1261,6 +1268,8 @@ cudaError_t launch_width(const QAttnArgs &a, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool qcache_attention_fits(const QAttnArgs &a) { return request_cost(a) <= kMostCost; }
 
 size_t qcache_attention_workspace_bytes(const QAttnArgs &a) {
     const size_t R = rows_per_unit(a);

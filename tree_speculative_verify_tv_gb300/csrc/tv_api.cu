@@ -670,10 +670,13 @@ tv_status qattn_dims(int32_t B, int32_t T, int32_t max_nodes, int32_t H, int32_t
     if (st != TV_OK) return st;
     if (H % Hkv || (int64_t)T > (int64_t)B * max_nodes) return TV_ERR_SHAPE;
     if (H / Hkv > 128 || max_nodes > TV_MAX_NODES) return TV_ERR_UNSUPPORTED;
-    if ((int64_t)B * Hkv * max_pages * tv::kQPage > 0x7fffffffLL ||
-        (int64_t)B * max_nodes * H > 0x7fffffffLL)
-        return TV_ERR_UNSUPPORTED;
-    return TV_OK;
+    if ((int64_t)B * max_nodes * H > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+    tv::QAttnArgs a{};
+    a.max_nodes = max_nodes;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.max_pages = max_pages;
+    return tv::qcache_attention_fits(a) ? TV_OK : TV_ERR_UNSUPPORTED;
 }
 
 }  // namespace

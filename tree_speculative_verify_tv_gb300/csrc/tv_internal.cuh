@@ -119,6 +119,8 @@ struct QAttnArgs {
     float *ws;
     int32_t *status;
 };
+// Whether a request of these limits may be as large as they allow.
+bool qcache_attention_fits(const QAttnArgs &a);
 size_t qcache_attention_workspace_bytes(const QAttnArgs &a);
 cudaError_t launch_qcache_attention(const QAttnArgs &a, cudaStream_t s);
 
