@@ -21,15 +21,18 @@ __device__ __forceinline__ int block_base(const int32_t *offs, int b) {
     return max(offs[b], 0) / kQPage + 2 * b;
 }
 
-// The request that block id `blk` belongs to.
+// The request that block id `blk` belongs to, by a whole warp: each round of loads leaves a
+// 32nd of the requests (a binary search is a chain of five loads for 32 of them).
 __device__ __forceinline__ int find_request(const int32_t *offs, int B, int blk) {
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (block_base(offs, mid) <= blk)
-            lo = mid;
-        else
-            hi = mid - 1;
+    const int lane = threadIdx.x % 32;
+    int lo = 0, n = B;
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const uint32_t begun =
+            __ballot_sync(0xffffffffu, at < n && block_base(offs, lo + at) <= blk);
+        const int k = max(__popc(begun) - 1, 0) * step;
+        lo += k;
+        n = min(step, n - k);
     }
     return lo;
 }
