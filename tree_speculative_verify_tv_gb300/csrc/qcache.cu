@@ -261,11 +261,11 @@ __device__ __forceinline__ void put_v(uint8_t *rec, const Staged<kStage> &stage,
 
 // One warp per part of K or V of a (block, head): half a page (of V at D = 64: all of it).
 //
-// 65536 rows of 8 heads x 128 channels: 74.5 us for the 268 MB read and the 71 MB written,
-// 4.6 TB/s, 68 % of the copy bandwidth.  The arithmetic pipe is the busiest unit (60 %: some
-// 130 instructions per 8 channels of a row, of which 8 multiply-adds place codes; shift and
-// mask in their place, 79 us), with the copies' latency beside it: eight CTAs of four warps
-// per SM (nine 76 us, six 79; 16 pieces in flight per lane and six CTAs 85).  A warp per whole
+// 65536 rows of 8 heads x 128 channels: 72.5 us for the 268 MB read and the 71 MB written,
+// 4.7 TB/s, 70 % of the copy bandwidth.  Instructions bound it (issue slots 70 %, arithmetic
+// pipe 54 %: some 120 per 8 channels of a row, of which 8 multiply-adds place codes; with
+// shift and mask in their place 79 us), with the copies' latency beside them: eight CTAs of
+// four warps per SM (16 pieces in flight per lane and six CTAs: 10 us more).  A warp per whole
 // page of K or V took 106 us, a thread per group of channels 330.
 template <int D>
 __global__ void __launch_bounds__(kThreadsQ, kWriteCtas) qcache_write_kernel(const QRowsArgs a) {
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreadsQ) qcache_read_kernel(const QRowsArgs 
 }
 
 // One CTA per request, so that the lengths may advance in place; latency bounds it (three
-// dependent loads, then the rows): with the positions read back 12.6 us for 16 requests, 47
+// dependent loads, then the rows): with the positions read back 12.4 us for 16 requests, 46
 // for 128 requests of 64-node trees.  Everything that reads
 // ctx_len has read it before the barrier.  A warp per K, or part of V, of a head: 24 of them
 // at 8 heads of 128 channels (16 warps, and two rounds, took 1.6 us longer per call).
