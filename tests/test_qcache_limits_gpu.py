@@ -1,9 +1,10 @@
-"""Attention over the 4-bit cache with page tables so wide that every request gets a launch of
-its own."""
+"""The 4-bit cache at sizes where its calls change shape: page tables so wide that every request
+gets an attention launch of its own, commits of more requests than the GPU has SMs."""
 import numpy as np
 import pytest
 
-from tests.test_qcache_gpu import attend, check_rows, make
+import workloads
+from tests.test_qcache_gpu import Cache, attend, check_rows, commit, make, strided
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +26,35 @@ def test_wide_page_tables():
     s, got, args = attend(c, b, ctx, 128, table=wide)
     assert s == 0
     check_rows(got, *args)
+
+
+@pytest.mark.parametrize("d,Hkv", [(64, 3), (128, 8)])
+def test_commits_of_many_requests(d, Hkv):
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import tree_speculative_verify_tv_gb300 as tv
+    tv.build()
+    tv.load()
+    rng = np.random.default_rng(d)
+    B = 200
+    b = workloads.random_batch(rng, rng.integers(0, 12, B), 1, 16, 16, depth_cap=6, max_depth=6)
+    lens, path = np.zeros(B, np.int32), np.full((B, 6), -1, np.int32)
+    for r in range(B):  # to a random node, or nowhere
+        s, n = b.node_offsets[r], b.node_offsets[r + 1] - b.node_offsets[r]
+        j, p = int(rng.integers(-1, n)) if n else -1, []
+        while j >= 0:
+            p.append(j)
+            j = int(b.parent[s + j])
+        lens[r] = len(p)
+        path[r, :len(p)] = p[::-1]
+    ctx = rng.integers(0, 120, B)
+    c = Cache(rng, B, 2, Hkv, d)
+    ((kt, kv), (vt, vv)), stride = strided(rng, b.T, [Hkv * d, Hkv * d], 8)
+    new = commit(c, b, ctx, lens, path, kt, vt, stride, in_place=True)
+    assert np.array_equal(new, ctx + lens)
+    for r in range(B):
+        for m in range(lens[r]):
+            at = b.node_offsets[r] + path[r, m]
+            c.put(r, int(ctx[r]) + m, kv[at].reshape(Hkv, d), vv[at].reshape(Hkv, d))
+    assert np.array_equal(c.fetch(), c.host)

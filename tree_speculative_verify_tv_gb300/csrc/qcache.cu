@@ -410,10 +410,12 @@ __global__ void __launch_bounds__(kThreadsQ) qcache_read_kernel(const QRowsArgs 
 // One CTA per request, so that the lengths may advance in place; latency bounds it (three
 // dependent loads, then the rows): with the positions read back 12.4 us for 16 requests, 46
 // for 128 requests of 64-node trees.  Everything that reads
-// ctx_len has read it before the barrier.  A warp per K, or part of V, of a head: 24 of them
-// at 8 heads of 128 channels (16 warps, and two rounds, took 1.6 us longer per call).
-constexpr int kThreadsCommit = 768, kCommitStage = 16;
-constexpr size_t kCommitShared = (size_t)kThreadsCommit * kCommitStage * sizeof(uint4);
+// ctx_len has read it before the barrier.  A warp per K, or part of V, of a head, in turn: 24
+// of them while every request has an SM to itself (8 heads of 128 channels; 16 warps, and two
+// rounds, for 16, 77 and 152 requests 3, 2.5 and 2.6 us longer), 16 beyond, when two CTAs
+// share an SM (304 requests 51.8 to 48.8 us, 1000 requests 148 to 135).
+constexpr int kThreadsCommit = 768, kThreadsMany = 512, kManyRequests = 152;
+constexpr int kCommitStage = 8;  // pieces of a lane in flight
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCommitArgs a) {
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCo
     if (bad) return;
     const Staged<kCommitStage> stage{s_stage + warp * kCommitStage * 32, lane};
     constexpr int kTasks = 1 + D / 64;  // K, and the parts of V
-    for (int u = warp; u < a.Hkv * kTasks; u += kThreadsCommit / 32) {
+    for (int u = warp; u < a.Hkv * kTasks; u += blockDim.x / 32) {
         const int h = u / kTasks, part = u % kTasks - 1;
         for (int m0 = 0; m0 < L;) {  // the pages that the path touches: one or two
             const int pos = ctx + m0, cnt = min(L - m0, kQPage - pos % kQPage);
@@ -486,8 +488,9 @@ template <int D>
 static cudaError_t launch_commit(const QCommitArgs &a, cudaStream_t s) {
     const cudaError_t e = configure_smem_once(qcache_commit_kernel<D>, false);
     if (e != cudaSuccess) return e;
-    return launch_pdl(qcache_commit_kernel<D>, dim3(a.B), dim3(kThreadsCommit), kCommitShared, s,
-                      a);
+    const int threads = a.B > kManyRequests ? kThreadsMany : kThreadsCommit;
+    return launch_pdl(qcache_commit_kernel<D>, dim3(a.B), dim3(threads),
+                      threads * kCommitStage * sizeof(uint4), s, a);
 }
 
 cudaError_t launch_qcache_commit(const QCommitArgs &a, cudaStream_t s) {
