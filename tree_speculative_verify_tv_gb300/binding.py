@@ -136,10 +136,10 @@ def load(path: Optional[str] = None):
 
 
 def _ptr(x) -> Optional[int]:
-    try:
-        return x.data_ptr()
-    except AttributeError:  # None or an address
+    # (ctypes would take bytes and arrays of its own, too, and pass their host addresses)
+    if x is None or isinstance(x, int):
         return x
+    return x.data_ptr()
 
 
 _current_stream = None
