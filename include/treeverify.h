@@ -656,6 +656,8 @@ tv_status tv_qcache_read(int32_t B, int32_t total_rows, int32_t Hkv, int32_t d,
  * Arithmetic: cache values are exact in bf16; scores, softmax sums and outputs
  * accumulate in fp32; softmax weights enter the value sums as two bf16 parts (2^-16
  * relative) for bf16 outputs and three (2^-24) for fp32.
+ * Scores may have any size that fp32 holds, q . k and scale * log2(e) times it; a row
+ * whose largest one is an infinity comes out as NaN.
  * Positions that a request's nodes do not see may hold anything; a NaN or an infinity
  * in one that some of them see may reach the outputs of the request's other rows.
  * Host errors: as tv_tree_attention, plus TV_ERR_DTYPE for out_dtype, TV_ERR_NULL for a

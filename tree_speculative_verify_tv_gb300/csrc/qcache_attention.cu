@@ -59,7 +59,7 @@ constexpr int kChunkB = 1024;          // requests per launch (their tile counts
 constexpr long long kMostCost = 0x7fffffff;  // of a launch's requests together
 constexpr uint32_t kSlab = kKeys * 128;  // 128 keys x 128 bytes
 constexpr float kHeadroom = 32.f;
-constexpr float kNoMax = 1e30f;        // -m of a row that has seen no key
+constexpr float kNoMax = 3.4028234e38f;  // -m of a row that has seen no key: the largest
 // What a unit costs beside its tiles, in tiles: 64 ragged single tokens 126.7, 122.4, 123.1,
 // 125.2 us at 2, 3, 4, 6; 256-node trees 122.9, 122.2, 121.4, 119.4.
 constexpr int kUnitCost = 3;
@@ -70,6 +70,7 @@ struct QParams {
     int b0, nb;   // this launch's requests
     int grp, grid;
     float sl2;    // scale * log2(e)
+    float zero;   // -0, see scaled_minus
 };
 
 // One request: its rows, the pages that any of its nodes sees, its tiles.
@@ -318,6 +319,16 @@ __device__ __forceinline__ void add2(float &x0, float &x1, float a0, float a1) {
         "add.rn.f32x2 x, x, a;\n\tmov.b64 {%0, %1}, x;\n\t}"
         : "+f"(x0), "+f"(x1)
         : "f"(a0), "f"(a1));
+}
+
+// (x0, x1) * s + (a0, a1) with the products rounded, so that the largest score and its own
+// product taken off leave 0: after a fused one they leave half a last place, which beyond 2^31
+// is more than an exponential holds.  The compiler fuses a product and a sum of pairs; a -0
+// that it does not know keeps them apart.
+__device__ __forceinline__ void scaled_minus(float &x0, float &x1, float s, float zero, float a0,
+                                             float a1) {
+    fma2(x0, x1, s, zero, zero);
+    add2(x0, x1, a0, a1);
 }
 
 // (x - 136) s, both steps exact: what value_pair gives, without a second operand per pair
@@ -613,8 +624,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             const int nrows = min(s.n * P.grp - s.mt * R, R);
             // the columns of S are looked at in blocks of 8 and 24: rows past the last, up to
             // the end of its block, repeat it (with what an earlier launch left there they
-            // raised the reference in every tile: 64 single tokens over 4096 positions, 8 x 9 heads, 132
-            // or 267 us)
+            // raised the reference in every tile: 64 single tokens over 4096 positions, 8 x 9
+            // heads, 132 or 267 us)
             const int part = nrows % 32;
             const int filled = nrows + (part == 0 ? 0 : part <= 8 ? 8 - part : 32 - part);
             constexpr int CH = D / 8, kStep = 32 / CH;  // a row per CH lanes, 16 bytes each
@@ -936,6 +947,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 l[c] = 0.f;
                 nm[c] = kNoMax;
             }
+            int first = s.j0;  // the tile that raises without a vote
 #pragma unroll 1
             for (int j = s.j0; j < j1; ++j, ++it) {
                 const int x2 = it & 1;
@@ -944,7 +956,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 ptx::tc_fence_after_sync();
                 float x[32];
 #pragma unroll 1
-                for (bool raise = j == s.j0;; raise = true) {
+                for (bool raise = j == (SW == 1 ? s.j0 : first);; raise = true) {
                     {
                         uint32_t u[32];
                         ptx::tmem_ld_x32_nowait(tl + L::kTS + R * x2, u);
@@ -998,6 +1010,24 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         }
 #pragma unroll
                         for (int c = 0; c < 32; ++c) nm[c] = s_nm[c];
+                        if constexpr (SW == 2) {
+                            // references beyond 2^24: the exponents in two steps (to nm, with
+                            // nothing for the fused one to add), here and in the next tile.
+                            // (Two steps for all at 64 rows, 256-node trees: 117.2 to 120.9
+                            // us; this at 32 rows, 64 single tokens with fp32 outputs: 139.6
+                            // to 144.2 us at d = 128, 123.2 to 132.0 at d = 64, where two
+                            // steps for all take 143.6 and 123.6)
+                            const float m = fabsf(s_nm[lane]);
+                            if (__any_sync(0xffffffffu,
+                                           lane < live && m > 16777216.f && m < kNoMax)) {
+                                first = j + 1;
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) {
+                                    nm[c] = __fadd_rn(__fmul_rn(x[c], P.sl2), nm[c]);
+                                    x[c] = 0.f;
+                                }
+                            }
+                        }
                     }
                     // exponents, and whether any is too large for the reference
                     float top[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
@@ -1006,7 +1036,10 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         if (8 * k < live) {
 #pragma unroll
                             for (int c = 8 * k; c < (k == 1 ? 32 : 8); c += 2) {
-                                fma2(x[c], x[c + 1], P.sl2, nm[c], nm[c + 1]);
+                                if constexpr (SW == 1)
+                                    scaled_minus(x[c], x[c + 1], P.sl2, P.zero, nm[c], nm[c + 1]);
+                                else
+                                    fma2(x[c], x[c + 1], P.sl2, nm[c], nm[c + 1]);
                                 top[c / 2 % 4] = fmaxf(fmaxf(top[c / 2 % 4], x[c]), x[c + 1]);
                             }
                         }
@@ -1249,6 +1282,7 @@ cudaError_t launch_parts(const QAttnArgs &a, cudaStream_t s) {
     P.grp = a.H / a.Hkv;
     P.grid = grid_size(a);
     P.sl2 = a.scale * 1.4426950408889634f;
+    P.zero = -0.f;
     // as many requests per launch as the costs' 32-bit sums have room for
     const int most = (int)std::min<long long>(kChunkB, kMostCost / request_cost(a));
     for (P.b0 = 0; P.b0 < a.B; P.b0 += most) {
