@@ -414,11 +414,12 @@ __global__ void __launch_bounds__(kThreadsQ) qcache_read_kernel(const QRowsArgs 
 // of them while every request has an SM to itself (8 heads of 128 channels; 16 warps, and two
 // rounds, for 16, 77 and 152 requests 3, 2.5 and 2.6 us longer), 16 beyond, when two CTAs
 // share an SM (304 requests 51.8 to 48.8 us, 1000 requests 148 to 135).
-constexpr int kThreadsCommit = 768, kThreadsMany = 512, kManyRequests = 152;
+constexpr int kThreadsCommit = 768, kThreadsMany = 512;
 constexpr int kCommitStage = 8;  // pieces of a lane in flight
 
-template <int D>
-__global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCommitArgs a) {
+template <int D, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == kThreadsMany ? 2 : 1)
+    qcache_commit_kernel(const QCommitArgs a) {
     extern __shared__ uint4 s_stage[];  // [warps][kCommitStage][32]
     __shared__ int s_node[kMaxDepth], s_page[2];
     __shared__ int s_bad;
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(kThreadsCommit) qcache_commit_kernel(const QCo
     if (bad) return;
     const Staged<kCommitStage> stage{s_stage + warp * kCommitStage * 32, lane};
     constexpr int kTasks = 1 + D / 64;  // K, and the parts of V
-    for (int u = warp; u < a.Hkv * kTasks; u += blockDim.x / 32) {
+    for (int u = warp; u < a.Hkv * kTasks; u += kThreads / 32) {
         const int h = u / kTasks, part = u % kTasks - 1;
         for (int m0 = 0; m0 < L;) {  // the pages that the path touches: one or two
             const int pos = ctx + m0, cnt = min(L - m0, kQPage - pos % kQPage);
@@ -484,17 +485,22 @@ cudaError_t launch_qcache_read(const QRowsArgs &a, cudaStream_t s) {
                      : launch_pdl(qcache_read_kernel<128>, grid, dim3(kThreadsQ), 0, s, a);
 }
 
-template <int D>
+template <int D, int kThreads>
 static cudaError_t launch_commit(const QCommitArgs &a, cudaStream_t s) {
-    const cudaError_t e = configure_smem_once(qcache_commit_kernel<D>, false);
+    const cudaError_t e = configure_smem_once(qcache_commit_kernel<D, kThreads>, false);
     if (e != cudaSuccess) return e;
-    const int threads = a.B > kManyRequests ? kThreadsMany : kThreadsCommit;
-    return launch_pdl(qcache_commit_kernel<D>, dim3(a.B), dim3(threads),
-                      threads * kCommitStage * sizeof(uint4), s, a);
+    return launch_pdl(qcache_commit_kernel<D, kThreads>, dim3(a.B), dim3(kThreads),
+                      kThreads * kCommitStage * sizeof(uint4), s, a);
+}
+
+template <int D>
+static cudaError_t launch_commit_width(const QCommitArgs &a, cudaStream_t s) {
+    return a.B > device_sms() ? launch_commit<D, kThreadsMany>(a, s)
+                              : launch_commit<D, kThreadsCommit>(a, s);
 }
 
 cudaError_t launch_qcache_commit(const QCommitArgs &a, cudaStream_t s) {
-    return a.d == 64 ? launch_commit<64>(a, s) : launch_commit<128>(a, s);
+    return a.d == 64 ? launch_commit_width<64>(a, s) : launch_commit_width<128>(a, s);
 }
 
 }  // namespace tv

@@ -1234,18 +1234,6 @@ __global__ void __launch_bounds__(256) qcache_attention_join_kernel(const QParam
     }
 }
 
-// SMs of the current device, asked once per device.
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-        return 152;
-    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 // Rows per unit: 32 when no request has more, else 64.  (Units of 64 for 8 live rows, 64
 // single tokens of 64 heads: 138.7 us against 120.0; units of 32 for 64 rows, which dequantise
 // everything twice, 16 trees of 16 nodes: 69.0 against 51.8, 256-node trees 190 against 119.)
@@ -1261,7 +1249,7 @@ long long request_cost(const QAttnArgs &a) {
 
 // One CTA per SM, or one per tile when a batch cannot have as many.
 int grid_size(const QAttnArgs &a) {
-    return (int)std::min<long long>(sm_count(), a.B * request_cost(a));
+    return (int)std::min<long long>(device_sms(), a.B * request_cost(a));
 }
 
 template <int D, int R, int NP>
@@ -1307,6 +1295,18 @@ cudaError_t launch_width(const QAttnArgs &a, cudaStream_t s) {
 }
 
 }  // namespace
+
+// SMs of the current device, asked once per device.
+int device_sms() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+        return 152;
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 bool qcache_attention_fits(const QAttnArgs &a) { return request_cost(a) <= kMostCost; }
 

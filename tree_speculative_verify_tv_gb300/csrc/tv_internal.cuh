@@ -81,6 +81,9 @@ __host__ __device__ constexpr uint32_t qrec_bytes(int d) {
     return 2 * (qrec_codes(d) + qrec_scales(d));
 }
 
+// SMs of the current device.
+int device_sms();
+
 // Rows of k and v are `stride` elements apart; `len` is read by the read back only.
 struct QRowsArgs {
     int32_t B, T, Hkv, d, num_pages, max_pages;
