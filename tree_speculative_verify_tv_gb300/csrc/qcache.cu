@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kThreadsQ = 128;
 constexpr int kWriteCtas = 8;  // writing CTAs per SM that registers leave room for
-constexpr int kWriteStage = 8;  // pieces of a lane in flight
+constexpr int kStage = 8;      // pieces of a lane in flight
 
 // Row blocks: request b's rows are cut where its positions enter a new page.  Block ids
 // are handed out by base(b) = row_offsets[b] / 64 + 2 b, which leaves every request at
@@ -107,7 +107,6 @@ __device__ __forceinline__ uint4 in_range(uint4 x, uint32_t b) {
 // own, so that kStage loads are in flight from a short loop.  (Loads into registers needed
 // the loops around them unrolled: 52 KB of code, more than the instruction cache holds, and
 // 2 us more on a call of ragged chunks, 4 on 65536 rows.)
-template <int kStage>
 struct Staged {
     uint4 *at;  // the warp's [kStage][32]
     int lane;
@@ -119,8 +118,8 @@ struct Staged {
 
 // K rows from .. cnt - 1 of those that go to places off + row: a warp takes 32 / (D / 8)
 // rows at a time.
-template <int D, int kStage, typename Row>
-__device__ __forceinline__ void put_k(uint8_t *rec, const Staged<kStage> &stage, int off, int from,
+template <int D, typename Row>
+__device__ __forceinline__ void put_k(uint8_t *rec, const Staged &stage, int off, int from,
                                       int cnt, const __nv_bfloat16 *k, Row row) {
     using R = qc::Rec<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
@@ -179,12 +178,12 @@ __device__ __forceinline__ uint32_t code_mask(int from, int to) {
 // consecutive positions, so that it ends with whole words, of 8 positions each.  Words that
 // keep some of their old codes are read first (a word being written has one writer, this
 // lane).
-template <int D, int kStage, typename Row>
-__device__ __forceinline__ void put_v(uint8_t *rec, const Staged<kStage> &stage, int part, int off,
+template <int D, typename Row>
+__device__ __forceinline__ void put_v(uint8_t *rec, const Staged &stage, int part, int off,
                                       int cnt, const __nv_bfloat16 *v, Row row) {
     using R = qc::Rec<D>;
     constexpr int kLanes = D / 8, kPos = 16;
-    static_assert(kStage == 8 || kStage == kPos, "a word or two of positions");
+    static_assert(kStage == 8, "a word of positions");
     const int lane = stage.lane, o = lane % kLanes, g = o / 4;
     const int p0 = part * kPos * (32 / kLanes) + lane / kLanes * kPos;
     const int lo = max(off - p0, 0), hi = min(off + cnt - p0, kPos);  // of this lane's places
@@ -194,14 +193,12 @@ __device__ __forceinline__ void put_v(uint8_t *rec, const Staged<kStage> &stage,
     for (int c = 0; c < 8; ++c) word[c] = 0;
 #pragma unroll 1
     for (int q = 0; q < kPos / 8; ++q) {
-        if (kStage == 8 || q == 0) {
 #pragma unroll 2
-            for (int i = 0; i < kStage; ++i) {
-                const int p = 8 * q + i;
-                if (p >= lo && p < hi) stage.load(i, v + row(p0 + p - off) + o * 8);
-            }
-            ptx::cp_async_wait_all();
+        for (int i = 0; i < kStage; ++i) {
+            const int p = 8 * q + i;
+            if (p >= lo && p < hi) stage.load(i, v + row(p0 + p - off) + o * 8);
         }
+        ptx::cp_async_wait_all();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             first[c] = word[c];
@@ -215,7 +212,7 @@ __device__ __forceinline__ void put_v(uint8_t *rec, const Staged<kStage> &stage,
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 // (a place without a row has whatever is staged: it is not stored)
-                const uint4 x = stage[(kStage == 8 ? 0 : 8 * q) + u + s];
+                const uint4 x = stage[u + s];
                 const uint32_t b = two[s] = group_scale(x);
                 const float inv = qc::scale_inverse(b);
                 const uint4 y = in_range(x, b);
@@ -270,9 +267,9 @@ __device__ __forceinline__ void put_v(uint8_t *rec, const Staged<kStage> &stage,
 template <int D>
 __global__ void __launch_bounds__(kThreadsQ, kWriteCtas) qcache_write_kernel(const QRowsArgs a) {
     constexpr int kParts = 2, kVParts = D / 64;
-    __shared__ uint4 s_stage[kThreadsQ / 32][kWriteStage][32];
+    __shared__ uint4 s_stage[kThreadsQ / 32][kStage][32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const Staged<kWriteStage> stage{s_stage[warp][0], lane};
+    const Staged stage{s_stage[warp][0], lane};
     const int h = blockIdx.x % a.Hkv, blk = blockIdx.x / a.Hkv;
     pdl_wait();
     pdl_launch_next();
@@ -415,12 +412,11 @@ __global__ void __launch_bounds__(kThreadsQ) qcache_read_kernel(const QRowsArgs 
 // rounds, for 16, 77 and 152 requests 3, 2.5 and 2.6 us longer), 16 beyond, when two CTAs
 // share an SM (304 requests 51.8 to 48.8 us, 1000 requests 148 to 135).
 constexpr int kThreadsCommit = 768, kThreadsMany = 512;
-constexpr int kCommitStage = 8;  // pieces of a lane in flight
 
 template <int D, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == kThreadsMany ? 2 : 1)
     qcache_commit_kernel(const QCommitArgs a) {
-    extern __shared__ uint4 s_stage[];  // [warps][kCommitStage][32]
+    extern __shared__ uint4 s_stage[];  // [warps][kStage][32]
     __shared__ int s_node[kMaxDepth], s_page[2];
     __shared__ int s_bad;
     const int b = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -449,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kThreadsMany ? 2 : 1)
         if (bad) report(a.status, bad);
     }
     if (bad) return;
-    const Staged<kCommitStage> stage{s_stage + warp * kCommitStage * 32, lane};
+    const Staged stage{s_stage + warp * kStage * 32, lane};
     constexpr int kTasks = 1 + D / 64;  // K, and the parts of V
     for (int u = warp; u < a.Hkv * kTasks; u += kThreads / 32) {
         const int h = u / kTasks, part = u % kTasks - 1;
@@ -490,7 +486,7 @@ static cudaError_t launch_commit(const QCommitArgs &a, cudaStream_t s) {
     const cudaError_t e = configure_smem_once(qcache_commit_kernel<D, kThreads>, false);
     if (e != cudaSuccess) return e;
     return launch_pdl(qcache_commit_kernel<D, kThreads>, dim3(a.B), dim3(kThreads),
-                      kThreads * kCommitStage * sizeof(uint4), s, a);
+                      kThreads * kStage * sizeof(uint4), s, a);
 }
 
 template <int D>

@@ -28,7 +28,7 @@
 // a row is raised only when a score exceeds it by more than 32 (log2 units; nothing
 // overflows before 2^127); the softmax warps vote per tile.  Weights enter the value product
 // as NP bf16 parts: two leave a relative 2^-16 for bf16 outputs, three 2^-24 for fp32 (one
-// alone, 2^-9, would double a bf16 output's rounding); sums l are kept in fp32 from the same
+// alone, 2^-8, would double a bf16 output's rounding); sums l are kept in fp32 from the same
 // weights.  Every mbarrier wait is bounded.
 //
 // Measured (32 query heads over 8, d = 128): 16 trees of 16 nodes over 4096 positions 51.5 us
@@ -214,7 +214,7 @@ struct Lay {
     static constexpr uint32_t kAl = kNm + R * 4;                       // float [R]
     static constexpr uint32_t kRed = kAl + R * 4;                      // float [kSW][4][32]
     static constexpr uint32_t kVs = kRed + kSW * 512;   // u32 [8][32]
-    static constexpr uint32_t kSeg = kVs + 8 * 32 * 4;                 // int [kSegs][16]
+    static constexpr uint32_t kSeg = kVs + 8 * 32 * 4;                 // int [kSegs][kSegInts]
     static constexpr uint32_t kBar = kSeg + kSegs * kSegInts * 4;
     // mbarriers: ring full / empty; K and V operands written; a unit's rows prepared /
     // done with; S ready; P written; P V done; segments written / taken; all done
