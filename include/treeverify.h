@@ -679,6 +679,15 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
                               size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
+ * Test hook, OR-ed into tv_qcache_attention's out_dtype: every CTA leaves the inputs of its
+ * first unit unprepared, so that what waits for them gives up (after a sixty-fourth of the
+ * usual limits) and the call takes the timeout path: TV_ERR_TIMEOUT in dev_status once the
+ * copies and products in flight are done, tensor memory freed, outputs undefined.  For tests
+ * of that path; never needed otherwise.
+ */
+#define TV_QCACHE_TEST_EXPIRE_WAIT 0x100
+
+/*
  * tv_verify_variant -- the kernel tv_verify (TV_VARIANT_AUTO) would launch for
  * this problem: TV_VARIANT_TC_STREAM, TV_VARIANT_TC, TV_VARIANT_TC_TILED (trees too
  * large for TV_VARIANT_TC's shared-memory plan, and per-channel decay trees of 64

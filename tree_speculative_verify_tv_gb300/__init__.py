@@ -34,6 +34,7 @@ from .binding import (  # noqa: F401
     tv_accept_stochastic, tv_tree_attention, tv_tree_attention_workspace_bytes,
     tv_qcache_bytes, tv_qcache_write, tv_qcache_commit, tv_qcache_read, tv_qcache_attention,
     tv_qcache_attention_workspace_bytes, TV_QCACHE_PAGE, TV_QCACHE_GROUP,
+    TV_QCACHE_TEST_EXPIRE_WAIT,
     TV_SERIAL_STATIC_BYTES,
     tv_problem, tv_status_string, tv_verify, tv_verify_variant, tv_verify_supports, tv_version, EXPORTED,
     TV_OK, TV_ERR_NULL, TV_ERR_SHAPE, TV_ERR_DTYPE, TV_ERR_ALIGN, TV_ERR_UNSUPPORTED,

@@ -29,6 +29,7 @@ TV_VARIANT_TEST_EXPIRE_WAIT = 0x100
 TV_MAX_NODES, TV_MAX_DEPTH, TV_MAX_DIM = 256, 32, 256
 TV_SERIAL_STATIC_BYTES = 16 << 20
 TV_QCACHE_PAGE, TV_QCACHE_GROUP = 64, 32
+TV_QCACHE_TEST_EXPIRE_WAIT = 0x100
 
 EXPORTED = ("tv_verify", "tv_verify_ex", "tv_verify_variant", "tv_verify_supports",
             "tv_workspace_bytes",

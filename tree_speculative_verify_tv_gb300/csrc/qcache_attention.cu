@@ -64,6 +64,8 @@ constexpr float kNoMax = 3.4028234e38f;  // -m of a row that has seen no key: th
 // 125.2 us at 2, 3, 4, 6; 256-node trees 122.9, 122.2, 121.4, 119.4.
 constexpr int kUnitCost = 3;
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTries = 1u << 20;     // of a wait for a neighbour's step
+constexpr long long kCycles = 1ll << 33;  // of a wait that may last as long as a unit
 
 struct QParams {
     QAttnArgs a;
@@ -71,6 +73,9 @@ struct QParams {
     int grp, grid;
     float sl2;    // scale * log2(e)
     float zero;   // -0, see scaled_minus
+    uint32_t tries;      // limits of the waits: tests, and clock cycles
+    long long cycles;
+    bool expire;  // test hook: the preparing warp gives up at its first unit
 };
 
 // One request: its rows, the pages that any of its nodes sees, its tiles.
@@ -238,29 +243,30 @@ struct Lay {
     static_assert(kTV + 128 <= kTmemCols, "tensor memory plan");
 };
 
-// Wait for a phase, giving up (and raising the CTA's abort flag) after 2^20 tries: 30 ms at
+// Wait for a phase, giving up (and raising the CTA's abort flag) after kTries tests: 30 ms at
 // least, 5 s at most, where the next step of a neighbour takes microseconds.  The whole wait
 // is one short loop: with clock reads and the flag in it the dozen places that wait made the
 // kernel several times larger than the instruction cache.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort) {
-    const bool ok = ptx::mbar_wait_tries(bar, parity, 1u << 20);
+__device__ __forceinline__ bool wait_phase(const QParams &P, uint32_t bar, uint32_t parity,
+                                           volatile int *abort) {
+    const bool ok = ptx::mbar_wait_tries(bar, parity, P.tries);
     if (!ok) *abort = 1;
     return ok;
 }
 
 // The same for waits that may take as long as a unit does, and may see its end late: up to
-// 2^33 cycles, some four seconds.
-__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t ns,
-                                          volatile int *abort) {
-    const bool ok = ptx::mbar_wait_asleep(bar, parity, ns, 1ll << 33);
+// kCycles, some four seconds.
+__device__ __forceinline__ bool wait_long(const QParams &P, uint32_t bar, uint32_t parity,
+                                          uint32_t ns, volatile int *abort) {
+    const bool ok = ptx::mbar_wait_asleep(bar, parity, ns, P.cycles);
     if (!ok) *abort = 1;
     return ok;
 }
 
 // The same for a warpgroup on named barrier `bid`: true in all 128 threads or in none.
-__device__ __forceinline__ bool group_wait(int bid, int quad, uint32_t bar, uint32_t parity,
-                                           volatile int *abort) {
-    return tcc::named_barrier_and(bid, 128, quad != 0 || wait_phase(bar, parity, abort));
+__device__ __forceinline__ bool group_wait(const QParams &P, int bid, int quad, uint32_t bar,
+                                           uint32_t parity, volatile int *abort) {
+    return tcc::named_barrier_and(bid, 128, quad != 0 || wait_phase(P, bar, parity, abort));
 }
 
 // One arrival of a converged warp, after what its lanes did before.
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
     // operand warps within their registers.)
     auto enter = [&](int i) -> const Seg * {
         const bool got = __all_sync(
-            0xffffffffu, wait_long(bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, 20, abort));
+            0xffffffffu, wait_long(P, bar(L::kSegFull + i % kSegs), (i / kSegs) & 1, 20, abort));
         const Seg *s = reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
         return got && s->j1 > 0 ? s : nullptr;
     };
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
         for (int i = 0; ok; ++i) {
             const Seg s = next_segment<R>(P, s_cum, t, t1);
-            ok = __all_sync(0xffffffffu, i < kSegs || wait_long(bar(L::kSegFree + i % kSegs),
+            ok = __all_sync(0xffffffffu, i < kSegs || wait_long(P, bar(L::kSegFree + i % kSegs),
                                                                 (i / kSegs - 1) & 1, 100, abort));
             if (!ok) break;
             if (lane == 0) {
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 }
                 const int st = rc % NS;
                 ok = __all_sync(0xffffffffu,
-                                rc < NS || wait_long(bar(L::kEmpty + st), ((rc / NS) - 1) & 1,
+                                rc < NS || wait_long(P, bar(L::kEmpty + st), ((rc / NS) - 1) & 1,
                                                      100, abort));
                 if (!ok) break;
                 const bool two = 2 * j + 1 < s.np;
@@ -518,7 +524,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         if (lane == 0)
 #pragma unroll 1
             for (int j = max(0, rc - NS); j < rc; ++j)
-                wait_phase(bar(L::kFull + j % NS), (j / NS) & 1, abort);
+                wait_phase(P, bar(L::kFull + j % NS), (j / NS) & 1, abort);
         __syncwarp();
     } else if (warp == kWarpS) {
         // ------------------------------------------------ S^T = K Q^T of every tile
@@ -533,14 +539,14 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             const int n = s->j1 - s->j0;
             leave(i);
             const uint32_t sQ = sbase + L::kQ + (i & 1) * L::kQBytes;
-            ok = wait_phase(bar(L::kPrep + (i & 1)), (i >> 1) & 1, abort);
+            ok = wait_phase(P, bar(L::kPrep + (i & 1)), (i >> 1) & 1, abort);
 #pragma unroll 1
             for (int j = 0; j < n; ++j, ++it) {
                 const int x = it & 1;
                 // P V of two tiles ago is done: so is the softmax with that S, and S being
                 // ready tells the softmax warps that its weights have been read
-                ok = ok && wait_phase(bar(L::kKReady + x), (it >> 1) & 1, abort) &&
-                     wait_phase(bar(L::kOReady + x), ((it >> 1) + 1) & 1, abort);
+                ok = ok && wait_phase(P, bar(L::kKReady + x), (it >> 1) & 1, abort) &&
+                     wait_phase(P, bar(L::kOReady + x), ((it >> 1) + 1) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll
@@ -554,7 +560,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         }
         __syncwarp();
         ptx::mma_commit_lead(bar(L::kDone), lead);
-        wait_phase(bar(L::kDone), 0, abort);
+        wait_phase(P, bar(L::kDone), 0, abort);
     } else if (warp == kWarpPv) {
         // ------------------------------------------------ O^T += V^T P^T of every tile
         constexpr uint32_t nPV = 2 * R;
@@ -572,8 +578,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < n; ++j, ++it) {
                 const int x = it & 1;
-                ok = wait_phase(bar(L::kVReady + x), (it >> 1) & 1, abort) &&
-                     wait_phase(bar(L::kPReady + x), (it >> 1) & 1, abort);
+                ok = wait_phase(P, bar(L::kVReady + x), (it >> 1) & 1, abort) &&
+                     wait_phase(P, bar(L::kPReady + x), (it >> 1) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
                 const uint32_t sP = sbase + L::kP + (uint32_t)x * L::kPSlabs * kSlab;
@@ -598,7 +604,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         }
         __syncwarp();
         ptx::mma_commit_lead(bar(L::kDone + 1), lead);
-        wait_phase(bar(L::kDone + 1), 0, abort);
+        wait_phase(P, bar(L::kDone + 1), 0, abort);
     } else if (warp == kWarpPrep) {
         // ------------------------------------------------ a unit's rows, one unit ahead:
         // queries, root-path masks, windows, output rows; the tree's and the pages' checks
@@ -607,9 +613,13 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         for (int i = 0;; ++i) {
             const Seg *sp = enter(i);
             const int x = i & 1;
-            if (!__all_sync(0xffffffffu, i < 2 || wait_long(bar(L::kPrepFree + x),
+            if (!__all_sync(0xffffffffu, i < 2 || wait_long(P, bar(L::kPrepFree + x),
                                                             ((i >> 1) - 1) & 1, 200, abort)))
                 break;
+            if (P.expire && sp) {
+                *abort = 1;
+                break;
+            }
             if (!sp) {  // (the softmax warps wait for rows before they look at the segment)
                 if (lane == 0 && !*abort) ptx::mbar_arrive(bar(L::kPrep + x));
                 break;
@@ -719,8 +729,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 // P V of two tiles ago has read the buffer; this tile's pages are here
                 const int x = it & 1;
                 const uint32_t dst = tl + 64u * x;
-                ok = wait_phase(bar(L::kOReady + x), ((it >> 1) + 1) & 1, abort) &&
-                     (j >= s.nct || wait_phase(bar(L::kFull + st), full, abort));
+                ok = wait_phase(P, bar(L::kOReady + x), ((it >> 1) + 1) & 1, abort) &&
+                     (j >= s.nct || wait_phase(P, bar(L::kFull + st), full, abort));
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
                 if (j < s.nct) {
@@ -832,8 +842,8 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                 // S of two tiles ago has read the buffer; this tile's pages are here
                 const int x = it & 1;
                 const uint32_t dst = tl + (D / 2) * x;
-                ok = wait_phase(bar(L::kSReady + x), ((it >> 1) + 1) & 1, abort) &&
-                     (j >= s.nct || wait_phase(bar(L::kFull + st), full, abort));
+                ok = wait_phase(P, bar(L::kSReady + x), ((it >> 1) + 1) & 1, abort) &&
+                     (j >= s.nct || wait_phase(P, bar(L::kFull + st), full, abort));
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ptx::tc_fence_after_sync();
                 if (j < s.nct) {
@@ -912,7 +922,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
         for (int i = 0; go; ++i) {
             // (the segment stays in its ring slot until the results are out)
             if (quad == 0) s_nm[lane] = kNoMax;
-            if (!group_wait(bid, quad, bar(L::kPrep + (i & 1)), (i >> 1) & 1, abort)) break;
+            if (!group_wait(P, bid, quad, bar(L::kPrep + (i & 1)), (i >> 1) & 1, abort)) break;
             const Seg &s = *reinterpret_cast<const Seg *>(s_seg + (i % kSegs) * kSegInts);
             const int j1 = s.j1;
             if (j1 == 0) break;
@@ -952,7 +962,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
             for (int j = s.j0; j < j1; ++j, ++it) {
                 const int x2 = it & 1;
                 // each warp for itself; the vote below brings the group together
-                const bool here = wait_phase(bar(L::kSReady + x2), (it >> 1) & 1, abort);
+                const bool here = wait_phase(P, bar(L::kSReady + x2), (it >> 1) & 1, abort);
                 ptx::tc_fence_after_sync();
                 float x[32];
 #pragma unroll 1
@@ -973,7 +983,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
                         // ---- raise the reference maxima that need it; P V of the previous
                         // tile is done, so that O may be rescaled
                         warp_columns<true>(s_red + quad * 32, lane, live, x);
-                        go = here && wait_phase(bar(L::kOReady + (x2 ^ 1)),
+                        go = here && wait_phase(P, bar(L::kOReady + (x2 ^ 1)),
                                                 ((it + 1) >> 1 & 1) ^ 1, abort);
                         if (!(go = tcc::named_barrier_and(bid, 128, go))) break;
                         ptx::tc_fence_after_sync();
@@ -1086,7 +1096,7 @@ __global__ void __launch_bounds__(Lay<D, R, NP>::kThreads, 1)
 
             // ---- results
             warp_columns<false>(s_red + quad * 32, lane, live, l);
-            if (!group_wait(bid, quad, bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1,
+            if (!group_wait(P, bid, quad, bar(L::kOReady + ((it - 1) & 1)), ((it - 1) >> 1) & 1,
                             abort))
                 break;
             ptx::tc_fence_after_sync();
@@ -1271,6 +1281,9 @@ cudaError_t launch_parts(const QAttnArgs &a, cudaStream_t s) {
     P.grid = grid_size(a);
     P.sl2 = a.scale * 1.4426950408889634f;
     P.zero = -0.f;
+    P.expire = a.expire_wait != 0;
+    P.tries = P.expire ? kTries >> 6 : kTries;
+    P.cycles = P.expire ? kCycles >> 6 : kCycles;
     // as many requests per launch as the costs' 32-bit sums have room for
     const int most = (int)std::min<long long>(kChunkB, kMostCost / request_cost(a));
     for (P.b0 = 0; P.b0 < a.B; P.b0 += most) {

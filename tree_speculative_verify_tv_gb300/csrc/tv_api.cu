@@ -712,6 +712,8 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
     if (num_pages < 1 || window < 0 || sinks < 0) return TV_ERR_SHAPE;
     if (bad_stride(q_stride, H, d) || bad_stride(kv_stride, Hkv, d)) return TV_ERR_SHAPE;
     if (!(scale > 0.f) || scale > 3.0e38f) return TV_ERR_SHAPE;  // positive and finite
+    const bool expire = (out_dtype & TV_QCACHE_TEST_EXPIRE_WAIT) != 0;
+    out_dtype &= ~TV_QCACHE_TEST_EXPIRE_WAIT;
     if (out_dtype != TV_BF16 && out_dtype != TV_F32) return TV_ERR_DTYPE;
     if (!dev_status) return TV_ERR_NULL;
     if (B == 0 || total_nodes == 0) return TV_OK;
@@ -721,7 +723,7 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
     tv::QAttnArgs a{B, total_nodes, max_nodes, H, Hkv, d, num_pages, max_pages,
                     node_offsets, parent, ctx_len, page_table, window, sinks, q, q_stride,
                     static_cast<const uint8_t *>(cache), k_tree, v_tree, kv_stride, scale,
-                    out_dtype == TV_F32, out, static_cast<float *>(workspace), dev_status};
+                    out_dtype == TV_F32, out, static_cast<float *>(workspace), dev_status, expire};
     const size_t need = tv::qcache_attention_workspace_bytes(a);
     if (need > 0) {
         st = check_ptrs({workspace});

@@ -121,6 +121,7 @@ struct QAttnArgs {
     void *out;
     float *ws;
     int32_t *status;
+    int32_t expire_wait;  // TV_QCACHE_TEST_EXPIRE_WAIT
 };
 // Whether a request of these limits may be as large as they allow.
 bool qcache_attention_fits(const QAttnArgs &a);
