@@ -65,7 +65,8 @@ constexpr float kNoMax = 3.4028234e38f;  // -m of a row that has seen no key: th
 constexpr int kUnitCost = 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTries = 1u << 20;     // of a wait for a neighbour's step
-constexpr long long kCycles = 1ll << 33;  // of a wait that may last as long as a unit
+// of a wait that may last as long as a unit: 4 s, and six times what its tiles take
+constexpr long long kCycles = 1ll << 33, kTileCycles = 1 << 14;
 
 struct QParams {
     QAttnArgs a;
@@ -254,8 +255,9 @@ __device__ __forceinline__ bool wait_phase(const QParams &P, uint32_t bar, uint3
     return ok;
 }
 
-// The same for waits that may take as long as a unit does, and may see its end late: up to
-// kCycles, some four seconds.
+// The same for waits that may take as long as a unit does, and may see its end late: some four
+// seconds and what a unit of as many tiles as the call allows for could take.  (With four
+// seconds alone a unit of 2^30 positions, 12 s of work, ended as a timeout.)
 __device__ __forceinline__ bool wait_long(const QParams &P, uint32_t bar, uint32_t parity,
                                           uint32_t ns, volatile int *abort) {
     const bool ok = ptx::mbar_wait_asleep(bar, parity, ns, P.cycles);
@@ -1249,12 +1251,14 @@ __global__ void __launch_bounds__(256) qcache_attention_join_kernel(const QParam
 // everything twice, 16 trees of 16 nodes: 69.0 against 51.8, 256-node trees 190 against 119.)
 int rows_per_unit(const QAttnArgs &a) { return a.max_nodes * (a.H / a.Hkv) <= 32 ? 32 : 64; }
 
-// The most that one request can cost.
+// The most tiles that a unit can have, and the most that one request can cost.
+long long unit_tiles(const QAttnArgs &a) {
+    return (a.max_pages + 1) / 2 + (a.max_nodes + kKeys - 1) / kKeys;
+}
 long long request_cost(const QAttnArgs &a) {
     const int R = rows_per_unit(a);
     const long long mts = ((long long)a.max_nodes * (a.H / a.Hkv) + R - 1) / R;
-    return a.Hkv * mts *
-           ((a.max_pages + 1) / 2 + (a.max_nodes + kKeys - 1) / kKeys + kUnitCost);
+    return a.Hkv * mts * (unit_tiles(a) + kUnitCost);
 }
 
 // One CTA per SM, or one per tile when a batch cannot have as many.
@@ -1283,7 +1287,7 @@ cudaError_t launch_parts(const QAttnArgs &a, cudaStream_t s) {
     P.zero = -0.f;
     P.expire = a.expire_wait != 0;
     P.tries = P.expire ? kTries >> 6 : kTries;
-    P.cycles = P.expire ? kCycles >> 6 : kCycles;
+    P.cycles = P.expire ? kCycles >> 6 : kCycles + unit_tiles(a) * kTileCycles;
     // as many requests per launch as the costs' 32-bit sums have room for
     const int most = (int)std::min<long long>(kChunkB, kMostCost / request_cost(a));
     for (P.b0 = 0; P.b0 < a.B; P.b0 += most) {
