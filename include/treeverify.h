@@ -506,8 +506,9 @@ tv_status tv_accept_commit_verify(const tv_problem *p, const tv_pending *prev,
  *              depend on the split beyond fp32 rounding.
  *   dev_status, stream   see conventions
  * Arithmetic: bf16 inputs, fp32 scores and accumulation on tensor cores; the
- * softmax weights enter the weighted sum of values as bf16 (relative rounding
- * 2^-9), so outputs carry a relative error of order 2^-9.
+ * softmax weights enter the weighted sum of values as two bf16 parts (2^-16
+ * relative).  Scores scale * q . k below 2^29 in magnitude: beyond 2^31 / log2(e) the
+ * rounding of a row's largest one can exceed what an exponential holds (NaN).
  * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for sizes out of
  * range (H not a multiple of Hkv, T > B * max_nodes, P < 1, scale not positive and
  * finite);

@@ -31,17 +31,22 @@
 // alone, 2^-8, would double a bf16 output's rounding); sums l are kept in fp32 from the same
 // weights.  Every mbarrier wait is bounded.
 //
-// Measured (32 query heads over 8, d = 128): 16 trees of 16 nodes over 4096 positions 51.5 us
+// Measured (32 query heads over 8, d = 128): 16 trees of 16 nodes over 4096 positions 49.8 us
 // (1.5 TB/s of cache, 22 % of the copy bandwidth; the bf16 cache's pass takes 57.5 us for 3.8
-// times the bytes), 64 single tokens over 1..8191 positions (64 heads) 119 us (3.0 TB/s,
-// 45 %), one token over 500 positions 9.5 us.  A tile costs a CTA some 1500 cycles at 8 live
-// rows and 2300 at 64.  What bounds it: instructions.  The dequantising warps, the softmax
-// and the waits fill 64 to 70 % of the issue slots over the whole run, the arithmetic pipe
-// 50 to 56 %, the tensor pipe 23 %, DRAM 22 to 45 %; without V's dequantising the same runs
-// take 46 and 102 us, without the weights 43 and 115, and without either, K's and the vote
-// 37 and 81, which is the chain of signals from role to role.  The rest is per unit (a first
-// reference, results: 6000 cycles) and per launch (15000 cycles to the first product with
-// cold caches, 5 us for the second kernel and the launches).
+// times the bytes), 64 single tokens over 1..8191 positions (64 heads) 122.8 us (2.9 TB/s,
+// 44 %), one token over 500 positions 9.9 us.  A tile costs a CTA some 1500 cycles at 8 live
+// rows and 2300 at 64.  What bounds it: first the chain of signals from role to role, with two
+// buffers each of S, P, K and V.  When the two runs took 51.8 and 121.6 us, they took 46 and 102
+// without V's dequantising, 43 and 115 without the weights, and 37 and 81, two thirds, without
+// either, K's and the vote.  The rest are instructions: the dequantising warps, the softmax and
+// the waits fill 63 to 68 % of the issue slots over the whole run, the arithmetic pipe 50 to
+// 54 %, the tensor pipe 23 %, DRAM 22 to 44 %.  Per unit come a first reference and results
+// (6000 cycles), per launch 15000 cycles to the first product with cold caches, and 5 us for
+// the second kernel and the launches.
+//
+// The kernels of 64 rows spill: 12 bytes a thread stored and 4 loaded at d = 128, 40 and 64 at
+// d = 64; 9120 requests among 30.5 million warp instructions in 16 trees of 16 nodes, 157
+// thousand among 21.2 million in 32 windowed trees of 64 at d = 64 (0.7 %).
 //
 // The instruction cache counts, too (32 KB per SM, 8 KB per scheduler): loops are kept
 // rolled and waits short.
