@@ -689,6 +689,158 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
 #define TV_QCACHE_TEST_EXPIRE_WAIT 0x100
 
 /*
+ * tv_prefill -- prompts through the recurrence layer: the outputs of every row and the state
+ * after the last one, which is the H0 that tv_verify and tv_commit go on from (Bole summary
+ * page, "Core techniques" §1: h_{t+1} = S_t h_t + u_t with S = diag(exp g), u = k v^T).
+ * Rows row_offsets[b] .. row_offsets[b+1]-1 are request b's, in order:
+ *     H_t = diag(exp g_t) H_{t-1} + k_t v_t^T,   out_t = H_t^T q_t,   H_new = H after the last.
+ * A long prompt may come in several calls, each going on from the state of the one before.
+ *
+ *   B, total_rows (R)   requests, and rows in all
+ *   max_rows            bound on any request's rows, >= 1 (an upper bound costs nothing in
+ *                       results; the closer it is the better the work is shared out)
+ *   H, dk, dv, decay, qkv_dtype   as in tv_problem
+ *   row_offsets [B+1]   int32 (device), like node_offsets
+ *   H0                  [B][H][dk][dv] fp32, or NULL: all states start from zero
+ *   q, k, v             rows of qkv_dtype: row r, head h, channel c at q[r * q_stride +
+ *                       h * dk + c] (v with dv); strides are >= heads * width and multiples
+ *                       of 8, so rows may be views into a fused projection
+ *   g                   fp32 log decay at g[r * g_stride + h], or with TV_DECAY_DIAG
+ *                       g[r * g_stride + h * dk + c]; g_stride 0: one decay for all rows;
+ *                       4-byte alignment will do
+ *   out_dtype           TV_BF16 or TV_F32: the type of out [R][H][dv]
+ *   H_new               [B][H][dk][dv] fp32; may be H0 (in place), must not overlap it
+ *                       otherwise.  A request without rows gets H0 (zeros without one)
+ *   workspace           optional device memory (16-byte aligned, scratch) for the states at
+ *                       the cuts where few long prompts are shared out over the SMs;
+ *                       tv_prefill_workspace_bytes gives the size that allows the library's
+ *                       preferred cut.  With less (or NULL, 0) it cuts less (not at all).
+ *                       Calls that may run at the same time need workspaces of their own.
+ * Arithmetic: states and sums in fp32.  bf16 inputs with a scalar decay, dk and dv in
+ * {64, 128}: tensor cores, chunks of 64 rows, decays as 64-bit fixed-point sums of log2
+ * (2^-32; a row's g counts as at most 4096 log2 units), weights and states as two (bf16
+ * outputs) or three (fp32) bf16 parts, what is added to the state as three.  Other cases:
+ * the recurrence row by row on CUDA cores.
+ * NaN and infinity in a request's rows stay in that request and head.
+ * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for
+ * sizes and strides out of range (total_rows > B * max_rows too); TV_ERR_DTYPE;
+ * TV_ERR_UNSUPPORTED for dk or dv > TV_MAX_DIM and B * H or the work items beyond 2^31.
+ * Device-detected errors: unusable row_offsets, or more rows than max_rows, give TV_ERR_TREE;
+ * that request's out and H_new are left untouched (with unusable offsets those of others
+ * may be too).
+ */
+size_t tv_prefill_workspace_bytes(int32_t B, int32_t total_rows, int32_t max_rows, int32_t H,
+                                  int32_t dk, int32_t dv, int32_t decay, int32_t qkv_dtype);
+tv_status tv_prefill(int32_t B, int32_t total_rows, int32_t max_rows, int32_t H, int32_t dk,
+                     int32_t dv, int32_t decay, int32_t qkv_dtype, const int32_t *row_offsets,
+                     const float *H0, const void *q, int64_t q_stride, const void *k,
+                     int64_t k_stride, const void *v, int64_t v_stride, const float *g,
+                     int64_t g_stride, int32_t out_dtype, void *out, float *H_new,
+                     void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * tv_decode -- one token of every request through the recurrence layer: tv_prefill's row for
+ * a batch that decodes without drafts.  Row b is request b's.
+ *   active   [B] int32 (device), or NULL for all: a request with active[b] == 0 (a padded
+ *            slot of a batch) keeps its H_new and out as they are
+ *   H0       [B][H][dk][dv] fp32;  H_new may be H0 (in place), must not overlap it otherwise
+ *   other arguments as in tv_prefill; out [B][H][dv]
+ * Arithmetic: fp32.  Host errors as tv_prefill; there are no device-detected ones.
+ */
+tv_status tv_decode(int32_t B, int32_t H, int32_t dk, int32_t dv, int32_t decay,
+                    int32_t qkv_dtype, const int32_t *active, const float *H0, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, const float *g, int64_t g_stride, int32_t out_dtype,
+                    void *out, float *H_new, void *stream);
+
+/* Which channels tv_qk_norm_rope turns together, of the first rotary_dim of a head. */
+typedef enum tv_rope {
+    TV_ROPE_HALVES = 0,     /* channel i with channel i + rotary_dim / 2 */
+    TV_ROPE_PAIRS = 1       /* channel 2 i with channel 2 i + 1 */
+} tv_rope;
+
+/*
+ * tv_qk_norm_rope -- queries and keys of an attention layer made ready for tv_qcache_write,
+ * tv_qcache_attention or tv_tree_attention: every head's row normed, then rotated at its
+ * position, in one pass.
+ *     y_c = x_c * weight_c / sqrt(mean_c(x_c^2) + eps)
+ *     (a, b) -> (a cos t - b sin t, b cos t + a sin t),   t = position * inv_freq[i]
+ * Row r of request b stands at start[b] + (r - row_offsets[b]), or, with depth (a batch of
+ * trees), at start[b] + depth[r] - 1: with start = ctx_len the position at which
+ * tv_qcache_attention sees a node.
+ *
+ *   B, total_rows, H, Hkv   requests, rows in all, query heads (>= 1) and key heads (>= 0;
+ *               with 0 k, k_weight and k_out are not used)
+ *   d           head width: 64, 128 or 256
+ *   rotary_dim  channels that turn, a multiple of 8 from 0 (norms alone) to d
+ *   layout      tv_rope
+ *   dtype       TV_BF16 or TV_F32: the type of q, k, the weights and the outputs
+ *   row_offsets [B+1], start [B]   int32 (device), as in tv_qcache_write
+ *   depth       [R] int32 (device), as in tv_problem; NULL: rows are consecutive positions
+ *   q, k        rows: row r, head h, channel c at q[r * q_stride + h * d + c]; all strides
+ *               are >= heads * d and multiples of 8
+ *   q_weight, k_weight   [d], or NULL for ones
+ *   eps         >= 0 and finite; negative: no norm (rows are only rotated, weights not read)
+ *   inv_freq    [rotary_dim / 2] fp64 (device): radians per position, finite
+ *   q_out, k_out   rows with strides of their own; q_out may be q and k_out k (in place, with
+ *               the same stride), they must not overlap the inputs otherwise
+ * Rows outside every request (behind the last one's) are left as they are.
+ * Arithmetic: fp32, rounded once; the angle's turns are a 64-bit fixed-point product, so
+ * far positions lose nothing.
+ * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for sizes, strides and eps
+ * out of range; TV_ERR_DTYPE for dtype and layout; TV_ERR_UNSUPPORTED for other d.
+ * Device-detected errors: unusable row_offsets give TV_ERR_TREE; that request's rows are left
+ * untouched (those of others may be too).
+ */
+tv_status tv_qk_norm_rope(int32_t B, int32_t total_rows, int32_t H, int32_t Hkv, int32_t d,
+                          int32_t rotary_dim, int32_t layout, int32_t dtype,
+                          const int32_t *row_offsets, const int32_t *start, const int32_t *depth,
+                          const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                          const void *q_weight, const void *k_weight, float eps,
+                          const double *inv_freq, void *q_out, int64_t q_out_stride, void *k_out,
+                          int64_t k_out_stride, int32_t *dev_status, void *stream);
+
+/* Most alternatives that tv_logprobs lists. */
+#define TV_LOGPROBS_MAX_TOP 32
+
+/*
+ * tv_logprobs -- log probabilities of given tokens under the target's logits, the entropy of
+ * their distributions and the most likely tokens: what is told beside the tokens that
+ * tv_accept_greedy_logits or tv_accept_stochastic emitted (or the drafts, or a prompt).
+ *     p = softmax(scale * row),   logprob = ln p[token],   entropy = -sum p ln p (nats)
+ *
+ *   R, num_rows, vocab   results, rows of logits and their length
+ *   logits       rows of logits_dtype (TV_BF16 or TV_F32), row n at logits[n * row_stride];
+ *                row_stride >= vocab
+ *   rows         [R] int32 (device): the row of each result, or NULL: result r is of row r
+ *                (then R <= num_rows).  The same row may stand there several times.
+ *                rows[r] < 0: no result (a path's padding): logprob and entropy 0, top_token
+ *                -1, top_logprob 0
+ *   tokens       [R] int32 (device), or NULL; tokens[r] < 0: no token, logprob 0
+ *   scale        positive and finite: one over the temperature
+ *   top_k        alternatives, 0 .. TV_LOGPROBS_MAX_TOP and at most vocab
+ *   logprob      [R] fp32 out; NULL exactly if tokens is
+ *   entropy      [R] fp32 out, or NULL
+ *   top_token, top_logprob   [R][top_k] int32, fp32 out (not used with top_k = 0): the
+ *                largest logits in falling order, the lower index first among equals (a NaN
+ *                counts as larger than any number, -0 equals +0: the first is
+ *                tv_accept_greedy_logits' argmax)
+ * Logits of -inf (forbidden tokens) have probability 0 and log probability -inf.  In a row
+ * with nothing else every log probability is -inf and the entropy 0; in a row with a NaN
+ * or +inf all of them and the entropy are NaN (top_token is still in order).
+ * Arithmetic: fp32 sums and exponentials; top_token is exact.
+ * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for sizes, row_stride and
+ * scale out of range; TV_ERR_DTYPE; TV_ERR_UNSUPPORTED for top_k > TV_LOGPROBS_MAX_TOP.
+ * Device-detected errors: a row >= num_rows or a token >= vocab gives TV_ERR_SHAPE, and what
+ * it would give is written as for a negative one.
+ */
+tv_status tv_logprobs(int32_t R, int32_t num_rows, int32_t vocab, int32_t logits_dtype,
+                      const void *logits, int64_t row_stride, const int32_t *rows,
+                      const int32_t *tokens, float scale, int32_t top_k, float *logprob,
+                      float *entropy, int32_t *top_token, float *top_logprob,
+                      int32_t *dev_status, void *stream);
+
+/*
  * tv_verify_variant -- the kernel tv_verify (TV_VARIANT_AUTO) would launch for
  * this problem: TV_VARIANT_TC_STREAM, TV_VARIANT_TC, TV_VARIANT_TC_TILED (trees too
  * large for TV_VARIANT_TC's shared-memory plan, and per-channel decay trees of 64

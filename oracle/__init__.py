@@ -12,8 +12,9 @@ against), the greedy acceptance walk (LLM Primer VI ch. 9, §9.1) and the
 commit of the accepted path's state (Bole §2).  This file builds the C source,
 marshals arrays and splits work over threads; the functions for the wider rows
 of the path are plain numpy here: the argmax of logits rows, best-first tree
-construction, stochastic acceptance, tree-masked softmax attention and the 4-bit KV
-cache (its quantiser, its records, windowed attention over it).
+construction, stochastic acceptance, tree-masked softmax attention, the 4-bit KV
+cache (its quantiser, its records, windowed attention over it), prompts through the
+recurrence, norms with position rotation and log probabilities.
 
 Parity pins for each function are in ``tests/test_oracle_pins.py``.
 """
@@ -603,3 +604,67 @@ def commit(batch, accept_len, path, units: Optional[Sequence[int]] = None, threa
             for part in ex.map(run, chunks):
                 res.update(part)
     return res
+
+
+def prefill(offsets, q, k, v, g, H0=None, diag: bool = False):
+    """Prompts through the recurrence, row after row.  q, k [R][H][dk], v [R][H][dv] (values),
+    g [R][H] or, with diag, [R][H][dk]; H0 [B][H][dk][dv] or None.  Returns out [R][H][dv] and
+    the states after each request's last row; rows outside every request stay zero."""
+    q, k, v, g = (_f64(x) for x in (q, k, v, g))
+    B, (R, H, dk), dv = len(offsets) - 1, q.shape, v.shape[-1]
+    out = np.zeros((R, H, dv))
+    S = np.zeros((B, H, dk, dv)) if H0 is None else _f64(H0).copy()
+    decay = np.exp(g) if diag else np.exp(g)[..., None]
+    for b in range(B):
+        for t in range(int(offsets[b]), int(offsets[b + 1])):
+            S[b] = decay[t][..., None] * S[b] + k[t][..., None] * v[t][:, None, :]
+            out[t] = np.einsum("hc,hcd->hd", q[t], S[b])
+    return out, S
+
+
+def qk_norm_rope(x, position, weight, eps, inv_freq, pairs: bool):
+    """Rows x [R][heads][d] normed (eps None: not) and rotated at position [R]; the first
+    2 len(inv_freq) channels turn."""
+    y = _f64(x).copy()
+    if eps is not None:
+        y = y / np.sqrt((y * y).mean(-1, keepdims=True) + eps)
+        if weight is not None:
+            y = y * _f64(weight)
+    half = len(inv_freq)
+    if pairs:
+        lo, hi = slice(0, 2 * half, 2), slice(1, 2 * half, 2)
+    else:
+        lo, hi = slice(0, half), slice(half, 2 * half)
+    t = np.asarray(position, np.float64)[:, None, None] * _f64(inv_freq)
+    a, b = y[..., lo].copy(), y[..., hi].copy()
+    y[..., lo] = a * np.cos(t) - b * np.sin(t)
+    y[..., hi] = b * np.cos(t) + a * np.sin(t)
+    return y
+
+
+def logprobs(logits, rows, tokens, scale, top):
+    """(logprob, entropy, top_token, top_logprob) of results r: row rows[r] of logits [N][V]
+    (values), token tokens[r]; negative ones as tv_logprobs defines them."""
+    x = _f64(logits)
+    R = len(rows)
+    lp, ent = np.zeros(R), np.zeros(R)
+    tt, tl = np.full((R, top), -1, np.int64), np.zeros((R, top))
+    for r, row in enumerate(rows):
+        if row < 0:
+            continue
+        y = x[row] * scale
+        if np.isnan(y).any() or np.isposinf(y).any():
+            full, ent[r] = np.full(len(y), np.nan), np.nan
+        elif np.isneginf(y).all():
+            full = y
+        else:
+            m = y.max()
+            full = y - (m + np.log(np.exp(y - m).sum()))
+            seen = full[full > -np.inf]
+            ent[r] = -(np.exp(seen) * seen).sum()
+        if tokens[r] >= 0:
+            lp[r] = full[tokens[r]]
+        order = np.lexsort((np.arange(len(y)), -np.where(np.isnan(x[row]), 0, x[row]),
+                            ~np.isnan(x[row])))[:top]
+        tt[r], tl[r] = order, full[order]
+    return lp, ent, tt, tl

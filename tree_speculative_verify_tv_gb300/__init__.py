@@ -16,6 +16,10 @@ include/treeverify.h; this package is the ctypes binding):
   4 bits: rows or an accepted path quantised into it, positions read back
 * ``tv_qcache_attention`` tree attention over that cache, with an optional sliding
   window and sinks
+* ``tv_prefill``, ``tv_decode`` prompts and single tokens through the recurrence: every
+  row's output and the state after the last
+* ``tv_qk_norm_rope``  queries and keys normed per head and rotated at their positions
+* ``tv_logprobs``  log probabilities of tokens, entropy and the most likely alternatives
 * ``tv_verify_serial``  the naive node-by-node verification with per-node states
   (a baseline for the closed form)
 * ``tv_commit_verify`` the previous step's commit applied to the state in place,
@@ -33,7 +37,9 @@ from .binding import (  # noqa: F401
     tv_verify_serial, tv_verify_serial_workspace_bytes, tv_verify_serial_static, tv_build_tree,
     tv_accept_stochastic, tv_tree_attention, tv_tree_attention_workspace_bytes,
     tv_qcache_bytes, tv_qcache_write, tv_qcache_commit, tv_qcache_read, tv_qcache_attention,
-    tv_qcache_attention_workspace_bytes, TV_QCACHE_PAGE, TV_QCACHE_GROUP,
+    tv_qcache_attention_workspace_bytes, tv_prefill, tv_prefill_workspace_bytes, tv_decode,
+    tv_qk_norm_rope, tv_logprobs, TV_ROPE_HALVES, TV_ROPE_PAIRS, TV_LOGPROBS_MAX_TOP,
+    TV_QCACHE_PAGE, TV_QCACHE_GROUP,
     TV_QCACHE_TEST_EXPIRE_WAIT,
     TV_SERIAL_STATIC_BYTES,
     tv_problem, tv_status_string, tv_verify, tv_verify_variant, tv_verify_supports, tv_version, EXPORTED,

@@ -30,6 +30,8 @@ TV_MAX_NODES, TV_MAX_DEPTH, TV_MAX_DIM = 256, 32, 256
 TV_SERIAL_STATIC_BYTES = 16 << 20
 TV_QCACHE_PAGE, TV_QCACHE_GROUP = 64, 32
 TV_QCACHE_TEST_EXPIRE_WAIT = 0x100
+TV_ROPE_HALVES, TV_ROPE_PAIRS = 0, 1
+TV_LOGPROBS_MAX_TOP = 32
 
 EXPORTED = ("tv_verify", "tv_verify_ex", "tv_verify_variant", "tv_verify_supports",
             "tv_workspace_bytes",
@@ -40,6 +42,8 @@ EXPORTED = ("tv_verify", "tv_verify_ex", "tv_verify_variant", "tv_verify_support
             "tv_accept_stochastic", "tv_tree_attention", "tv_tree_attention_workspace_bytes",
             "tv_qcache_bytes", "tv_qcache_write", "tv_qcache_commit", "tv_qcache_read",
             "tv_qcache_attention", "tv_qcache_attention_workspace_bytes",
+            "tv_prefill", "tv_prefill_workspace_bytes", "tv_decode", "tv_qk_norm_rope",
+            "tv_logprobs",
             "tv_status_string", "tv_version")
 
 
@@ -112,6 +116,14 @@ def load(path: Optional[str] = None):
         L.tv_qcache_attention_workspace_bytes.restype = size
         L.tv_qcache_attention.argtypes = ([i32] * 8 + [vp] * 4 + [i32] * 2 + [vp, i64] + [vp] * 3 +
                                           [i64, ctypes.c_float, i32, vp, vp, size, vp, vp])
+        L.tv_prefill_workspace_bytes.argtypes = [i32] * 8
+        L.tv_prefill_workspace_bytes.restype = size
+        L.tv_prefill.argtypes = ([i32] * 8 + [vp, vp] + [vp, i64] * 4 + [i32] + [vp] * 3 +
+                                 [size, vp, vp])
+        L.tv_decode.argtypes = [i32] * 6 + [vp, vp] + [vp, i64] * 4 + [i32] + [vp] * 3
+        L.tv_qk_norm_rope.argtypes = ([i32] * 8 + [vp] * 3 + [vp, i64] * 2 +
+                                      [vp, vp, ctypes.c_float, vp] + [vp, i64] * 2 + [vp, vp])
+        L.tv_logprobs.argtypes = ([i32] * 4 + [vp, i64, vp, vp, ctypes.c_float, i32] + [vp] * 6)
         L.tv_verify_serial_workspace_bytes.argtypes = [P]
         L.tv_verify_serial_workspace_bytes.restype = ctypes.c_size_t
         L.tv_workspace_bytes.argtypes = [P]
@@ -121,7 +133,8 @@ def load(path: Optional[str] = None):
                   L.tv_accept_greedy_logits,
                   L.tv_verify_serial, L.tv_verify_serial_static, L.tv_build_tree,
                   L.tv_accept_stochastic, L.tv_tree_attention, L.tv_qcache_write,
-                  L.tv_qcache_commit, L.tv_qcache_read, L.tv_qcache_attention):
+                  L.tv_qcache_commit, L.tv_qcache_read, L.tv_qcache_attention, L.tv_prefill,
+                  L.tv_decode, L.tv_qk_norm_rope, L.tv_logprobs):
             f.restype = ctypes.c_int32
         L.tv_status_string.argtypes = [i32]
         L.tv_status_string.restype = ctypes.c_char_p
@@ -321,6 +334,56 @@ def tv_qcache_attention(B, total_nodes, max_nodes, H, Hkv, d, num_pages, max_pag
                                     int(out_dtype), _ptr(out), _ptr(workspace),
                                     int(workspace_bytes), _ptr(dev_status), _stream(stream))
     return _check(rc, "tv_qcache_attention", check)
+
+
+def tv_prefill_workspace_bytes(B, total_rows, max_rows, H, dk, dv, decay, qkv_dtype) -> int:
+    """Workspace with which tv_prefill cuts long prompts as it prefers (0: it cuts none)."""
+    return int(load().tv_prefill_workspace_bytes(int(B), int(total_rows), int(max_rows), int(H),
+                                                 int(dk), int(dv), int(decay), int(qkv_dtype)))
+
+
+def tv_prefill(B, total_rows, max_rows, H, dk, dv, decay, qkv_dtype, row_offsets, H0, q, q_stride,
+               k, k_stride, v, v_stride, g, g_stride, out_dtype, out, H_new, workspace=None,
+               workspace_bytes=0, dev_status=None, stream=None, check: bool = True) -> int:
+    rc = load().tv_prefill(int(B), int(total_rows), int(max_rows), int(H), int(dk), int(dv),
+                           int(decay), int(qkv_dtype), _ptr(row_offsets), _ptr(H0), _ptr(q),
+                           int(q_stride), _ptr(k), int(k_stride), _ptr(v), int(v_stride), _ptr(g),
+                           int(g_stride), int(out_dtype), _ptr(out), _ptr(H_new),
+                           _ptr(workspace), int(workspace_bytes), _ptr(dev_status),
+                           _stream(stream))
+    return _check(rc, "tv_prefill", check)
+
+
+def tv_decode(B, H, dk, dv, decay, qkv_dtype, active, H0, q, q_stride, k, k_stride, v, v_stride, g,
+              g_stride, out_dtype, out, H_new, stream=None, check: bool = True) -> int:
+    rc = load().tv_decode(int(B), int(H), int(dk), int(dv), int(decay), int(qkv_dtype),
+                          _ptr(active), _ptr(H0), _ptr(q), int(q_stride), _ptr(k), int(k_stride),
+                          _ptr(v), int(v_stride), _ptr(g), int(g_stride), int(out_dtype),
+                          _ptr(out), _ptr(H_new), _stream(stream))
+    return _check(rc, "tv_decode", check)
+
+
+def tv_qk_norm_rope(B, total_rows, H, Hkv, d, rotary_dim, layout, dtype, row_offsets, start, depth,
+                    q, q_stride, k, k_stride, q_weight, k_weight, eps, inv_freq, q_out,
+                    q_out_stride, k_out, k_out_stride, dev_status, stream=None,
+                    check: bool = True) -> int:
+    rc = load().tv_qk_norm_rope(int(B), int(total_rows), int(H), int(Hkv), int(d),
+                                int(rotary_dim), int(layout), int(dtype), _ptr(row_offsets),
+                                _ptr(start), _ptr(depth), _ptr(q), int(q_stride), _ptr(k),
+                                int(k_stride), _ptr(q_weight), _ptr(k_weight), float(eps),
+                                _ptr(inv_freq), _ptr(q_out), int(q_out_stride), _ptr(k_out),
+                                int(k_out_stride), _ptr(dev_status), _stream(stream))
+    return _check(rc, "tv_qk_norm_rope", check)
+
+
+def tv_logprobs(R, num_rows, vocab, logits_dtype, logits, row_stride, rows, tokens, scale, top_k,
+                logprob, entropy, top_token, top_logprob, dev_status, stream=None,
+                check: bool = True) -> int:
+    rc = load().tv_logprobs(int(R), int(num_rows), int(vocab), int(logits_dtype), _ptr(logits),
+                            int(row_stride), _ptr(rows), _ptr(tokens), float(scale), int(top_k),
+                            _ptr(logprob), _ptr(entropy), _ptr(top_token), _ptr(top_logprob),
+                            _ptr(dev_status), _stream(stream))
+    return _check(rc, "tv_logprobs", check)
 
 
 def tv_build_tree(B, C, depth_cap, n, marginals, cost, parent, token, rho, count, stream=None,

@@ -1,0 +1,163 @@
+// prefill.cu -- prompts through the gated linear recurrence, row by row on CUDA cores, and the
+// choice between this kernel and the tensor-core one.
+//
+//   H_t = diag(e^{g_t}) H_{t-1} + k_t v_t^T,   out_t = H_t^T q_t
+// (Bole summary page, "Core techniques" §1: h_{t+1} = S_t h_t + u_t)
+//
+// A CTA takes 16 columns of one (request, head) and walks down the rows.  Eight lanes share a
+// column, each with 4 ceil(dk / 32) rows of the state in registers; blocks of kRows rows of
+// q, k, v land in shared memory by asynchronous copies a block ahead.  5 dk dv / 128 cycles of
+// an SM a row and head (the decay's second part takes one of them) against dk-sized loads:
+// instructions bound it.
+#include "recurrence.cuh"
+#include "tc_ptx.cuh"
+
+namespace tv {
+namespace {
+
+constexpr int kThreadsP = 128;
+constexpr int kCols = 16;  // columns per CTA
+constexpr int kRows = 8;   // rows per block of copies
+
+template <typename E, bool DIAG, int R>
+struct RowsSmem {
+    E k[2][kRows][32 * R], q[2][kRows][32 * R], v[2][kRows][kCols];
+    rec::Pair d[2][kRows][DIAG ? 32 * R : 1];
+};
+
+// R: groups of 32 key rows.
+template <typename E, bool DIAG, int R>
+__global__ void __launch_bounds__(kThreadsP) prefill_rows_kernel(PrefillArgs a) {
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    auto &s = *reinterpret_cast<RowsSmem<E, DIAG, R> *>(s_raw);
+    constexpr int kPiece = 16 / sizeof(E);  // elements per copy
+    const int unit = blockIdx.x, b = unit / a.H, h = unit % a.H, tid = threadIdx.x;
+    const int c0 = blockIdx.y * kCols, cols = min(kCols, a.dv - c0);
+    const int r = tid % 8, col = tid / 8;
+    pdl_wait();
+    pdl_launch_next();
+    int off, n;
+    if (!request_range(a.offsets, b, a.R, a.max_rows, off, n)) {
+        if (tid == 0) report(a.status, TV_ERR_TREE);
+        return;
+    }
+    // channels past dk stay zero in both buffers
+    for (int i = tid; i < 2 * kRows * (32 * R - a.dk); i += kThreadsP) {
+        const int c = a.dk + i % (32 * R - a.dk), t = i / (32 * R - a.dk);
+        s.k[t / kRows][t % kRows][c] = E(0.f);
+        s.q[t / kRows][t % kRows][c] = E(0.f);
+        if (DIAG) s.d[t / kRows][t % kRows][c] = {0.f, 0.f};
+    }
+    const bool live = col < cols;
+    const size_t state = (size_t)unit * a.dk * a.dv + c0 + col;
+    float x[4 * R];
+#pragma unroll
+    for (int i = 0; i < 4 * R; ++i) {
+        const int row = (i / 4) * 32 + 4 * r + i % 4;
+        x[i] = a.H0 && live && row < a.dk ? a.H0[state + (size_t)row * a.dv] : 0.f;
+    }
+
+    constexpr int kGates = DIAG ? kRows * 32 * R / kThreadsP : 1;
+    float gates[kGates];
+    const auto fetch = [&](int t0, int buf) {  // rows t0 .. of the request into a buffer
+        const int cnt = min(kRows, n - t0), pk = a.dk / kPiece, pv = cols / kPiece;
+        for (int i = tid; i < cnt * pk; i += kThreadsP) {
+            const int t = i / pk, c = i % pk * kPiece;
+            const size_t row = (size_t)off + t0 + t;
+            ptx::cp_async_16(ptx::smem_addr(&s.k[buf][t][c]),
+                             static_cast<const E *>(a.k) + row * a.k_stride + (size_t)h * a.dk + c);
+            ptx::cp_async_16(ptx::smem_addr(&s.q[buf][t][c]),
+                             static_cast<const E *>(a.q) + row * a.q_stride + (size_t)h * a.dk + c);
+        }
+        for (int i = tid; i < cnt * pv; i += kThreadsP) {
+            const int t = i / pv, c = i % pv * kPiece;
+            ptx::cp_async_16(ptx::smem_addr(&s.v[buf][t][c]),
+                             static_cast<const E *>(a.v) + ((size_t)off + t0 + t) * a.v_stride +
+                                 (size_t)h * a.dv + c0 + c);
+        }
+#pragma unroll
+        for (int j = 0; j < kGates; ++j) {
+            const int i = tid + j * kThreadsP, t = DIAG ? i / a.dk : i, c = DIAG ? i % a.dk : 0;
+            gates[j] = t < cnt ? a.g[((size_t)off + t0 + t) * a.g_stride +
+                                     (size_t)h * (DIAG ? a.dk : 1) + c]
+                               : 0.f;
+        }
+    };
+    if (n > 0) fetch(0, 0);
+    for (int t0 = 0, buf = 0; t0 < n; t0 += kRows, buf ^= 1) {
+        const int cnt = min(kRows, n - t0);
+#pragma unroll
+        for (int j = 0; j < kGates; ++j) {
+            const int i = tid + j * kThreadsP, t = DIAG ? i / a.dk : i, c = DIAG ? i % a.dk : 0;
+            if (t < kRows) s.d[buf][t][c] = rec::exp_pair(gates[j]);
+        }
+        ptx::cp_async_wait_all();
+        __syncthreads();
+        if (t0 + kRows < n) fetch(t0 + kRows, buf ^ 1);
+        float mine = 0.f;
+#pragma unroll 2
+        for (int t = 0; t < cnt; ++t) {
+            const float vc = to_f32(s.v[buf][t][col]);
+            rec::Pair d = s.d[buf][t][0];
+            float o = 0.f;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int c = i * 32 + 4 * r;
+                const float4 k4 = rec::load4(&s.k[buf][t][c]), q4 = rec::load4(&s.q[buf][t][c]);
+                const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (DIAG) d = s.d[buf][t][c + e];
+                    float &y = x[4 * i + e];
+                    y = fmaf(y, d.hi, fmaf(y, d.lo, kk[e] * vc));
+                    o = fmaf(y, qq[e], o);
+                }
+            }
+            o += __shfl_xor_sync(0xffffffffu, o, 1);
+            o += __shfl_xor_sync(0xffffffffu, o, 2);
+            o += __shfl_xor_sync(0xffffffffu, o, 4);
+            if (t == r) mine = o;
+        }
+        if (live && r < cnt)
+            rec::store_out(a.out, a.out_f32,
+                           (((size_t)off + t0 + r) * a.H + h) * a.dv + c0 + col, mine);
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * R; ++i) {
+        const int row = (i / 4) * 32 + 4 * r + i % 4;
+        if (live && row < a.dk) a.H_new[state + (size_t)row * a.dv] = x[i];
+    }
+}
+
+template <typename E, bool DIAG, int R>
+cudaError_t launch_rows(const PrefillArgs &a, cudaStream_t s) {
+    const cudaError_t e = configure_smem_once(prefill_rows_kernel<E, DIAG, R>, false);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(prefill_rows_kernel<E, DIAG, R>,
+                      dim3((unsigned)(a.B * a.H), (unsigned)((a.dv + kCols - 1) / kCols)),
+                      dim3(kThreadsP), sizeof(RowsSmem<E, DIAG, R>), s, a);
+}
+
+template <typename E, bool DIAG>
+cudaError_t launch_rows(const PrefillArgs &a, cudaStream_t s) {
+    if (a.dk <= 32) return launch_rows<E, DIAG, 1>(a, s);
+    if (a.dk <= 64) return launch_rows<E, DIAG, 2>(a, s);
+    if (a.dk <= 128) return launch_rows<E, DIAG, 4>(a, s);
+    return launch_rows<E, DIAG, 8>(a, s);
+}
+
+}  // namespace
+
+bool prefill_fits(const PrefillArgs &) { return true; }
+
+size_t prefill_workspace_bytes(const PrefillArgs &) { return 0; }
+
+cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s) {
+    const bool diag = a.decay == TV_DECAY_DIAG;
+    if (a.qkv_dtype == TV_BF16)
+        return diag ? launch_rows<__nv_bfloat16, true>(a, s)
+                    : launch_rows<__nv_bfloat16, false>(a, s);
+    return diag ? launch_rows<float, true>(a, s) : launch_rows<float, false>(a, s);
+}
+
+}  // namespace tv

@@ -735,3 +735,169 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
 }
 
 }  // extern "C"
+
+namespace {
+
+// Sizes and strides that tv_prefill and tv_decode share.
+tv_status recurrence_dims(int32_t B, int32_t H, int32_t dk, int32_t dv, int32_t decay,
+                          int32_t qkv_dtype) {
+    if (B < 0 || H < 1) return TV_ERR_SHAPE;
+    if (dk < 8 || dv < 8 || dk % 8 || dv % 8) return TV_ERR_SHAPE;
+    if (dk > TV_MAX_DIM || dv > TV_MAX_DIM) return TV_ERR_UNSUPPORTED;
+    if (decay != TV_DECAY_SCALAR && decay != TV_DECAY_DIAG) return TV_ERR_DTYPE;
+    if (qkv_dtype != TV_BF16 && qkv_dtype != TV_F32) return TV_ERR_DTYPE;
+    if ((int64_t)B * H > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+    return TV_OK;
+}
+
+tv_status recurrence_strides(int32_t H, int32_t dk, int32_t dv, int32_t decay, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int64_t g_stride,
+                             int32_t out_dtype) {
+    if (bad_stride(q_stride, H, dk) || bad_stride(k_stride, H, dk) || bad_stride(v_stride, H, dv))
+        return TV_ERR_SHAPE;
+    if (g_stride && g_stride < (int64_t)H * (decay == TV_DECAY_DIAG ? dk : 1)) return TV_ERR_SHAPE;
+    if (out_dtype != TV_BF16 && out_dtype != TV_F32) return TV_ERR_DTYPE;
+    return TV_OK;
+}
+
+// Decays are read one by one: rows of any slice will do.
+tv_status check_gates(const float *g) {
+    if (!g) return TV_ERR_NULL;
+    return reinterpret_cast<uintptr_t>(g) % alignof(float) ? TV_ERR_ALIGN : TV_OK;
+}
+
+tv_status prefill_dims(int32_t B, int32_t R, int32_t max_rows, int32_t H, int32_t dk, int32_t dv,
+                       int32_t decay, int32_t qkv_dtype) {
+    if (R < 0 || max_rows < 1) return TV_ERR_SHAPE;
+    tv_status st = recurrence_dims(B, H, dk, dv, decay, qkv_dtype);
+    if (st != TV_OK) return st;
+    if ((int64_t)R > (int64_t)B * max_rows) return TV_ERR_SHAPE;
+    tv::PrefillArgs a{};
+    a.B = B;
+    a.R = R;
+    a.H = H;
+    return tv::prefill_fits(a) ? TV_OK : TV_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tv_prefill_workspace_bytes(int32_t B, int32_t total_rows, int32_t max_rows, int32_t H,
+                                  int32_t dk, int32_t dv, int32_t decay, int32_t qkv_dtype) {
+    if (prefill_dims(B, total_rows, max_rows, H, dk, dv, decay, qkv_dtype) != TV_OK) return 0;
+    tv::PrefillArgs a{};
+    a.B = B;
+    a.R = total_rows;
+    a.max_rows = max_rows;
+    a.H = H;
+    a.dk = dk;
+    a.dv = dv;
+    a.decay = decay;
+    a.qkv_dtype = qkv_dtype;
+    return tv::prefill_workspace_bytes(a);
+}
+
+tv_status tv_prefill(int32_t B, int32_t total_rows, int32_t max_rows, int32_t H, int32_t dk,
+                     int32_t dv, int32_t decay, int32_t qkv_dtype, const int32_t *row_offsets,
+                     const float *H0, const void *q, int64_t q_stride, const void *k,
+                     int64_t k_stride, const void *v, int64_t v_stride, const float *g,
+                     int64_t g_stride, int32_t out_dtype, void *out, float *H_new,
+                     void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                     void *stream) {
+    tv_status st = prefill_dims(B, total_rows, max_rows, H, dk, dv, decay, qkv_dtype);
+    if (st != TV_OK) return st;
+    st = recurrence_strides(H, dk, dv, decay, q_stride, k_stride, v_stride, g_stride, out_dtype);
+    if (st != TV_OK) return st;
+    if (!dev_status) return TV_ERR_NULL;
+    if (B == 0) return TV_OK;
+    st = check_ptrs({row_offsets, H_new, dev_status});
+    if (st == TV_OK && total_rows > 0) st = check_ptrs({q, k, v, out});
+    if (st == TV_OK && total_rows > 0) st = check_gates(g);
+    if (st != TV_OK) return st;
+    if (!aligned16(H0) || !aligned16(workspace)) return TV_ERR_ALIGN;
+    tv::PrefillArgs a{B, total_rows, max_rows, H, dk, dv, decay, qkv_dtype, out_dtype == TV_F32,
+                      row_offsets, H0, q, k, v, q_stride, k_stride, v_stride, g, g_stride, out,
+                      H_new, static_cast<uint8_t *>(workspace), workspace ? workspace_bytes : 0,
+                      dev_status};
+    cudaError_t e = tv::launch_prefill(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+tv_status tv_decode(int32_t B, int32_t H, int32_t dk, int32_t dv, int32_t decay,
+                    int32_t qkv_dtype, const int32_t *active, const float *H0, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, const float *g, int64_t g_stride, int32_t out_dtype,
+                    void *out, float *H_new, void *stream) {
+    tv_status st = recurrence_dims(B, H, dk, dv, decay, qkv_dtype);
+    if (st != TV_OK) return st;
+    st = recurrence_strides(H, dk, dv, decay, q_stride, k_stride, v_stride, g_stride, out_dtype);
+    if (st != TV_OK) return st;
+    if (B == 0) return TV_OK;
+    st = check_ptrs({H0, q, k, v, out, H_new});
+    if (st == TV_OK) st = check_gates(g);
+    if (st != TV_OK) return st;
+    if (!aligned16(active)) return TV_ERR_ALIGN;
+    tv::DecodeArgs a{B, H, dk, dv, decay, qkv_dtype, out_dtype == TV_F32, active, H0, q, k, v,
+                     q_stride, k_stride, v_stride, g, g_stride, out, H_new};
+    cudaError_t e = tv::launch_decode(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+tv_status tv_qk_norm_rope(int32_t B, int32_t total_rows, int32_t H, int32_t Hkv, int32_t d,
+                          int32_t rotary_dim, int32_t layout, int32_t dtype,
+                          const int32_t *row_offsets, const int32_t *start, const int32_t *depth,
+                          const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                          const void *q_weight, const void *k_weight, float eps,
+                          const double *inv_freq, void *q_out, int64_t q_out_stride, void *k_out,
+                          int64_t k_out_stride, int32_t *dev_status, void *stream) {
+    if (B < 0 || total_rows < 0 || H < 1 || Hkv < 0 || d < 1) return TV_ERR_SHAPE;
+    if (d != 64 && d != 128 && d != 256) return TV_ERR_UNSUPPORTED;
+    if (rotary_dim < 0 || rotary_dim > d || rotary_dim % 8) return TV_ERR_SHAPE;
+    if (layout != TV_ROPE_HALVES && layout != TV_ROPE_PAIRS) return TV_ERR_DTYPE;
+    if (dtype != TV_BF16 && dtype != TV_F32) return TV_ERR_DTYPE;
+    if (bad_stride(q_stride, H, d) || bad_stride(q_out_stride, H, d)) return TV_ERR_SHAPE;
+    if (Hkv > 0 && (bad_stride(k_stride, Hkv, d) || bad_stride(k_out_stride, Hkv, d)))
+        return TV_ERR_SHAPE;
+    if (!(eps < 3.0e38f) || eps < -3.0e38f) return TV_ERR_SHAPE;  // NaN and infinities
+    if ((int64_t)H + Hkv > 0x7fffffffLL / 2) return TV_ERR_UNSUPPORTED;
+    if (!dev_status) return TV_ERR_NULL;
+    if (B == 0 || total_rows == 0) return TV_OK;
+    tv_status st = check_ptrs({row_offsets, start, q, q_out, dev_status});
+    if (st == TV_OK && Hkv > 0) st = check_ptrs({k, k_out});
+    if (st == TV_OK && rotary_dim > 0) st = check_ptrs({inv_freq});
+    if (st != TV_OK) return st;
+    if (!aligned16(depth) || !aligned16(q_weight) || !aligned16(k_weight)) return TV_ERR_ALIGN;
+    tv::RopeArgs a{B, total_rows, H, Hkv, d, rotary_dim, layout == TV_ROPE_PAIRS, dtype,
+                   row_offsets, start, depth, q, k, q_weight, k_weight, q_stride, k_stride, eps,
+                   inv_freq, q_out, k_out, q_out_stride, k_out_stride, dev_status};
+    cudaError_t e = tv::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+tv_status tv_logprobs(int32_t R, int32_t num_rows, int32_t vocab, int32_t logits_dtype,
+                      const void *logits, int64_t row_stride, const int32_t *rows,
+                      const int32_t *tokens, float scale, int32_t top_k, float *logprob,
+                      float *entropy, int32_t *top_token, float *top_logprob,
+                      int32_t *dev_status, void *stream) {
+    if (R < 0 || num_rows < 0 || vocab < 1 || row_stride < vocab) return TV_ERR_SHAPE;
+    if (!rows && R > num_rows) return TV_ERR_SHAPE;
+    if (logits_dtype != TV_BF16 && logits_dtype != TV_F32) return TV_ERR_DTYPE;
+    if (!(scale > 0.f) || scale > 3.0e38f) return TV_ERR_SHAPE;  // positive and finite
+    if (top_k < 0 || top_k > vocab) return TV_ERR_SHAPE;
+    if (top_k > TV_LOGPROBS_MAX_TOP) return TV_ERR_UNSUPPORTED;
+    if (!dev_status || !tokens != !logprob) return TV_ERR_NULL;
+    if (R == 0 || (!tokens && !entropy && top_k == 0)) return TV_OK;
+    tv_status st = check_ptrs({dev_status});
+    if (st == TV_OK && num_rows > 0) st = check_ptrs({logits});
+    if (st == TV_OK && top_k > 0) st = check_ptrs({top_token, top_logprob});
+    if (st != TV_OK) return st;
+    if (!aligned16(rows) || !aligned16(tokens) || !aligned16(logprob) || !aligned16(entropy))
+        return TV_ERR_ALIGN;
+    tv::LogprobsArgs a{R, num_rows, vocab, logits_dtype, logits, row_stride, rows, tokens, scale,
+                       top_k, logprob, entropy, top_token, top_logprob, dev_status};
+    cudaError_t e = tv::launch_logprobs(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+}  // extern "C"

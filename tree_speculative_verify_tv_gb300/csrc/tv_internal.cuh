@@ -128,6 +128,68 @@ bool qcache_attention_fits(const QAttnArgs &a);
 size_t qcache_attention_workspace_bytes(const QAttnArgs &a);
 cudaError_t launch_qcache_attention(const QAttnArgs &a, cudaStream_t s);
 
+// Prompts and single tokens through the recurrence (tv_prefill, tv_decode).
+struct PrefillArgs {
+    int32_t B, R, max_rows, H, dk, dv, decay, qkv_dtype, out_f32;
+    const int32_t *offsets;
+    const float *H0;  // null: zeros
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g;
+    int64_t g_stride;
+    void *out;
+    float *H_new;
+    uint8_t *ws;  // may be null
+    size_t ws_bytes;
+    int32_t *status;
+};
+size_t prefill_workspace_bytes(const PrefillArgs &a);
+// Whether the call's work items can be counted in 32 bits.
+bool prefill_fits(const PrefillArgs &a);
+cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s);
+
+struct DecodeArgs {
+    int32_t B, H, dk, dv, decay, qkv_dtype, out_f32;
+    const int32_t *active;  // null: all
+    const float *H0;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g;
+    int64_t g_stride;
+    void *out;
+    float *H_new;
+};
+cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t s);
+
+// Norms and position rotation of queries and keys (tv_qk_norm_rope).
+struct RopeArgs {
+    int32_t B, R, H, Hkv, d, rot, pairs, dtype;
+    const int32_t *offsets, *start, *depth;  // depth may be null
+    const void *q, *k, *q_weight, *k_weight;
+    int64_t q_stride, k_stride;
+    float eps;  // negative: no norm
+    const double *inv_freq;
+    void *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+    int32_t *status;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs &a, cudaStream_t s);
+
+// Log probabilities, entropy and top tokens (tv_logprobs).
+struct LogprobsArgs {
+    int32_t R, N, V, dtype;
+    const void *logits;
+    int64_t stride;
+    const int32_t *rows, *tokens;  // may be null
+    float scale;
+    int32_t top;
+    float *logprob, *entropy;  // may be null
+    int32_t *top_token;
+    float *top_logprob;
+    int32_t *status;
+};
+cudaError_t launch_logprobs(const LogprobsArgs &a, cudaStream_t s);
+
 // Best-first draft-tree construction (tv_build_tree).
 struct BuildArgs {
     int32_t B, C, depth_cap, n;
