@@ -739,6 +739,14 @@ tv_status tv_prefill(int32_t B, int32_t total_rows, int32_t max_rows, int32_t H,
                      void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
+ * Test hook, OR-ed into tv_prefill's out_dtype where the tensor cores take the call: every CTA
+ * leaves the copies of its first chunk out, so that what waits for them gives up (after a
+ * sixty-fourth of the usual limit) and the call takes the timeout path: TV_ERR_TIMEOUT in
+ * dev_status, tensor memory freed, outputs undefined.  For tests of that path.
+ */
+#define TV_PREFILL_TEST_EXPIRE_WAIT 0x100
+
+/*
  * tv_decode -- one token of every request through the recurrence layer: tv_prefill's row for
  * a batch that decodes without drafts.  Row b is request b's.
  *   active   [B] int32 (device), or NULL for all: a request with active[b] == 0 (a padded

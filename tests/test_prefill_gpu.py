@@ -330,3 +330,25 @@ def test_decode_goes_on_from_a_prompt():
         outs.append(decode(s, H, True, H_new=H)[0])
     torch.cuda.synchronize()
     r.check((torch.cat(outs), H, torch.zeros(1)))
+
+
+# ---------------------------------------------------------------- the timeout path
+
+
+def test_expired_waits_are_reported_and_leave_the_gpu_usable():
+    import torch
+    import tree_speculative_verify_tv_gb300 as tv
+    rng = np.random.default_rng(23)
+    r = Rows(rng, [300, 77], 2, 128, 64)
+    want = [x.clone() for x in r.prefill()[:2]]
+    out, H_new = (torch.zeros_like(x) for x in want)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tv.tv_prefill(2, r.R, 300, 2, 128, 64, 0, 0, torch.from_numpy(r.offsets).cuda(), None,
+                  r.dev["q"], r.stride["q"], r.dev["k"], r.stride["k"], r.dev["v"], r.stride["v"],
+                  r.g, r.g_stride, tv.TV_F32 | tv.TV_PREFILL_TEST_EXPIRE_WAIT, out, H_new, None, 0,
+                  status)
+    torch.cuda.synchronize()
+    assert int(status[0]) == tv.TV_ERR_TIMEOUT
+    again = r.prefill()
+    torch.cuda.synchronize()
+    assert int(again[2][0]) == 0 and all(torch.equal(x, y) for x, y in zip(want, again))

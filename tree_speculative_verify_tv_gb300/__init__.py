@@ -39,6 +39,7 @@ from .binding import (  # noqa: F401
     tv_qcache_bytes, tv_qcache_write, tv_qcache_commit, tv_qcache_read, tv_qcache_attention,
     tv_qcache_attention_workspace_bytes, tv_prefill, tv_prefill_workspace_bytes, tv_decode,
     tv_qk_norm_rope, tv_logprobs, TV_ROPE_HALVES, TV_ROPE_PAIRS, TV_LOGPROBS_MAX_TOP,
+    TV_PREFILL_TEST_EXPIRE_WAIT,
     TV_QCACHE_PAGE, TV_QCACHE_GROUP,
     TV_QCACHE_TEST_EXPIRE_WAIT,
     TV_SERIAL_STATIC_BYTES,

@@ -32,6 +32,7 @@ TV_QCACHE_PAGE, TV_QCACHE_GROUP = 64, 32
 TV_QCACHE_TEST_EXPIRE_WAIT = 0x100
 TV_ROPE_HALVES, TV_ROPE_PAIRS = 0, 1
 TV_LOGPROBS_MAX_TOP = 32
+TV_PREFILL_TEST_EXPIRE_WAIT = 0x100
 
 EXPORTED = ("tv_verify", "tv_verify_ex", "tv_verify_variant", "tv_verify_supports",
             "tv_workspace_bytes",

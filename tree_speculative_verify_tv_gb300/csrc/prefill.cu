@@ -148,11 +148,17 @@ cudaError_t launch_rows(const PrefillArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-bool prefill_fits(const PrefillArgs &) { return true; }
+bool prefill_fits(const PrefillArgs &a) {
+    // rows and a chunk behind them, and segments, are counted in 32 bits
+    return a.R <= 0x7fff0000 && a.R / 64LL + a.B <= 0x7fffffffLL;
+}
 
-size_t prefill_workspace_bytes(const PrefillArgs &) { return 0; }
+size_t prefill_workspace_bytes(const PrefillArgs &a) {
+    return a.B > 0 && prefill_tc_supported(a) ? prefill_tc_workspace_bytes(a) : 0;
+}
 
-cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s) {
+cudaError_t launch_prefill(const PrefillArgs &a, bool expire, cudaStream_t s) {
+    if (prefill_tc_supported(a)) return launch_prefill_tc(a, expire, s);
     const bool diag = a.decay == TV_DECAY_DIAG;
     if (a.qkv_dtype == TV_BF16)
         return diag ? launch_rows<__nv_bfloat16, true>(a, s)

@@ -295,6 +295,18 @@ __device__ __forceinline__ void mma_bf16_ts_lead(uint32_t d_tmem, uint32_t a_tme
         : "memory");
 }
 
+// mma_bf16 executed by a converged warp, issued by the lane with `lead`.
+__device__ __forceinline__ void mma_bf16_lead(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+
 // mma_commit by the lane with `lead` of a converged warp.
 __device__ __forceinline__ void mma_commit_lead(uint32_t bar, uint32_t lead) {
     asm volatile(
@@ -461,6 +473,14 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 // The same with B MN-major (B's M/N index contiguous in shared memory).
 __host__ __device__ constexpr uint32_t idesc_bf16_f32_bmn(int M, int N) {
     return idesc_bf16_f32(M, N) | (1u << 16);
+}
+
+// The same with A MN-major too, or alone.
+__host__ __device__ constexpr uint32_t idesc_bf16_f32_amn(int M, int N) {
+    return idesc_bf16_f32(M, N) | (1u << 15);
+}
+__host__ __device__ constexpr uint32_t idesc_bf16_f32_abmn(int M, int N) {
+    return idesc_bf16_f32(M, N) | (1u << 15) | (1u << 16);
 }
 
 }  // namespace ptx

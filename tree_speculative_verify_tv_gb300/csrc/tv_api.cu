@@ -807,6 +807,8 @@ tv_status tv_prefill(int32_t B, int32_t total_rows, int32_t max_rows, int32_t H,
                      void *stream) {
     tv_status st = prefill_dims(B, total_rows, max_rows, H, dk, dv, decay, qkv_dtype);
     if (st != TV_OK) return st;
+    const bool expire = (out_dtype & TV_PREFILL_TEST_EXPIRE_WAIT) != 0;
+    out_dtype &= ~TV_PREFILL_TEST_EXPIRE_WAIT;
     st = recurrence_strides(H, dk, dv, decay, q_stride, k_stride, v_stride, g_stride, out_dtype);
     if (st != TV_OK) return st;
     if (!dev_status) return TV_ERR_NULL;
@@ -820,7 +822,7 @@ tv_status tv_prefill(int32_t B, int32_t total_rows, int32_t max_rows, int32_t H,
                       row_offsets, H0, q, k, v, q_stride, k_stride, v_stride, g, g_stride, out,
                       H_new, static_cast<uint8_t *>(workspace), workspace ? workspace_bytes : 0,
                       dev_status};
-    cudaError_t e = tv::launch_prefill(a, static_cast<cudaStream_t>(stream));
+    cudaError_t e = tv::launch_prefill(a, expire, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 

@@ -146,7 +146,12 @@ struct PrefillArgs {
 size_t prefill_workspace_bytes(const PrefillArgs &a);
 // Whether the call's work items can be counted in 32 bits.
 bool prefill_fits(const PrefillArgs &a);
-cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s);
+// `expire`: the test hook of TV_PREFILL_TEST_EXPIRE_WAIT.
+cudaError_t launch_prefill(const PrefillArgs &a, bool expire, cudaStream_t s);
+// Its tensor-core kernels: bf16, scalar decay, dk and dv 64 or 128.
+bool prefill_tc_supported(const PrefillArgs &a);
+size_t prefill_tc_workspace_bytes(const PrefillArgs &a);
+cudaError_t launch_prefill_tc(const PrefillArgs &a, bool expire, cudaStream_t s);
 
 struct DecodeArgs {
     int32_t B, H, dk, dv, decay, qkv_dtype, out_f32;
