@@ -149,8 +149,7 @@ cudaError_t launch_rows(const PrefillArgs &a, cudaStream_t s) {
 }  // namespace
 
 bool prefill_fits(const PrefillArgs &a) {
-    // rows and a chunk behind them, and segments, are counted in 32 bits
-    return a.R <= 0x7fff0000 && a.R / 64LL + a.B <= 0x7fffffffLL;
+    return a.R <= 0x7fff0000;  // rows, and a chunk behind them, are counted in 32 bits
 }
 
 size_t prefill_workspace_bytes(const PrefillArgs &a) {

@@ -24,31 +24,34 @@
 // around the middle R of the chunk's range, or, where a chunk spans more than 2^120, the
 // exponential of each difference.
 //
-// Roles (28 warps): plan, copies and decays (1), products (1), K~ (4), H (16), outputs (4), P (2).
+// Roles (32 warps): plan and decays (1), copies (1), products (1), K~ (6), H (16), outputs (4),
+// P (3).
 //
 // Few long prompts: the rows of a request are cut into segments.  A first launch computes what
 // each segment adds to a zero state, a second chains these sums, and the segments then run at
 // the same time, each from its own state.
+#include <type_traits>
+
 #include "recurrence.cuh"
 #include "tc_common.cuh"
 
 namespace tv {
 namespace {
 
-using tcc::pack_bf16;
-
 constexpr int kC = 64;        // rows per chunk
 constexpr int kStages = 3;    // chunks of q, k, v in flight
 constexpr int kSlots = 4;     // chunks whose decays are ready
-constexpr int kWarps = 28;
+constexpr int kWarps = 32;
+constexpr int kKeyWarps = 6, kScoreWarps = 3;  // of K~ and of P
 constexpr int kThreadsT = kWarps * 32;
 constexpr int kWaitTries = 1 << 20;  // 7800 cycles each at most: some 4 s
 constexpr uint32_t kSlab = kC * 128; // 64 rows of 64 channels
 
+enum { kA, kB, kW, kE };  // Slot::factor
 enum Flags { kFirst = 1, kLast = 2, kEnd = 4, kMild = 8 };
 
 struct alignas(16) Slot {
-    float a[kC], b[kC], w[kC], e[kC];
+    float factor[4][kC];  // 2^{L - R}, 2^{R - L}, 2^{d - L}, 2^L
     long long L[kC];
     float2 d;             // 2^d as a pair
     int row, cnt, flags, head;
@@ -58,9 +61,9 @@ struct alignas(16) Slot {
 struct TcParams {
     PrefillArgs a;
     int seg;        // rows per segment, a multiple of kC
-    int slots;      // segment slots: R / seg + B
-    float *states;  // [slots][H][dk][dv]
-    float2 *decays; // [slots][H]
+    int pieces;     // segments of a request of max_rows rows
+    float *states;  // [B][pieces][H][dk][dv]: the state before each segment
+    float2 *decays; // [B][pieces][H]
     int expire;     // test hook: leave the first chunk's copies out
 };
 
@@ -79,22 +82,48 @@ struct Lay {
     static_assert(kBytes <= tcc::kSmemLimit - 512, "shared memory");
 };
 
-// x as NP packed pairs of bf16 parts: upper bits cut off, the last part rounded.
+// Two floats in a register pair, for the packed fp32 instructions.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t two(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ void halves(uint64_t x, uint32_t &lo, uint32_t &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// A pair as NP packed pairs of bf16 parts: upper bits cut off, the last part rounded.
 template <int NP>
-__device__ __forceinline__ void split_pair(float x0, float x1, uint32_t (&part)[NP]) {
+__device__ __forceinline__ void split_pair(uint64_t x, uint32_t (&part)[NP]) {
+    uint32_t b0, b1;
 #pragma unroll
     for (int p = 0; p + 1 < NP; ++p) {
-        const uint32_t b0 = __float_as_uint(x0), b1 = __float_as_uint(x1);
+        halves(x, b0, b1);
         part[p] = __byte_perm(b0, b1, 0x7632);
-        asm("{\n\t.reg .b64 x, h, d;\n\t"
-            "mov.b64 x, {%0, %1};\n\t"
-            "mov.b64 h, {%2, %3};\n\t"
-            "sub.rn.f32x2 d, x, h;\n\t"
-            "mov.b64 {%0, %1}, d;\n\t}"
-            : "+f"(x0), "+f"(x1)
-            : "r"(b0 & 0xFFFF0000u), "r"(b1 & 0xFFFF0000u));
+        x = sub2(x, two(b0 & 0xFFFF0000u, b1 & 0xFFFF0000u));
     }
-    const __nv_bfloat162 l = __floats2bfloat162_rn(x0, x1);
+    halves(x, b0, b1);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(__uint_as_float(b0), __uint_as_float(b1));
     part[NP - 1] = *reinterpret_cast<const uint32_t *>(&l);
 }
 
@@ -104,67 +133,26 @@ __device__ __forceinline__ rec::Pair exp2_fixed(long long x) {
     const float f = (float)(int32_t)(x - (n << 32)) * 2.3283064365386963e-10f;
     return rec::exp2_pair((float)(int)max(min(n, 4096LL), -4096LL), f);
 }
+// The same as one float, by the hardware's exponential (2^-22) of the fraction.
 __device__ __forceinline__ float exp2_single(long long x) {
-    const rec::Pair e = exp2_fixed(x);
-    return e.hi + e.lo;
+    const long long n = (x + (1LL << 31)) >> 32;
+    const float f = (float)(int32_t)(x - (n << 32)) * 2.3283064365386963e-10f;
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
+    return e * __int_as_float(((int)max(min(n, 128LL), -127LL) + 127) << 23);
 }
 
-__device__ __forceinline__ int slot_base(const int32_t *offs, int b, int seg) {
-    return max(offs[b], 0) / seg + b;
-}
-
-// The request that segment slot `slot` belongs to, by a whole warp.
-__device__ __forceinline__ int find_request(const int32_t *offs, int B, int slot, int seg) {
-    const int lane = threadIdx.x % 32;
-    int lo = 0, n = B;
-    while (n > 1) {
-        const int step = (n + 31) / 32, at = lane * step;
-        const uint32_t begun =
-            __ballot_sync(0xffffffffu, at < n && slot_base(offs, lo + at, seg) <= slot);
-        const int k = max(__popc(begun) - 1, 0) * step;
-        lo += k;
-        n = min(step, n - k);
-    }
-    return lo;
-}
-
-// A CTA's walk over its chunks.
+// A CTA's walk over its chunks.  An item is a segment of a request and head; a CTA begins with
+// the item of its block index and then takes over items of CTAs that have not been launched, so
+// that long and short ones even out.
 struct Walk {
-    long long item;        // slot * H + head of the next item
-    int row, end, head;    // of the current one; row >= end: none left of it
+    int item;              // (b * pieces + segment) * H + head, without the last segments if !OUT
+    int asked;             // items asked for so far
+    int row, end, head;    // of the current item; row >= end: none left of it
     bool first, done;
-    long long unit, ws;    // b * H + head, and slot * H + head
-    int piece, pieces;
+    long long unit, ws;    // b * H + head, and the segment's place in the workspace
+    int piece, pieces;     // its number, and the request's segments
 };
-
-template <bool OUT>
-__device__ __forceinline__ void next_item(const TcParams &p, Walk &w) {
-    const PrefillArgs &a = p.a;
-    const long long items = (long long)p.slots * a.H;
-    for (;; w.item += gridDim.x) {
-        if (w.item >= items) {
-            w.done = true;
-            return;
-        }
-        const int slot = (int)(w.item / a.H);
-        const int b = find_request(a.offsets, a.B, slot, p.seg);
-        int off, n;
-        if (!request_range(a.offsets, b, a.R, a.max_rows, off, n)) continue;
-        const int i = slot - slot_base(a.offsets, b, p.seg);
-        const int pieces = max(1, (n + p.seg - 1) / p.seg);
-        if (i < 0 || i >= pieces || (!OUT && i == pieces - 1)) continue;
-        w.head = (int)(w.item % a.H);
-        w.row = off + i * p.seg;
-        w.end = w.row + min(p.seg, n - i * p.seg);
-        w.first = true;
-        w.unit = (long long)b * a.H + w.head;
-        w.ws = w.item;
-        w.piece = i;
-        w.pieces = pieces;
-        w.item += gridDim.x;
-        return;
-    }
-}
 
 template <int DK, int DV, int NP, bool OUT>
 __global__ void __launch_bounds__(kThreadsT, 1)
@@ -178,7 +166,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ __align__(8) uint64_t s_gate_full[kSlots], s_gate_free[kSlots], s_full[kStages],
-        s_empty[kStages], s_s_full, s_p_full, s_kt_full, s_h_full, s_kv_done, s_o_full, s_o_free, s_drain;
+        s_empty[kStages], s_s_full, s_p_full, s_kt_full, s_h_full, s_kv_done, s_o_full, s_o_free, s_drain, s_asked;
+    __shared__ __align__(16) uint64_t s_answer[2];
     const PrefillArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     uint8_t *s_base = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
@@ -190,21 +179,23 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         s_abort = 0;
         for (int i = 0; i < kSlots; ++i) {
             ptx::mbar_init(bar(s_gate_full[i]), 1);
-            // readers: products, K~, H and, with outputs, the outputs' and P's warps
-            ptx::mbar_init(bar(s_gate_free[i]), 1 + 4 + 4 * kQuads + (OUT ? kQuads + 2 : 0));
+            // readers: copies, products, K~, H and, with outputs, the outputs' and P's warps
+            ptx::mbar_init(bar(s_gate_free[i]),
+                           2 + kKeyWarps + 4 * kQuads + (OUT ? kQuads + kScoreWarps : 0));
         }
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(bar(s_full[i]), 1);
             ptx::mbar_init(bar(s_empty[i]), 1);
         }
         ptx::mbar_init(bar(s_s_full), 1);
-        ptx::mbar_init(bar(s_p_full), 2);
-        ptx::mbar_init(bar(s_kt_full), 4);
+        ptx::mbar_init(bar(s_p_full), kScoreWarps);
+        ptx::mbar_init(bar(s_kt_full), kKeyWarps);
         ptx::mbar_init(bar(s_h_full), 4 * kQuads);
         ptx::mbar_init(bar(s_kv_done), 1);
         ptx::mbar_init(bar(s_o_full), 1);
         ptx::mbar_init(bar(s_o_free), kQuads);
         ptx::mbar_init(bar(s_drain), 1);
+        ptx::mbar_init(bar(s_asked), 1);
         ptx::fence_mbar_init();
         if (OUT) ptx::prefetch_tensormap(&map_q);
         ptx::prefetch_tensormap(&map_k);
@@ -243,14 +234,54 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 
     if (warp == 0) {
         // ---- plan, copies, decays
-        for (long long b = (long long)blockIdx.x * 32 + lane; b < a.B; b += gridDim.x * 32LL) {
-            int off, n;
-            if (!request_range(a.offsets, (int)b, a.R, a.max_rows, off, n))
-                report(a.status, TV_ERR_TREE);
-        }
         Walk w{};
-        w.item = blockIdx.x;
-        next_item<OUT>(p, w);
+        const int per = OUT ? p.pieces : p.pieces - 1;
+        const auto ask = [&]() {
+            if (lane == 0) {
+                ptx::fence_proxy_async_smem();  // (the answer before has been read)
+                ptx::mbar_arrive_expect_tx(bar(s_asked), 16);
+                ptx::try_cancel(ptx::smem_addr(s_answer), bar(s_asked));
+            }
+            __syncwarp();
+            ++w.asked;
+        };
+        const auto next_item = [&](bool begin) {
+            for (;; begin = false) {
+                if (begin) {
+                    w.item = blockIdx.x;
+                } else {
+                    if (!wait(s_asked, (w.asked - 1) & 1)) {
+                        w.done = true;
+                        return;
+                    }
+                    w.item = ptx::cancelled_cta(ptx::smem_addr(s_answer));
+                    __syncwarp();
+                    if (w.item < 0) {
+                        w.done = true;
+                        return;
+                    }
+                }
+                ask();
+                const int slot = w.item / a.H, b = slot / per, i = slot - b * per;
+                int off, n;
+                if (!request_range(a.offsets, b, a.R, a.max_rows, off, n)) {
+                    if (lane == 0) report(a.status, TV_ERR_TREE);
+                    continue;
+                }
+                const int pieces = max(1, (n + p.seg - 1) / p.seg);
+                if (i >= pieces || (!OUT && i == pieces - 1)) continue;
+                w.head = w.item - slot * a.H;
+                w.row = off + i * p.seg;
+                w.end = w.row + min(p.seg, n - i * p.seg);
+                w.first = true;
+                w.unit = (long long)b * a.H + w.head;
+                w.ws = ((long long)b * p.pieces + i) * a.H + w.head;
+                w.piece = i;
+                w.pieces = pieces;
+                return;
+            }
+        };
+        next_item(true);
         float g0 = 0.f, g1 = 0.f;
         const auto fetch = [&](const Walk &at) {  // the decays of the chunk at w
             const int t = at.row + 2 * lane, cnt = at.done ? 0 : min(kC, at.end - at.row);
@@ -261,8 +292,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         fetch(w);
         long long total = 0;  // log2 of the item's decay so far
         bool total_nan = false;
-        int n = 0, issued = 0;
-        for (;; ++n) {
+        for (int n = 0;; ++n) {
             Slot *s = slots + n % kSlots;
             if (n >= kSlots && !wait(s_gate_free[n % kSlots], ((n / kSlots) & 1) ^ 1)) break;
             if (w.done) {
@@ -270,29 +300,17 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 arrive(s_gate_full[n % kSlots]);
                 break;
             }
-            // a stage is free once every product of the chunk before in it is done
-            if (n >= kStages && !wait(s_empty[n % kStages], ((n / kStages) & 1) ^ 1)) break;
-            if (p.expire) break;
-            if (lane == 0) {
-                const uint32_t at = base + n % kStages * L::kStage, full = bar(s_full[n % kStages]);
-                ptx::mbar_arrive_expect_tx(full, OUT ? L::kStage : L::kStage - L::kK);
-                for (int c = 0; c < DK / 64; ++c) {
-                    if (OUT)
-                        ptx::tma_load_3d(at + L::kQ + c * kSlab, &map_q, c * 64, w.head, w.row, full);
-                    ptx::tma_load_3d(at + L::kK + c * kSlab, &map_k, c * 64, w.head, w.row, full);
-                }
-                for (int c = 0; c < DV / 64; ++c)
-                    ptx::tma_load_3d(at + L::kV + c * kSlab, &map_v, c * 64, w.head, w.row, full);
+            if (p.expire) {
+                wait(s_asked, (w.asked - 1) & 1);
+                break;
             }
-            __syncwarp();
-            issued = n + 1;
             const int row = w.row, cnt = min(kC, w.end - row), head = w.head;
             const bool first = w.first, last = row + kC >= w.end;
             const Walk now = w;
             const float x0 = g0, x1 = g1;
             w.first = false;
             w.row += kC;
-            if (last) next_item<OUT>(p, w);
+            if (last) next_item(false);
             fetch(w);  // the next chunk's, on its way while this one's are summed
 
             const float most = 2839.f;  // 4096 log2 units
@@ -319,22 +337,28 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             const uint32_t upto = 0xffffffffu >> (31 - lane);
             const bool n0 = (bad0 & upto) || (bad1 & (upto >> 1)), n1 = ((bad0 | bad1) & upto) != 0;
             const float nanf = __int_as_float(0x7fffffff);
-            float2 av = make_float2(1.f, 1.f), bv = av;
-            if (mild) {
-                av = make_float2(exp2_single(l0 - mid), exp2_single(l1 - mid));
-                bv = make_float2(exp2_single(mid - l0), exp2_single(mid - l1));
-            } else {
+            if (!mild) {
                 s->L[2 * lane] = l0;
                 s->L[2 * lane + 1] = l1;
             }
-            float2 ev = make_float2(exp2_single(l0), exp2_single(l1));
-            if (n0) av.x = ev.x = nanf;
-            if (n1) av.y = ev.y = nanf;
-            *reinterpret_cast<float2 *>(s->a + 2 * lane) = av;
-            *reinterpret_cast<float2 *>(s->b + 2 * lane) = bv;
-            *reinterpret_cast<float2 *>(s->e + 2 * lane) = ev;
-            *reinterpret_cast<float2 *>(s->w + 2 * lane) =
-                make_float2(exp2_single(end - l0), exp2_single(end - l1));
+            // a, b, w, e: 2^{L - R}, 2^{R - L}, 2^{d - L}, 2^L (a and b are 1 where R will not do)
+            const long long zero = mild ? mid : 0;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                const long long from = c == 3 ? 0 : c == 2 ? end : zero;
+                long long z0 = l0 - from, z1 = l1 - from;
+                if (c == 1 || c == 2) {
+                    z0 = -z0;
+                    z1 = -z1;
+                }
+                if (c < 2 && !mild) z0 = z1 = 0;
+                float2 f = make_float2(exp2_single(z0), exp2_single(z1));
+                if (c == 0 || c == 3) {
+                    if (n0) f.x = nanf;
+                    if (n1) f.y = nanf;
+                }
+                *reinterpret_cast<float2 *>(s->factor[c] + 2 * lane) = f;
+            }
             if (first) {
                 total = 0;
                 total_nan = false;
@@ -363,6 +387,30 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             }
             arrive(s_gate_full[n % kSlots]);
         }
+    } else if (warp == 2) {
+        // ---- copies
+        int issued = 0;
+        for (int n = 0;; ++n) {
+            Slot *s;
+            if (!gate(n, s)) break;
+            if (s->flags & kEnd) break;
+            // a stage is free once every product of the chunk before in it is done
+            if (n >= kStages && !wait(s_empty[n % kStages], ((n / kStages) & 1) ^ 1)) break;
+            if (lane == 0) {
+                const int head = s->head, row = s->row;
+                const uint32_t at = base + n % kStages * L::kStage, full = bar(s_full[n % kStages]);
+                ptx::mbar_arrive_expect_tx(full, OUT ? L::kStage : L::kStage - L::kK);
+                for (int c = 0; c < DK / 64; ++c) {
+                    if (OUT)
+                        ptx::tma_load_3d(at + L::kQ + c * kSlab, &map_q, c * 64, head, row, full);
+                    ptx::tma_load_3d(at + L::kK + c * kSlab, &map_k, c * 64, head, row, full);
+                }
+                for (int c = 0; c < DV / 64; ++c)
+                    ptx::tma_load_3d(at + L::kV + c * kSlab, &map_v, c * 64, head, row, full);
+            }
+            issued = n + 1;
+            arrive(s_gate_free[n % kSlots]);
+        }
         // copies that nobody waited for (after a timeout)
         if (*(volatile int *)&s_abort)
             for (int i = max(0, issued - kStages); i < issued; ++i)
@@ -371,69 +419,79 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         // ---- products
         const uint32_t lead = ptx::elect_one();
         const auto stage = [&](int n) { return base + n % kStages * L::kStage; };
+        // descriptors move by their address field, in units of 16 bytes
         const auto scores = [&](int n) {
-            const uint32_t q = stage(n) + L::kQ, k = stage(n) + L::kK;
+            // 128 lanes take the 64 rows behind the tile along; nobody reads their results
+            const uint64_t q = ptx::desc_kmajor_sw128(stage(n) + L::kQ, 1024),
+                           k = ptx::desc_kmajor_sw128(stage(n) + L::kK, 1024);
 #pragma unroll
             for (int kk = 0; kk < DK / 16; ++kk) {
-                const uint32_t o = kk / 4 * kSlab + kk % 4 * 32;
-                // 128 lanes take the 64 rows behind the tile along; nobody reads their results
-                ptx::mma_bf16_lead(tmem + L::tS, ptx::desc_kmajor_sw128(q + o, 1024),
-                                   ptx::desc_kmajor_sw128(k + o, 1024),
-                                   ptx::idesc_bf16_f32(128, kC), kk > 0, lead);
+                const uint32_t o = (kk / 4 * kSlab + kk % 4 * 32) / 16;
+                ptx::mma_bf16_lead(tmem + L::tS, q + o, k + o, ptx::idesc_bf16_f32(128, kC), kk > 0,
+                                   lead);
             }
             ptx::mma_commit_lead(bar(s_s_full), lead);
         };
-        Slot *s;
-        bool ok = gate(0, s);
-        if (ok && OUT && !(s->flags & kEnd)) {
+        // (the flags by a reduction, so that the flow is known to be the whole warp's and the
+        // products' operands stay in uniform registers)
+        const auto more = [&](int n) {
+            Slot *s;
+            return gate(n, s) && !(__reduce_or_sync(0xffffffffu, s->flags) & kEnd);
+        };
+        bool ok = more(0);
+        if (ok && OUT) {
             ok = wait(s_full[0], 0);
             ptx::tc_fence_after_sync();
             if (ok) scores(0);
         }
-        for (int n = 0; ok && !(s->flags & kEnd); ++n) {
+        for (int n = 0; ok; ++n) {
             const uint32_t ph = n & 1, q = stage(n) + L::kQ, v = stage(n) + L::kV;
             if (!OUT && !(ok = wait(s_full[n % kStages], (n / kStages) & 1))) break;
             if (OUT && n > 0 && !(ok = wait(s_o_free, ph ^ 1))) break;
             if (!(ok = wait(s_h_full, ph))) break;
             ptx::tc_fence_after_sync();
+            const uint64_t vd = ptx::desc_mnmajor_sw128(v, kSlab, 1024);
             if (OUT) {
-#pragma unroll
+                const uint64_t qd = ptx::desc_kmajor_sw128(q, 1024);
+#pragma unroll 1
                 for (int part = NP - 1; part >= 0; --part)
 #pragma unroll
                     for (int kk = 0; kk < DK / 16; ++kk)
                         ptx::mma_bf16_ts_lead(
                             tmem + L::tO2, tmem + L::tH + part * (DK / 2) + kk * 8,
-                            ptx::desc_kmajor_sw128(q + kk / 4 * kSlab + kk % 4 * 32, 1024),
+                            qd + (kk / 4 * kSlab + kk % 4 * 32) / 16,
                             ptx::idesc_bf16_f32(128, kC), part < NP - 1 || kk > 0, lead);
             }
             if (!(ok = wait(s_kt_full, ph))) break;
             ptx::tc_fence_after_sync();
-#pragma unroll
-            for (int part = 2; part >= 0; --part)
+#pragma unroll 1
+            for (int part = 2; part >= 0; --part) {
+                const uint64_t kd =
+                    ptx::desc_mnmajor_sw128(base + L::kKt + part * L::kKtPart, kSlab, 1024);
 #pragma unroll
                 for (int kk = 0; kk < kC / 16; ++kk)
-                    ptx::mma_bf16_lead(
-                        tmem + L::tD, ptx::desc_mnmajor_sw128(v + kk * 2048, kSlab, 1024),
-                        ptx::desc_mnmajor_sw128(base + L::kKt + part * L::kKtPart + kk * 2048, kSlab,
-                                                1024),
-                        ptx::idesc_bf16_f32_abmn(128, DK), part < 2 || kk > 0, lead);
+                    ptx::mma_bf16_lead(tmem + L::tD, vd + kk * 128, kd + kk * 128,
+                                       ptx::idesc_bf16_f32_abmn(128, DK), part < 2 || kk > 0, lead);
+            }
             ptx::mma_commit_lead(bar(s_kv_done), lead);
             if (OUT) {
                 if (!(ok = wait(s_p_full, ph))) break;
                 ptx::tc_fence_after_sync();
-#pragma unroll
-                for (int part = NP - 1; part >= 0; --part)
+#pragma unroll 1
+                for (int part = NP - 1; part >= 0; --part) {
+                    const uint64_t pd =
+                        ptx::desc_kmajor_sw128(base + L::kP + part * L::kPPart, 1024);
 #pragma unroll
                     for (int kk = 0; kk < kC / 16; ++kk)
-                        ptx::mma_bf16_lead(
-                            tmem + L::tO1, ptx::desc_mnmajor_sw128(v + kk * 2048, kSlab, 1024),
-                            ptx::desc_kmajor_sw128(base + L::kP + part * L::kPPart + kk * 32, 1024),
-                            ptx::idesc_bf16_f32_amn(128, kC), part < NP - 1 || kk > 0, lead);
+                        ptx::mma_bf16_lead(tmem + L::tO1, vd + kk * 128, pd + kk * 2,
+                                           ptx::idesc_bf16_f32_amn(128, kC), part < NP - 1 || kk > 0,
+                                           lead);
+                }
                 ptx::mma_commit_lead(bar(s_o_full), lead);
             }
             ptx::mma_commit_lead(bar(s_empty[n % kStages]), lead);
             arrive(s_gate_free[n % kSlots]);
-            if (!(ok = gate(n + 1, s)) || (s->flags & kEnd)) break;
+            if (!(ok = more(n + 1))) break;
             if (OUT) {
                 // (P of chunk n has been written, so its scores have been read)
                 if (!(ok = wait(s_full[(n + 1) % kStages], ((n + 1) / kStages) & 1))) break;
@@ -444,9 +502,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         ptx::mma_commit_lead(bar(s_drain), lead);
         __syncwarp();
         ptx::mbar_wait_tries(bar(s_drain), 0, 1 << 18);
-    } else if (warp < 4 || warp >= 26) {
+    } else if (warp == 3 || (warp >= 26 && warp != 29)) {
         // ---- K~: keys times 2^{d - L}, in three parts, laid out as the keys are
-        const int t = (warp < 4 ? warp - 2 : warp - 24) * 32 + lane;
+        const int t = (warp == 3 ? 0 : warp < 29 ? warp - 25 : warp - 26) * 32 + lane;
         for (int n = 0;; ++n) {
             Slot *s;
             if (!gate(n, s)) break;
@@ -456,27 +514,27 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             uint8_t *st = s_base + n % kStages * L::kStage;
             const int cnt = s->cnt;
             if (cnt < kC) {  // rows past the segment belong to others: they may hold anything
-                for (int i = t; i < (kC - cnt) * (DV / 8); i += 128) {
+                for (int i = t; i < (kC - cnt) * (DV / 8); i += kKeyWarps * 32) {
                     const int r = cnt + i / (DV / 8), c = i % (DV / 8);
                     *reinterpret_cast<uint4 *>(st + L::kV + c / 8 * kSlab + r * 128 + c % 8 * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
             }
 #pragma unroll 2
-            for (int i = 0; i < DK / 16; ++i) {
-                const uint32_t at = (t + i * 128) * 16;
+            for (int at = t * 16; at < DK * 128; at += kKeyWarps * 32 * 16) {
                 const int r = at / 128 % kC;
-                const uint4 x = *reinterpret_cast<const uint4 *>(st + L::kK + at);
-                const float w = s->w[r];
+                uint4 x = *reinterpret_cast<const uint4 *>(st + L::kK + at);
+                if (r >= cnt) x = make_uint4(0, 0, 0, 0);
+                const float w = s->factor[kW][r];
+                const uint64_t w2 = two(w, w);
                 const uint32_t in[4] = {x.x, x.y, x.z, x.w};
                 uint32_t out[3][4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t part[3];
-                    split_pair<3>(__uint_as_float(in[e] << 16) * w,
-                                  __uint_as_float(in[e] & 0xFFFF0000u) * w, part);
+                    split_pair<3>(mul2(two(in[e] << 16, in[e] & 0xFFFF0000u), w2), part);
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) out[j][e] = r < cnt ? part[j] : 0;
+                    for (int j = 0; j < 3; ++j) out[j][e] = part[j];
                 }
 #pragma unroll
                 for (int j = 0; j < 3; ++j)
@@ -492,7 +550,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const int quad = warp % 4, c0 = (warp - 4) / 4 * kChan, col = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)quad << 21);  // lane quad * 32
         if (quad < kQuads) {
-            float h[kChan];
+            uint64_t h[kChan / 2];
             for (int n = 0;; ++n) {
                 Slot *s;
                 if (!gate(n, s)) break;
@@ -505,49 +563,56 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                                         : a.H0     ? a.H0 + (size_t)src * DK * DV
                                                    : nullptr;
 #pragma unroll
-                    for (int i = 0; i < kChan; ++i)
-                        h[i] = from ? from[(c0 + i) * DV + col] : 0.f;
+                    for (int i = 0; i < kChan / 2; ++i)
+                        h[i] = from ? two(from[(c0 + 2 * i) * DV + col],
+                                          from[(c0 + 2 * i + 1) * DV + col])
+                                    : 0;
                 }
                 if (OUT) {
-                    uint32_t part[NP][kChan / 2];
 #pragma unroll
-                    for (int i = 0; i < kChan / 2; ++i) {
-                        uint32_t x[NP];
-                        split_pair<NP>(h[2 * i], h[2 * i + 1], x);
+                    for (int i0 = 0; i0 < kChan / 2; i0 += 8) {
+                        uint32_t part[NP][8];
 #pragma unroll
-                        for (int j = 0; j < NP; ++j) part[j][i] = x[j];
-                    }
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t x[NP];
+                            split_pair<NP>(h[i0 + i], x);
 #pragma unroll
-                    for (int j = 0; j < NP; ++j) {
-                        const uint32_t to = lanes + L::tH + j * (DK / 2) + c0 / 2;
-                        if constexpr (kChan == 32)
-                            ptx::tmem_st_x16(to, part[j]);
-                        else
-                            ptx::tmem_st_x8(to, part[j]);
+                            for (int j = 0; j < NP; ++j) part[j][i] = x[j];
+                        }
+#pragma unroll
+                        for (int j = 0; j < NP; ++j)
+                            ptx::tmem_st_x8(lanes + L::tH + j * (DK / 2) + c0 / 2 + i0, part[j]);
                     }
                     ptx::tmem_wait_st();
                 }
                 ptx::tc_fence_before_sync();
                 arrive(s_h_full);
-                const float2 d = s->d;
+                const uint64_t dx = two(s->d.x, s->d.x), dy = two(s->d.y, s->d.y);
                 const long long dst = s->dst;
                 arrive(s_gate_free[n % kSlots]);
                 if (!wait(s_kv_done, n & 1)) break;
                 ptx::tc_fence_after_sync();
-                uint32_t x[kChan];
-                if constexpr (kChan == 32)
-                    ptx::tmem_ld_x32_nowait(lanes + L::tD + c0, x);
-                else
-                    ptx::tmem_ld_x16_nowait(lanes + L::tD + c0, x);
-                ptx::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < kChan; ++i)
-                    h[i] = fmaf(h[i], d.x, fmaf(h[i], d.y, __uint_as_float(x[i])));
+                for (int i0 = 0; i0 < kChan; i0 += 16) {
+                    uint32_t x[16];
+                    ptx::tmem_ld_x16_nowait(lanes + L::tD + c0 + i0, x);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint64_t &y = h[i0 / 2 + i];
+                        y = fma2(y, dx, fma2(y, dy, two(x[2 * i], x[2 * i + 1])));
+                    }
+                }
                 if ((flags & kLast) && (!OUT || dst >= 0)) {
                     float *to = dst < 0 ? p.states + (size_t)~dst * DK * DV
                                         : a.H_new + (size_t)dst * DK * DV;
 #pragma unroll
-                    for (int i = 0; i < kChan; ++i) to[(c0 + i) * DV + col] = h[i];
+                    for (int i = 0; i < kChan / 2; ++i) {
+                        uint32_t x, y;
+                        halves(h[i], x, y);
+                        to[(c0 + 2 * i) * DV + col] = __uint_as_float(x);
+                        to[(c0 + 2 * i + 1) * DV + col] = __uint_as_float(y);
+                    }
                 }
             }
         }
@@ -561,11 +626,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 if (!gate(n, s)) break;
                 if (s->flags & kEnd) break;
                 const int cnt = s->cnt;
-                const size_t at = ((size_t)s->row * a.H + s->head) * DV + col,
-                             step = (size_t)a.H * DV;
+                using O = std::conditional_t<NP == 3, float, __nv_bfloat16>;
+                const size_t step = (size_t)a.H * DV;
+                O *to = static_cast<O *>(a.out) + s->row * step + s->head * DV + col;
                 if (!wait(s_o_full, n & 1)) break;
                 ptx::tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                 for (int t0 = 0; t0 < kC; t0 += 16) {
                     uint32_t x[16], y[16];
                     ptx::tmem_ld_x16_nowait(lanes + L::tO1 + t0, x);
@@ -575,22 +641,37 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                         ptx::tc_fence_before_sync();
                         arrive(s_o_free);
                     }
+                    const float4 *e4 = reinterpret_cast<const float4 *>(s->factor[kE] + t0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float o = fmaf(s->e[t0 + i], __uint_as_float(y[i]),
-                                             __uint_as_float(x[i]));
-                        if (t0 + i < cnt)
-                            rec::store_out(a.out, NP == 3, at + (t0 + i) * step, o);
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = e4[i];
+                        uint32_t o[4];
+                        halves(fma2(two(f.x, f.y), two(y[4 * i], y[4 * i + 1]),
+                                    two(x[4 * i], x[4 * i + 1])), o[0], o[1]);
+                        halves(fma2(two(f.z, f.w), two(y[4 * i + 2], y[4 * i + 3]),
+                                    two(x[4 * i + 2], x[4 * i + 3])), o[2], o[3]);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if (t0 + 4 * i + u < cnt) *to = O(__uint_as_float(o[u]));
+                            to += step;
+                        }
                     }
                 }
                 arrive(s_gate_free[n % kSlots]);
             }
         }
     } else {
-        // ---- P (warps 24 and 25): lane = row of the chunk
+        // ---- P: lane = row of the chunk; two blocks of 16 columns each for warp 24 (rows 0-31,
+        // which reach no further), 25 and 29 (rows 32-63)
         if (OUT) {
-            const int quad = warp % 4, i = quad * 32 + lane;
+            const int quad = warp % 4, i = quad * 32 + lane, from = warp == 29 ? 2 : 0;
             const uint32_t lanes = tmem + ((uint32_t)quad << 21);
+            uint8_t *row = s_base + L::kP + i * 128;
+            if (warp == 24)  // zero once and for all: columns past the rows
+                for (int c = 4; c < 8; ++c)
+                    for (int j = 0; j < NP; ++j)
+                        *reinterpret_cast<uint4 *>(row + j * L::kPPart + ((c ^ (i & 7)) * 16)) =
+                            make_uint4(0, 0, 0, 0);
             for (int n = 0;; ++n) {
                 Slot *s;
                 if (!gate(n, s)) break;
@@ -599,47 +680,49 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 if (!wait(s_s_full, n & 1)) break;
                 if (n > 0 && !wait(s_o_full, (n & 1) ^ 1)) break;  // P of the chunk before is read
                 ptx::tc_fence_after_sync();
-                const float ai = s->a[i];
-                uint8_t *row = s_base + L::kP + i * 128;
+                const float ai = s->factor[kA][i];
+                const uint64_t a2 = two(ai, ai);
+#pragma unroll 1
+                for (int jb = from; jb < from + 2; ++jb) {
+                    uint32_t x[16];
+                    uint64_t f[8];
+                    ptx::tmem_ld_x16_nowait(lanes + L::tS + jb * 16, x);
+                    if (flags & kMild) {
+                        const float4 *b4 = reinterpret_cast<const float4 *>(s->factor[kB] + jb * 16);
 #pragma unroll
-                for (int j0 = 0; j0 < kC; j0 += 16) {
-                    if (j0 < quad * 32 + 32) {  // (the same for a whole warp)
-                        uint32_t x[16];
-                        ptx::tmem_ld_x16_nowait(lanes + L::tS + j0, x);
-                        ptx::tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t out[NP][4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float y[2];
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const int k = c * 8 + e * 2 + u, j = j0 + k;
-                                    const float f = (flags & kMild)
-                                                        ? ai * s->b[j]
-                                                        : ai * exp2_single(s->L[i] - s->L[j]);
-                                    y[u] = j <= i ? __uint_as_float(x[k]) * f : 0.f;
-                                }
-                                uint32_t part[NP];
-                                split_pair<NP>(y[0], y[1], part);
-#pragma unroll
-                                for (int j = 0; j < NP; ++j) out[j][e] = part[j];
-                            }
-#pragma unroll
-                            for (int j = 0; j < NP; ++j)
-                                *reinterpret_cast<uint4 *>(row + j * L::kPPart +
-                                                           (((j0 / 8 + c) ^ (i & 7)) * 16)) =
-                                    make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]);
+                        for (int u = 0; u < 4; ++u) {
+                            const float4 b = b4[u];
+                            f[2 * u] = mul2(a2, two(b.x, b.y));
+                            f[2 * u + 1] = mul2(a2, two(b.z, b.w));
                         }
                     } else {
+                        // decays that span too much for factors around a middle (rare)
+                        const long long Li = s->L[i];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                        for (int u = 0; u < 8; ++u) {
+                            const int j = jb * 16 + 2 * u;
+                            f[u] = mul2(a2, two(exp2_single(Li - s->L[j]),
+                                                exp2_single(Li - s->L[j + 1])));
+                        }
+                    }
+                    ptx::tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < NP; ++j)
-                                *reinterpret_cast<uint4 *>(row + j * L::kPPart +
-                                                           (((j0 / 8 + c) ^ (i & 7)) * 16)) =
-                                    make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t out[NP][4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int u = 4 * c + e, j = jb * 16 + 2 * u;
+                            uint32_t y0, y1, part[NP];
+                            halves(mul2(two(x[2 * u], x[2 * u + 1]), f[u]), y0, y1);
+                            split_pair<NP>(two(j <= i ? y0 : 0u, j < i ? y1 : 0u), part);
+#pragma unroll
+                            for (int q = 0; q < NP; ++q) out[q][e] = part[q];
+                        }
+                        uint8_t *at = row + (((jb * 2 + c) ^ (i & 7)) * 16);
+#pragma unroll
+                        for (int q = 0; q < NP; ++q)
+                            *reinterpret_cast<uint4 *>(at + q * L::kPPart) =
+                                make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
                     }
                 }
                 ptx::tc_fence_before_sync();
@@ -670,7 +753,7 @@ __global__ void __launch_bounds__(kThreadsChain) prefill_chain_kernel(TcParams p
     if (at >= quads || !request_range(a.offsets, b, a.R, a.max_rows, off, n)) return;
     const int pieces = (n + p.seg - 1) / p.seg;
     if (pieces < 2) return;
-    const size_t first = (size_t)slot_base(a.offsets, b, p.seg) * a.H + h;
+    const size_t first = (size_t)b * p.pieces * a.H + h;
     float4 *state = reinterpret_cast<float4 *>(p.states) + first * quads + at;
     const float2 *decay = p.decays + first;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -699,6 +782,7 @@ int best_pieces(const PrefillArgs &a) {
     const auto waves = [&](long long items) { return (double)((items + sms - 1) / sms); };
     int best = 1;
     double least = waves(units) * (chunks + 4.0);
+    if (units > 8 * sms) return 1;
     for (int s = 2; s <= 64 && s <= chunks; ++s) {
         const double per = (double)((chunks + s - 1) / s);
         const double cost = waves(units * s) * (per + 4.0) + waves(units * (s - 1)) * (0.6 * per + 4.0) + 8.0;
@@ -715,8 +799,8 @@ int segment_rows(const PrefillArgs &a, int pieces) {
     return (int)std::min<long long>((chunks + pieces - 1) / pieces * kC, 0x40000000);
 }
 
-size_t cut_bytes(const PrefillArgs &a, int seg) {
-    const size_t items = ((size_t)a.R / seg + a.B) * a.H;
+size_t cut_bytes(const PrefillArgs &a, int pieces) {
+    const size_t items = (size_t)a.B * pieces * a.H;
     return items * a.dk * a.dv * 4 + (items * 8 + 15) / 16 * 16;
 }
 
@@ -735,9 +819,8 @@ template <int DK, int DV, int NP, bool OUT>
 cudaError_t launch_kernel(const TcParams &p, const CUtensorMap *m, cudaStream_t s) {
     const cudaError_t e = configure_smem_once(prefill_tc_kernel<DK, DV, NP, OUT>, false);
     if (e != cudaSuccess) return e;
-    const long long items = (long long)p.slots * p.a.H;
-    const unsigned grid = (unsigned)std::min<long long>(items, device_sms());
-    return launch_pdl(prefill_tc_kernel<DK, DV, NP, OUT>, dim3(grid), dim3(kThreadsT),
+    const unsigned items = (unsigned)p.a.B * (OUT ? p.pieces : p.pieces - 1) * p.a.H;
+    return launch_pdl(prefill_tc_kernel<DK, DV, NP, OUT>, dim3(items), dim3(kThreadsT),
                       Lay<DK, DV, NP>::kBytes, s, m[0], m[1], m[2], p);
 }
 
@@ -752,12 +835,12 @@ cudaError_t launch_widths(const PrefillArgs &a, bool expire, cudaStream_t s) {
     p.a = a;
     p.expire = expire;
     int pieces = best_pieces(a);
-    while (pieces > 1 && cut_bytes(a, segment_rows(a, pieces)) > a.ws_bytes) --pieces;
+    while (pieces > 1 && cut_bytes(a, pieces) > a.ws_bytes) --pieces;
     p.seg = segment_rows(a, pieces);
-    p.slots = a.R / p.seg + a.B;
+    p.pieces = pieces;
     if (pieces > 1) {
         p.states = reinterpret_cast<float *>(a.ws);
-        p.decays = reinterpret_cast<float2 *>(a.ws + (size_t)p.slots * a.H * DK * DV * 4);
+        p.decays = reinterpret_cast<float2 *>(a.ws + (size_t)a.B * pieces * a.H * DK * DV * 4);
         cudaError_t e = launch_kernel<DK, DV, 2, false>(p, m, s);
         if (e != cudaSuccess) return e;
         e = launch_pdl(prefill_chain_kernel,
@@ -780,7 +863,7 @@ bool prefill_tc_supported(const PrefillArgs &a) {
 
 size_t prefill_tc_workspace_bytes(const PrefillArgs &a) {
     const int pieces = best_pieces(a);
-    return pieces > 1 ? cut_bytes(a, segment_rows(a, pieces)) : 0;
+    return pieces > 1 ? cut_bytes(a, pieces) : 0;
 }
 
 cudaError_t launch_prefill_tc(const PrefillArgs &a, bool expire, cudaStream_t s) {

@@ -218,6 +218,34 @@ __device__ __forceinline__ void grid_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- cluster launch control
+
+// Ask for a CTA of this grid that has not been launched, to do its work here: 16 bytes at
+// `dst` (16-byte aligned), completing on `bar` as bytes of a copy.  Not asked again once an
+// answer was that there is none.
+__device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+        " [%0], [%1];"
+        ::"r"(dst), "r"(bar)
+        : "memory");
+}
+
+// The answer's blockIdx.x, or -1.
+__device__ __forceinline__ int cancelled_cta(uint32_t src) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "mov.b32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n\t}"
+        : "=r"(x)
+        : "r"(src)
+        : "memory");
+    return x;
+}
+
 // ---------------------------------------------------------------- tcgen05
 
 // Warp-wide: allocate `ncols` (power of two >= 32) TMEM columns; base address -> [dst].
