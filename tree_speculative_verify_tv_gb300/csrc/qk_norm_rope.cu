@@ -13,13 +13,16 @@
 // so f is held as a 64-bit fraction and the product is taken modulo 2^64: exact, whatever the
 // position.  The nearest quarter turn is taken off before the rest (at most 1/8 turn) becomes
 // a float.
+#include <algorithm>
+
 #include "tv_internal.cuh"
 
 namespace tv {
 namespace {
 
 constexpr int kThreadsR = 256;
-constexpr int kUnroll = 4;  // heads whose loads are in flight together
+constexpr int kUnroll = 4;   // heads whose loads are in flight together
+constexpr int kPerSm = 4;    // CTAs that registers leave room for
 
 template <typename E>
 struct Quad;
@@ -48,12 +51,16 @@ struct Quad<float> {
     __device__ void set(const float (&x)[4]) { w = make_float4(x[0], x[1], x[2], x[3]); }
 };
 
-// cos and sin of 2 pi position f.
-__device__ __forceinline__ void turn(long long position, double inv_freq, float &c, float &s) {
-    double f = inv_freq * 0.15915494309189533577;  // turns per position
+// Turns per position as a 64-bit fraction.
+__device__ __forceinline__ uint64_t turns(double inv_freq) {
+    double f = inv_freq * 0.15915494309189533577;  // 1 / 2 pi
     f -= floor(f);
-    const uint64_t part = (uint64_t)(f * 18446744073709551616.0);
-    const uint64_t t = (uint64_t)position * part;
+    return (uint64_t)(f * 18446744073709551616.0);
+}
+
+// cos and sin of 2 pi position f.
+__device__ __forceinline__ void turn(long long position, uint64_t f, float &c, float &s) {
+    const uint64_t t = (uint64_t)position * f;
     const uint64_t quarter = (t + (1ull << 61)) >> 62;
     const int32_t rest = (int32_t)(int64_t)((t - (quarter << 62)) >> 32);  // in 2^-32 turns
     float s0, c0;
@@ -65,143 +72,177 @@ __device__ __forceinline__ void turn(long long position, double inv_freq, float 
     if ((quarter + 1) & 2) c = -c;
 }
 
-// Request of row `row`: the last one that begins at or before it.
+// Request of row `row`: the last one that begins at or before it, by a whole warp: a round of
+// loads leaves a 32nd of the requests.
 __device__ __forceinline__ int request_of(const int32_t *offs, int B, int row) {
+    const int lane = threadIdx.x % 32;
     int lo = 0, n = B;
     while (n > 1) {
-        const int half = n / 2;
-        if (offs[lo + half] <= row) {
-            lo += half;
-            n -= half;
-        } else {
-            n = half;
-        }
+        const int each = (n + 31) / 32, at = lane * each;
+        const uint32_t begun = __ballot_sync(0xffffffffu, at < n && offs[lo + at] <= row);
+        const int skip = max(__popc(begun) - 1, 0) * each;
+        lo += skip;
+        n = min(each, n - skip);
     }
     return lo;
 }
 
+// 1 / sqrt(x): the hardware's and a step of Newton's method.
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float y = rsqrtf(x);
+    return x < 3.0e38f ? y * fmaf(-0.5f * x * y, y, 1.5f) : y;
+}
+
 template <typename E, int D, bool PAIRS>
-__global__ void __launch_bounds__(kThreadsR) qk_norm_rope_kernel(RopeArgs a, int per_item) {
+__global__ void __launch_bounds__(kThreadsR, sizeof(E) == 2 ? kPerSm : kPerSm / 2)
+    qk_norm_rope_kernel(RopeArgs a, int per_item, int items_row) {
     constexpr int kLanes = D / 8;
-    const int heads = a.H + a.Hkv, items_row = (heads + per_item - 1) / per_item;
-    const int slot = threadIdx.x % kLanes;
-    const long long item =
-        ((long long)blockIdx.x * kThreadsR + threadIdx.x) / kLanes;
-    const int row = (int)min(item / items_row, (long long)a.R);
-    const int h0 = (int)(item % items_row) * per_item, h1 = min(h0 + per_item, heads);
-    pdl_wait();
-    pdl_launch_next();
-    // malformed offsets are told by the threads of the first items, one request each
-    for (long long b = (long long)blockIdx.x * kThreadsR + threadIdx.x; b < a.B;
-         b += (long long)gridDim.x * kThreadsR) {
-        int o, n;
-        if (!request_range(a.offsets, (int)b, a.R, 0x7fffffff, o, n)) report(a.status, TV_ERR_TREE);
-    }
-    bool live = row < a.R;
-    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    __shared__ uint64_t s_turns[D / 2];
+    const int heads = a.H + a.Hkv;
+    const int lane = threadIdx.x % 32, slot = threadIdx.x % kLanes;
+    const long long items = (long long)a.R * items_row;
+    const long long step = (long long)gridDim.x * (kThreadsR / kLanes);
     // channels of the lane's two quads
     const bool turned = slot < a.rot / 8;
     const int rest = slot - a.rot / 8;
     const int cA = PAIRS ? 8 * slot : turned ? 4 * slot : a.rot + 8 * rest;
     const int cB = PAIRS || !turned ? cA + 4 : a.rot / 2 + 4 * slot;
-    if (live) {
-        const int b = request_of(a.offsets, a.B, row);
-        int off, n;
-        live = request_range(a.offsets, b, a.R, 0x7fffffff, off, n) && row >= off && row < off + n;
-        if (live && turned) {
-            const long long pos = (long long)a.start[b] + (a.depth ? a.depth[row] - 1LL : row - off);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) turn(pos, a.inv_freq[4 * slot + e], cs[e], sn[e]);
-        }
-    }
     using Q = Quad<E>;
     const bool norm = a.eps >= 0.f;
-    float w[2][8];  // weights of queries and keys
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const E *weight = static_cast<const E *>(p ? a.k_weight : a.q_weight);
-        float x[4] = {1.f, 1.f, 1.f, 1.f}, y[4] = {1.f, 1.f, 1.f, 1.f};
-        if (norm && weight && (p == 0 || a.Hkv > 0)) {
-            reinterpret_cast<const Q *>(weight + cA)->get(x);
-            reinterpret_cast<const Q *>(weight + cB)->get(y);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            w[p][e] = x[e];
-            w[p][4 + e] = y[e];
-        }
+    pdl_wait();
+    pdl_launch_next();
+    // malformed offsets are told by one thread for each request
+    for (long long b = (long long)blockIdx.x * kThreadsR + threadIdx.x; b < a.B;
+         b += (long long)gridDim.x * kThreadsR) {
+        int o, n;
+        if (!request_range(a.offsets, (int)b, a.R, 0x7fffffff, o, n)) report(a.status, TV_ERR_TREE);
     }
-    const size_t at = live ? row : 0;
-    const E *q = static_cast<const E *>(a.q) + at * a.q_stride;
-    const E *k = static_cast<const E *>(a.k) + at * a.k_stride;
-    E *q_out = static_cast<E *>(a.q_out) + at * a.q_out_stride;
-    E *k_out = static_cast<E *>(a.k_out) + at * a.k_out_stride;
-    // (every lane takes the same steps, whatever its row: the sums are shuffled)
-    for (int i = 0; i < per_item; i += kUnroll) {
-        Q rawA[kUnroll], rawB[kUnroll];
+    // up to 32 requests: their first rows and positions, one in each lane
+    const int begins = lane < a.B ? a.offsets[lane] : 0x7fffffff;
+    const int starts = lane < a.B ? a.start[lane] : 0;
+    Q qA, qB, kA, kB;  // weights
+    const float ones[4] = {1.f, 1.f, 1.f, 1.f};
+    qA.set(ones);
+    qB.set(ones);
+    kA.set(ones);
+    kB.set(ones);
+    if (norm && a.q_weight) {
+        qA = *reinterpret_cast<const Q *>(static_cast<const E *>(a.q_weight) + cA);
+        qB = *reinterpret_cast<const Q *>(static_cast<const E *>(a.q_weight) + cB);
+    }
+    if (norm && a.k_weight && a.Hkv > 0) {
+        kA = *reinterpret_cast<const Q *>(static_cast<const E *>(a.k_weight) + cA);
+        kB = *reinterpret_cast<const Q *>(static_cast<const E *>(a.k_weight) + cB);
+    }
+    // a warp's first item, whose lanes' items follow it; every lane takes the same steps
+    for (long long first = ((long long)blockIdx.x * kThreadsR + threadIdx.x - lane) / kLanes,
+                   begin = first;
+         first < items || begin == first; first += step) {
+        const long long item = first + lane / kLanes;
+        const bool there = item < items;
+        const int row = there ? (int)(item / items_row) : 0;
+        const int h0 = there ? (int)(item - (long long)row * items_row) * per_item : 0;
+        const E *q = static_cast<const E *>(a.q) + (size_t)row * a.q_stride;
+        const E *k = static_cast<const E *>(a.k) + (size_t)row * a.k_stride;
+        const auto load = [&](int i, Q (&A)[kUnroll], Q (&B)[kUnroll]) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = h0 + i + u;
-            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-            rawA[u].set(zero);
-            rawB[u].set(zero);
-            if (live && i + u < per_item && h < heads) {
-                const E *in = h < a.H ? q + (size_t)h * D : k + (size_t)(h - a.H) * D;
-                rawA[u] = *reinterpret_cast<const Q *>(in + cA);
-                rawB[u] = *reinterpret_cast<const Q *>(in + cB);
+            for (int u = 0; u < kUnroll; ++u) {
+                const int h = h0 + i + u;
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                A[u].set(zero);
+                B[u].set(zero);
+                if (there && i + u < per_item && h < heads) {
+                    const E *in = h < a.H ? q + h * D : k + (h - a.H) * D;
+                    A[u] = *reinterpret_cast<const Q *>(in + cA);
+                    B[u] = *reinterpret_cast<const Q *>(in + cB);
+                }
+            }
+        };
+        Q A[kUnroll], B[kUnroll];
+        load(0, A, B);
+        const int depth = a.depth && there ? a.depth[row] : 1;
+        if (first == begin) {
+            for (int i = threadIdx.x; i < a.rot / 2; i += kThreadsR)
+                s_turns[i] = turns(a.inv_freq[i]);
+            __syncthreads();
+        }
+        // the rows' requests and positions, a row of the warp after the other
+        bool live = false;
+        long long pos = 0;
+#pragma unroll
+        for (int g = 0; g < 32 / kLanes; ++g) {
+            const int at = __shfl_sync(0xffffffffu, row, g * kLanes);
+            const int b = a.B <= 32 ? max(__popc(__ballot_sync(0xffffffffu, begins <= at)) - 1, 0)
+                                    : request_of(a.offsets, a.B, at);
+            const int begin_row = a.offsets[b];
+            const int p = a.B <= 32 ? __shfl_sync(0xffffffffu, starts, b) : a.start[b];
+            int off, n;
+            const bool in = request_range(a.offsets, b, a.R, 0x7fffffff, off, n) && at >= off &&
+                            at < off + n;
+            if (lane / kLanes == g) {
+                live = there && in;
+                pos = (long long)p + (a.depth ? depth - 1LL : at - begin_row);
             }
         }
+        float cs[4], sn[4];
+        if (turned) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = h0 + i + u;
-            const bool key = h >= a.H;
-            float x[4], y[4];
-            rawA[u].get(x);
-            rawB[u].get(y);
-            if (norm) {
-                float sum = 0.f;
+            for (int e = 0; e < 4; ++e) turn(pos, s_turns[4 * slot + e], cs[e], sn[e]);
+        }
+        E *q_out = static_cast<E *>(a.q_out) + (size_t)row * a.q_out_stride;
+        E *k_out = static_cast<E *>(a.k_out) + (size_t)row * a.k_out_stride;
+        for (int i = 0; i < per_item; i += kUnroll) {
+            if (i > 0) load(i, A, B);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum = fmaf(x[e], x[e], fmaf(y[e], y[e], sum));
+            for (int u = 0; u < kUnroll; ++u) {
+                const int h = h0 + i + u;
+                const bool key = h >= a.H;
+                float x[4], y[4];
+                A[u].get(x);
+                B[u].get(y);
+                if (norm) {
+                    float sum = 0.f, wA[4], wB[4];
 #pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                const float inv = 1.f / sqrtf(sum * (1.f / D) + a.eps);
+                    for (int e = 0; e < 4; ++e) sum = fmaf(x[e], x[e], fmaf(y[e], y[e], sum));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = x[e] * inv * (key ? w[1][e] : w[0][e]);
-                    y[e] = y[e] * inv * (key ? w[1][4 + e] : w[0][4 + e]);
-                }
-            }
-            if (turned) {
-                if (PAIRS) {
-                    const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-                    float t[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        t[2 * e] = z[2 * e] * cs[e] - z[2 * e + 1] * sn[e];
-                        t[2 * e + 1] = z[2 * e + 1] * cs[e] + z[2 * e] * sn[e];
-                    }
+                    for (int o = kLanes / 2; o > 0; o >>= 1)
+                        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    const float inv = inv_sqrt(fmaf(sum, 1.f / D, a.eps));
+                    (key ? kA : qA).get(wA);
+                    (key ? kB : qB).get(wB);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        x[e] = t[e];
-                        y[e] = t[4 + e];
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float t = x[e] * cs[e] - y[e] * sn[e];
-                        y[e] = y[e] * cs[e] + x[e] * sn[e];
-                        x[e] = t;
+                        x[e] = x[e] * inv * wA[e];
+                        y[e] = y[e] * inv * wB[e];
                     }
                 }
-            }
-            if (live && i + u < per_item && h < heads) {
-                E *out = key ? k_out + (size_t)(h - a.H) * D : q_out + (size_t)h * D;
-                Q o;
-                o.set(x);
-                *reinterpret_cast<Q *>(out + cA) = o;
-                o.set(y);
-                *reinterpret_cast<Q *>(out + cB) = o;
+                if (turned) {
+                    if (PAIRS) {
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const float x0 = x[e], y0 = y[e];
+                            x[e] = x0 * cs[e / 2] - x[e + 1] * sn[e / 2];
+                            x[e + 1] = x[e + 1] * cs[e / 2] + x0 * sn[e / 2];
+                            y[e] = y0 * cs[2 + e / 2] - y[e + 1] * sn[2 + e / 2];
+                            y[e + 1] = y[e + 1] * cs[2 + e / 2] + y0 * sn[2 + e / 2];
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float t = x[e] * cs[e] - y[e] * sn[e];
+                            y[e] = y[e] * cs[e] + x[e] * sn[e];
+                            x[e] = t;
+                        }
+                    }
+                }
+                if (live && i + u < per_item && h < heads) {
+                    E *out = key ? k_out + (h - a.H) * D : q_out + h * D;
+                    Q o;
+                    o.set(x);
+                    *reinterpret_cast<Q *>(out + cA) = o;
+                    o.set(y);
+                    *reinterpret_cast<Q *>(out + cB) = o;
+                }
             }
         }
     }
@@ -209,15 +250,18 @@ __global__ void __launch_bounds__(kThreadsR) qk_norm_rope_kernel(RopeArgs a, int
 
 template <typename E, int D, bool PAIRS>
 cudaError_t launch(const RopeArgs &a, cudaStream_t s) {
-    // heads per item: many rows share an angle among sixteen heads; few rows spread their heads
-    // over the SMs
-    const long long heads = (long long)a.H + a.Hkv, rows_wave = device_sms() * 2048LL / (D / 8);
-    const int per_item = a.R * heads >= 16 * rows_wave ? 16 : kUnroll;
-    const long long threads = a.R * ((heads + per_item - 1) / per_item) * (D / 8);
-    const long long blocks = (threads + kThreadsR - 1) / kThreadsR;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_pdl(qk_norm_rope_kernel<E, D, PAIRS>, dim3((unsigned)blocks), dim3(kThreadsR), 0,
-                      s, a, per_item);
+    // Heads per item: about twenty where the rows alone fill the SMs, so that an angle serves many;
+    // four where rows are few, so that their heads spread over the SMs.
+    const long long heads = (long long)a.H + a.Hkv, lanes = device_sms() * 1024LL;
+    const bool many = a.R * heads * (D / 8) >= 20 * lanes;
+    long long items_row = many ? std::max(1LL, (heads + 10) / 20) : (heads + kUnroll - 1) / kUnroll;
+    const int per_item = (int)(((heads + items_row - 1) / items_row + kUnroll - 1) / kUnroll * kUnroll);
+    items_row = (heads + per_item - 1) / per_item;
+    const int per_sm = sizeof(E) == 2 ? kPerSm : kPerSm / 2;
+    const long long blocks = (a.R * items_row * (D / 8) + kThreadsR - 1) / kThreadsR;
+    return launch_pdl(qk_norm_rope_kernel<E, D, PAIRS>,
+                      dim3((unsigned)std::min(blocks, (long long)device_sms() * per_sm)),
+                      dim3(kThreadsR), 0, s, a, per_item, (int)items_row);
 }
 
 template <typename E, int D>

@@ -862,7 +862,7 @@ tv_status tv_qk_norm_rope(int32_t B, int32_t total_rows, int32_t H, int32_t Hkv,
     if (Hkv > 0 && (bad_stride(k_stride, Hkv, d) || bad_stride(k_out_stride, Hkv, d)))
         return TV_ERR_SHAPE;
     if (!(eps < 3.0e38f) || eps < -3.0e38f) return TV_ERR_SHAPE;  // NaN and infinities
-    if ((int64_t)H + Hkv > 0x7fffffffLL / 2) return TV_ERR_UNSUPPORTED;
+    if ((int64_t)H + Hkv > 0x7fffffffLL / 256) return TV_ERR_UNSUPPORTED;
     if (!dev_status) return TV_ERR_NULL;
     if (B == 0 || total_rows == 0) return TV_OK;
     tv_status st = check_ptrs({row_offsets, start, q, q_out, dev_status});
