@@ -5,15 +5,18 @@
 // A tree node stands at the position that tree attention gives it: context length + depth - 1
 // (LLM Primer VI ch. 9 §9.2: a candidate tree is checked in one pass with positions by depth).
 //
-// Every element is read and written once: HBM bounds it.  D / 8 lanes hold a head's row, eight
-// channels each, chosen so that both of a rotated pair are in the same lane; they share out the
-// row's heads in groups, with the angles computed once per group.
+// Every element is read and written once: HBM bounds it, if the instructions stay few.  D / 8
+// lanes hold a head's row, eight channels each, chosen so that both of a rotated pair are in the
+// same lane; the lanes walk over heads of one row with weight * cos and weight * sin in
+// registers, so a channel costs a multiply-add and a multiply of the packed kind beside its
+// square and its conversions.
 //
 // Angles: t / 2 pi = position * f, f = inv_freq / 2 pi.  Only the fraction of the turns counts,
 // so f is held as a 64-bit fraction and the product is taken modulo 2^64: exact, whatever the
 // position.  The nearest quarter turn is taken off before the rest (at most 1/8 turn) becomes
 // a float.
 #include <algorithm>
+#include <type_traits>
 
 #include "tv_internal.cuh"
 
@@ -22,22 +25,51 @@ namespace {
 
 constexpr int kThreadsR = 256;
 constexpr int kUnroll = 4;   // heads whose loads are in flight together
-constexpr int kPerSm = 4;    // CTAs that registers leave room for
+// CTAs per SM that registers are kept to: three (78 registers a thread) for bf16, two for fp32.
+// 32768 bf16 rows of 40 heads: 113 us, with four 121 (spills), with two 134.
+template <typename E>
+constexpr int kPerSm = sizeof(E) == 2 ? 3 : 2;
 
+// Two floats in a register pair, for the packed fp32 instructions.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float lo, float hi) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 halves(Two x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ Two swap(Two x) {
+    const float2 y = halves(x);
+    return two(y.y, y.x);
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Four channels as they lie in memory.
 template <typename E>
 struct Quad;
 template <>
 struct Quad<__nv_bfloat16> {
     uint2 w;
-    __device__ void get(float (&x)[4]) const {
-        x[0] = __uint_as_float(w.x << 16);
-        x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(w.y << 16);
-        x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    __device__ void get(Two (&x)[2]) const {
+        x[0] = two(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u));
+        x[1] = two(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
     }
-    __device__ void set(const float (&x)[4]) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]),
-                             b = __floats2bfloat162_rn(x[2], x[3]);
+    __device__ void set(const Two (&x)[2]) {
+        const __nv_bfloat162 a = __float22bfloat162_rn(halves(x[0])),
+                             b = __float22bfloat162_rn(halves(x[1]));
         w.x = *reinterpret_cast<const uint32_t *>(&a);
         w.y = *reinterpret_cast<const uint32_t *>(&b);
     }
@@ -45,10 +77,14 @@ struct Quad<__nv_bfloat16> {
 template <>
 struct Quad<float> {
     float4 w;
-    __device__ void get(float (&x)[4]) const {
-        x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+    __device__ void get(Two (&x)[2]) const {
+        x[0] = two(w.x, w.y);
+        x[1] = two(w.z, w.w);
     }
-    __device__ void set(const float (&x)[4]) { w = make_float4(x[0], x[1], x[2], x[3]); }
+    __device__ void set(const Two (&x)[2]) {
+        const float2 a = halves(x[0]), b = halves(x[1]);
+        w = make_float4(a.x, a.y, b.x, b.y);
+    }
 };
 
 // Turns per position as a 64-bit fraction.
@@ -93,24 +129,37 @@ __device__ __forceinline__ float inv_sqrt(float x) {
     return x < 3.0e38f ? y * fmaf(-0.5f * x * y, y, 1.5f) : y;
 }
 
+// A projection's weights with the rotation, for a lane's two quads (x: the first, y: the second).
+struct Turned {
+    Two xc[2], xs[2], yc[2], ys[2];
+};
+
 template <typename E, int D, bool PAIRS>
-__global__ void __launch_bounds__(kThreadsR, sizeof(E) == 2 ? kPerSm : kPerSm / 2)
+__global__ void __launch_bounds__(kThreadsR, kPerSm<E>)
     qk_norm_rope_kernel(RopeArgs a, int per_item, int items_row) {
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / 8, kRowsWarp = 32 / kLanes;
+    using Q = Quad<E>;
     __shared__ uint64_t s_turns[D / 2];
     const int heads = a.H + a.Hkv;
     const int lane = threadIdx.x % 32, slot = threadIdx.x % kLanes;
-    const long long items = (long long)a.R * items_row;
-    const long long step = (long long)gridDim.x * (kThreadsR / kLanes);
+    // items: kRowsWarp rows and per_item heads, a warp each
+    const long long rows_of = (a.R + kRowsWarp - 1) / kRowsWarp;
+    const long long items = rows_of * items_row, step = (long long)gridDim.x * (kThreadsR / 32);
+    const long long begin = (long long)blockIdx.x * (kThreadsR / 32) + threadIdx.x / 32;
     // channels of the lane's two quads
     const bool turned = slot < a.rot / 8;
     const int rest = slot - a.rot / 8;
     const int cA = PAIRS ? 8 * slot : turned ? 4 * slot : a.rot + 8 * rest;
     const int cB = PAIRS || !turned ? cA + 4 : a.rot / 2 + 4 * slot;
-    using Q = Quad<E>;
     const bool norm = a.eps >= 0.f;
     pdl_wait();
     pdl_launch_next();
+    {  // the first item's first heads come nearer while angles and requests are looked up
+        const int row = (int)min((begin / items_row) * kRowsWarp + lane / kLanes, a.R - 1LL);
+        const int h = min((int)(begin % items_row) * per_item, a.H - 1);
+        const E *x = static_cast<const E *>(a.q) + (size_t)row * a.q_stride + (size_t)h * D + cA;
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(x));
+    }
     // malformed offsets are told by one thread for each request
     for (long long b = (long long)blockIdx.x * kThreadsR + threadIdx.x; b < a.B;
          b += (long long)gridDim.x * kThreadsR) {
@@ -120,148 +169,148 @@ __global__ void __launch_bounds__(kThreadsR, sizeof(E) == 2 ? kPerSm : kPerSm / 
     // up to 32 requests: their first rows and positions, one in each lane
     const int begins = lane < a.B ? a.offsets[lane] : 0x7fffffff;
     const int starts = lane < a.B ? a.start[lane] : 0;
-    Q qA, qB, kA, kB;  // weights
-    const float ones[4] = {1.f, 1.f, 1.f, 1.f};
-    qA.set(ones);
-    qB.set(ones);
-    kA.set(ones);
-    kB.set(ones);
-    if (norm && a.q_weight) {
-        qA = *reinterpret_cast<const Q *>(static_cast<const E *>(a.q_weight) + cA);
-        qB = *reinterpret_cast<const Q *>(static_cast<const E *>(a.q_weight) + cB);
-    }
-    if (norm && a.k_weight && a.Hkv > 0) {
-        kA = *reinterpret_cast<const Q *>(static_cast<const E *>(a.k_weight) + cA);
-        kB = *reinterpret_cast<const Q *>(static_cast<const E *>(a.k_weight) + cB);
-    }
-    // a warp's first item, whose lanes' items follow it; every lane takes the same steps
-    for (long long first = ((long long)blockIdx.x * kThreadsR + threadIdx.x - lane) / kLanes,
-                   begin = first;
-         first < items || begin == first; first += step) {
-        const long long item = first + lane / kLanes;
-        const bool there = item < items;
-        const int row = there ? (int)(item / items_row) : 0;
-        const int h0 = there ? (int)(item - (long long)row * items_row) * per_item : 0;
-        const E *q = static_cast<const E *>(a.q) + (size_t)row * a.q_stride;
-        const E *k = static_cast<const E *>(a.k) + (size_t)row * a.k_stride;
-        const auto load = [&](int i, Q (&A)[kUnroll], Q (&B)[kUnroll]) {
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int h = h0 + i + u;
-                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                A[u].set(zero);
-                B[u].set(zero);
-                if (there && i + u < per_item && h < heads) {
-                    const E *in = h < a.H ? q + h * D : k + (h - a.H) * D;
-                    A[u] = *reinterpret_cast<const Q *>(in + cA);
-                    B[u] = *reinterpret_cast<const Q *>(in + cB);
-                }
-            }
-        };
-        Q A[kUnroll], B[kUnroll];
-        load(0, A, B);
-        const int depth = a.depth && there ? a.depth[row] : 1;
-        if (first == begin) {
-            for (int i = threadIdx.x; i < a.rot / 2; i += kThreadsR)
-                s_turns[i] = turns(a.inv_freq[i]);
-            __syncthreads();
-        }
+    for (int i = threadIdx.x; i < a.rot / 2; i += kThreadsR) s_turns[i] = turns(a.inv_freq[i]);
+    __syncthreads();
+
+    for (long long item = begin; item < items; item += step) {
+        const long long rows = item / items_row;
+        const int h0 = (int)(item - rows * items_row) * per_item, h1 = min(h0 + per_item, heads);
+        const long long mine = rows * kRowsWarp + lane / kLanes;
+        const int row = (int)min(mine, a.R - 1LL);
+        const int depth = a.depth ? a.depth[row] : 1;
         // the rows' requests and positions, a row of the warp after the other
         bool live = false;
         long long pos = 0;
 #pragma unroll
-        for (int g = 0; g < 32 / kLanes; ++g) {
+        for (int g = 0; g < kRowsWarp; ++g) {
             const int at = __shfl_sync(0xffffffffu, row, g * kLanes);
             const int b = a.B <= 32 ? max(__popc(__ballot_sync(0xffffffffu, begins <= at)) - 1, 0)
                                     : request_of(a.offsets, a.B, at);
-            const int begin_row = a.offsets[b];
             const int p = a.B <= 32 ? __shfl_sync(0xffffffffu, starts, b) : a.start[b];
             int off, n;
             const bool in = request_range(a.offsets, b, a.R, 0x7fffffff, off, n) && at >= off &&
                             at < off + n;
             if (lane / kLanes == g) {
-                live = there && in;
-                pos = (long long)p + (a.depth ? depth - 1LL : at - begin_row);
+                live = mine < a.R && in;
+                pos = (long long)p + (a.depth ? depth - 1LL : at - off);
             }
         }
-        float cs[4], sn[4];
+        float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
         if (turned) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) turn(pos, s_turns[4 * slot + e], cs[e], sn[e]);
         }
-        E *q_out = static_cast<E *>(a.q_out) + (size_t)row * a.q_out_stride;
-        E *k_out = static_cast<E *>(a.k_out) + (size_t)row * a.k_out_stride;
-        for (int i = 0; i < per_item; i += kUnroll) {
-            if (i > 0) load(i, A, B);
+        // `n` heads of one projection
+        const auto project = [&](const E *in, E *out, int n, const E *weight) {
+            Two wx[2] = {two(1.f, 1.f), two(1.f, 1.f)}, wy[2] = {wx[0], wx[0]};
+            if (norm && weight) {
+                reinterpret_cast<const Q *>(weight + cA)->get(wx);
+                reinterpret_cast<const Q *>(weight + cB)->get(wy);
+            }
+            // HALVES: x' = x wx cos - y wy sin, y' = y wy cos + x wx sin.
+            // PAIRS: (a, b)' = (a, b) w (cos, cos) + (b, a) w' (-sin, sin), within x and within y.
+            Turned f;
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int h = h0 + i + u;
-                const bool key = h >= a.H;
-                float x[4], y[4];
-                A[u].get(x);
-                B[u].get(y);
-                if (norm) {
-                    float sum = 0.f, wA[4], wB[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum = fmaf(x[e], x[e], fmaf(y[e], y[e], sum));
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1)
-                        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    const float inv = inv_sqrt(fmaf(sum, 1.f / D, a.eps));
-                    (key ? kA : qA).get(wA);
-                    (key ? kB : qB).get(wB);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = x[e] * inv * wA[e];
-                        y[e] = y[e] * inv * wB[e];
-                    }
-                }
-                if (turned) {
-                    if (PAIRS) {
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            const float x0 = x[e], y0 = y[e];
-                            x[e] = x0 * cs[e / 2] - x[e + 1] * sn[e / 2];
-                            x[e + 1] = x[e + 1] * cs[e / 2] + x0 * sn[e / 2];
-                            y[e] = y0 * cs[2 + e / 2] - y[e + 1] * sn[2 + e / 2];
-                            y[e + 1] = y[e + 1] * cs[2 + e / 2] + y0 * sn[2 + e / 2];
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float t = x[e] * cs[e] - y[e] * sn[e];
-                            y[e] = y[e] * cs[e] + x[e] * sn[e];
-                            x[e] = t;
-                        }
-                    }
-                }
-                if (live && i + u < per_item && h < heads) {
-                    E *out = key ? k_out + (h - a.H) * D : q_out + h * D;
-                    Q o;
-                    o.set(x);
-                    *reinterpret_cast<Q *>(out + cA) = o;
-                    o.set(y);
-                    *reinterpret_cast<Q *>(out + cB) = o;
+            for (int e = 0; e < 2; ++e) {
+                if (PAIRS) {
+                    f.xc[e] = mul2(wx[e], two(cs[e], cs[e]));
+                    f.yc[e] = mul2(wy[e], two(cs[2 + e], cs[2 + e]));
+                    f.xs[e] = mul2(swap(wx[e]), two(-sn[e], sn[e]));
+                    f.ys[e] = mul2(swap(wy[e]), two(-sn[2 + e], sn[2 + e]));
+                } else {
+                    const Two c = two(cs[2 * e], cs[2 * e + 1]), s = two(sn[2 * e], sn[2 * e + 1]);
+                    f.xc[e] = mul2(wx[e], c);
+                    f.yc[e] = mul2(wy[e], c);
+                    f.xs[e] = mul2(wx[e], s);
+                    f.ys[e] = mul2(wy[e], two(-sn[2 * e], -sn[2 * e + 1]));
                 }
             }
+            in += cA;
+            out += cA;
+            const int over = cB - cA;
+            const auto some = [&](auto count) {
+                constexpr int kCount = decltype(count)::value;
+                Q A[kCount], B[kCount];
+#pragma unroll
+                for (int u = 0; u < kCount; ++u) {
+                    A[u] = *reinterpret_cast<const Q *>(in + u * D);
+                    B[u] = *reinterpret_cast<const Q *>(in + u * D + over);
+                }
+#pragma unroll
+                for (int u = 0; u < kCount; ++u) {
+                    Two x[2], y[2];
+                    A[u].get(x);
+                    B[u].get(y);
+                    Two inv = two(1.f, 1.f);
+                    if (norm) {
+                        const float2 q = halves(
+                            fma2(x[0], x[0], fma2(x[1], x[1], fma2(y[0], y[0], mul2(y[1], y[1])))));
+                        float sum = q.x + q.y;
+#pragma unroll
+                        for (int o = kLanes / 2; o > 0; o >>= 1)
+                            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                        const float i = inv_sqrt(fmaf(sum, 1.f / D, a.eps));
+                        inv = two(i, i);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const Two p = mul2(x[e], inv), r = mul2(y[e], inv);
+                        if (!turned) {
+                            x[e] = mul2(p, f.xc[e]);
+                            y[e] = mul2(r, f.yc[e]);
+                        } else if (PAIRS) {
+                            x[e] = fma2(p, f.xc[e], mul2(swap(p), f.xs[e]));
+                            y[e] = fma2(r, f.yc[e], mul2(swap(r), f.ys[e]));
+                        } else {
+                            x[e] = fma2(p, f.xc[e], mul2(r, f.ys[e]));
+                            y[e] = fma2(r, f.yc[e], mul2(p, f.xs[e]));
+                        }
+                    }
+                    if (live) {
+                        Q o;
+                        o.set(x);
+                        *reinterpret_cast<Q *>(out + u * D) = o;
+                        o.set(y);
+                        *reinterpret_cast<Q *>(out + u * D + over) = o;
+                    }
+                }
+                in += kCount * D;
+                out += kCount * D;
+            };
+            int h = 0;
+#pragma unroll 1
+            for (; h + kUnroll <= n; h += kUnroll) some(std::integral_constant<int, kUnroll>());
+#pragma unroll 1
+            for (; h < n; ++h) some(std::integral_constant<int, 1>());
+        };
+        if (h0 < a.H)
+            project(static_cast<const E *>(a.q) + (size_t)row * a.q_stride + (size_t)h0 * D,
+                    static_cast<E *>(a.q_out) + (size_t)row * a.q_out_stride + (size_t)h0 * D,
+                    min(h1, a.H) - h0, static_cast<const E *>(a.q_weight));
+        if (h1 > a.H) {
+            const int from = max(h0, a.H);
+            project(static_cast<const E *>(a.k) + (size_t)row * a.k_stride + (size_t)(from - a.H) * D,
+                    static_cast<E *>(a.k_out) + (size_t)row * a.k_out_stride +
+                        (size_t)(from - a.H) * D,
+                    h1 - from, static_cast<const E *>(a.k_weight));
         }
     }
 }
 
 template <typename E, int D, bool PAIRS>
 cudaError_t launch(const RopeArgs &a, cudaStream_t s) {
-    // Heads per item: about twenty where the rows alone fill the SMs, so that an angle serves many;
-    // four where rows are few, so that their heads spread over the SMs.
-    const long long heads = (long long)a.H + a.Hkv, lanes = device_sms() * 1024LL;
-    const bool many = a.R * heads * (D / 8) >= 20 * lanes;
-    long long items_row = many ? std::max(1LL, (heads + 10) / 20) : (heads + kUnroll - 1) / kUnroll;
+    // Heads per item: about twenty where the rows alone fill the SMs twice, so that an angle serves
+    // many; down to four where rows are few, so that their heads spread over the SMs.
+    const long long heads = (long long)a.H + a.Hkv, warps = kThreadsR / 32;
+    const long long rows = (a.R + 256 / D - 1LL) / (256 / D);
+    const long long resident = device_sms() * kPerSm<E> * warps;
+    long long items_row = std::max((2 * resident + rows - 1) / rows, std::max(1LL, (heads + 10) / 20));
+    items_row = std::min(items_row, (heads + kUnroll - 1) / kUnroll);
     const int per_item = (int)(((heads + items_row - 1) / items_row + kUnroll - 1) / kUnroll * kUnroll);
     items_row = (heads + per_item - 1) / per_item;
-    const int per_sm = sizeof(E) == 2 ? kPerSm : kPerSm / 2;
-    const long long blocks = (a.R * items_row * (D / 8) + kThreadsR - 1) / kThreadsR;
+    const long long blocks = std::min((rows * items_row + warps - 1) / warps, resident / warps);
     return launch_pdl(qk_norm_rope_kernel<E, D, PAIRS>,
-                      dim3((unsigned)std::min(blocks, (long long)device_sms() * per_sm)),
-                      dim3(kThreadsR), 0, s, a, per_item, (int)items_row);
+                      dim3((unsigned)blocks), dim3(kThreadsR), 0, s, a, per_item, (int)items_row);
 }
 
 template <typename E, int D>
