@@ -11,21 +11,28 @@
 // tensor memory's lanes:
 //   S     = Q K^T           64 x 64     operands in shared memory
 //   O1^T  = V^T P^T         dv x 64     V as it lies (MN-major), P's parts in shared memory
-//   O2^T  = H^T Q^T         dv x 64     H's parts in tensor memory, Q as it lies
+//   O2^T  = H^T Q^T         dv x 64     H's parts in tensor memory, Q as it lies; added to O1^T
 //   D^T   = V^T K~          dv x dk     V as it lies, K~ = diag(2^{d - L}) K in three parts
 // H itself stays in the registers of sixteen warps (a lane per dv, dk / 4 channels a warp):
 // H = 2^d H + D rounds once a chunk and to nearest, which the tensor cores' accumulation does
 // not, and the next chunk's D can start as soon as this one's has been read.
 //
-// Precision.  P and H enter their products as NP bf16 parts, two for bf16 outputs (2^-16, far
-// below the output's own rounding) and three for fp32; K~ always as three, since the state is
-// fp32.  Small parts are accumulated first.  Decays are 64-bit fixed-point sums of log2 units
-// (2^-32): differences of sums over a chunk lose nothing.  P's factor is 2^{L_i - R} 2^{R - L_j}
-// around the middle R of the chunk's range, or, where a chunk spans more than 2^120, the
-// exponential of each difference.
+// O1 and O2 are summed in one accumulator: both carry the factor 2^{R - L} of the middle R of the
+// chunk's range of L, and the output's 2^{L - R} comes last:
+//   O = diag(2^{L - R}) (Q (2^R H) + P V),   P_ij = 2^{R - L_j} q_i . k_j
+// A chunk ends early where L would span more than 2^120.
 //
-// Roles (32 warps): plan and decays (1), copies (1), products (1), K~ (6), H (16), outputs (4),
-// P (3).
+// Precision.  P and H enter their products as NP bf16 parts, two for bf16 outputs (2^-16, far
+// below the output's own rounding) and three for fp32; K~ (or V~, see below) always as three,
+// since the state is fp32.  Small parts are accumulated first.  Decays are 64-bit fixed-point sums
+// of log2 units (2^-32): differences of sums over a chunk lose nothing.
+//
+// The decays of D's product may stand with either factor: V~ = diag(2^{d - L}) V where dv is the
+// smaller (half the conversions at dk = 128, dv = 64), else K~.
+//
+// Roles (32 warps): plan, decays and copies (1), D's product (1), the outputs' products (1), K~ or
+// V~ (6), H (16), outputs (4), P (3).  D waits for nothing but H's sums of the chunk before, so
+// that parts, outputs and scores stay off the chain from chunk to chunk.
 //
 // Few long prompts: the rows of a request are cut into segments.  A first launch computes what
 // each segment adds to a zero state, a second chains these sums, and the segments then run at
@@ -40,20 +47,22 @@ namespace {
 
 constexpr int kC = 64;        // rows per chunk
 constexpr int kStages = 3;    // chunks of q, k, v in flight
-constexpr int kSlots = 4;     // chunks whose decays are ready
+constexpr int kSlots = 5;     // see the plan's wait
 constexpr int kWarps = 32;
-constexpr int kKeyWarps = 6, kScoreWarps = 3;  // of K~ and of P
+constexpr int kScaleWarps = 6, kScoreWarps = 3;  // of K~ or V~, and of P
 constexpr int kThreadsT = kWarps * 32;
 constexpr int kWaitTries = 1 << 20;  // 7800 cycles each at most: some 4 s
 constexpr uint32_t kSlab = kC * 128; // 64 rows of 64 channels
+constexpr int kSpan = 120;           // log2 units that L may span in a chunk
 
-enum { kA, kB, kW, kE };  // Slot::factor
-enum Flags { kFirst = 1, kLast = 2, kEnd = 4, kMild = 8 };
+enum { kB, kW, kE };  // Slot::factor
+enum Flags { kFirst = 1, kLast = 2, kEnd = 4 };
 
+// What the roles need to know of a chunk.
 struct alignas(16) Slot {
-    float factor[4][kC];  // 2^{L - R}, 2^{R - L}, 2^{d - L}, 2^L
-    long long L[kC];
+    float factor[3][kC];  // 2^{R - L}, 2^{d - L}, 2^{L - R}
     float2 d;             // 2^d as a pair
+    float r;              // 2^R
     int row, cnt, flags, head;
     long long src, dst;   // states: a (request, head), or ~index of one in the workspace
 };
@@ -69,16 +78,19 @@ struct TcParams {
 
 template <int DK, int DV, int NP>
 struct Lay {
+    static constexpr bool kScaleV = DV < DK;
+    static constexpr int kX = kScaleV ? DV : DK;  // width of the scaled factor
     static constexpr uint32_t kQ = 0, kK = DK * 128, kV = 2 * DK * 128,
                               kStage = (2 * DK + DV) * 128;
-    static constexpr uint32_t kKt = kStages * kStage, kKtPart = DK * 128;
-    static constexpr uint32_t kP = kKt + 3 * kKtPart, kPPart = kC * 128;
+    static constexpr int kXBufs = DK == 128 && DV == 128 ? 1 : 2;
+    static constexpr uint32_t kXt = kStages * kStage, kXPart = kX * 128, kXBuf = 3 * kXPart;
+    static constexpr uint32_t kP = kXt + kXBufs * kXBuf, kPPart = kC * 128;
     static constexpr uint32_t kSlot0 = kP + NP * kPPart;
     static constexpr uint32_t kBytes = kSlot0 + kSlots * (uint32_t)sizeof(Slot) + 1024;
     // tensor memory columns
-    static constexpr uint32_t tD = 0, tH = DK, tS = tH + NP * DK / 2, tO1 = tS + kC,
-                              tO2 = tO1 + kC, kCols = 512;
-    static_assert(tO2 + kC <= kCols, "tensor memory");
+    static constexpr uint32_t tD = 0, tH = DK, tO = tH + NP * DK / 2, tS = tO + 2 * kC, kCols = 512;
+    static constexpr int kSBufs = tS + 2 * kC <= kCols ? 2 : 1;
+    static_assert(tS + kSBufs * kC <= kCols, "tensor memory");
     static_assert(kBytes <= tcc::kSmemLimit - 512, "shared memory");
 };
 
@@ -165,11 +177,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     extern __shared__ uint8_t s_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ __align__(8) uint64_t s_gate_full[kSlots], s_gate_free[kSlots], s_full[kStages],
-        s_empty[kStages], s_s_full, s_p_full, s_kt_full, s_h_full, s_kv_done, s_o_full, s_o_free, s_drain, s_asked;
+    __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_empty[kStages], s_s_full[2],
+        s_p_full, s_x_full[2], s_x_free[2], s_h_full, s_h_free, s_d_full, s_d_free, s_o_full[2], s_o_free[2], s_drain[2], s_asked;
     __shared__ __align__(16) uint64_t s_answer[2];
     const PrefillArgs &a = p.a;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, lane = tid % 32;
+    const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);  // (known to be the whole warp's)
     uint8_t *s_base = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
     const uint32_t base = ptx::smem_addr(s_base);
     Slot *slots = reinterpret_cast<Slot *>(s_base + L::kSlot0);
@@ -177,63 +190,82 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     const auto bar = [](const uint64_t &b) { return ptx::smem_addr(&b); };
     if (tid == 0) {
         s_abort = 0;
-        for (int i = 0; i < kSlots; ++i) {
-            ptx::mbar_init(bar(s_gate_full[i]), 1);
-            // readers: copies, products, K~, H and, with outputs, the outputs' and P's warps
-            ptx::mbar_init(bar(s_gate_free[i]),
-                           2 + kKeyWarps + 4 * kQuads + (OUT ? kQuads + kScoreWarps : 0));
-        }
+        for (int i = 0; i < kSlots; ++i) ptx::mbar_init(bar(s_gate[i]), 1);
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(bar(s_full[i]), 1);
-            ptx::mbar_init(bar(s_empty[i]), 1);
+            ptx::mbar_init(bar(s_empty[i]), OUT ? 2 : 1);
         }
-        ptx::mbar_init(bar(s_s_full), 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(s_s_full[i]), 1);
+            ptx::mbar_init(bar(s_x_full[i]), kScaleWarps);
+            ptx::mbar_init(bar(s_x_free[i]), 1);
+            ptx::mbar_init(bar(s_o_full[i]), 1);
+            ptx::mbar_init(bar(s_o_free[i]), kQuads);
+        }
         ptx::mbar_init(bar(s_p_full), kScoreWarps);
-        ptx::mbar_init(bar(s_kt_full), kKeyWarps);
         ptx::mbar_init(bar(s_h_full), 4 * kQuads);
-        ptx::mbar_init(bar(s_kv_done), 1);
-        ptx::mbar_init(bar(s_o_full), 1);
-        ptx::mbar_init(bar(s_o_free), kQuads);
-        ptx::mbar_init(bar(s_drain), 1);
+        ptx::mbar_init(bar(s_h_free), 1);
+        ptx::mbar_init(bar(s_d_full), 1);
+        ptx::mbar_init(bar(s_d_free), 4 * kQuads);
+        ptx::mbar_init(bar(s_drain[0]), 1);
+        ptx::mbar_init(bar(s_drain[1]), 1);
         ptx::mbar_init(bar(s_asked), 1);
         ptx::fence_mbar_init();
         if (OUT) ptx::prefetch_tensormap(&map_q);
         ptx::prefetch_tensormap(&map_k);
         ptx::prefetch_tensormap(&map_v);
     }
-    if (warp == 1) {
+    if (warp == 2) {
         ptx::tmem_alloc(ptx::smem_addr(&s_tmem), L::kCols);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     pdl_wait();
     pdl_launch_next();
 
-    // A wait that expires raises the CTA's flag; its warp leaves, and the others' waits end early.
+    // A wait that expires raises the CTA's flag and its warp leaves; the others' expire in turn.
+    // (The whole wait is one short loop, and what a warp does next is a vote: the compiler then
+    // knows that warps stay whole, and keeps the products' operands in uniform registers.)
     const int tries = p.expire ? kWaitTries / 64 : kWaitTries;
     const auto wait = [&](const uint64_t &b, uint32_t parity) {
-        bool ok = ptx::mbar_wait_tries(bar(b), parity, 16);
-        for (int i = 16; !ok && i < tries && *(volatile int *)&s_abort == 0; i += 64)
-            ok = ptx::mbar_wait_tries(bar(b), parity, 64);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok && lane == 0) *(volatile int *)&s_abort = 1;
+        const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait_tries(bar(b), parity, tries));
+        if (!ok) *(volatile int *)&s_abort = 1;
         return ok;
     };
     const auto arrive = [&](const uint64_t &b) {  // once per warp, after all of its lanes
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(b));
     };
-    // the slot of chunk n, once its decays are there
-    const auto gate = [&](int n, Slot *&s) {
-        s = slots + n % kSlots;
-        return wait(s_gate_full[n % kSlots], (n / kSlots) & 1);
+    // No barrier runs a phase ahead of those who wait for it: whoever completes chunk n's phase
+    // needs something of every waiter's for chunk n - 1 (or n - 2, where there are two buffers and
+    // barriers) first.
+    // A role's walk over the chunks: number, slot, stage and the parities of their barriers.
+    struct Turn {
+        int n = 0, slot = 0, stage = 0;
+        uint32_t slot_ph = 0, stage_ph = 0;
+        __device__ void next() {
+            ++n;
+            if (++slot == kSlots) {
+                slot = 0;
+                slot_ph ^= 1;
+            }
+            if (++stage == kStages) {
+                stage = 0;
+                stage_ph ^= 1;
+            }
+        }
+    };
+    // the chunk's flags once its decays are there; kEnd if there is none
+    const auto gate = [&](const Turn &t) {
+        if (!wait(s_gate[t.slot], t.slot_ph)) return (int)kEnd;
+        return (int)__reduce_or_sync(0xffffffffu, (uint32_t)slots[t.slot].flags);
     };
 
     if (warp == 0) {
-        // ---- plan, copies, decays
+        // ---- plan, decays and copies
         Walk w{};
         const int per = OUT ? p.pieces : p.pieces - 1;
         const auto ask = [&]() {
@@ -283,122 +315,34 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         };
         next_item(true);
         float g0 = 0.f, g1 = 0.f;
-        const auto fetch = [&](const Walk &at) {  // the decays of the chunk at w
-            const int t = at.row + 2 * lane, cnt = at.done ? 0 : min(kC, at.end - at.row);
-            const float *g = a.g + at.head;
+        const auto fetch = [&]() {  // the decays of the chunk at w
+            const int t = w.row + 2 * lane, cnt = w.done ? 0 : min(kC, w.end - w.row);
+            const float *g = a.g + w.head;
             g0 = 2 * lane < cnt ? g[(size_t)t * a.g_stride] : 0.f;
             g1 = 2 * lane + 1 < cnt ? g[((size_t)t + 1) * a.g_stride] : 0.f;
         };
-        fetch(w);
+        fetch();
         long long total = 0;  // log2 of the item's decay so far
         bool total_nan = false;
-        for (int n = 0;; ++n) {
-            Slot *s = slots + n % kSlots;
-            if (n >= kSlots && !wait(s_gate_free[n % kSlots], ((n / kSlots) & 1) ^ 1)) break;
+        int issued = 0;
+        Turn t;
+        for (;; t.next()) {
+            Slot *s = slots + t.slot;
+            // Chunk n - 3's products are done: its stage is free.  Chunk n - 5's outputs have been
+            // read, which the products of chunk n - 3 waited for, and with them its slot.
+            if (t.n >= kStages && !wait(s_empty[t.stage], t.stage_ph ^ 1)) break;
             if (w.done) {
                 if (lane == 0) s->flags = kEnd;
-                arrive(s_gate_full[n % kSlots]);
+                arrive(s_gate[t.slot]);
                 break;
             }
             if (p.expire) {
                 wait(s_asked, (w.asked - 1) & 1);
                 break;
             }
-            const int row = w.row, cnt = min(kC, w.end - row), head = w.head;
-            const bool first = w.first, last = row + kC >= w.end;
-            const Walk now = w;
-            const float x0 = g0, x1 = g1;
-            w.first = false;
-            w.row += kC;
-            if (last) next_item(false);
-            fetch(w);  // the next chunk's, on its way while this one's are summed
-
-            const float most = 2839.f;  // 4096 log2 units
-            const bool nan0 = x0 != x0, nan1 = x1 != x1;
-            const double unit = 1.4426950408889634 * 4294967296.0;
-            const long long y0 = nan0 ? 0 : __double2ll_rn((double)fminf(fmaxf(x0, -most), most) * unit);
-            const long long y1 = nan1 ? 0 : __double2ll_rn((double)fminf(fmaxf(x1, -most), most) * unit);
-            long long sum = y0 + y1;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long up = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += up;
-            }
-            const long long l0 = sum - y1, l1 = sum, end = __shfl_sync(0xffffffffu, sum, 31);
-            const int h0 = (int)(l0 >> 32), h1 = (int)(l1 >> 32);
-            const int lo = __reduce_min_sync(0xffffffffu, min(h0, h1));
-            const int hi = __reduce_max_sync(0xffffffffu, max(h0, h1));
-            const bool mild = hi - lo <= 120;
-            const long long mid = (long long)((lo + hi) / 2) * (1LL << 32);
-            // from the first NaN on, everything of this request and head is one
-            const uint32_t bad0 = __ballot_sync(0xffffffffu, nan0),
-                           bad1 = __ballot_sync(0xffffffffu, nan1);
-            const bool any = (bad0 | bad1) != 0;
-            const uint32_t upto = 0xffffffffu >> (31 - lane);
-            const bool n0 = (bad0 & upto) || (bad1 & (upto >> 1)), n1 = ((bad0 | bad1) & upto) != 0;
-            const float nanf = __int_as_float(0x7fffffff);
-            if (!mild) {
-                s->L[2 * lane] = l0;
-                s->L[2 * lane + 1] = l1;
-            }
-            // a, b, w, e: 2^{L - R}, 2^{R - L}, 2^{d - L}, 2^L (a and b are 1 where R will not do)
-            const long long zero = mild ? mid : 0;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                const long long from = c == 3 ? 0 : c == 2 ? end : zero;
-                long long z0 = l0 - from, z1 = l1 - from;
-                if (c == 1 || c == 2) {
-                    z0 = -z0;
-                    z1 = -z1;
-                }
-                if (c < 2 && !mild) z0 = z1 = 0;
-                float2 f = make_float2(exp2_single(z0), exp2_single(z1));
-                if (c == 0 || c == 3) {
-                    if (n0) f.x = nanf;
-                    if (n1) f.y = nanf;
-                }
-                *reinterpret_cast<float2 *>(s->factor[c] + 2 * lane) = f;
-            }
-            if (first) {
-                total = 0;
-                total_nan = false;
-            }
-            total += end;
-            total_nan |= any;
+            const int row = w.row, head = w.head;
             if (lane == 0) {
-                const rec::Pair d = exp2_fixed(end);
-                s->d = any ? make_float2(nanf, nanf) : make_float2(d.hi, d.lo);
-                s->row = row;
-                s->cnt = cnt;
-                s->head = head;
-                s->flags = (first ? kFirst : 0) | (last ? kLast : 0) | (mild ? kMild : 0);
-                if (OUT) {
-                    s->src = now.pieces > 1 ? ~now.ws : now.unit;
-                    s->dst = now.piece == now.pieces - 1 ? now.unit : -1;
-                } else {
-                    s->src = -1;
-                    s->dst = ~(now.ws + a.H);  // where the next segment begins
-                    if (last) {
-                        const rec::Pair t = exp2_fixed(total);
-                        p.decays[now.ws] = total_nan ? make_float2(nanf, nanf)
-                                                     : make_float2(t.hi, t.lo);
-                    }
-                }
-            }
-            arrive(s_gate_full[n % kSlots]);
-        }
-    } else if (warp == 2) {
-        // ---- copies
-        int issued = 0;
-        for (int n = 0;; ++n) {
-            Slot *s;
-            if (!gate(n, s)) break;
-            if (s->flags & kEnd) break;
-            // a stage is free once every product of the chunk before in it is done
-            if (n >= kStages && !wait(s_empty[n % kStages], ((n / kStages) & 1) ^ 1)) break;
-            if (lane == 0) {
-                const int head = s->head, row = s->row;
-                const uint32_t at = base + n % kStages * L::kStage, full = bar(s_full[n % kStages]);
+                const uint32_t at = base + t.stage * L::kStage, full = bar(s_full[t.stage]);
                 ptx::mbar_arrive_expect_tx(full, OUT ? L::kStage : L::kStage - L::kK);
                 for (int c = 0; c < DK / 64; ++c) {
                     if (OUT)
@@ -408,125 +352,242 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 for (int c = 0; c < DV / 64; ++c)
                     ptx::tma_load_3d(at + L::kV + c * kSlab, &map_v, c * 64, head, row, full);
             }
-            issued = n + 1;
-            arrive(s_gate_free[n % kSlots]);
+            __syncwarp();
+            issued = t.n + 1;
+
+            int cnt = min(kC, w.end - row);
+            const float most = 2839.f;  // 4096 log2 units
+            const bool nan0 = g0 != g0, nan1 = g1 != g1;
+            const double unit = 1.4426950408889634 * 4294967296.0;
+            const long long y0 = nan0 ? 0 : __double2ll_rn((double)fminf(fmaxf(g0, -most), most) * unit);
+            const long long y1 = nan1 ? 0 : __double2ll_rn((double)fminf(fmaxf(g1, -most), most) * unit);
+            long long sum = y0 + y1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += up;
+            }
+            const long long l0 = sum - y1, l1 = sum;
+            long long end = __shfl_sync(0xffffffffu, sum, 31);
+            const int h0 = (int)(l0 >> 32), h1 = (int)(l1 >> 32);
+            int lo = __reduce_min_sync(0xffffffffu, min(h0, h1));
+            int hi = __reduce_max_sync(0xffffffffu, max(h0, h1));
+            if (hi - lo > kSpan) {
+                // the first row whose L is too far from one before it ends the chunk (rare: running
+                // extremes row by row)
+                lo = hi = __shfl_sync(0xffffffffu, h0, 0);
+                for (int r = 1; r < cnt; ++r) {
+                    const int h = __shfl_sync(0xffffffffu, r & 1 ? h1 : h0, r / 2);
+                    if (max(hi, h) - min(lo, h) > kSpan) {
+                        cnt = r;
+                        const long long e0 = __shfl_sync(0xffffffffu, l0, (r - 1) / 2);
+                        const long long e1 = __shfl_sync(0xffffffffu, l1, (r - 1) / 2);
+                        end = (r - 1) & 1 ? e1 : e0;
+                        break;
+                    }
+                    lo = min(lo, h);
+                    hi = max(hi, h);
+                }
+            }
+            const long long mid = (long long)((lo + hi) / 2) * (1LL << 32);
+            const bool first = w.first, last = row + cnt >= w.end;
+            const long long unit_of = w.unit, ws = w.ws;
+            const bool cut = w.pieces > 1, final_piece = w.piece == w.pieces - 1;
+            w.first = false;
+            w.row += cnt;
+            if (last) next_item(false);
+            fetch();  // the next chunk's, on its way while this one's become factors
+
+            // from the first NaN on, everything of this request and head is one
+            const uint32_t within = 2 * lane < cnt ? 1u : 0u;
+            const uint32_t bad0 = __ballot_sync(0xffffffffu, nan0 && within),
+                           bad1 = __ballot_sync(0xffffffffu, nan1 && 2 * lane + 1 < cnt);
+            const bool any = (bad0 | bad1) != 0;
+            const float nanf = __int_as_float(0x7fffffff);
+            *reinterpret_cast<float2 *>(s->factor[kB] + 2 * lane) =
+                make_float2(exp2_single(mid - l0), exp2_single(mid - l1));
+            *reinterpret_cast<float2 *>(s->factor[kW] + 2 * lane) =
+                make_float2(exp2_single(end - l0), exp2_single(end - l1));
+            float2 ev = make_float2(exp2_single(l0 - mid), exp2_single(l1 - mid));
+            if (any) {
+                const uint32_t upto = 0xffffffffu >> (31 - lane);
+                if ((bad0 & upto) || (bad1 & (upto >> 1))) ev.x = nanf;
+                if ((bad0 | bad1) & upto) ev.y = nanf;
+            }
+            *reinterpret_cast<float2 *>(s->factor[kE] + 2 * lane) = ev;
+            if (first) {
+                total = 0;
+                total_nan = false;
+            }
+            total += end;
+            total_nan |= any;
+            if (lane == 0) {
+                const rec::Pair d = exp2_fixed(end);
+                s->d = any ? make_float2(nanf, nanf) : make_float2(d.hi, d.lo);
+                s->r = exp2_single(mid);
+                s->row = row;
+                s->cnt = cnt;
+                s->head = head;
+                s->flags = (first ? kFirst : 0) | (last ? kLast : 0);
+                if (OUT) {
+                    s->src = cut ? ~ws : unit_of;
+                    s->dst = final_piece ? unit_of : -1;
+                } else {
+                    s->src = -1;
+                    s->dst = ~(ws + a.H);  // where the next segment begins
+                    if (last) {
+                        const rec::Pair d = exp2_fixed(total);
+                        p.decays[ws] = total_nan ? make_float2(nanf, nanf) : make_float2(d.hi, d.lo);
+                    }
+                }
+            }
+            arrive(s_gate[t.slot]);
         }
         // copies that nobody waited for (after a timeout)
         if (*(volatile int *)&s_abort)
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 ptx::mbar_wait_tries(bar(s_full[i % kStages]), (i / kStages) & 1, 1 << 14);
-    } else if (warp == 1) {
-        // ---- products
+    } else if (warp == 2) {
+        // ---- what a chunk adds to the state: D^T = V^T K~ (or V~^T K)
         const uint32_t lead = ptx::elect_one();
-        const auto stage = [&](int n) { return base + n % kStages * L::kStage; };
-        // descriptors move by their address field, in units of 16 bytes
-        const auto scores = [&](int n) {
+        for (Turn t;; t.next()) {
+            if (gate(t) & kEnd) break;
+            const int xb = t.n % L::kXBufs;
+            if (!wait(s_x_full[xb], (t.n / L::kXBufs) & 1)) break;
+            if (!wait(s_full[t.stage], t.stage_ph)) break;
+            if (t.n > 0 && !wait(s_d_free, (t.n & 1) ^ 1)) break;
+            ptx::tc_fence_after_sync();
+            // descriptors move by their address field, in units of 16 bytes
+            const uint32_t st = base + t.stage * L::kStage;
+            const uint64_t raw =
+                ptx::desc_mnmajor_sw128(st + (L::kScaleV ? L::kK : L::kV), kSlab, 1024);
+            const uint64_t scaled =
+                ptx::desc_mnmajor_sw128(base + L::kXt + xb * L::kXBuf, kSlab, 1024);
+#pragma unroll
+            for (int part = 2; part >= 0; --part)
+#pragma unroll
+                for (int kk = 0; kk < kC / 16; ++kk) {
+                    const uint64_t x = scaled + part * (L::kXPart / 16) + kk * 128;
+                    const uint64_t y = raw + kk * 128;
+                    ptx::mma_bf16_lead(tmem + L::tD, L::kScaleV ? x : y, L::kScaleV ? y : x,
+                                       ptx::idesc_bf16_f32_abmn(128, DK), part < 2 || kk > 0, lead);
+                }
+            ptx::mma_commit_lead(bar(s_d_full), lead);
+            ptx::mma_commit_lead(bar(s_x_free[xb]), lead);
+            ptx::mma_commit_lead(bar(s_empty[t.stage]), lead);
+        }
+        ptx::mma_commit_lead(bar(s_drain[0]), lead);
+        __syncwarp();
+        ptx::mbar_wait_tries(bar(s_drain[0]), 0, 1 << 18);
+    } else if (warp == 31) {
+        // ---- the outputs' products: S, H^T Q^T and V^T P^T
+        const uint32_t lead = ptx::elect_one();
+        const auto scores = [&](const Turn &t) {
             // 128 lanes take the 64 rows behind the tile along; nobody reads their results
-            const uint64_t q = ptx::desc_kmajor_sw128(stage(n) + L::kQ, 1024),
-                           k = ptx::desc_kmajor_sw128(stage(n) + L::kK, 1024);
+            const uint32_t st = base + t.stage * L::kStage, buf = t.n % L::kSBufs;
+            const uint64_t q = ptx::desc_kmajor_sw128(st + L::kQ, 1024),
+                           k = ptx::desc_kmajor_sw128(st + L::kK, 1024);
 #pragma unroll
             for (int kk = 0; kk < DK / 16; ++kk) {
                 const uint32_t o = (kk / 4 * kSlab + kk % 4 * 32) / 16;
-                ptx::mma_bf16_lead(tmem + L::tS, q + o, k + o, ptx::idesc_bf16_f32(128, kC), kk > 0,
-                                   lead);
+                ptx::mma_bf16_lead(tmem + L::tS + buf * kC, q + o, k + o,
+                                   ptx::idesc_bf16_f32(128, kC), kk > 0, lead);
             }
-            ptx::mma_commit_lead(bar(s_s_full), lead);
+            ptx::mma_commit_lead(bar(s_s_full[buf]), lead);
         };
-        // (the flags by a reduction, so that the flow is known to be the whole warp's and the
-        // products' operands stay in uniform registers)
-        const auto more = [&](int n) {
-            Slot *s;
-            return gate(n, s) && !(__reduce_or_sync(0xffffffffu, s->flags) & kEnd);
-        };
-        bool ok = more(0);
-        if (ok && OUT) {
+        Turn t;
+        bool ok = OUT && !(gate(t) & kEnd);
+        if (ok) {
             ok = wait(s_full[0], 0);
             ptx::tc_fence_after_sync();
-            if (ok) scores(0);
+            if (ok) scores(t);
         }
-        for (int n = 0; ok; ++n) {
-            const uint32_t ph = n & 1, q = stage(n) + L::kQ, v = stage(n) + L::kV;
-            if (!OUT && !(ok = wait(s_full[n % kStages], (n / kStages) & 1))) break;
-            if (OUT && n > 0 && !(ok = wait(s_o_free, ph ^ 1))) break;
+        while (ok) {
+            const int n = t.n, ob = n & 1;
+            const uint32_t ph = n & 1, st = base + t.stage * L::kStage;
+            const uint32_t o = tmem + L::tO + ob * kC;
+            if (n >= 2 && !(ok = wait(s_o_free[ob], ((n >> 1) & 1) ^ 1))) break;
             if (!(ok = wait(s_h_full, ph))) break;
             ptx::tc_fence_after_sync();
-            const uint64_t vd = ptx::desc_mnmajor_sw128(v, kSlab, 1024);
-            if (OUT) {
-                const uint64_t qd = ptx::desc_kmajor_sw128(q, 1024);
-#pragma unroll 1
-                for (int part = NP - 1; part >= 0; --part)
+            const uint64_t qd = ptx::desc_kmajor_sw128(st + L::kQ, 1024);
 #pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk)
-                        ptx::mma_bf16_ts_lead(
-                            tmem + L::tO2, tmem + L::tH + part * (DK / 2) + kk * 8,
-                            qd + (kk / 4 * kSlab + kk % 4 * 32) / 16,
-                            ptx::idesc_bf16_f32(128, kC), part < NP - 1 || kk > 0, lead);
+            for (int part = NP - 1; part >= 0; --part)
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    ptx::mma_bf16_ts_lead(o, tmem + L::tH + part * (DK / 2) + kk * 8,
+                                          qd + (kk / 4 * kSlab + kk % 4 * 32) / 16,
+                                          ptx::idesc_bf16_f32(128, kC), part < NP - 1 || kk > 0,
+                                          lead);
+            ptx::mma_commit_lead(bar(s_h_free), lead);
+            Turn u = t;
+            u.next();
+            // the next chunk's scores ahead of this one's weights, if it is there and they have
+            // a buffer of their own
+            bool scored = false;
+            if (L::kSBufs == 2 &&
+                __all_sync(0xffffffffu, ptx::mbar_test_wait(bar(s_gate[u.slot]), u.slot_ph)) &&
+                !(gate(u) & kEnd) &&
+                __all_sync(0xffffffffu, ptx::mbar_test_wait(bar(s_full[u.stage]), u.stage_ph))) {
+                scores(u);
+                scored = true;
             }
-            if (!(ok = wait(s_kt_full, ph))) break;
+            if (!(ok = wait(s_p_full, ph))) break;
             ptx::tc_fence_after_sync();
-#pragma unroll 1
-            for (int part = 2; part >= 0; --part) {
-                const uint64_t kd =
-                    ptx::desc_mnmajor_sw128(base + L::kKt + part * L::kKtPart, kSlab, 1024);
+            const uint64_t vd = ptx::desc_mnmajor_sw128(st + L::kV, kSlab, 1024);
+            const uint64_t pd = ptx::desc_kmajor_sw128(base + L::kP, 1024);
+#pragma unroll
+            for (int part = NP - 1; part >= 0; --part)
 #pragma unroll
                 for (int kk = 0; kk < kC / 16; ++kk)
-                    ptx::mma_bf16_lead(tmem + L::tD, vd + kk * 128, kd + kk * 128,
-                                       ptx::idesc_bf16_f32_abmn(128, DK), part < 2 || kk > 0, lead);
-            }
-            ptx::mma_commit_lead(bar(s_kv_done), lead);
-            if (OUT) {
-                if (!(ok = wait(s_p_full, ph))) break;
+                    ptx::mma_bf16_lead(o, vd + kk * 128, pd + part * (L::kPPart / 16) + kk * 2,
+                                       ptx::idesc_bf16_f32_amn(128, kC), 1, lead);
+            ptx::mma_commit_lead(bar(s_o_full[ob]), lead);
+            ptx::mma_commit_lead(bar(s_empty[t.stage]), lead);
+            t = u;
+            if (!(ok = !(gate(t) & kEnd))) break;
+            if (!scored) {
+                // (P of the chunk before has been written, so its scores have been read)
+                if (!(ok = wait(s_full[t.stage], t.stage_ph))) break;
                 ptx::tc_fence_after_sync();
-#pragma unroll 1
-                for (int part = NP - 1; part >= 0; --part) {
-                    const uint64_t pd =
-                        ptx::desc_kmajor_sw128(base + L::kP + part * L::kPPart, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < kC / 16; ++kk)
-                        ptx::mma_bf16_lead(tmem + L::tO1, vd + kk * 128, pd + kk * 2,
-                                           ptx::idesc_bf16_f32_amn(128, kC), part < NP - 1 || kk > 0,
-                                           lead);
-                }
-                ptx::mma_commit_lead(bar(s_o_full), lead);
-            }
-            ptx::mma_commit_lead(bar(s_empty[n % kStages]), lead);
-            arrive(s_gate_free[n % kSlots]);
-            if (!(ok = more(n + 1))) break;
-            if (OUT) {
-                // (P of chunk n has been written, so its scores have been read)
-                if (!(ok = wait(s_full[(n + 1) % kStages], ((n + 1) / kStages) & 1))) break;
-                ptx::tc_fence_after_sync();
-                scores(n + 1);
+                scores(t);
             }
         }
-        ptx::mma_commit_lead(bar(s_drain), lead);
+        ptx::mma_commit_lead(bar(s_drain[1]), lead);
         __syncwarp();
-        ptx::mbar_wait_tries(bar(s_drain), 0, 1 << 18);
-    } else if (warp == 3 || (warp >= 26 && warp != 29)) {
-        // ---- K~: keys times 2^{d - L}, in three parts, laid out as the keys are
-        const int t = (warp == 3 ? 0 : warp < 29 ? warp - 25 : warp - 26) * 32 + lane;
-        for (int n = 0;; ++n) {
-            Slot *s;
-            if (!gate(n, s)) break;
-            if (s->flags & kEnd) break;
-            if (!wait(s_full[n % kStages], (n / kStages) & 1)) break;
-            if (n > 0 && !wait(s_kv_done, (n & 1) ^ 1)) break;
-            uint8_t *st = s_base + n % kStages * L::kStage;
+        ptx::mbar_wait_tries(bar(s_drain[1]), 0, 1 << 18);
+    } else if (warp == 3 || (warp >= 26 && warp < 31)) {
+        // ---- K~ or V~: rows times 2^{d - L}, in three parts, laid out as the rows are.  Six
+        // threads to two rows; a quarter warp's eight rows keep their 16-byte pieces on different
+        // banks.
+        const int i0 = (warp == 3 ? 0 : warp - 25) * 32 + lane, r = i0 % kC, sub = i0 / kC;
+        const uint32_t line = r * 128, swz = (r & 7) * 16;
+        for (Turn t;; t.next()) {
+            if (gate(t) & kEnd) break;
+            const Slot *s = slots + t.slot;
             const int cnt = s->cnt;
-            if (cnt < kC) {  // rows past the segment belong to others: they may hold anything
-                for (int i = t; i < (kC - cnt) * (DV / 8); i += kKeyWarps * 32) {
-                    const int r = cnt + i / (DV / 8), c = i % (DV / 8);
-                    *reinterpret_cast<uint4 *>(st + L::kV + c / 8 * kSlab + r * 128 + c % 8 * 16) =
-                        make_uint4(0, 0, 0, 0);
+            const bool live = r < cnt;
+            const float w = live ? s->factor[kW][r] : 0.f;  // (past the chunk it may be infinite)
+            const uint64_t w2 = two(w, w);
+            if (!wait(s_full[t.stage], t.stage_ph)) break;
+            const int xb = t.n % L::kXBufs;
+            if (t.n >= L::kXBufs && !wait(s_x_free[xb], ((t.n / L::kXBufs) & 1) ^ 1)) break;
+            uint8_t *st = s_base + t.stage * L::kStage;
+            if (cnt < kC) {  // rows past the chunk may hold anything: the products take zeros
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                if (!live) {
+                    for (int c = sub; c < DV / 8; c += 3)
+                        *reinterpret_cast<uint4 *>(st + L::kV + c / 8 * kSlab + line + c % 8 * 16) = zero;
+                    for (int c = sub; c < DK / 8; c += 3)
+                        *reinterpret_cast<uint4 *>(st + L::kK + c / 8 * kSlab + line + c % 8 * 16) = zero;
                 }
             }
+            const uint8_t *from = st + (L::kScaleV ? L::kV : L::kK);
+            uint8_t *to = s_base + L::kXt + xb * L::kXBuf;
 #pragma unroll 2
-            for (int at = t * 16; at < DK * 128; at += kKeyWarps * 32 * 16) {
-                const int r = at / 128 % kC;
-                uint4 x = *reinterpret_cast<const uint4 *>(st + L::kK + at);
-                if (r >= cnt) x = make_uint4(0, 0, 0, 0);
-                const float w = s->factor[kW][r];
-                const uint64_t w2 = two(w, w);
+            for (int c = sub; c < L::kX / 8; c += 3) {
+                const uint32_t at = c / 8 * kSlab + line + ((c % 8 * 16) ^ swz);
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (live) x = *reinterpret_cast<const uint4 *>(from + at);
                 const uint32_t in[4] = {x.x, x.y, x.z, x.w};
                 uint32_t out[3][4];
 #pragma unroll
@@ -538,24 +599,22 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 }
 #pragma unroll
                 for (int j = 0; j < 3; ++j)
-                    *reinterpret_cast<uint4 *>(s_base + L::kKt + j * L::kKtPart + at) =
+                    *reinterpret_cast<uint4 *>(to + j * L::kXPart + at) =
                         make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]);
             }
             ptx::fence_proxy_async_smem();
-            arrive(s_kt_full);
-            arrive(s_gate_free[n % kSlots]);
+            arrive(s_x_full[xb]);
         }
-    } else if (warp < 20) {
+    } else if (warp >= 4 && warp < 20) {
         // ---- H: lane = column of the state, kChan of its channels in registers
         const int quad = warp % 4, c0 = (warp - 4) / 4 * kChan, col = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)quad << 21);  // lane quad * 32
         if (quad < kQuads) {
             uint64_t h[kChan / 2];
-            for (int n = 0;; ++n) {
-                Slot *s;
-                if (!gate(n, s)) break;
-                const int flags = s->flags;
+            for (Turn t;; t.next()) {
+                const int flags = gate(t);
                 if (flags & kEnd) break;
+                const Slot *s = slots + t.slot;
                 if (flags & kFirst) {
                     const long long src = s->src;
                     const float *from = !OUT       ? nullptr
@@ -569,13 +628,17 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                                     : 0;
                 }
                 if (OUT) {
+                    const uint64_t r2 = two(s->r, s->r);
+                    // the chunk's before are read
+                    if (t.n > 0 && !wait(s_h_free, (t.n & 1) ^ 1)) break;
+                    ptx::tc_fence_after_sync();
 #pragma unroll
                     for (int i0 = 0; i0 < kChan / 2; i0 += 8) {
                         uint32_t part[NP][8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             uint32_t x[NP];
-                            split_pair<NP>(h[i0 + i], x);
+                            split_pair<NP>(mul2(h[i0 + i], r2), x);
 #pragma unroll
                             for (int j = 0; j < NP; ++j) part[j][i] = x[j];
                         }
@@ -585,12 +648,13 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     }
                     ptx::tmem_wait_st();
                 }
-                ptx::tc_fence_before_sync();
-                arrive(s_h_full);
                 const uint64_t dx = two(s->d.x, s->d.x), dy = two(s->d.y, s->d.y);
                 const long long dst = s->dst;
-                arrive(s_gate_free[n % kSlots]);
-                if (!wait(s_kv_done, n & 1)) break;
+                if (OUT) {
+                    ptx::tc_fence_before_sync();
+                    arrive(s_h_full);
+                }
+                if (!wait(s_d_full, t.n & 1)) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll
                 for (int i0 = 0; i0 < kChan; i0 += 16) {
@@ -603,6 +667,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                         y = fma2(y, dx, fma2(y, dy, two(x[2 * i], x[2 * i + 1])));
                     }
                 }
+                ptx::tc_fence_before_sync();
+                arrive(s_d_free);
                 if ((flags & kLast) && (!OUT || dst >= 0)) {
                     float *to = dst < 0 ? p.states + (size_t)~dst * DK * DV
                                         : a.H_new + (size_t)dst * DK * DV;
@@ -616,55 +682,67 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 }
             }
         }
-    } else if (warp < 24) {
-        // ---- outputs: lane = column, 64 rows
+    } else if (warp >= 20 && warp < 24) {
+        // ---- outputs: lane = column, 64 rows.  bf16: neighbouring lanes trade halves, so that an
+        // even lane stores both columns of an even row and an odd lane those of the next.
         const int quad = warp % 4, col = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)quad << 21);
         if (OUT && quad < kQuads) {
-            for (int n = 0;; ++n) {
-                Slot *s;
-                if (!gate(n, s)) break;
-                if (s->flags & kEnd) break;
-                const int cnt = s->cnt;
-                using O = std::conditional_t<NP == 3, float, __nv_bfloat16>;
-                const size_t step = (size_t)a.H * DV;
-                O *to = static_cast<O *>(a.out) + s->row * step + s->head * DV + col;
-                if (!wait(s_o_full, n & 1)) break;
+            const uint32_t step = (uint32_t)a.H * DV;  // elements from row to row
+            for (Turn t;; t.next()) {
+                if (gate(t) & kEnd) break;
+                const Slot *s = slots + t.slot;
+                const int cnt = s->cnt, ob = t.n & 1;
+                const size_t at = ((size_t)s->row * a.H + s->head) * DV;
+                if (!wait(s_o_full[ob], (t.n >> 1) & 1)) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll 1
                 for (int t0 = 0; t0 < kC; t0 += 16) {
-                    uint32_t x[16], y[16];
-                    ptx::tmem_ld_x16_nowait(lanes + L::tO1 + t0, x);
-                    ptx::tmem_ld_x16_nowait(lanes + L::tO2 + t0, y);
-                    ptx::tmem_wait_ld();
-                    if (t0 == kC - 16) {
-                        ptx::tc_fence_before_sync();
-                        arrive(s_o_free);
-                    }
+                    uint32_t x[16];
+                    ptx::tmem_ld_x16_nowait(lanes + L::tO + ob * kC + t0, x);
                     const float4 *e4 = reinterpret_cast<const float4 *>(s->factor[kE] + t0);
+                    ptx::tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float4 f = e4[i];
+                        const uint64_t o01 = mul2(two(f.x, f.y), two(x[4 * i], x[4 * i + 1]));
+                        const uint64_t o23 = mul2(two(f.z, f.w), two(x[4 * i + 2], x[4 * i + 3]));
                         uint32_t o[4];
-                        halves(fma2(two(f.x, f.y), two(y[4 * i], y[4 * i + 1]),
-                                    two(x[4 * i], x[4 * i + 1])), o[0], o[1]);
-                        halves(fma2(two(f.z, f.w), two(y[4 * i + 2], y[4 * i + 3]),
-                                    two(x[4 * i + 2], x[4 * i + 3])), o[2], o[3]);
+                        halves(o01, o[0], o[1]);
+                        halves(o23, o[2], o[3]);
+                        const int r = t0 + 4 * i;
+                        if (NP == 3) {
+                            float *to = static_cast<float *>(a.out) + at + col;
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if (t0 + 4 * i + u < cnt) *to = O(__uint_as_float(o[u]));
-                            to += step;
+                            for (int u = 0; u < 4; ++u)
+                                if (r + u < cnt)
+                                    to[(size_t)(uint32_t)(r + u) * step] = __uint_as_float(o[u]);
+                        } else {
+                            const int odd = lane & 1;
+                            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.out) + at + (col - odd);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(
+                                    __uint_as_float(o[2 * u]), __uint_as_float(o[2 * u + 1]));
+                                const uint32_t own = *reinterpret_cast<const uint32_t *>(&b);
+                                const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+                                const int rr = r + 2 * u + odd;
+                                if (rr < cnt)
+                                    *reinterpret_cast<uint32_t *>(to + (size_t)(uint32_t)rr * step) =
+                                        __byte_perm(own, other, odd ? 0x3276 : 0x5410);
+                            }
                         }
                     }
                 }
-                arrive(s_gate_free[n % kSlots]);
+                ptx::tc_fence_before_sync();
+                arrive(s_o_free[ob]);
             }
         }
-    } else {
+    } else if (warp == 24 || warp == 25 || warp == 1) {
         // ---- P: lane = row of the chunk; two blocks of 16 columns each for warp 24 (rows 0-31,
-        // which reach no further), 25 and 29 (rows 32-63)
+        // which reach no further), 25 and 1 (rows 32-63)
         if (OUT) {
-            const int quad = warp % 4, i = quad * 32 + lane, from = warp == 29 ? 2 : 0;
+            const int quad = warp % 4, i = quad * 32 + lane, from = warp == 1 ? 2 : 0;
             const uint32_t lanes = tmem + ((uint32_t)quad << 21);
             uint8_t *row = s_base + L::kP + i * 128;
             if (warp == 24)  // zero once and for all: columns past the rows
@@ -672,51 +750,44 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     for (int j = 0; j < NP; ++j)
                         *reinterpret_cast<uint4 *>(row + j * L::kPPart + ((c ^ (i & 7)) * 16)) =
                             make_uint4(0, 0, 0, 0);
-            for (int n = 0;; ++n) {
-                Slot *s;
-                if (!gate(n, s)) break;
-                const int flags = s->flags;
-                if (flags & kEnd) break;
-                if (!wait(s_s_full, n & 1)) break;
-                if (n > 0 && !wait(s_o_full, (n & 1) ^ 1)) break;  // P of the chunk before is read
+            for (Turn t;; t.next()) {
+                if (gate(t) & kEnd) break;
+                const Slot *s = slots + t.slot;
+                const int sb = t.n % L::kSBufs;
+                if (!wait(s_s_full[sb], (t.n / L::kSBufs) & 1)) break;
+                if (s->cnt < kC) {  // rows past the chunk: V as V^T P^T takes it (K~'s warps see to
+                                    // the other product on their own)
+                    const int w3 = warp == 1 ? 2 : warp - 24, rows = kC - s->cnt;
+                    uint8_t *v = s_base + t.stage * L::kStage + L::kV + s->cnt * 128;
+                    for (int z = w3 * 32 + lane; z < rows * (DV / 8); z += 96)
+                        *reinterpret_cast<uint4 *>(v + z / (rows * 8) * kSlab + z % (rows * 8) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                // P of the chunk before has been read
+                if (t.n > 0 && !wait(s_o_full[(t.n - 1) & 1], ((t.n - 1) >> 1) & 1)) break;
                 ptx::tc_fence_after_sync();
-                const float ai = s->factor[kA][i];
-                const uint64_t a2 = two(ai, ai);
 #pragma unroll 1
                 for (int jb = from; jb < from + 2; ++jb) {
                     uint32_t x[16];
-                    uint64_t f[8];
-                    ptx::tmem_ld_x16_nowait(lanes + L::tS + jb * 16, x);
-                    if (flags & kMild) {
-                        const float4 *b4 = reinterpret_cast<const float4 *>(s->factor[kB] + jb * 16);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float4 b = b4[u];
-                            f[2 * u] = mul2(a2, two(b.x, b.y));
-                            f[2 * u + 1] = mul2(a2, two(b.z, b.w));
-                        }
-                    } else {
-                        // decays that span too much for factors around a middle (rare)
-                        const long long Li = s->L[i];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const int j = jb * 16 + 2 * u;
-                            f[u] = mul2(a2, two(exp2_single(Li - s->L[j]),
-                                                exp2_single(Li - s->L[j + 1])));
-                        }
-                    }
+                    ptx::tmem_ld_x16_nowait(lanes + L::tS + sb * kC + jb * 16, x);
+                    const float4 *b4 = reinterpret_cast<const float4 *>(s->factor[kB] + jb * 16);
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t out[NP][4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int u = 4 * c + e, j = jb * 16 + 2 * u;
-                            uint32_t y0, y1, part[NP];
-                            halves(mul2(two(x[2 * u], x[2 * u + 1]), f[u]), y0, y1);
-                            split_pair<NP>(two(j <= i ? y0 : 0u, j < i ? y1 : 0u), part);
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 b = b4[2 * c + h];
 #pragma unroll
-                            for (int q = 0; q < NP; ++q) out[q][e] = part[q];
+                            for (int e = 0; e < 2; ++e) {
+                                const int u = 8 * c + 4 * h + 2 * e, j = jb * 16 + u;
+                                uint32_t y0, y1, part[NP];
+                                halves(mul2(two(x[u], x[u + 1]), e ? two(b.z, b.w) : two(b.x, b.y)),
+                                       y0, y1);
+                                split_pair<NP>(two(j <= i ? y0 : 0u, j < i ? y1 : 0u), part);
+#pragma unroll
+                                for (int q = 0; q < NP; ++q) out[q][2 * h + e] = part[q];
+                            }
                         }
                         uint8_t *at = row + (((jb * 2 + c) ^ (i & 7)) * 16);
 #pragma unroll
@@ -728,14 +799,13 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 ptx::tc_fence_before_sync();
                 ptx::fence_proxy_async_smem();
                 arrive(s_p_full);
-                arrive(s_gate_free[n % kSlots]);
             }
         }
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
     if (tid == 0 && s_abort) report(a.status, TV_ERR_TIMEOUT);
-    if (warp == 1) {
+    if (warp == 2) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, L::kCols);
     }
@@ -858,7 +928,7 @@ bool prefill_tc_supported(const PrefillArgs &a) {
     const int64_t most = 1LL << 38;  // a tensor map's strides are below 2^40 bytes
     return a.qkv_dtype == TV_BF16 && a.decay == TV_DECAY_SCALAR && (a.dk == 64 || a.dk == 128) &&
            (a.dv == 64 || a.dv == 128) && a.R > 0 && a.q_stride < most && a.k_stride < most &&
-           a.v_stride < most;
+           a.v_stride < most && (int64_t)a.H * a.dv < 0x7fffffff;
 }
 
 size_t prefill_tc_workspace_bytes(const PrefillArgs &a) {
