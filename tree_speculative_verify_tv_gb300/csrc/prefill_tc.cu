@@ -46,10 +46,9 @@ namespace tv {
 namespace {
 
 constexpr int kC = 64;        // rows per chunk
-constexpr int kStages = 3;    // chunks of q, k, v in flight
-constexpr int kSlots = 5;     // see the plan's wait
+constexpr int kMaxStages = 3; // chunks of q, k, v in flight
 constexpr int kWarps = 32;
-constexpr int kScaleWarps = 6, kScoreWarps = 3;  // of K~ or V~, and of P
+constexpr int kScoreWarps = 3;  // of P
 constexpr int kThreadsT = kWarps * 32;
 constexpr int kWaitTries = 1 << 20;  // 7800 cycles each at most: some 4 s
 constexpr uint32_t kSlab = kC * 128; // 64 rows of 64 channels
@@ -80,9 +79,15 @@ template <int DK, int DV, int NP>
 struct Lay {
     static constexpr bool kScaleV = DV < DK;
     static constexpr int kX = kScaleV ? DV : DK;  // width of the scaled factor
+    // warps that scale it; what 64 channels do not need leaves one for the copies, which
+    // otherwise are the plan's
+    static constexpr int kScaleWarps = kX == 64 ? 4 : 6;
+    static constexpr bool kCopyWarp = kX == 64;
     static constexpr uint32_t kQ = 0, kK = DK * 128, kV = 2 * DK * 128,
                               kStage = (2 * DK + DV) * 128;
-    static constexpr int kXBufs = DK == 128 && DV == 128 ? 1 : 2;
+    static constexpr int kStages = DK == 128 && DV == 128 ? 2 : kMaxStages;
+    static constexpr int kSlots = kStages + 2;  // see the plan's wait
+    static constexpr int kXBufs = 2;
     static constexpr uint32_t kXt = kStages * kStage, kXPart = kX * 128, kXBuf = 3 * kXPart;
     static constexpr uint32_t kP = kXt + kXBufs * kXBuf, kPPart = kC * 128;
     static constexpr uint32_t kSlot0 = kP + NP * kPPart;
@@ -139,19 +144,37 @@ __device__ __forceinline__ void split_pair(uint64_t x, uint32_t (&part)[NP]) {
     part[NP - 1] = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// 2^(x 2^-32).
-__device__ __forceinline__ rec::Pair exp2_fixed(long long x) {
-    const long long n = (x + (1LL << 31)) >> 32;
-    const float f = (float)(int32_t)(x - (n << 32)) * 2.3283064365386963e-10f;
-    return rec::exp2_pair((float)(int)max(min(n, 4096LL), -4096LL), f);
+// g log2 e in 2^-32, by a whole product of the mantissa (|g| at most 2839: 4096 log2 units); 0 for
+// a NaN.
+__device__ __forceinline__ long long log2_fixed(float g) {
+    const float x = fminf(fabsf(g), 2839.f);
+    const uint32_t bits = __float_as_uint(x), m = (bits & 0x7FFFFFu) | 0x800000u;
+    // x = m 2^(e - 150), log2 e = 3098164009 2^-31: the product's unit is 2^(e - 181)
+    const uint32_t shift = 149u - (bits >> 23);  // 11 at least (and subnormals end as zero)
+    const unsigned long long y = shift < 64 ? (unsigned long long)m * 3098164009u >> shift : 0;
+    const long long z = g < 0.f ? -(long long)y : (long long)y;
+    return g == g ? z : 0;
 }
-// The same as one float, by the hardware's exponential (2^-22) of the fraction.
+
+// 2^(x 2^-32) as a whole power and the rest of at most half a unit.
+__device__ __forceinline__ void split_exponent(long long x, int &n, float &f) {
+    const int low = (int)(uint32_t)x;  // of 2^-32; from a half on it counts as negative
+    n = (int)(x >> 32) + ((uint32_t)low >> 31);
+    f = (float)low * 2.3283064365386963e-10f;
+}
+__device__ __forceinline__ rec::Pair exp2_fixed(long long x) {
+    int n;
+    float f;
+    split_exponent(x, n, f);
+    return rec::exp2_pair((float)n, f);
+}
+// The same as one float, by the hardware's exponential (2^-22) of the rest.
 __device__ __forceinline__ float exp2_single(long long x) {
-    const long long n = (x + (1LL << 31)) >> 32;
-    const float f = (float)(int32_t)(x - (n << 32)) * 2.3283064365386963e-10f;
-    float e;
+    int n;
+    float f, e;
+    split_exponent(x, n, f);
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
-    return e * __int_as_float(((int)max(min(n, 128LL), -127LL) + 127) << 23);
+    return e * __int_as_float((max(min(n, 128), -127) + 127) << 23);
 }
 
 // A CTA's walk over its chunks.  An item is a segment of a request and head; a CTA begins with
@@ -172,13 +195,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                       const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const TcParams p) {
     using L = Lay<DK, DV, NP>;
+    constexpr int kStages = L::kStages, kSlots = L::kSlots;
     constexpr int kQuads = DV / 32;           // quadrants of lanes that hold something
     constexpr int kChan = DK / 4;             // channels of a lane of the H warps
     extern __shared__ uint8_t s_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_empty[kStages], s_s_full[2],
-        s_p_full, s_x_full[2], s_x_free[2], s_h_full, s_h_free, s_d_full, s_d_free, s_o_full[2], s_o_free[2], s_drain[2], s_asked;
+    __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_s_full[2], s_p_full,
+        s_x_full[2], s_h_full, s_h_free, s_d_full[kStages], s_d_free, s_o_full[kStages], s_o_free[2], s_drain[2], s_asked;
     __shared__ __align__(16) uint64_t s_answer[2];
     const PrefillArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid % 32;
@@ -193,19 +217,17 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         for (int i = 0; i < kSlots; ++i) ptx::mbar_init(bar(s_gate[i]), 1);
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(bar(s_full[i]), 1);
-            ptx::mbar_init(bar(s_empty[i]), OUT ? 2 : 1);
+            ptx::mbar_init(bar(s_d_full[i]), 1);
+            ptx::mbar_init(bar(s_o_full[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(s_s_full[i]), 1);
-            ptx::mbar_init(bar(s_x_full[i]), kScaleWarps);
-            ptx::mbar_init(bar(s_x_free[i]), 1);
-            ptx::mbar_init(bar(s_o_full[i]), 1);
+            ptx::mbar_init(bar(s_x_full[i]), L::kScaleWarps);
             ptx::mbar_init(bar(s_o_free[i]), kQuads);
         }
         ptx::mbar_init(bar(s_p_full), kScoreWarps);
         ptx::mbar_init(bar(s_h_full), 4 * kQuads);
         ptx::mbar_init(bar(s_h_free), 1);
-        ptx::mbar_init(bar(s_d_full), 1);
         ptx::mbar_init(bar(s_d_free), 4 * kQuads);
         ptx::mbar_init(bar(s_drain[0]), 1);
         ptx::mbar_init(bar(s_drain[1]), 1);
@@ -264,6 +286,29 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         return (int)__reduce_or_sync(0xffffffffu, (uint32_t)slots[t.slot].flags);
     };
 
+    // The rows of a chunk on their way to a stage, by one lane; whole at t's phase of s_full.
+    const auto copy = [&](const Turn &t, int head, int row) {
+        if (lane == 0) {
+            const uint32_t at = base + t.stage * L::kStage, full = bar(s_full[t.stage]);
+            ptx::mbar_arrive_expect_tx(full, OUT ? L::kStage : L::kStage - L::kK);
+            ptx::tma_load_4d(at + L::kK, &map_k, 0, head, row, 0, full);
+            ptx::tma_load_4d(at + L::kV, &map_v, 0, head, row, 0, full);
+            if (OUT) ptx::tma_load_4d(at + L::kQ, &map_q, 0, head, row, 0, full);
+        }
+        __syncwarp();
+    };
+    // The products of the chunk that had t's stage are done.
+    const auto stage_free = [&](const Turn &t) {
+        return t.n < kStages || (wait(s_d_full[t.stage], t.stage_ph ^ 1) &&
+                                 (!OUT || wait(s_o_full[t.stage], t.stage_ph ^ 1)));
+    };
+    // Copies that nobody waited for (after a timeout) may not land later.
+    const auto copies_end = [&](int issued) {
+        if (*(volatile int *)&s_abort)
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                ptx::mbar_wait_tries(bar(s_full[i % kStages]), (i / kStages) & 1, 1 << 14);
+    };
+
     if (warp == 0) {
         // ---- plan, decays and copies
         Walk w{};
@@ -320,6 +365,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             const float *g = a.g + w.head;
             g0 = 2 * lane < cnt ? g[(size_t)t * a.g_stride] : 0.f;
             g1 = 2 * lane + 1 < cnt ? g[((size_t)t + 1) * a.g_stride] : 0.f;
+            // those of two chunks later come nearer: a load that has to go to memory takes longer
+            // than a chunk's turn
+            if (!w.done && t + 2 * kC + 1 < w.end) {
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(g + ((size_t)t + 2 * kC) * a.g_stride));
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(g + ((size_t)t + 2 * kC + 1) * a.g_stride));
+            }
         };
         fetch();
         long long total = 0;  // log2 of the item's decay so far
@@ -328,9 +379,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         Turn t;
         for (;; t.next()) {
             Slot *s = slots + t.slot;
-            // Chunk n - 3's products are done: its stage is free.  Chunk n - 5's outputs have been
-            // read, which the products of chunk n - 3 waited for, and with them its slot.
-            if (t.n >= kStages && !wait(s_empty[t.stage], t.stage_ph ^ 1)) break;
+            // Those products waited for the outputs of two chunks earlier to be read, so that chunk's
+            // slot is free.
+            if (!stage_free(t)) break;
             if (w.done) {
                 if (lane == 0) s->flags = kEnd;
                 arrive(s_gate[t.slot]);
@@ -341,26 +392,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 break;
             }
             const int row = w.row, head = w.head;
-            if (lane == 0) {
-                const uint32_t at = base + t.stage * L::kStage, full = bar(s_full[t.stage]);
-                ptx::mbar_arrive_expect_tx(full, OUT ? L::kStage : L::kStage - L::kK);
-                for (int c = 0; c < DK / 64; ++c) {
-                    if (OUT)
-                        ptx::tma_load_3d(at + L::kQ + c * kSlab, &map_q, c * 64, head, row, full);
-                    ptx::tma_load_3d(at + L::kK + c * kSlab, &map_k, c * 64, head, row, full);
-                }
-                for (int c = 0; c < DV / 64; ++c)
-                    ptx::tma_load_3d(at + L::kV + c * kSlab, &map_v, c * 64, head, row, full);
+            if (!L::kCopyWarp) {
+                copy(t, head, row);
+                issued = t.n + 1;
             }
-            __syncwarp();
-            issued = t.n + 1;
 
             int cnt = min(kC, w.end - row);
-            const float most = 2839.f;  // 4096 log2 units
             const bool nan0 = g0 != g0, nan1 = g1 != g1;
-            const double unit = 1.4426950408889634 * 4294967296.0;
-            const long long y0 = nan0 ? 0 : __double2ll_rn((double)fminf(fmaxf(g0, -most), most) * unit);
-            const long long y1 = nan1 ? 0 : __double2ll_rn((double)fminf(fmaxf(g1, -most), most) * unit);
+            const long long y0 = log2_fixed(g0), y1 = log2_fixed(g1);
             long long sum = y0 + y1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -421,10 +460,11 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             }
             total += end;
             total_nan |= any;
+            const rec::Pair d = exp2_fixed(end);
+            const float r = exp2_single(mid);
             if (lane == 0) {
-                const rec::Pair d = exp2_fixed(end);
                 s->d = any ? make_float2(nanf, nanf) : make_float2(d.hi, d.lo);
-                s->r = exp2_single(mid);
+                s->r = r;
                 s->row = row;
                 s->cnt = cnt;
                 s->head = head;
@@ -443,10 +483,18 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             }
             arrive(s_gate[t.slot]);
         }
-        // copies that nobody waited for (after a timeout)
-        if (*(volatile int *)&s_abort)
-            for (int i = max(0, issued - kStages); i < issued; ++i)
-                ptx::mbar_wait_tries(bar(s_full[i % kStages]), (i / kStages) & 1, 1 << 14);
+        copies_end(issued);
+    } else if (L::kCopyWarp && warp == 30) {
+        // ---- copies
+        int issued = 0;
+        for (Turn t;; t.next()) {
+            if (gate(t) & kEnd) break;
+            const int head = slots[t.slot].head, row = slots[t.slot].row;
+            if (!stage_free(t)) break;
+            copy(t, head, row);
+            issued = t.n + 1;
+        }
+        copies_end(issued);
     } else if (warp == 2) {
         // ---- what a chunk adds to the state: D^T = V^T K~ (or V~^T K)
         const uint32_t lead = ptx::elect_one();
@@ -472,9 +520,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     ptx::mma_bf16_lead(tmem + L::tD, L::kScaleV ? x : y, L::kScaleV ? y : x,
                                        ptx::idesc_bf16_f32_abmn(128, DK), part < 2 || kk > 0, lead);
                 }
-            ptx::mma_commit_lead(bar(s_d_full), lead);
-            ptx::mma_commit_lead(bar(s_x_free[xb]), lead);
-            ptx::mma_commit_lead(bar(s_empty[t.stage]), lead);
+            ptx::mma_commit_lead(bar(s_d_full[t.stage]), lead);
         }
         ptx::mma_commit_lead(bar(s_drain[0]), lead);
         __syncwarp();
@@ -541,8 +587,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 for (int kk = 0; kk < kC / 16; ++kk)
                     ptx::mma_bf16_lead(o, vd + kk * 128, pd + part * (L::kPPart / 16) + kk * 2,
                                        ptx::idesc_bf16_f32_amn(128, kC), 1, lead);
-            ptx::mma_commit_lead(bar(s_o_full[ob]), lead);
-            ptx::mma_commit_lead(bar(s_empty[t.stage]), lead);
+            ptx::mma_commit_lead(bar(s_o_full[t.stage]), lead);
             t = u;
             if (!(ok = !(gate(t) & kEnd))) break;
             if (!scored) {
@@ -555,11 +600,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         ptx::mma_commit_lead(bar(s_drain[1]), lead);
         __syncwarp();
         ptx::mbar_wait_tries(bar(s_drain[1]), 0, 1 << 18);
-    } else if (warp == 3 || (warp >= 26 && warp < 31)) {
-        // ---- K~ or V~: rows times 2^{d - L}, in three parts, laid out as the rows are.  Six
-        // threads to two rows; a quarter warp's eight rows keep their 16-byte pieces on different
+    } else if (warp == 3 || (warp >= 26 && warp < 25 + L::kScaleWarps)) {
+        // ---- K~ or V~: rows times 2^{d - L}, in three parts, laid out as the rows are.  A few
+        // threads to a row; a quarter warp's eight rows keep their 16-byte pieces on different
         // banks.
         const int i0 = (warp == 3 ? 0 : warp - 25) * 32 + lane, r = i0 % kC, sub = i0 / kC;
+        constexpr int kSubs = L::kScaleWarps / 2;
         const uint32_t line = r * 128, swz = (r & 7) * 16;
         for (Turn t;; t.next()) {
             if (gate(t) & kEnd) break;
@@ -570,21 +616,24 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             const uint64_t w2 = two(w, w);
             if (!wait(s_full[t.stage], t.stage_ph)) break;
             const int xb = t.n % L::kXBufs;
-            if (t.n >= L::kXBufs && !wait(s_x_free[xb], ((t.n / L::kXBufs) & 1) ^ 1)) break;
+            // (the product that read the buffer last)
+            if (t.n >= L::kXBufs && !wait(s_d_full[(t.n - L::kXBufs) % kStages],
+                                          ((t.n - L::kXBufs) / kStages) & 1))
+                break;
             uint8_t *st = s_base + t.stage * L::kStage;
             if (cnt < kC) {  // rows past the chunk may hold anything: the products take zeros
                 const uint4 zero = make_uint4(0, 0, 0, 0);
                 if (!live) {
-                    for (int c = sub; c < DV / 8; c += 3)
+                    for (int c = sub; c < DV / 8; c += kSubs)
                         *reinterpret_cast<uint4 *>(st + L::kV + c / 8 * kSlab + line + c % 8 * 16) = zero;
-                    for (int c = sub; c < DK / 8; c += 3)
+                    for (int c = sub; c < DK / 8; c += kSubs)
                         *reinterpret_cast<uint4 *>(st + L::kK + c / 8 * kSlab + line + c % 8 * 16) = zero;
                 }
             }
             const uint8_t *from = st + (L::kScaleV ? L::kV : L::kK);
             uint8_t *to = s_base + L::kXt + xb * L::kXBuf;
 #pragma unroll 2
-            for (int c = sub; c < L::kX / 8; c += 3) {
+            for (int c = sub; c < L::kX / 8; c += kSubs) {
                 const uint32_t at = c / 8 * kSlab + line + ((c % 8 * 16) ^ swz);
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (live) x = *reinterpret_cast<const uint4 *>(from + at);
@@ -654,7 +703,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     ptx::tc_fence_before_sync();
                     arrive(s_h_full);
                 }
-                if (!wait(s_d_full, t.n & 1)) break;
+                if (!wait(s_d_full[t.stage], t.stage_ph)) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll
                 for (int i0 = 0; i0 < kChan; i0 += 16) {
@@ -694,7 +743,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 const Slot *s = slots + t.slot;
                 const int cnt = s->cnt, ob = t.n & 1;
                 const size_t at = ((size_t)s->row * a.H + s->head) * DV;
-                if (!wait(s_o_full[ob], (t.n >> 1) & 1)) break;
+                if (!wait(s_o_full[t.stage], t.stage_ph)) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll 1
                 for (int t0 = 0; t0 < kC; t0 += 16) {
@@ -764,7 +813,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                             make_uint4(0, 0, 0, 0);
                 }
                 // P of the chunk before has been read
-                if (t.n > 0 && !wait(s_o_full[(t.n - 1) & 1], ((t.n - 1) >> 1) & 1)) break;
+                if (t.n > 0 && !wait(s_o_full[(t.n - 1) % kStages], ((t.n - 1) / kStages) & 1)) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll 1
                 for (int jb = from; jb < from + 2; ++jb) {
@@ -874,12 +923,14 @@ size_t cut_bytes(const PrefillArgs &a, int pieces) {
     return items * a.dk * a.dv * 4 + (items * 8 + 15) / 16 * 16;
 }
 
+// Boxes of 64 rows of one head, in slabs of 64 channels (the last dimension, so that a box is a
+// slab after the other).
 bool rows_map(CUtensorMap *m, const void *base, int width, int H, int R, int64_t stride) {
-    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)H, (cuuint64_t)R};
-    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, 1, kC}, one[3] = {1, 1, 1};
+    const cuuint64_t dims[4] = {64, (cuuint64_t)H, (cuuint64_t)R, (cuuint64_t)width / 64};
+    const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2, 128};
+    const cuuint32_t box[4] = {64, 1, kC, (cuuint32_t)width / 64}, one[4] = {1, 1, 1, 1};
     const auto encode = tcc::encode_fn();
-    return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+    return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims,
                             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
