@@ -30,8 +30,8 @@
 // The decays of D's product may stand with either factor: V~ = diag(2^{d - L}) V where dv is the
 // smaller (half the conversions at dk = 128, dv = 64), else K~.
 //
-// Roles (32 warps): plan, decays and copies (1), D's product (1), the outputs' products (1), K~ or
-// V~ (6), H (16), outputs (4), P (3).  D waits for nothing but H's sums of the chunk before, so
+// Roles (32 warps): plan and decays, copies, D's product, the outputs' products (one or two warps
+// in all for the first two, one each), K~ or V~ (4 to 8), H (16), outputs (4), P (3).  D waits for nothing but H's sums of the chunk before, so
 // that parts, outputs and scores stay off the chain from chunk to chunk.
 //
 // Few long prompts: the rows of a request are cut into segments.  A first launch computes what
@@ -79,14 +79,24 @@ template <int DK, int DV, int NP>
 struct Lay {
     static constexpr bool kScaleV = DV < DK;
     static constexpr int kX = kScaleV ? DV : DK;  // width of the scaled factor
-    // warps that scale it; what 64 channels do not need leaves one for the copies, which
-    // otherwise are the plan's
-    static constexpr int kScaleWarps = kX == 64 ? 4 : 6;
-    static constexpr bool kCopyWarp = kX == 64;
+    // Warps by role.  A warp reaches the lanes 32 (warp % 4) .. of tensor memory and issues from
+    // scheduler warp % 4: with dv = 64 nothing lies in the upper lanes, and what does not touch
+    // tensor memory goes to the warps that would be H's and the outputs' there.
+    //   always   2: D's product   31: the outputs' products   24, 25, 1: P
+    //   dv 128   0: plan, copies  4-19: H  20-23: outputs  3, 26-30: K~  (dk 64: 3, 26-28, 30 copies)
+    //   dv 64    22: plan  23: copies  quadrants 0, 1 of 4-19: H, 2, 3: V~ or K~  20, 21: outputs
+    static constexpr int kScaleWarps = DV == 64 ? 8 : kX == 64 ? 4 : 6;
+    static constexpr int kPlanWarp = DV == 64 ? 22 : 0;
+    static constexpr int kCopyWarp = DV == 64 ? 23 : kX == 64 ? 30 : -1;  // -1: the plan's
+    __device__ static int scale_index(int warp) {  // -1: not one of them
+        if (DV == 64)
+            return warp >= 4 && warp < 20 && warp % 4 >= 2 ? (warp - 4) / 4 * 2 + warp % 4 - 2 : -1;
+        return warp == 3 ? 0 : warp >= 26 && warp < 25 + kScaleWarps ? warp - 25 : -1;
+    }
     static constexpr uint32_t kQ = 0, kK = DK * 128, kV = 2 * DK * 128,
                               kStage = (2 * DK + DV) * 128;
     static constexpr int kStages = DK == 128 && DV == 128 ? 2 : kMaxStages;
-    static constexpr int kSlots = kStages + 2;  // see the plan's wait
+    static constexpr int kSlots = kStages + 3;  // see the plan's wait
     static constexpr int kXBufs = 2;
     static constexpr uint32_t kXt = kStages * kStage, kXPart = kX * 128, kXBuf = 3 * kXPart;
     static constexpr uint32_t kP = kXt + kXBufs * kXBuf, kPPart = kC * 128;
@@ -309,7 +319,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 ptx::mbar_wait_tries(bar(s_full[i % kStages]), (i / kStages) & 1, 1 << 14);
     };
 
-    if (warp == 0) {
+    const int scale = L::scale_index(warp);
+    if (warp == L::kPlanWarp) {
         // ---- plan, decays and copies
         Walk w{};
         const int per = OUT ? p.pieces : p.pieces - 1;
@@ -376,12 +387,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         long long total = 0;  // log2 of the item's decay so far
         bool total_nan = false;
         int issued = 0;
-        Turn t;
-        for (;; t.next()) {
+        for (Turn t;; t.next()) {
             Slot *s = slots + t.slot;
-            // Those products waited for the outputs of two chunks earlier to be read, so that chunk's
-            // slot is free.
-            if (!stage_free(t)) break;
             if (w.done) {
                 if (lane == 0) s->flags = kEnd;
                 arrive(s_gate[t.slot]);
@@ -392,11 +399,6 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 break;
             }
             const int row = w.row, head = w.head;
-            if (!L::kCopyWarp) {
-                copy(t, head, row);
-                issued = t.n + 1;
-            }
-
             int cnt = min(kC, w.end - row);
             const bool nan0 = g0 != g0, nan1 = g1 != g1;
             const long long y0 = log2_fixed(g0), y1 = log2_fixed(g1);
@@ -482,9 +484,17 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 }
             }
             arrive(s_gate[t.slot]);
+            // A chunk's decays are ready before its stage is free.  The products of the chunk that
+            // had the stage waited for the outputs of two chunks earlier to be read: the slot that
+            // the next turn takes is free.
+            if (!stage_free(t)) break;
+            if (L::kCopyWarp < 0) {
+                copy(t, head, row);
+                issued = t.n + 1;
+            }
         }
         copies_end(issued);
-    } else if (L::kCopyWarp && warp == 30) {
+    } else if (warp == L::kCopyWarp) {
         // ---- copies
         int issued = 0;
         for (Turn t;; t.next()) {
@@ -600,11 +610,11 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         ptx::mma_commit_lead(bar(s_drain[1]), lead);
         __syncwarp();
         ptx::mbar_wait_tries(bar(s_drain[1]), 0, 1 << 18);
-    } else if (warp == 3 || (warp >= 26 && warp < 25 + L::kScaleWarps)) {
+    } else if (scale >= 0) {
         // ---- K~ or V~: rows times 2^{d - L}, in three parts, laid out as the rows are.  A few
         // threads to a row; a quarter warp's eight rows keep their 16-byte pieces on different
         // banks.
-        const int i0 = (warp == 3 ? 0 : warp - 25) * 32 + lane, r = i0 % kC, sub = i0 / kC;
+        const int i0 = scale * 32 + lane, r = i0 % kC, sub = i0 / kC;
         constexpr int kSubs = L::kScaleWarps / 2;
         const uint32_t line = r * 128, swz = (r & 7) * 16;
         for (Turn t;; t.next()) {
