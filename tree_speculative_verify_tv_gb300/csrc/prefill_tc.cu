@@ -75,7 +75,7 @@ struct TcParams {
     int expire;     // test hook: leave the first chunk's copies out
 };
 
-template <int DK, int DV, int NP>
+template <int DK, int DV, int NP, bool OUT>
 struct Lay {
     static constexpr bool kScaleV = DV < DK;
     static constexpr int kX = kScaleV ? DV : DK;  // width of the scaled factor
@@ -85,13 +85,15 @@ struct Lay {
     //   always   2: D's product   31: the outputs' products   24, 25, 1: P
     //   dv 128   0: plan, copies  4-19: H  20-23: outputs  3, 26-30: K~  (dk 64: 3, 26-28, 30 copies)
     //   dv 64    22: plan  23: copies  quadrants 0, 1 of 4-19: H, 2, 3: V~ or K~  20, 21: outputs
-    static constexpr int kScaleWarps = DV == 64 ? 8 : kX == 64 ? 4 : 6;
+    // Without outputs 3 and 20-30 scale and 31 copies where dv is 128.
+    static constexpr int kScaleWarps = DV == 64 ? 8 : !OUT ? 12 : kX == 64 ? 4 : 6;
     static constexpr int kPlanWarp = DV == 64 ? 22 : 0;
-    static constexpr int kCopyWarp = DV == 64 ? 23 : kX == 64 ? 30 : -1;  // -1: the plan's
+    static constexpr int kCopyWarp = DV == 64 ? 23 : !OUT ? 31 : kX == 64 ? 30 : -1;  // -1: the plan's
     __device__ static int scale_index(int warp) {  // -1: not one of them
         if (DV == 64)
             return warp >= 4 && warp < 20 && warp % 4 >= 2 ? (warp - 4) / 4 * 2 + warp % 4 - 2 : -1;
-        return warp == 3 ? 0 : warp >= 26 && warp < 25 + kScaleWarps ? warp - 25 : -1;
+        const int from = OUT ? 26 : 20;
+        return warp == 3 ? 0 : warp >= from && warp < from - 1 + kScaleWarps ? warp - from + 1 : -1;
     }
     static constexpr uint32_t kQ = 0, kK = DK * 128, kV = 2 * DK * 128,
                               kStage = (2 * DK + DV) * 128;
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const TcParams p) {
-    using L = Lay<DK, DV, NP>;
+    using L = Lay<DK, DV, NP, OUT>;
     constexpr int kStages = L::kStages, kSlots = L::kSlots;
     constexpr int kQuads = DV / 32;           // quadrants of lanes that hold something
     constexpr int kChan = DK / 4;             // channels of a lane of the H warps
@@ -445,17 +447,20 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                            bad1 = __ballot_sync(0xffffffffu, nan1 && 2 * lane + 1 < cnt);
             const bool any = (bad0 | bad1) != 0;
             const float nanf = __int_as_float(0x7fffffff);
-            *reinterpret_cast<float2 *>(s->factor[kB] + 2 * lane) =
-                make_float2(exp2_single(mid - l0), exp2_single(mid - l1));
+            if (OUT)
+                *reinterpret_cast<float2 *>(s->factor[kB] + 2 * lane) =
+                    make_float2(exp2_single(mid - l0), exp2_single(mid - l1));
             *reinterpret_cast<float2 *>(s->factor[kW] + 2 * lane) =
                 make_float2(exp2_single(end - l0), exp2_single(end - l1));
-            float2 ev = make_float2(exp2_single(l0 - mid), exp2_single(l1 - mid));
-            if (any) {
-                const uint32_t upto = 0xffffffffu >> (31 - lane);
-                if ((bad0 & upto) || (bad1 & (upto >> 1))) ev.x = nanf;
-                if ((bad0 | bad1) & upto) ev.y = nanf;
+            if (OUT) {
+                float2 ev = make_float2(exp2_single(l0 - mid), exp2_single(l1 - mid));
+                if (any) {
+                    const uint32_t upto = 0xffffffffu >> (31 - lane);
+                    if ((bad0 & upto) || (bad1 & (upto >> 1))) ev.x = nanf;
+                    if ((bad0 | bad1) & upto) ev.y = nanf;
+                }
+                *reinterpret_cast<float2 *>(s->factor[kE] + 2 * lane) = ev;
             }
-            *reinterpret_cast<float2 *>(s->factor[kE] + 2 * lane) = ev;
             if (first) {
                 total = 0;
                 total_nan = false;
@@ -535,7 +540,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         ptx::mma_commit_lead(bar(s_drain[0]), lead);
         __syncwarp();
         ptx::mbar_wait_tries(bar(s_drain[0]), 0, 1 << 18);
-    } else if (warp == 31) {
+    } else if (OUT && warp == 31) {
         // ---- the outputs' products: S, H^T Q^T and V^T P^T
         const uint32_t lead = ptx::elect_one();
         const auto scores = [&](const Turn &t) {
@@ -552,7 +557,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             ptx::mma_commit_lead(bar(s_s_full[buf]), lead);
         };
         Turn t;
-        bool ok = OUT && !(gate(t) & kEnd);
+        bool ok = !(gate(t) & kEnd);
         if (ok) {
             ok = wait(s_full[0], 0);
             ptx::tc_fence_after_sync();
@@ -952,7 +957,7 @@ cudaError_t launch_kernel(const TcParams &p, const CUtensorMap *m, cudaStream_t 
     if (e != cudaSuccess) return e;
     const unsigned items = (unsigned)p.a.B * (OUT ? p.pieces : p.pieces - 1) * p.a.H;
     return launch_pdl(prefill_tc_kernel<DK, DV, NP, OUT>, dim3(items), dim3(kThreadsT),
-                      Lay<DK, DV, NP>::kBytes, s, m[0], m[1], m[2], p);
+                      Lay<DK, DV, NP, OUT>::kBytes, s, m[0], m[1], m[2], p);
 }
 
 template <int DK, int DV>
