@@ -516,9 +516,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         for (Turn t;; t.next()) {
             if (gate(t) & kEnd) break;
             const int xb = t.n % L::kXBufs;
-            if (!wait(s_x_full[xb], (t.n / L::kXBufs) & 1)) break;
             if (!wait(s_full[t.stage], t.stage_ph)) break;
             if (t.n > 0 && !wait(s_d_free, (t.n & 1) ^ 1)) break;
+            if (!wait(s_x_full[xb], (t.n / L::kXBufs) & 1)) break;
             ptx::tc_fence_after_sync();
             // descriptors move by their address field, in units of 16 bytes
             const uint32_t st = base + t.stage * L::kStage;
@@ -623,17 +623,25 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         constexpr int kSubs = L::kScaleWarps / 2;
         const uint32_t line = r * 128, swz = (r & 7) * 16;
         for (Turn t;; t.next()) {
-            if (gate(t) & kEnd) break;
+            // (what the chunk needs, tested together: a test that finds its phase complete takes
+            // a few hundred cycles when shared memory is busy)
+            const int was = t.n - L::kXBufs;  // the chunk whose product read the buffer last
+            const bool all = __all_sync(
+                0xffffffffu,
+                ptx::mbar_test_wait(bar(s_gate[t.slot]), t.slot_ph) &
+                    ptx::mbar_test_wait(bar(s_full[t.stage]), t.stage_ph) &
+                    (was < 0 ||
+                     ptx::mbar_test_wait(bar(s_d_full[was % kStages]), (was / kStages) & 1)));
+            if (!all && !wait(s_gate[t.slot], t.slot_ph)) break;
             const Slot *s = slots + t.slot;
+            if (__any_sync(0xffffffffu, s->flags & kEnd)) break;
             const int cnt = s->cnt;
             const bool live = r < cnt;
             const float w = live ? s->factor[kW][r] : 0.f;  // (past the chunk it may be infinite)
             const uint64_t w2 = two(w, w);
-            if (!wait(s_full[t.stage], t.stage_ph)) break;
             const int xb = t.n % L::kXBufs;
-            // (the product that read the buffer last)
-            if (t.n >= L::kXBufs && !wait(s_d_full[(t.n - L::kXBufs) % kStages],
-                                          ((t.n - L::kXBufs) / kStages) & 1))
+            if (!all && (!wait(s_full[t.stage], t.stage_ph) ||
+                         (was >= 0 && !wait(s_d_full[was % kStages], (was / kStages) & 1))))
                 break;
             uint8_t *st = s_base + t.stage * L::kStage;
             if (cnt < kC) {  // rows past the chunk may hold anything: the products take zeros
@@ -675,9 +683,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const uint32_t lanes = tmem + ((uint32_t)quad << 21);  // lane quad * 32
         if (quad < kQuads) {
             uint64_t h[kChan / 2];
-            for (Turn t;; t.next()) {
-                const int flags = gate(t);
-                if (flags & kEnd) break;
+            Turn t;
+            int flags = gate(t);
+            while (!(flags & kEnd)) {
                 const Slot *s = slots + t.slot;
                 if (flags & kFirst) {
                     const long long src = s->src;
@@ -693,9 +701,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 }
                 if (OUT) {
                     const uint64_t r2 = two(s->r, s->r);
-                    // the chunk's before are read
-                    if (t.n > 0 && !wait(s_h_free, (t.n & 1) ^ 1)) break;
-                    ptx::tc_fence_after_sync();
+                    bool ok = true;
 #pragma unroll
                     for (int i0 = 0; i0 < kChan / 2; i0 += 8) {
                         uint32_t part[NP][8];
@@ -706,10 +712,15 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 #pragma unroll
                             for (int j = 0; j < NP; ++j) part[j][i] = x[j];
                         }
+                        if (i0 == 0 && t.n > 0) {  // the chunk's before are read
+                            if (!(ok = wait(s_h_free, (t.n & 1) ^ 1))) break;
+                            ptx::tc_fence_after_sync();
+                        }
 #pragma unroll
                         for (int j = 0; j < NP; ++j)
                             ptx::tmem_st_x8(lanes + L::tH + j * (DK / 2) + c0 / 2 + i0, part[j]);
                     }
+                    if (!ok) break;
                     ptx::tmem_wait_st();
                 }
                 const uint64_t dx = two(s->d.x, s->d.x), dy = two(s->d.y, s->d.y);
@@ -718,6 +729,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     ptx::tc_fence_before_sync();
                     arrive(s_h_full);
                 }
+                // (the next chunk's flags while D is on its way)
+                Turn u = t;
+                u.next();
+                const int next = gate(u);
                 if (!wait(s_d_full[t.stage], t.stage_ph)) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll
@@ -744,6 +759,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                         to[(c0 + 2 * i + 1) * DV + col] = __uint_as_float(y);
                     }
                 }
+                t = u;
+                flags = next;
             }
         }
     } else if (warp >= 20 && warp < 24) {
