@@ -94,6 +94,56 @@ def test_single_precision_outputs_keep_it():
         assert np.linalg.norm(x - y) <= 1e-6 * np.linalg.norm(y)
 
 
+def test_cuts_without_a_state():
+    run(24, [4000, 130], 2, 64, 64, out32=False, decay=0.02)
+
+
+def test_two_streams_and_threads():
+    """Calls at the same time, each with a workspace of its own, give what they give alone."""
+    import threading
+
+    import torch
+    rows = [Rows(np.random.default_rng(25 + i), lens, 2, 128, dv) for i, (lens, dv) in
+            enumerate([([2000, 5], 64), ([64] * 9, 128)])]
+    want = [[x.clone() for x in r.prefill()[:2]] for r in rows]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(8):
+                got = rows[i].prefill(stream=stream)
+                stream.synchronize()
+                if int(got[2][0]) or not all(torch.equal(x, y) for x, y in zip(want[i], got)):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_resets_and_mixed_decays():
+    """Rows that forget everything (as between packed documents: -inf, or so large that 2^4096 is
+    left behind), beside rows that keep all of it."""
+    import torch
+    rng = np.random.default_rng(27)
+    r = Rows(rng, [300, 64], 2, 128, 64)
+    g = r.g.clone()
+    g[:] = 0.0
+    g[50], g[51], g[130], g[191], g[320, 1] = -3000.0, -200.0, -1e30, -float("inf"), -float("inf")
+    g[200:240] = -2.5
+    r.g, r.host["g"] = g, g.cpu().numpy().astype(np.float64)
+    H0, h0 = r.state(rng)
+    for out32 in (False, True):
+        got = r.prefill(H0, out32)
+        torch.cuda.synchronize()
+        r.check(got, h0, out32)
+
+
 def test_max_rows_is_only_a_bound():
     for max_rows in (200, 1000, 1 << 20):
         run(9, [200, 150], 2, 128, 128, max_rows=max_rows)
