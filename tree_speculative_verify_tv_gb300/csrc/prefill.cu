@@ -6,9 +6,9 @@
 //
 // A CTA takes 16 columns of one (request, head) and walks down the rows.  Eight lanes share a
 // column, each with 4 ceil(dk / 32) rows of the state in registers; blocks of kRows rows of
-// q, k, v land in shared memory by asynchronous copies a block ahead.  5 dk dv / 128 cycles of
-// an SM a row and head (the decay's second part takes one of them) against dk-sized loads:
-// instructions bound it.
+// q, k, v land in shared memory by asynchronous copies a block ahead.  A pair of the state takes
+// four packed instructions (one for the decay's second part) against dk-sized loads: instructions
+// bound it.
 #include "recurrence.cuh"
 #include "tc_ptx.cuh"
 
@@ -16,23 +16,23 @@ namespace tv {
 namespace {
 
 constexpr int kThreadsP = 128;
-constexpr int kCols = 16;  // columns per CTA
+constexpr int kCols = 16;  // columns per CTA, one or two times
 constexpr int kRows = 8;   // rows per block of copies
 
-template <typename E, bool DIAG, int R>
+template <typename E, bool DIAG, int R, int N>
 struct RowsSmem {
-    E k[2][kRows][32 * R], q[2][kRows][32 * R], v[2][kRows][kCols];
+    E k[2][kRows][32 * R], q[2][kRows][32 * R], v[2][kRows][N * kCols];
     rec::Pair d[2][kRows][DIAG ? 32 * R : 1];
 };
 
-// R: groups of 32 key rows.
-template <typename E, bool DIAG, int R>
+// R: groups of 32 key rows; N: columns of a thread.
+template <typename E, bool DIAG, int R, int N>
 __global__ void __launch_bounds__(kThreadsP) prefill_rows_kernel(PrefillArgs a) {
     extern __shared__ __align__(16) uint8_t s_raw[];
-    auto &s = *reinterpret_cast<RowsSmem<E, DIAG, R> *>(s_raw);
+    auto &s = *reinterpret_cast<RowsSmem<E, DIAG, R, N> *>(s_raw);
     constexpr int kPiece = 16 / sizeof(E);  // elements per copy
     const int unit = blockIdx.x, b = unit / a.H, h = unit % a.H, tid = threadIdx.x;
-    const int c0 = blockIdx.y * kCols, cols = min(kCols, a.dv - c0);
+    const int c0 = blockIdx.y * N * kCols, cols = min(N * kCols, a.dv - c0);
     const int r = tid % 8, col = tid / 8;
     pdl_wait();
     pdl_launch_next();
@@ -48,14 +48,17 @@ __global__ void __launch_bounds__(kThreadsP) prefill_rows_kernel(PrefillArgs a) 
         s.q[t / kRows][t % kRows][c] = E(0.f);
         if (DIAG) s.d[t / kRows][t % kRows][c] = {0.f, 0.f};
     }
-    const bool live = col < cols;
     const size_t state = (size_t)unit * a.dk * a.dv + c0 + col;
-    float x[4 * R];
+    Two x[N][2 * R];  // pairs of rows
 #pragma unroll
-    for (int i = 0; i < 4 * R; ++i) {
-        const int row = (i / 4) * 32 + 4 * r + i % 4;
-        x[i] = a.H0 && live && row < a.dk ? a.H0[state + (size_t)row * a.dv] : 0.f;
-    }
+    for (int w = 0; w < N; ++w)
+#pragma unroll
+        for (int i = 0; i < 2 * R; ++i) {
+            const int row = (i / 2) * 32 + 4 * r + i % 2 * 2;  // (dk is even)
+            const bool have = a.H0 && col + w * kCols < cols && row < a.dk;
+            const float *from = a.H0 + state + w * kCols;
+            x[w][i] = have ? two(from[(size_t)row * a.dv], from[(size_t)(row + 1) * a.dv]) : 0;
+        }
 
     constexpr int kGates = DIAG ? kRows * 32 * R / kThreadsP : 1;
     float gates[kGates];
@@ -94,48 +97,84 @@ __global__ void __launch_bounds__(kThreadsP) prefill_rows_kernel(PrefillArgs a) 
         ptx::cp_async_wait_all();
         __syncthreads();
         if (t0 + kRows < n) fetch(t0 + kRows, buf ^ 1);
-        float mine = 0.f;
+        float mine[N] = {};
 #pragma unroll 2
         for (int t = 0; t < cnt; ++t) {
-            const float vc = to_f32(s.v[buf][t][col]);
-            rec::Pair d = s.d[buf][t][0];
-            float o = 0.f;
+            const rec::Pair d = s.d[buf][t][0];
+            Two v2[N], hi = two(d.hi, d.hi), lo = two(d.lo, d.lo), o2[N] = {};
+#pragma unroll
+            for (int w = 0; w < N; ++w) {
+                const float vc = to_f32(s.v[buf][t][col + w * kCols]);
+                v2[w] = two(vc, vc);
+            }
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int c = i * 32 + 4 * r;
                 const float4 k4 = rec::load4(&s.k[buf][t][c]), q4 = rec::load4(&s.q[buf][t][c]);
-                const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+                const Two kk[2] = {two(k4.x, k4.y), two(k4.z, k4.w)};
+                const Two qq[2] = {two(q4.x, q4.y), two(q4.z, q4.w)};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (DIAG) d = s.d[buf][t][c + e];
-                    float &y = x[4 * i + e];
-                    y = fmaf(y, d.hi, fmaf(y, d.lo, kk[e] * vc));
-                    o = fmaf(y, qq[e], o);
+                for (int e = 0; e < 2; ++e) {
+                    if (DIAG) {
+                        const rec::Pair d0 = s.d[buf][t][c + 2 * e], d1 = s.d[buf][t][c + 2 * e + 1];
+                        hi = two(d0.hi, d1.hi);
+                        lo = two(d0.lo, d1.lo);
+                    }
+#pragma unroll
+                    for (int w = 0; w < N; ++w) {
+                        Two &y = x[w][2 * i + e];
+                        y = fma2(y, hi, fma2(y, lo, mul2(kk[e], v2[w])));
+                        o2[w] = fma2(y, qq[e], o2[w]);
+                    }
                 }
             }
-            o += __shfl_xor_sync(0xffffffffu, o, 1);
-            o += __shfl_xor_sync(0xffffffffu, o, 2);
-            o += __shfl_xor_sync(0xffffffffu, o, 4);
-            if (t == r) mine = o;
+#pragma unroll
+            for (int w = 0; w < N; ++w) {
+                const float2 os = halves(o2[w]);
+                float o = os.x + os.y;
+                o += __shfl_xor_sync(0xffffffffu, o, 1);
+                o += __shfl_xor_sync(0xffffffffu, o, 2);
+                o += __shfl_xor_sync(0xffffffffu, o, 4);
+                if (t == r) mine[w] = o;
+            }
         }
-        if (live && r < cnt)
-            rec::store_out(a.out, a.out_f32,
-                           (((size_t)off + t0 + r) * a.H + h) * a.dv + c0 + col, mine);
+#pragma unroll
+        for (int w = 0; w < N; ++w)
+            if (col + w * kCols < cols && r < cnt)
+                rec::store_out(a.out, a.out_f32,
+                               (((size_t)off + t0 + r) * a.H + h) * a.dv + c0 + col + w * kCols,
+                               mine[w]);
     }
 #pragma unroll
-    for (int i = 0; i < 4 * R; ++i) {
-        const int row = (i / 4) * 32 + 4 * r + i % 4;
-        if (live && row < a.dk) a.H_new[state + (size_t)row * a.dv] = x[i];
-    }
+    for (int w = 0; w < N; ++w)
+#pragma unroll
+        for (int i = 0; i < 2 * R; ++i) {
+            const int row = (i / 2) * 32 + 4 * r + i % 2 * 2;
+            const float2 y = halves(x[w][i]);
+            float *to = a.H_new + state + w * kCols;
+            if (col + w * kCols < cols && row < a.dk) {
+                to[(size_t)row * a.dv] = y.x;
+                to[(size_t)(row + 1) * a.dv] = y.y;
+            }
+        }
+}
+
+constexpr int kTwo = 2;
+
+template <typename E, bool DIAG, int R, int N>
+cudaError_t launch_columns(const PrefillArgs &a, cudaStream_t s) {
+    const cudaError_t e = configure_smem_once(prefill_rows_kernel<E, DIAG, R, N>, false);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(prefill_rows_kernel<E, DIAG, R, N>,
+                      dim3((unsigned)(a.B * a.H), (unsigned)((a.dv + N * kCols - 1) / (N * kCols))),
+                      dim3(kThreadsP), sizeof(RowsSmem<E, DIAG, R, N>), s, a);
 }
 
 template <typename E, bool DIAG, int R>
 cudaError_t launch_rows(const PrefillArgs &a, cudaStream_t s) {
-    const cudaError_t e = configure_smem_once(prefill_rows_kernel<E, DIAG, R>, false);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(prefill_rows_kernel<E, DIAG, R>,
-                      dim3((unsigned)(a.B * a.H), (unsigned)((a.dv + kCols - 1) / kCols)),
-                      dim3(kThreadsP), sizeof(RowsSmem<E, DIAG, R>), s, a);
+    // Two columns a thread halve the loads of q and k per column, where that leaves enough CTAs.
+    const bool two = (long long)a.B * a.H * ((a.dv + 2 * kCols - 1) / (2 * kCols)) >= kTwo * device_sms();
+    return two ? launch_columns<E, DIAG, R, 2>(a, s) : launch_columns<E, DIAG, R, 1>(a, s);
 }
 
 template <typename E, bool DIAG>

@@ -111,39 +111,21 @@ struct Lay {
     static_assert(kBytes <= tcc::kSmemLimit - 512, "shared memory");
 };
 
-// Two floats in a register pair, for the packed fp32 instructions.
-__device__ __forceinline__ uint64_t two(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t two(uint32_t lo, uint32_t hi) {
-    uint64_t r;
+// (bits of floats, as tensor memory and shared memory hold them)
+using tv::halves;
+using tv::two;
+__device__ __forceinline__ Two two(uint32_t lo, uint32_t hi) {
+    Two r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
     return r;
 }
-__device__ __forceinline__ void halves(uint64_t x, uint32_t &lo, uint32_t &hi) {
+__device__ __forceinline__ void halves(Two x, uint32_t &lo, uint32_t &hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 // A pair as NP packed pairs of bf16 parts: upper bits cut off, the last part rounded.
 template <int NP>
-__device__ __forceinline__ void split_pair(uint64_t x, uint32_t (&part)[NP]) {
+__device__ __forceinline__ void split_pair(Two x, uint32_t (&part)[NP]) {
     uint32_t b0, b1;
 #pragma unroll
     for (int p = 0; p + 1 < NP; ++p) {
@@ -643,7 +625,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             const int cnt = s->cnt;
             const bool live = r < cnt;
             const float w = live ? s->factor[kW][r] : 0.f;  // (past the chunk it may be infinite)
-            const uint64_t w2 = two(w, w);
+            const Two w2 = two(w, w);
             const int xb = t.n % L::kXBufs;
             if (!all && (!wait(s_full[t.stage], t.stage_ph) ||
                          (was >= 0 && !wait(s_d_full[was % kStages], (was / kStages) & 1))))
@@ -687,7 +669,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const int quad = warp % 4, c0 = (warp - 4) / 4 * kChan, col = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)quad << 21);  // lane quad * 32
         if (quad < kQuads) {
-            uint64_t h[kChan / 2];
+            Two h[kChan / 2];
             Turn t;
             int flags = gate(t);
             while (!(flags & kEnd)) {
@@ -705,7 +687,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                                     : 0;
                 }
                 if (OUT) {
-                    const uint64_t r2 = two(s->r, s->r);
+                    const Two r2 = two(s->r, s->r);
                     bool ok = true;
 #pragma unroll
                     for (int i0 = 0; i0 < kChan / 2; i0 += 8) {
@@ -728,7 +710,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     if (!ok) break;
                     ptx::tmem_wait_st();
                 }
-                const uint64_t dx = two(s->d.x, s->d.x), dy = two(s->d.y, s->d.y);
+                const Two dx = two(s->d.x, s->d.x), dy = two(s->d.y, s->d.y);
                 const long long dst = s->dst;
                 if (OUT) {
                     ptx::tc_fence_before_sync();
@@ -747,7 +729,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        uint64_t &y = h[i0 / 2 + i];
+                        Two &y = h[i0 / 2 + i];
                         y = fma2(y, dx, fma2(y, dy, two(x[2 * i], x[2 * i + 1])));
                     }
                 }
@@ -791,8 +773,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float4 f = e4[i];
-                        const uint64_t o01 = mul2(two(f.x, f.y), two(x[4 * i], x[4 * i + 1]));
-                        const uint64_t o23 = mul2(two(f.z, f.w), two(x[4 * i + 2], x[4 * i + 3]));
+                        const Two o01 = mul2(two(f.x, f.y), two(x[4 * i], x[4 * i + 1]));
+                        const Two o23 = mul2(two(f.z, f.w), two(x[4 * i + 2], x[4 * i + 3]));
                         uint32_t o[4];
                         halves(o01, o[0], o[1]);
                         halves(o23, o[2], o[3]);

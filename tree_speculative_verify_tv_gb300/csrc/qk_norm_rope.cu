@@ -30,31 +30,9 @@ constexpr int kUnroll = 4;   // heads whose loads are in flight together
 template <typename E>
 constexpr int kPerSm = sizeof(E) == 2 ? 3 : 2;
 
-// Two floats in a register pair, for the packed fp32 instructions.
-using Two = unsigned long long;
-__device__ __forceinline__ Two two(float lo, float hi) {
-    Two r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 halves(Two x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
 __device__ __forceinline__ Two swap(Two x) {
     const float2 y = halves(x);
     return two(y.y, y.x);
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-    Two r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-    Two r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 // Four channels as they lie in memory.
