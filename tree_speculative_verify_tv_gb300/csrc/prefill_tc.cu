@@ -359,18 +359,22 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             }
         };
         next_item(true);
-        float g0 = 0.f, g1 = 0.f;
-        const auto fetch = [&]() {  // the decays of the chunk at w
-            const int t = w.row + 2 * lane, cnt = w.done ? 0 : min(kC, w.end - w.row);
-            const float *g = a.g + w.head;
-            g0 = 2 * lane < cnt ? g[(size_t)t * a.g_stride] : 0.f;
-            g1 = 2 * lane + 1 < cnt ? g[((size_t)t + 1) * a.g_stride] : 0.f;
-            // those of two chunks later come nearer: a load that has to go to memory takes longer
-            // than a chunk's turn
-            if (!w.done && t + 2 * kC + 1 < w.end) {
-                asm volatile("prefetch.global.L1 [%0];" ::"l"(g + ((size_t)t + 2 * kC) * a.g_stride));
-                asm volatile("prefetch.global.L1 [%0];" ::"l"(g + ((size_t)t + 2 * kC + 1) * a.g_stride));
-            }
+        // decays of the chunk at w, and of the 64 rows that begin at `ahead`, on their way from memory
+        // for a whole turn
+        float g0 = 0.f, g1 = 0.f, next0 = 0.f, next1 = 0.f;
+        int ahead = -1;
+        const auto load = [&](int row, float &x0, float &x1) {
+            const int t = row + 2 * lane;
+            const float *g = a.g + w.head + (size_t)t * a.g_stride;
+            x0 = !w.done && t < w.end ? g[0] : 0.f;
+            x1 = !w.done && t + 1 < w.end ? g[a.g_stride] : 0.f;
+        };
+        const auto fetch = [&]() {
+            g0 = next0;
+            g1 = next1;
+            if (w.first || w.row != ahead) load(w.row, g0, g1);
+            ahead = w.row + kC;
+            load(ahead, next0, next1);
         };
         fetch();
         long long total = 0;  // log2 of the item's decay so far
@@ -831,7 +835,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                         *reinterpret_cast<uint4 *>(v + z / (rows * 8) * kSlab + z % (rows * 8) * 16) =
                             make_uint4(0, 0, 0, 0);
                 }
-                // P of the chunk before has been read
+                // P of the chunk before has been read (a second buffer of P gained nothing)
                 if (t.n > 0 && !wait(s_o_full[(t.n - 1) % kStages], ((t.n - 1) / kStages) & 1)) break;
                 ptx::tc_fence_after_sync();
 #pragma unroll 1
