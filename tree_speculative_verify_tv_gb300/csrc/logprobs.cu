@@ -11,8 +11,9 @@
 //
 // Top tokens without another pass: threads form 64 groups with a maximum each.  The K-th largest
 // of these, tau, is no larger than the K-th largest element, so the K are among the elements
-// >= tau, which only the threads whose own maximum reaches tau have: those few threads' parts
-// are read again (from L2), by whole warps.  Equal values at tau beyond what the list holds
+// >= tau, which only the threads whose own maximum reaches tau have: those few read the turn of
+// their maximum again, or all of their part if another turn reaches tau too (4096 rows of 131072
+// bf16: 14 % more bytes from memory with whole parts, rows being far out of L2 by then).  Equal values at tau beyond what the list holds
 // (constant or masked rows) are found in index order instead, and rows with a NaN, or a list
 // that still overflows, by K searches.  Keys are (value, -index), so all of it is exact.
 #include <cooperative_groups.h>
@@ -210,6 +211,9 @@ __global__ void __launch_bounds__(NT, kPerSmThreads / NT) logprobs_kernel(Logpro
     float at_token = 0.f;  // (on its way while the row is read)
     if (tid == 0 && part == 0 && token >= 0 && token < V) at_token = to_f32(x[token]);
     Sums mine{-INFINITY, 0.f, 0.f};
+    // of this thread's turns: the largest value, where it came first, and the largest of the others
+    float first = -INFINITY, second = -INFINITY;
+    int where = v0 + tid;
     for (int v = v0 + tid; v < v1; v += NT * kUnroll) {
         uint4 w[kUnroll];
 #pragma unroll
@@ -217,7 +221,12 @@ __global__ void __launch_bounds__(NT, kPerSmThreads / NT) logprobs_kernel(Logpro
             w[u] = v + u * NT < v1 ? __ldg(x4 + v + u * NT)
                                    : make_uint4(P::kNothing, P::kNothing, P::kNothing, P::kNothing);
         const float most = P::largest(w);
-        if (most > mine.m) mine.move(most, c);
+        second = fmaxf(second, fminf(most, first));
+        if (most > first) {
+            first = most;
+            where = v;
+            mine.move(most, c);
+        }
         const float m = mine.m > -INFINITY ? mine.m : 0.f;
         const Two less = two(-m, -m), c2 = two(c, c);
         Two z = 0, t = 0;
@@ -237,9 +246,8 @@ __global__ void __launch_bounds__(NT, kPerSmThreads / NT) logprobs_kernel(Logpro
         mine.t += ts.x + ts.y;
     }
     if (loose >= 0) mine.add(to_f32(x[loose]), c);
-    const float own = mine.m;  // the largest of this thread's
 
-    float g = own;
+    float g = mine.m;
     if (NT == 4 * kGroups) {
         g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
         g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__(NT, kPerSmThreads / NT) logprobs_kernel(Logpro
     } else {
         s.group[tid] = g;
     }
-    float most = own;
+    float most = mine.m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     mine.move(most, c);
@@ -283,7 +291,22 @@ __global__ void __launch_bounds__(NT, kPerSmThreads / NT) logprobs_kernel(Logpro
                     if (at < kList) s.list[at] = make_key(y, i);
                 }
             };
-            uint32_t who = __ballot_sync(0xffffffffu, equal ? own >= tau : own > tau);
+            const bool has = equal ? first >= tau : first > tau;
+            const bool more = equal ? second >= tau : second > tau;
+            // a thread whose values all came in one turn reads that one again; the others' parts are
+            // read by whole warps
+            if (has && !more) {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int v = where + u * NT;
+                    if (v < v1) {
+                        const uint4 w = __ldg(x4 + v);
+#pragma unroll
+                        for (int e = 0; e < P::kN; ++e) put(P::at(w, e), ahead + v * P::kN + e);
+                    }
+                }
+            }
+            uint32_t who = __ballot_sync(0xffffffffu, more);
             while (who) {
                 const int t = warp * 32 + __ffs(who) - 1;  // this thread's pieces
                 who &= who - 1;
