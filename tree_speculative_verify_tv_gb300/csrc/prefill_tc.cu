@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_s_full[2], s_p_full,
-        s_x_full[2], s_h_full, s_h_free, s_d_full[kStages], s_d_free, s_o_full[kStages], s_o_free[2], s_drain[2], s_asked;
+        s_x_full[2], s_h_full, s_h_free, s_d_full[kStages], s_d_free, s_o_full[kStages], s_o_free[2],
+        s_copied, s_drain[2], s_asked;
     __shared__ __align__(16) uint64_t s_answer[2];
     const PrefillArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid % 32;
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         ptx::mbar_init(bar(s_h_full), 4 * kQuads);
         ptx::mbar_init(bar(s_h_free), 1);
         ptx::mbar_init(bar(s_d_free), 4 * kQuads);
+        ptx::mbar_init(bar(s_copied), 1);
         ptx::mbar_init(bar(s_drain[0]), 1);
         ptx::mbar_init(bar(s_drain[1]), 1);
         ptx::mbar_init(bar(s_asked), 1);
@@ -483,8 +485,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             // A chunk's decays are ready before its stage is free.  The products of the chunk that
             // had the stage waited for the outputs of two chunks earlier to be read: the slot that
             // the next turn takes is free.
-            if (!stage_free(t)) break;
-            if (L::kCopyWarp < 0) {
+            // (With a warp for the copies it is that one's word: chunk n's products may be done, and
+            // their barriers a phase on, before the plan has looked at them.)
+            if (L::kCopyWarp >= 0) {
+                if (!wait(s_copied, t.n & 1)) break;
+            } else {
+                if (!stage_free(t)) break;
                 copy(t, head, row);
                 issued = t.n + 1;
             }
@@ -497,6 +503,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             if (gate(t) & kEnd) break;
             const int head = slots[t.slot].head, row = slots[t.slot].row;
             if (!stage_free(t)) break;
+            arrive(s_copied);  // (head and row have been read too)
             copy(t, head, row);
             issued = t.n + 1;
         }
