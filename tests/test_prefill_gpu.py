@@ -169,6 +169,34 @@ def test_in_place_and_in_pieces(dk):
     r.check((torch.cat(outs), H, torch.zeros(1)), h0)
 
 
+def test_decays_past_any_count_over_many_rows():
+    """Half a million rows a segment that each leave 2^4096 behind: the segment's decay is 0, although
+    its logarithm is past what a 64-bit sum of 2^-32 holds.  An output is its own row's product."""
+    import torch
+    import tree_speculative_verify_tv_gb300 as tv
+    n, d = (1 << 20) + 128, 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(n, d, generator=gen, device="cuda").bfloat16() for _ in range(3))
+    H0 = torch.randn(1, 1, d, d, generator=gen, device="cuda")
+    g = torch.full((1,), -float("inf"), device="cuda")
+    out = torch.full((n, 1, d), float("nan"), device="cuda")
+    H_new, status = torch.full_like(H0, float("nan")), torch.zeros(1, dtype=torch.int32, device="cuda")
+    size = 2 * (d * d * 4 + 8)  # for two segments
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    tv.tv_prefill(1, n, n, 1, d, d, tv.TV_DECAY_SCALAR, tv.TV_BF16,
+                  torch.tensor([0, n], dtype=torch.int32, device="cuda"), H0, q, d, k, d, v, d, g, 0,
+                  tv.TV_F32, out, H_new, ws, size, status)
+    torch.cuda.synchronize()
+    assert int(status[0]) == 0
+    q, k, v = q.double(), k.double(), v.double()
+    want = (q * k).sum(1, keepdim=True) * v
+    # 64 products accumulated (2^-23 a step of 16 and its inside), three parts of the weight
+    bound = 2.0 ** -19 * (q * k).abs().sum(1, keepdim=True) * v.abs()
+    assert ((out[:, 0] - want).abs() <= bound).all()
+    state = k[-1][:, None] * v[-1][None]
+    assert ((H_new[0, 0] - state).abs() <= 2.0 ** -22 * state.abs()).all()
+
+
 def test_in_place_with_cuts():
     import torch
     rng = np.random.default_rng(11)

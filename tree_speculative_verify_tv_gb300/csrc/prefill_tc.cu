@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 total = 0;
                 total_nan = false;
             }
-            total += end;
+            // (2^28 units either way are as good as any more, and many rows of 4096 may not wrap around)
+            total = max(min(total + end, 1LL << 60), -(1LL << 60));
             total_nan |= any;
             const rec::Pair d = exp2_fixed(end);
             const float r = exp2_single(mid);
