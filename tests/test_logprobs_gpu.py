@@ -204,6 +204,30 @@ def test_rows_past_32_bits_of_offset():
     assert abs(float(lp[0]) + np.log(z)) < 2.0 ** -18 and int(st[0]) == 0
 
 
+def test_the_largest_scale():
+    """The base-2 factor is past single precision, the scale is not."""
+    x = np.array([[0.0, 0.5, 1.0, -1.0]], np.float32)
+    lp, ent, tt, tl = call(x, True, [0, 0, 0], [0, 1, 2], 2.9e38, 3)
+    want = np.array([-2.9e38, -1.45e38, 0.0])
+    assert np.allclose(lp, want, rtol=2.0 ** -22) and (ent == 0).all()
+    assert (tt == [2, 1, 0]).all() and np.allclose(tl, want[::-1], rtol=2.0 ** -22)
+
+
+def test_the_longest_row():
+    """2^31 - 1 equal logits: the sum is one row's, ties go to the first indexes."""
+    import torch
+    import tree_speculative_verify_tv_gb300 as tv
+    V = 2 ** 31 - 1
+    logits = torch.zeros(V, dtype=torch.bfloat16, device="cuda")
+    lp, ent = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    tt, tl = torch.empty(3, dtype=torch.int32, device="cuda"), torch.empty(3, device="cuda")
+    st, token = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (0, V - 1))
+    tv.tv_logprobs(1, 1, V, tv.TV_BF16, logits, V, None, token, 1.0, 3, lp, ent, tt, tl, st)
+    assert tt.tolist() == [0, 1, 2] and int(st[0]) == 0
+    for y in (lp, -ent, tl):  # ln z: 2^-20 of the sum, and two roundings of 21.5
+        assert (y.double() + np.log(V)).abs().max() <= 2.0 ** -18
+
+
 def test_replayed_from_a_graph():
     import torch
     import tree_speculative_verify_tv_gb300 as tv

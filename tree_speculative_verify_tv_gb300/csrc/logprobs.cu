@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(NT, kPerSmThreads / NT) logprobs_kernel(Logpro
     }
     const E *x = static_cast<const E *>(a.logits) + (size_t)row * a.stride;
     const int V = a.V, K = min(a.top, V);
-    const float c = a.scale * 1.44269504f;
+    const float c = fminf(a.scale * 1.44269504f, 3.0e38f);
     // elements ahead of the first 16-byte boundary, pieces, elements behind the last
     const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(E));
     const int ahead = min((P::kN - off) % P::kN, V), pieces = (V - ahead) / P::kN;
@@ -333,13 +333,14 @@ __global__ void __launch_bounds__(NT, kPerSmThreads / NT) logprobs_kernel(Logpro
                 search = n > kList;
                 if (!search && n < want) {
                     // the first few elements equal to tau, each warp in a stretch of its own
-                    const int lo = part == 0 ? 0 : ahead + v0 * P::kN;
-                    const int hi = part == parts - 1 ? V - (parts > 1 ? behind : 0)
-                                                     : ahead + v1 * P::kN;
-                    const int each = (hi - lo + NT / 32 - 1) / (NT / 32);
-                    const int from = lo + warp * each, to = min(from + each, hi);
+                    // (unsigned: a step may pass 2^31)
+                    const uint32_t lo = part == 0 ? 0 : ahead + v0 * P::kN;
+                    const uint32_t hi = part == parts - 1 ? V - (parts > 1 ? behind : 0)
+                                                          : ahead + v1 * P::kN;
+                    const uint32_t each = (hi - lo + NT / 32 - 1) / (NT / 32);
+                    const uint32_t from = lo + warp * each, to = min(from + each, hi);
                     int found = 0;
-                    for (int i = from; i < to && found < want; i += 32) {
+                    for (uint32_t i = from; i < to && found < want; i += 32) {
                         const bool hit = i + lane < to && to_f32(x[i + lane]) == tau;
                         const uint32_t hits = __ballot_sync(0xffffffffu, hit);
                         const int at = found + __popc(hits & ((1u << lane) - 1));
