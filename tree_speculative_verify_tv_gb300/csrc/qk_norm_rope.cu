@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreadsR, kPerSm<E>)
     const int heads = a.H + a.Hkv;
     const int lane = threadIdx.x % 32, slot = threadIdx.x % kLanes;
     // items: kRowsWarp rows and per_item heads, a warp each
-    const long long rows_of = (a.R + kRowsWarp - 1) / kRowsWarp;
+    const long long rows_of = (a.R + kRowsWarp - 1LL) / kRowsWarp;
     const long long items = rows_of * items_row, step = (long long)gridDim.x * (kThreadsR / 32);
     const long long begin = (long long)blockIdx.x * (kThreadsR / 32) + threadIdx.x / 32;
     // channels of the lane's two quads
