@@ -721,10 +721,11 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
  * (2^-32; a row's g counts as at most 4096 log2 units), weights and states as two (bf16
  * outputs) or three (fp32) bf16 parts, what is added to the state as three.  Other cases:
  * the recurrence row by row on CUDA cores.
- * NaN and infinity in a request's rows stay in that request and head.
+ * NaN and infinity in a request's rows stay in that request and head (on tensor cores those of
+ * v may reach outputs of up to 63 rows ahead of theirs: a chunk's).
  * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for
  * sizes and strides out of range (total_rows > B * max_rows too); TV_ERR_DTYPE;
- * TV_ERR_UNSUPPORTED for dk or dv > TV_MAX_DIM and B * H or the work items beyond 2^31.
+ * TV_ERR_UNSUPPORTED for dk or dv > TV_MAX_DIM, total_rows > 0x7fff0000 and B * H >= 2^31.
  * Device-detected errors: unusable row_offsets, or more rows than max_rows, give TV_ERR_TREE;
  * that request's out and H_new are left untouched (with unusable offsets those of others
  * may be too).
@@ -796,7 +797,8 @@ typedef enum tv_rope {
  * Arithmetic: fp32, rounded once; the angle's turns are a 64-bit fixed-point product, so
  * far positions lose nothing.
  * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for sizes, strides and eps
- * out of range; TV_ERR_DTYPE for dtype and layout; TV_ERR_UNSUPPORTED for other d.
+ * out of range; TV_ERR_DTYPE for dtype and layout; TV_ERR_UNSUPPORTED for other d and
+ * H + Hkv >= 2^23.
  * Device-detected errors: unusable row_offsets give TV_ERR_TREE; that request's rows are left
  * untouched (those of others may be too).
  */

@@ -131,3 +131,13 @@ def test_constants_match_the_header():
     for name in ("TV_ROPE_HALVES", "TV_ROPE_PAIRS", "TV_LOGPROBS_MAX_TOP"):
         m = re.search(r"%s\s*=?\s*(\d+)" % name, src[src.index("enum tv_rope"):])
         assert m and int(m.group(1)) == getattr(tv, name), name
+    m = re.search(r"#define TV_PREFILL_TEST_EXPIRE_WAIT\s+(0x[0-9a-f]+)", src)
+    assert m and int(m.group(1), 16) == tv.TV_PREFILL_TEST_EXPIRE_WAIT
+
+
+@pytest.mark.parametrize("f,base,kw", [
+    (tv.tv_prefill, PREFILL, dict(total_rows=0x7fff0001, max_rows=0x7fffffff)),
+    (tv.tv_qk_norm_rope, ROPE, dict(H=1 << 23, q_stride=1 << 30, q_out_stride=1 << 30)),
+])
+def test_counts_past_the_limit(f, base, kw):
+    assert rc(f, base, **kw) == tv.TV_ERR_UNSUPPORTED
