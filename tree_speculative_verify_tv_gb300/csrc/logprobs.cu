@@ -13,9 +13,13 @@
 // of these, tau, is no larger than the K-th largest element, so the K are among the elements
 // >= tau, which only the threads whose own maximum reaches tau have: those few read the turn of
 // their maximum again, or all of their part if another turn reaches tau too (4096 rows of 131072
-// bf16: 14 % more bytes from memory with whole parts, rows being far out of L2 by then).  Equal values at tau beyond what the list holds
-// (constant or masked rows) are found in index order instead, and rows with a NaN, or a list
-// that still overflows, by K searches.  Keys are (value, -index), so all of it is exact.
+// bf16: 14 % more bytes from memory with whole parts, rows being far out of L2 by then).  Equal
+// values at tau beyond what the list holds (constant or masked rows) are found in index order
+// instead, and rows with a NaN, or a list that still overflows, by K searches.  Keys are (value,
+// -index), so all of it is exact.
+//
+// Measured: those 4096 rows with 8 alternatives 185 us, 5.8 TB/s; 256 rows of 32000 bf16 9.4 us (2.4
+// at the copy bandwidth) and one row of 50001 fp32 7.7 us, both of them latency.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -32,8 +36,8 @@ constexpr int kList = 1024;  // candidates that a CTA has room for
 constexpr int kMaxTop = TV_LOGPROBS_MAX_TOP;
 constexpr int kMaxCluster = 8;
 constexpr int kUnroll = 4;   // 16-byte loads of a thread in flight
-// Threads per SM that registers are kept to.  4096 rows of 131072 bf16: 193 us, with 1536 (spills)
-// 208, with 1024 200.
+// Threads per SM that registers are kept to.  4096 rows of 131072 bf16, before a thread read
+// one turn again: 193 us, with 1536 (spills) 208, with 1024 200.
 constexpr int kPerSmThreads = 1280;
 
 using Key = unsigned long long;

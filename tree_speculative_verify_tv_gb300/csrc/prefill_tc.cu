@@ -30,9 +30,18 @@
 // The decays of D's product may stand with either factor: V~ = diag(2^{d - L}) V where dv is the
 // smaller (half the conversions at dk = 128, dv = 64), else K~.
 //
-// Roles (32 warps): plan and decays, copies, D's product, the outputs' products (one or two warps
-// in all for the first two, one each), K~ or V~ (4 to 8), H (16), outputs (4), P (3).  D waits for nothing but H's sums of the chunk before, so
-// that parts, outputs and scores stay off the chain from chunk to chunk.
+// Roles (32 warps): plan with the decays, and copies (one or two warps), D's product, the outputs'
+// products (a warp each), K~ or V~ (4 to 8), H (16), outputs (4), P (3).  D waits for nothing but
+// H's sums of the chunk before, so that parts, outputs and scores stay off the chain from chunk to
+// chunk.
+//
+// What bounds it.  That chain: D's product, its sums into H, the next D.  16 prompts of 4096 rows, 24
+// heads of 128 x 64, bf16 outputs: 300 us for 1.23 GB (181 us at the copy bandwidth); one of 32768
+// rows, 32 heads of 128 x 128: 413 us, 155 of them for the segments' sums (1.36 us a chunk), 8 for
+// their chain, 250 for the outputs (2.2 us a chunk).  Without conversions and most products a chunk
+// still takes three quarters of that, so neither tensor cores (50 to 68 % busy) nor issue slots (51
+// to 57 %) are the limit, but signals from role to role.  Tried and not faster: H in eight warps
+// of 64 channels (440 against 432 us), one commit for D's and the outputs' products.
 //
 // Few long prompts: the rows of a request are cut into segments.  A first launch computes what
 // each segment adds to a zero state, a second chains these sums, and the segments then run at
@@ -930,7 +939,7 @@ long long most_chunks(const PrefillArgs &a) {
 
 // Pieces that a request of that length is cut into: what makes the longest SM's work least,
 // counted in chunks.  A segment costs a few chunks to start, and its first launch 0.6 of what a
-// chunk costs (1.36 against 2.33 us at 128 x 128).  One prompt of 32768 rows and 32 heads: 466 us
+// chunk costs (1.36 against 2.2 us at 128 x 128).  One prompt of 32768 rows and 32 heads: 466 us
 // in 4 pieces, 433 in 9 (taken), 432 in 14, 463 in 28.
 int best_pieces(const PrefillArgs &a) {
     const long long units = (long long)a.B * a.H, sms = device_sms(), chunks = most_chunks(a);
