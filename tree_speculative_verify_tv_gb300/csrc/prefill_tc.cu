@@ -46,6 +46,7 @@
 // Few long prompts: the rows of a request are cut into segments.  A first launch computes what
 // each segment adds to a zero state, a second chains these sums, and the segments then run at
 // the same time, each from its own state.
+#include <algorithm>
 #include <type_traits>
 
 #include "recurrence.cuh"
@@ -104,19 +105,22 @@ struct Lay {
         const int from = OUT ? 26 : 20;
         return warp == 3 ? 0 : warp >= from && warp < from - 1 + kScaleWarps ? warp - from + 1 : -1;
     }
-    static constexpr uint32_t kQ = 0, kK = DK * 128, kV = 2 * DK * 128,
-                              kStage = (2 * DK + DV) * 128;
-    static constexpr int kStages = DK == 128 && DV == 128 ? 2 : kMaxStages;
-    static constexpr int kSlots = kStages + 3;  // see the plan's wait
+    static constexpr uint32_t kQ = 0, kK = OUT ? DK * 128 : 0, kV = kK + DK * 128,
+                              kStage = kV + DV * 128;
+    static constexpr int kStages = OUT && DK == 128 && DV == 128 ? 2 : kMaxStages;
+    // Buffers of D (no more than stages, see the barriers' rule)
+    static constexpr int kDBufs = !OUT ? 3 : DK == 64 ? 2 : 1;
+    static constexpr int kSlots = kStages + 1 + std::max(2, kDBufs);  // see the plan's wait
     static constexpr int kXBufs = 2;
     static constexpr uint32_t kXt = kStages * kStage, kXPart = kX * 128, kXBuf = 3 * kXPart;
     static constexpr uint32_t kP = kXt + kXBufs * kXBuf, kPPart = kC * 128;
     static constexpr uint32_t kSlot0 = kP + NP * kPPart;
     static constexpr uint32_t kBytes = kSlot0 + kSlots * (uint32_t)sizeof(Slot) + 1024;
     // tensor memory columns
-    static constexpr uint32_t tD = 0, tH = DK, tO = tH + NP * DK / 2, tS = tO + 2 * kC, kCols = 512;
+    static constexpr uint32_t tD = 0, tH = kDBufs * DK, tO = tH + NP * DK / 2, tS = tO + 2 * kC, kCols = 512;
     static constexpr int kSBufs = tS + 2 * kC <= kCols ? 2 : 1;
-    static_assert(tS + kSBufs * kC <= kCols, "tensor memory");
+    static_assert(OUT ? tS + kSBufs * kC <= kCols : kDBufs * DK <= kCols, "tensor memory");
+    static_assert(kDBufs <= kStages, "see the barriers' rule");
     static_assert(kBytes <= tcc::kSmemLimit - 512, "shared memory");
 };
 
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_s_full[2], s_p_full,
-        s_x_full[2], s_h_full, s_h_free, s_d_full[kStages], s_d_free, s_o_full[kStages], s_o_free[2],
+        s_x_full[2], s_h_full, s_h_free, s_d_full[kStages], s_d_free[L::kDBufs], s_o_full[kStages], s_o_free[2],
         s_copied, s_drain[2], s_asked;
     __shared__ __align__(16) uint64_t s_answer[2];
     const PrefillArgs &a = p.a;
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         ptx::mbar_init(bar(s_p_full), kScoreWarps);
         ptx::mbar_init(bar(s_h_full), 4 * kQuads);
         ptx::mbar_init(bar(s_h_free), 1);
-        ptx::mbar_init(bar(s_d_free), 4 * kQuads);
+        for (int i = 0; i < L::kDBufs; ++i) ptx::mbar_init(bar(s_d_free[i]), 4 * kQuads);
         ptx::mbar_init(bar(s_copied), 1);
         ptx::mbar_init(bar(s_drain[0]), 1);
         ptx::mbar_init(bar(s_drain[1]), 1);
@@ -493,8 +497,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             }
             arrive(s_gate[t.slot]);
             // A chunk's decays are ready before its stage is free.  The products of the chunk that
-            // had the stage waited for the outputs of two chunks earlier to be read: the slot that
-            // the next turn takes is free.
+            // had the stage waited for the outputs of two chunks earlier to be read, and for H's sums
+            // of kDBufs chunks earlier: the slot that the next turn takes is free.
             // (With a warp for the copies it is that one's word: chunk n's products may be done, and
             // their barriers a phase on, before the plan has looked at them.)
             if (L::kCopyWarp >= 0) {
@@ -523,9 +527,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const uint32_t lead = ptx::elect_one();
         for (Turn t;; t.next()) {
             if (gate(t) & kEnd) break;
-            const int xb = t.n % L::kXBufs;
+            const int xb = t.n % L::kXBufs, db = t.n % L::kDBufs;
             if (!wait(s_full[t.stage], t.stage_ph)) break;
-            if (t.n > 0 && !wait(s_d_free, (t.n & 1) ^ 1)) break;
+            if (t.n >= L::kDBufs && !wait(s_d_free[db], (t.n / L::kDBufs & 1) ^ 1)) break;
             if (!wait(s_x_full[xb], (t.n / L::kXBufs) & 1)) break;
             ptx::tc_fence_after_sync();
             // descriptors move by their address field, in units of 16 bytes
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 for (int kk = 0; kk < kC / 16; ++kk) {
                     const uint64_t x = scaled + part * (L::kXPart / 16) + kk * 128;
                     const uint64_t y = raw + kk * 128;
-                    ptx::mma_bf16_lead(tmem + L::tD, L::kScaleV ? x : y, L::kScaleV ? y : x,
+                    ptx::mma_bf16_lead(tmem + L::tD + db * DK, L::kScaleV ? x : y, L::kScaleV ? y : x,
                                        ptx::idesc_bf16_f32_abmn(128, DK), part < 2 || kk > 0, lead);
                 }
             ptx::mma_commit_lead(bar(s_d_full[t.stage]), lead);
@@ -731,6 +735,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     if (!ok) break;
                     ptx::tmem_wait_st();
                 }
+                const int db = t.n % L::kDBufs;
                 const Two dx = two(s->d.x, s->d.x), dy = two(s->d.y, s->d.y);
                 const long long dst = s->dst;
                 if (OUT) {
@@ -746,7 +751,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 #pragma unroll
                 for (int i0 = 0; i0 < kChan; i0 += 16) {
                     uint32_t x[16];
-                    ptx::tmem_ld_x16_nowait(lanes + L::tD + c0 + i0, x);
+                    ptx::tmem_ld_x16_nowait(lanes + L::tD + db * DK + c0 + i0, x);
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     }
                 }
                 ptx::tc_fence_before_sync();
-                arrive(s_d_free);
+                arrive(s_d_free[db]);
                 if ((flags & kLast) && (!OUT || dst >= 0)) {
                     float *to = dst < 0 ? p.states + (size_t)~dst * DK * DV
                                         : a.H_new + (size_t)dst * DK * DV;
