@@ -110,7 +110,8 @@ struct Lay {
     static constexpr int kStages = OUT && DK == 128 && DV == 128 ? 2 : kMaxStages;
     // Buffers of D (no more than stages, see the barriers' rule)
     static constexpr int kDBufs = !OUT ? 3 : DK == 64 ? 2 : 1;
-    static constexpr int kSlots = kStages + 1 + std::max(2, kDBufs);  // see the plan's wait
+    static constexpr int kAhead = 4;  // chunks that the plan may be ahead of the copies
+    static constexpr int kSlots = kStages + kAhead + std::max(2, kDBufs);  // see the plan's wait
     static constexpr int kXBufs = 2;
     static constexpr uint32_t kXt = kStages * kStage, kXPart = kX * 128, kXBuf = 3 * kXPart;
     static constexpr uint32_t kP = kXt + kXBufs * kXBuf, kPPart = kC * 128;
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     __shared__ int s_abort;
     __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_s_full[2], s_p_full,
         s_x_full[2], s_h_full, s_h_free, s_d_full[kStages], s_d_free[L::kDBufs], s_o_full[kStages], s_o_free[2],
-        s_copied, s_drain[2], s_asked;
+        s_copied[L::kAhead], s_drain[2], s_asked;
     __shared__ __align__(16) uint64_t s_answer[2];
     const PrefillArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid % 32;
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         ptx::mbar_init(bar(s_h_full), 4 * kQuads);
         ptx::mbar_init(bar(s_h_free), 1);
         for (int i = 0; i < L::kDBufs; ++i) ptx::mbar_init(bar(s_d_free[i]), 4 * kQuads);
-        ptx::mbar_init(bar(s_copied), 1);
+        for (int i = 0; i < L::kAhead; ++i) ptx::mbar_init(bar(s_copied[i]), 1);
         ptx::mbar_init(bar(s_drain[0]), 1);
         ptx::mbar_init(bar(s_drain[1]), 1);
         ptx::mbar_init(bar(s_asked), 1);
@@ -398,6 +399,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         for (Turn t;; t.next()) {
             Slot *s = slots + t.slot;
             if (w.done) {
+                if (L::kCopyWarp >= 0 && t.n >= L::kAhead &&
+                    !wait(s_copied[t.n % L::kAhead], (t.n / L::kAhead & 1) ^ 1))
+                    break;
                 if (lane == 0) s->flags = kEnd;
                 arrive(s_gate[t.slot]);
                 break;
@@ -446,6 +450,13 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             w.row += cnt;
             if (last) next_item(false);
             fetch();  // the next chunk's, on its way while this one's become factors
+
+            // The slot is free: the copies of kAhead chunks earlier found their stage free, so the
+            // products of the chunk that had that stage are done.  These waited for the outputs of
+            // two chunks earlier to be read, and for H's sums of kDBufs chunks earlier.
+            if (L::kCopyWarp >= 0 && t.n >= L::kAhead &&
+                !wait(s_copied[t.n % L::kAhead], (t.n / L::kAhead & 1) ^ 1))
+                break;
 
             // from the first NaN on, everything of this request and head is one
             const uint32_t within = 2 * lane < cnt ? 1u : 0u;
@@ -496,14 +507,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 }
             }
             arrive(s_gate[t.slot]);
-            // A chunk's decays are ready before its stage is free.  The products of the chunk that
-            // had the stage waited for the outputs of two chunks earlier to be read, and for H's sums
-            // of kDBufs chunks earlier: the slot that the next turn takes is free.
-            // (With a warp for the copies it is that one's word: chunk n's products may be done, and
-            // their barriers a phase on, before the plan has looked at them.)
-            if (L::kCopyWarp >= 0) {
-                if (!wait(s_copied, t.n & 1)) break;
-            } else {
+            // (With a warp for the copies the plan goes by its word alone: chunk n's products may be
+            // done, and their barriers a phase on, before the plan has looked at them.)
+            if (L::kCopyWarp < 0) {
                 if (!stage_free(t)) break;
                 copy(t, head, row);
                 issued = t.n + 1;
@@ -517,7 +523,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             if (gate(t) & kEnd) break;
             const int head = slots[t.slot].head, row = slots[t.slot].row;
             if (!stage_free(t)) break;
-            arrive(s_copied);  // (head and row have been read too)
+            arrive(s_copied[t.n % L::kAhead]);  // (head and row have been read too)
             copy(t, head, row);
             issued = t.n + 1;
         }
