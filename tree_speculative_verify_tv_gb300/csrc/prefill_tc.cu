@@ -115,8 +115,10 @@ struct Lay {
     static constexpr int kXBufs = 2;
     static constexpr uint32_t kXt = kStages * kStage, kXPart = kX * 128, kXBuf = 3 * kXPart;
     static constexpr uint32_t kP = kXt + kXBufs * kXBuf, kPPart = kC * 128;
-    static constexpr uint32_t kSlot0 = kP + NP * kPPart;
-    static constexpr uint32_t kBytes = kSlot0 + kSlots * (uint32_t)sizeof(Slot) + 1024;
+    static constexpr uint32_t kPBuf = NP * kPPart;
+    static constexpr uint32_t kOther = kSlots * (uint32_t)sizeof(Slot) + 1024;
+    static constexpr int kPBufs = kP + 2 * kPBuf + kOther <= tcc::kSmemLimit - 512 ? 2 : 1;
+    static constexpr uint32_t kSlot0 = kP + (OUT ? kPBufs * kPBuf : 0), kBytes = kSlot0 + kOther;
     // tensor memory columns
     static constexpr uint32_t tD = 0, tH = kDBufs * DK, tO = tH + NP * DK / 2, tS = tO + 2 * kC, kCols = 512;
     static constexpr int kSBufs = tS + 2 * kC <= kCols ? 2 : 1;
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     extern __shared__ uint8_t s_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_s_full[2], s_p_full,
+    __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_s_full[2], s_p_full[2],
         s_x_full[2], s_h_full, s_h_free, s_d_full[kStages], s_d_free[L::kDBufs], s_o_full[kStages], s_o_free[2],
         s_copied[L::kAhead], s_drain[2], s_asked;
     __shared__ __align__(16) uint64_t s_answer[2];
@@ -236,10 +238,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(s_s_full[i]), 1);
+            ptx::mbar_init(bar(s_p_full[i]), kScoreWarps);
             ptx::mbar_init(bar(s_x_full[i]), L::kScaleWarps);
             ptx::mbar_init(bar(s_o_free[i]), kQuads);
         }
-        ptx::mbar_init(bar(s_p_full), kScoreWarps);
         ptx::mbar_init(bar(s_h_full), 4 * kQuads);
         ptx::mbar_init(bar(s_h_free), 1);
         for (int i = 0; i < L::kDBufs; ++i) ptx::mbar_init(bar(s_d_free[i]), 4 * kQuads);
@@ -585,8 +587,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             const int n = t.n, ob = n & 1;
             const uint32_t ph = n & 1, st = base + t.stage * L::kStage;
             const uint32_t o = tmem + L::tO + ob * kC;
-            if (n >= 2 && !(ok = wait(s_o_free[ob], ((n >> 1) & 1) ^ 1))) break;
-            if (!(ok = wait(s_h_full, ph))) break;
+            if (!__all_sync(0xffffffffu,
+                            ptx::mbar_test_wait(bar(s_h_full), ph) &&
+                                (n < 2 || ptx::mbar_test_wait(bar(s_o_free[ob]), ((n >> 1) & 1) ^ 1)))) {
+                if (n >= 2 && !(ok = wait(s_o_free[ob], ((n >> 1) & 1) ^ 1))) break;
+                if (!(ok = wait(s_h_full, ph))) break;
+            }
             ptx::tc_fence_after_sync();
             const uint64_t qd = ptx::desc_kmajor_sw128(st + L::kQ, 1024);
 #pragma unroll
@@ -603,17 +609,21 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             // the next chunk's scores ahead of this one's weights, if it is there and they have
             // a buffer of their own
             bool scored = false;
-            if (L::kSBufs == 2 &&
-                __all_sync(0xffffffffu, ptx::mbar_test_wait(bar(s_gate[u.slot]), u.slot_ph)) &&
-                !(gate(u) & kEnd) &&
-                __all_sync(0xffffffffu, ptx::mbar_test_wait(bar(s_full[u.stage]), u.stage_ph))) {
-                scores(u);
-                scored = true;
+            int next = -1;  // its flags, once they are known
+            if (__all_sync(0xffffffffu, ptx::mbar_test_wait(bar(s_gate[u.slot]), u.slot_ph))) {
+                next = (int)__reduce_or_sync(0xffffffffu, (uint32_t)slots[u.slot].flags);
+                if (L::kSBufs == 2 && !(next & kEnd) &&
+                    __all_sync(0xffffffffu, ptx::mbar_test_wait(bar(s_full[u.stage]), u.stage_ph))) {
+                    ptx::tc_fence_after_sync();
+                    scores(u);
+                    scored = true;
+                }
             }
-            if (!(ok = wait(s_p_full, ph))) break;
+            const int pb = n % L::kPBufs;
+            if (!(ok = wait(s_p_full[pb], (n / L::kPBufs) & 1))) break;
             ptx::tc_fence_after_sync();
             const uint64_t vd = ptx::desc_mnmajor_sw128(st + L::kV, kSlab, 1024);
-            const uint64_t pd = ptx::desc_kmajor_sw128(base + L::kP, 1024);
+            const uint64_t pd = ptx::desc_kmajor_sw128(base + L::kP + pb * L::kPBuf, 1024);
 #pragma unroll
             for (int part = NP - 1; part >= 0; --part)
 #pragma unroll
@@ -622,7 +632,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                                        ptx::idesc_bf16_f32_amn(128, kC), 1, lead);
             ptx::mma_commit_lead(bar(s_o_full[t.stage]), lead);
             t = u;
-            if (!(ok = !(gate(t) & kEnd))) break;
+            if (next < 0) next = gate(t);
+            if (next & kEnd) break;
             if (!scored) {
                 // (P of the chunk before has been written, so its scores have been read)
                 if (!(ok = wait(s_full[t.stage], t.stage_ph))) break;
@@ -847,7 +858,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             uint8_t *row = s_base + L::kP + i * 128;
             if (warp == 24)  // zero once and for all: columns past the rows
                 for (int c = 4; c < 8; ++c)
-                    for (int j = 0; j < NP; ++j)
+                    for (int j = 0; j < NP * L::kPBufs; ++j)
                         *reinterpret_cast<uint4 *>(row + j * L::kPPart + ((c ^ (i & 7)) * 16)) =
                             make_uint4(0, 0, 0, 0);
             for (Turn t;; t.next()) {
@@ -863,8 +874,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                         *reinterpret_cast<uint4 *>(v + z / (rows * 8) * kSlab + z % (rows * 8) * 16) =
                             make_uint4(0, 0, 0, 0);
                 }
-                // P of the chunk before has been read (a second buffer of P gained nothing)
-                if (t.n > 0 && !wait(s_o_full[(t.n - 1) % kStages], ((t.n - 1) / kStages) & 1)) break;
+                const int was = t.n - L::kPBufs;  // its P has been read
+                if (was >= 0 && !wait(s_o_full[was % kStages], (was / kStages) & 1)) break;
+                uint8_t *mine = row + t.n % L::kPBufs * L::kPBuf;
                 ptx::tc_fence_after_sync();
 #pragma unroll 1
                 for (int jb = from; jb < from + 2; ++jb) {
@@ -889,7 +901,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                                 for (int q = 0; q < NP; ++q) out[q][2 * h + e] = part[q];
                             }
                         }
-                        uint8_t *at = row + (((jb * 2 + c) ^ (i & 7)) * 16);
+                        uint8_t *at = mine + (((jb * 2 + c) ^ (i & 7)) * 16);
 #pragma unroll
                         for (int q = 0; q < NP; ++q)
                             *reinterpret_cast<uint4 *>(at + q * L::kPPart) =
@@ -898,7 +910,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 }
                 ptx::tc_fence_before_sync();
                 ptx::fence_proxy_async_smem();
-                arrive(s_p_full);
+                arrive(s_p_full[t.n % L::kPBufs]);
             }
         }
     }
