@@ -63,6 +63,7 @@ constexpr int kThreadsT = kWarps * 32;
 constexpr int kWaitTries = 1 << 20;  // 7800 cycles each at most: some 4 s
 constexpr uint32_t kSlab = kC * 128; // 64 rows of 64 channels
 constexpr int kSpan = 120;           // log2 units that L may span in a chunk
+constexpr int kSorted = 64;          // requests whose lengths the plan sorts
 
 enum { kB, kW, kE };  // Slot::factor
 enum Flags { kFirst = 1, kLast = 2, kEnd = 4 };
@@ -82,6 +83,7 @@ struct TcParams {
     int pieces;     // segments of a request of max_rows rows
     float *states;  // [B][pieces][H][dk][dv]: the state before each segment
     float2 *decays; // [B][pieces][H]
+    int sorted;     // items in order of their requests' lengths (at most kSorted requests)
     int expire;     // test hook: leave the first chunk's copies out
 };
 
@@ -194,9 +196,10 @@ __device__ __forceinline__ int pieces_of(int n, int seg) {
 
 // A CTA's walk over its chunks.  An item is a segment of a request and head; a CTA begins with
 // the item of its block index and then takes over items of CTAs that have not been launched, so
-// that long and short ones even out.
+// that long and short ones even out: the longest requests first, where there are more items than
+// SMs (12 requests of up to 3000 rows, 32 heads: 240 us in the order given).
 struct Walk {
-    int item;              // (b * pieces + segment) * H + head, without the last segments if !OUT
+    int item;              // (place * pieces + segment) * H + head, without the last segments if !OUT
     int asked;             // items asked for so far
     int row, end, head;    // of the current item; row >= end: none left of it
     bool first, done;
@@ -216,6 +219,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     extern __shared__ uint8_t s_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ uint8_t s_order[kSorted];  // requests by length, written and read by the plan
     __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_s_full[2], s_p_full[2],
         s_x_full[2], s_h_full, s_h_free, s_d_full[kStages], s_d_free[L::kDBufs], s_o_full[kStages], s_o_free[2],
         s_copied[L::kAhead], s_drain[2], s_asked;
@@ -357,7 +361,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     }
                 }
                 ask();
-                const int slot = w.item / a.H, b = slot / per, i = slot - b * per;
+                const int slot = w.item / a.H, place = slot / per, i = slot - place * per;
+                const int b = p.sorted ? s_order[place] : place;
                 int off, n;
                 if (!request_range(a.offsets, b, a.R, a.max_rows, off, n)) {
                     if (lane == 0) report(a.status, TV_ERR_TREE);
@@ -376,6 +381,28 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 return;
             }
         };
+        if (p.sorted) {
+            const auto rows = [&](int b) {
+                int off, n = 0;
+                return b < a.B && request_range(a.offsets, b, a.R, a.max_rows, off, n) ? n : 0;
+            };
+#pragma unroll 1
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+                const int b = b0 + lane, n = rows(b);
+                int place = 0;
+#pragma unroll 1
+                for (int j0 = 0; j0 < a.B; j0 += 32) {
+                    const int m = rows(j0 + lane);
+#pragma unroll 1
+                    for (int j = j0; j < min(a.B, j0 + 32); ++j) {
+                        const int x = __shfl_sync(0xffffffffu, m, j - j0);
+                        place += x > n || (x == n && j < b);
+                    }
+                }
+                if (b < a.B) s_order[place] = b;
+            }
+            __syncwarp();
+        }
         next_item(true);
         // decays of the chunk at w, and of the 64 rows that begin at `ahead`, on their way from memory
         // for a whole turn
@@ -1025,6 +1052,9 @@ cudaError_t launch_widths(const PrefillArgs &a, bool expire, cudaStream_t s) {
     p.expire = expire;
     int pieces = best_pieces(a);
     while (pieces > 1 && cut_bytes(a, pieces) > a.ws_bytes) --pieces;
+    // (a microsecond or two of every CTA's start, lost on short requests and on equal ones)
+    p.sorted = a.B <= kSorted && (long long)a.B * a.H > device_sms() && most_chunks(a) >= 8 &&
+               a.R < (long long)a.B * a.max_rows;
     p.seg = segment_rows(a, pieces);
     p.pieces = pieces;
     if (pieces > 1) {
