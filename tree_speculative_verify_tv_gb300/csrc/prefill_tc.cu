@@ -118,7 +118,7 @@ struct Lay {
     static constexpr uint32_t kXt = kStages * kStage, kXPart = kX * 128, kXBuf = 3 * kXPart;
     static constexpr uint32_t kP = kXt + kXBufs * kXBuf, kPPart = kC * 128;
     static constexpr uint32_t kPBuf = NP * kPPart;
-    static constexpr uint32_t kOther = kSlots * (uint32_t)sizeof(Slot) + 1024;
+    static constexpr uint32_t kOther = kSlots * (uint32_t)sizeof(Slot) + kSorted + 1024;
     static constexpr int kPBufs = kP + 2 * kPBuf + kOther <= tcc::kSmemLimit - 512 ? 2 : 1;
     static constexpr uint32_t kSlot0 = kP + (OUT ? kPBufs * kPBuf : 0), kBytes = kSlot0 + kOther;
     // tensor memory columns
@@ -219,7 +219,6 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     extern __shared__ uint8_t s_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ uint8_t s_order[kSorted];  // requests by length, written and read by the plan
     __shared__ __align__(8) uint64_t s_gate[kSlots], s_full[kStages], s_s_full[2], s_p_full[2],
         s_x_full[2], s_h_full, s_h_free, s_d_full[kStages], s_d_free[L::kDBufs], s_o_full[kStages], s_o_free[2],
         s_copied[L::kAhead], s_drain[2], s_asked;
@@ -230,6 +229,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     uint8_t *s_base = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
     const uint32_t base = ptx::smem_addr(s_base);
     Slot *slots = reinterpret_cast<Slot *>(s_base + L::kSlot0);
+    uint8_t *s_order = reinterpret_cast<uint8_t *>(slots + kSlots);  // requests by length: the plan's
 
     const auto bar = [](const uint64_t &b) { return ptx::smem_addr(&b); };
     if (tid == 0) {
