@@ -950,8 +950,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     }
 }
 
-// The segments' states from what each adds: S_{i+1} = 2^{d_i} S_i + added_i.
+// The segments' states from what each adds: S_{i+1} = 2^{d_i} S_i + added_i.  Latency bounds it (a
+// dependent load each: 1 us a segment), so kChain segments' sums are on their way together.
 constexpr int kThreadsChain = 256;
+constexpr int kChain = 8;
 __global__ void __launch_bounds__(kThreadsChain) prefill_chain_kernel(TcParams p) {
     const PrefillArgs &a = p.a;
     const int unit = blockIdx.x, b = unit / a.H, h = unit % a.H;
@@ -968,15 +970,24 @@ __global__ void __launch_bounds__(kThreadsChain) prefill_chain_kernel(TcParams p
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (a.H0) x = reinterpret_cast<const float4 *>(a.H0)[(size_t)unit * quads + at];
     *state = x;
-    for (int i = 1; i < pieces; ++i) {
-        const float2 d = decay[(size_t)(i - 1) * a.H];
-        float4 &to = state[(size_t)i * a.H * quads];
-        const float4 y = to;
-        x.x = fmaf(x.x, d.x, fmaf(x.x, d.y, y.x));
-        x.y = fmaf(x.y, d.x, fmaf(x.y, d.y, y.y));
-        x.z = fmaf(x.z, d.x, fmaf(x.z, d.y, y.z));
-        x.w = fmaf(x.w, d.x, fmaf(x.w, d.y, y.w));
-        to = x;
+    for (int i0 = 1; i0 < pieces; i0 += kChain) {
+        float4 y[kChain];
+        float2 d[kChain];
+#pragma unroll
+        for (int u = 0; u < kChain; ++u) {
+            const size_t i = min(i0 + u, pieces - 1);
+            y[u] = state[i * a.H * quads];
+            d[u] = decay[(i - 1) * a.H];
+        }
+#pragma unroll
+        for (int u = 0; u < kChain; ++u) {
+            if (i0 + u >= pieces) break;
+            x.x = fmaf(x.x, d[u].x, fmaf(x.x, d[u].y, y[u].x));
+            x.y = fmaf(x.y, d[u].x, fmaf(x.y, d[u].y, y[u].y));
+            x.z = fmaf(x.z, d[u].x, fmaf(x.z, d[u].y, y[u].z));
+            x.w = fmaf(x.w, d[u].x, fmaf(x.w, d[u].y, y[u].w));
+            state[(size_t)(i0 + u) * a.H * quads] = x;
+        }
     }
 }
 
