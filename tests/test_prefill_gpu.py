@@ -294,6 +294,35 @@ def test_many_requests():
         state=True)
 
 
+@pytest.mark.parametrize("B,H", [(33, 5), (64, 3), (32, 6), (65, 3)])
+def test_requests_of_all_lengths(B, H):
+    """More units than SMs: the longest requests go first (up to 64 requests), among them equal and
+    empty ones."""
+    lens = [int(x) for x in np.random.default_rng(B).integers(0, 200, B)]
+    lens[B // 2], lens[3], lens[7], lens[B - 1] = 700, 0, lens[5], 520
+    run(28, lens, H, 64, 64, state=True)
+
+
+def test_an_unusable_request_among_many():
+    """One request with more rows than the bound, where the order of the others goes by lengths."""
+    import torch
+    import tree_speculative_verify_tv_gb300 as tv
+    rng = np.random.default_rng(29)
+    lens = [int(x) for x in rng.integers(1, 90, 40)]
+    lens[11], lens[30] = 600, 530
+    r = Rows(rng, lens, 4, 64, 64)
+    want = r.prefill()
+    out, H_new, status = r.prefill(max_rows=560)
+    torch.cuda.synchronize()
+    assert int(status[0]) == tv.TV_ERR_TREE
+    rows = torch.zeros(r.R, dtype=torch.bool)
+    rows[int(r.offsets[11]):int(r.offsets[12])] = True
+    assert torch.isnan(out[rows]).all() and torch.isnan(H_new[11]).all()
+    assert torch.equal(out[~rows], want[0][~rows])
+    keep = torch.arange(40) != 11
+    assert torch.equal(H_new[keep], want[1][keep])
+
+
 def test_the_same_call_gives_the_same_bits():
     import torch
     rng = np.random.default_rng(18)
