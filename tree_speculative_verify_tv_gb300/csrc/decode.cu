@@ -3,7 +3,7 @@
 //   H' = diag(e^g) H + k v^T,   out = H'^T q   (Bole summary page, "Core techniques" §1, one step)
 //
 // The state is read and written once, 8 bytes an element against 5 operations: HBM bounds it (128
-// requests of 32 heads, 128 x 128: 86 us, 6.2 TB/s).
+// requests of 32 heads, 128 x 128: 87 us, 6.2 TB/s).
 // A CTA takes columns of one (request, head): a thread holds a float4 of columns and walks down
 // the key rows, kItems of its loads in flight; the read-out's partial sums of the row groups
 // meet in shared memory.

@@ -37,10 +37,10 @@
 //
 // What bounds it.  That chain: D's product, its sums into H, the next D.  16 prompts of 4096 rows, 24
 // heads of 128 x 64, bf16 outputs: 300 us for 1.23 GB (181 us at the copy bandwidth); one of 32768
-// rows, 32 heads of 128 x 128: 413 us, 155 of them for the segments' sums (1.36 us a chunk), 8 for
-// their chain, 250 for the outputs (2.2 us a chunk).  Without conversions and most products a chunk
-// still takes three quarters of that, so neither tensor cores (50 to 68 % busy) nor issue slots (51
-// to 57 %) are the limit, but signals from role to role.  Tried and not faster: H in eight warps
+// rows, 32 heads of 128 x 128: 394 us, about 125 of them for the segments' sums (1.1 us a chunk), 5
+// for their chain, 265 for the outputs (2.3 us a chunk).  Without conversions and most products a
+// chunk still takes three quarters of that, so neither tensor cores (50 to 69 % busy) nor issue slots
+// (51 to 58 %) are the limit, but signals from role to role.  Tried and not faster: H in eight warps
 // of 64 channels (440 against 432 us), one commit for D's and the outputs' products.
 //
 // Few long prompts: the rows of a request are cut into segments.  A first launch computes what
@@ -999,9 +999,9 @@ long long most_chunks(const PrefillArgs &a) {
 }
 
 // Pieces that a request of that length is cut into: what makes the longest SM's work least,
-// counted in chunks.  A segment costs a few chunks to start, and its first launch 0.6 of what a
-// chunk costs (1.36 against 2.2 us at 128 x 128).  One prompt of 32768 rows and 32 heads: 466 us
-// in 4 pieces, 433 in 9 (taken), 432 in 14, 463 in 28.
+// counted in chunks.  A segment costs a few chunks to start, and its first launch half of what a
+// chunk costs (1.1 against 2.3 us at 128 x 128).  One prompt of 32768 rows and 32 heads, at an
+// earlier step: 466 us in 4 pieces, 433 in 9 (taken), 432 in 14, 463 in 28.
 int best_pieces(const PrefillArgs &a) {
     const long long units = (long long)a.B * a.H, sms = device_sms(), chunks = most_chunks(a);
     if (units > 8 * sms) return 1;
@@ -1011,7 +1011,7 @@ int best_pieces(const PrefillArgs &a) {
     for (int s = 2; s <= 64 && s <= chunks; ++s) {
         const double per = (double)((chunks + s - 1) / s);
         const double cost =
-            waves(units * s) * (per + 4.0) + waves(units * (s - 1)) * (0.6 * per + 4.0) + 8.0;
+            waves(units * s) * (per + 4.0) + waves(units * (s - 1)) * (0.5 * per + 4.0) + 8.0;
         if (cost < 0.95 * least) {
             least = cost;
             best = s;
