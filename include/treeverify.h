@@ -721,8 +721,8 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
  * (2^-32; a row's g counts as at most 4096 log2 units), weights and states as two (bf16
  * outputs) or three (fp32) bf16 parts, what is added to the state as three.  Other cases:
  * the recurrence row by row on CUDA cores.
- * NaN and infinity in a request's rows stay in that request and head (on tensor cores those of
- * v may reach outputs of up to 63 rows ahead of theirs: a chunk's).
+ * NaN and infinity in a request's rows stay in that request and head, and those of v in their
+ * column (on tensor cores they may reach its outputs of up to 63 rows ahead of theirs: a chunk's).
  * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for
  * sizes and strides out of range (total_rows > B * max_rows too); TV_ERR_DTYPE;
  * TV_ERR_UNSUPPORTED for dk or dv > TV_MAX_DIM, total_rows > 0x7fff0000 and B * H >= 2^31.

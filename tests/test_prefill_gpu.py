@@ -247,6 +247,38 @@ def test_a_bad_value_stays_in_its_request_and_head(kind, what, value):
     assert torch.equal(H_new[keep], clean[1][keep])
 
 
+@pytest.mark.parametrize("dk,dv", WIDTHS + [(40, 24)])
+@pytest.mark.parametrize("out32", [False, True])
+@pytest.mark.parametrize("lens,workspace", [([20, 150, 9], True), ([3000], True)])
+def test_a_bad_value_of_v_stays_in_its_column(dk, dv, out32, lens, workspace):
+    """NaN and infinities in three columns of v: those columns are no numbers from their rows on (in
+    the state too; on tensor cores up to 63 rows ahead of them may be none either), all else is
+    what it is without them."""
+    import torch
+    rng = np.random.default_rng(30)
+    r = Rows(rng, lens, 2, dk, dv)
+    H0, _ = r.state(rng)
+    clean = [x.clone() for x in r.prefill(H0, out32, workspace=workspace)[:2]]
+    b = len(lens) // 2
+    first, end = int(r.offsets[b]), int(r.offsets[b + 1])
+    bad, near = (torch.zeros_like(clean[0], dtype=torch.bool) for _ in range(2))
+    v = r.dev["v"].view(r.R, 2, dv)
+    for row, col, value in ((37, 5, float("nan")), (70, 20, float("inf")), (63, dv - 1, -float("inf")),
+                            (130, 5, float("inf"))):
+        v[first + row, 1, col] = value
+        bad[first + row:end, 1, col] = True
+        if r.tensor_cores():
+            near[first + max(0, row - 63):first + row, 1, col] = True
+    out, H_new, status = r.prefill(H0, out32, workspace=workspace)
+    torch.cuda.synchronize()
+    assert int(status[0]) == 0
+    assert not torch.isfinite(out[bad]).any()
+    assert torch.equal(out[~bad & ~near], clean[0][~bad & ~near])
+    lost = torch.zeros_like(H_new, dtype=torch.bool)
+    lost[b, 1][:, [5, 20, dv - 1]] = True
+    assert not torch.isfinite(H_new[lost]).any() and torch.equal(H_new[~lost], clean[1][~lost])
+
+
 @pytest.mark.parametrize("kind", ["tensor", "f32"])
 @pytest.mark.parametrize("offsets", [[0, 50, 20, 90], [-1, 30, 60, 90], [0, 30, 60, 500]])
 def test_unusable_offsets(kind, offsets):
