@@ -42,9 +42,10 @@ constexpr int kPerSmThreads = 1280;
 
 using Key = unsigned long long;
 
-// Order of logits: larger value, larger key; a NaN above all, -0 equal to +0.
+// Order of logits: larger value, larger key; a NaN above +inf (0xff800000), -0 equal to +0.  No
+// key is all ones, a NaN at index 0 neither: that stands for "above every key".
 __device__ __forceinline__ uint32_t order_key(float x) {
-    if (x != x) return 0xffffffffu;
+    if (x != x) return 0xfffffffeu;
     const uint32_t u = __float_as_uint(x + 0.f);
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
