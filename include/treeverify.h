@@ -723,6 +723,9 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
  * the recurrence row by row on CUDA cores.
  * NaN and infinity in a request's rows stay in that request and head, and those of v in their
  * column (on tensor cores they may reach its outputs of up to 63 rows ahead of theirs: a chunk's).
+ * Infinite elements of a state stay infinite under decays above 0 (exp g in fp32, a segment's where
+ * the prompt is cut); outputs of their column are infinite or NaN.  A decay of 2^128 and more makes
+ * infinity of every element but 0, and NaN of that.
  * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for
  * sizes and strides out of range (total_rows > B * max_rows too); TV_ERR_DTYPE;
  * TV_ERR_UNSUPPORTED for dk or dv > TV_MAX_DIM, total_rows > 0x7fff0000 and B * H >= 2^31.

@@ -7,7 +7,9 @@
 namespace tv {
 namespace rec {
 
-// A number as the unevaluated sum hi + lo of two floats.
+// A number >= 0 as the unevaluated sum hi + lo of two floats.  hi is rounded down, and lo is above
+// 0 wherever hi is (2^-149 at least): an infinite x stays x in x hi + x lo, where a lo of 0 or
+// below would make NaN of it.
 struct Pair {
     float hi, lo;
 };
@@ -28,13 +30,14 @@ __device__ __forceinline__ Pair exp2_pair(float n, float f) {
     p = fmaf(p, t, 1.f);
     const float r = t * p;
     Pair e;
-    e.hi = 1.f + r;
+    e.hi = __fadd_rd(1.f, r);
     e.lo = r - (e.hi - 1.f);
     const int k = (int)fminf(fmaxf(n, -252.f), 254.f), k0 = k / 2, k1 = k - k0;  // two factors
     const float s0 = __int_as_float((k0 + 127) << 23), s1 = __int_as_float((k1 + 127) << 23);
     e.hi = e.hi * s0 * s1;
     e.lo = e.lo * s0 * s1;
     if (n < -252.f) e.hi = e.lo = 0.f;
+    if (e.hi > 0.f) e.lo = fmaxf(e.lo, __int_as_float(1));  // (past 2^128 both may be infinite)
     return e;
 }
 
@@ -45,9 +48,7 @@ __device__ __forceinline__ Pair exp_pair(float g) {
     const float log2e = 1.44269502f, rest = 1.92596303e-8f;
     const float y = x * log2e, lo = fmaf(x, rest, fmaf(x, log2e, -y));
     const float n = rintf(y);
-    Pair e = exp2_pair(n, (y - n) + lo);
-    if (e.hi > 3.0e38f) e = {__int_as_float(0x7F800000), 0.f};
-    return e;
+    return exp2_pair(n, (y - n) + lo);
 }
 
 __device__ __forceinline__ float4 load4(const float *p) {
