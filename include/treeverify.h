@@ -757,7 +757,9 @@ tv_status tv_prefill(int32_t B, int32_t total_rows, int32_t max_rows, int32_t H,
  *            slot of a batch) keeps its H_new and out as they are
  *   H0       [B][H][dk][dv] fp32;  H_new may be H0 (in place), must not overlap it otherwise
  *   other arguments as in tv_prefill; out [B][H][dv]
- * Arithmetic: fp32.  Host errors as tv_prefill; there are no device-detected ones.
+ * Arithmetic: fp32, exp g as a pair of floats, as tv_prefill has it: decays near 1 do not drift over
+ * many tokens.  Infinite elements of a state as in tv_prefill.  Host errors as tv_prefill; there
+ * are no device-detected ones.
  */
 tv_status tv_decode(int32_t B, int32_t H, int32_t dk, int32_t dv, int32_t decay,
                     int32_t qkv_dtype, const int32_t *active, const float *H0, const void *q,
