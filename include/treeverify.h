@@ -718,9 +718,9 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
  *                       Calls that may run at the same time need workspaces of their own.
  * Arithmetic: states and sums in fp32.  bf16 inputs with a scalar decay, dk and dv in
  * {64, 128}: tensor cores, chunks of 64 rows, decays as 64-bit fixed-point sums of log2
- * (2^-32; a row's g counts as at most 4096 log2 units), weights and states as two (bf16
- * outputs) or three (fp32) bf16 parts, what is added to the state as three.  Other cases:
- * the recurrence row by row on CUDA cores.
+ * (2^-40; a row's g counts as at most 4096 log2 units), weights and states as two (bf16 outputs) or
+ * three (fp32) bf16 parts, what is added to the state as three; factors within a chunk from the
+ * hardware's exponential (2^-22).  Other cases: the recurrence row by row on CUDA cores.
  * NaN and infinity in a request's rows stay in that request and head, and those of v in their
  * column (on tensor cores they may reach its outputs of up to 63 rows ahead of theirs: a chunk's).
  * Infinite elements of a state stay infinite under decays above 0 (exp g in fp32, a segment's where

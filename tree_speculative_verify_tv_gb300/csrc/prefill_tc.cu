@@ -25,7 +25,8 @@
 // Precision.  P and H enter their products as NP bf16 parts, two for bf16 outputs (2^-16, far
 // below the output's own rounding) and three for fp32; K~ (or V~, see below) always as three,
 // since the state is fp32.  Small parts are accumulated first.  Decays are 64-bit fixed-point sums
-// of log2 units (2^-32): differences of sums over a chunk lose nothing.
+// of log2 units (2^-40, what a row's is cut to): differences of sums over a chunk lose nothing more.
+// The factors 2^{R - L}, 2^{d - L} and 2^{L - R} come from the hardware's exponential (2^-22).
 //
 // The decays of D's product may stand with either factor: V~ = diag(2^{d - L}) V where dv is the
 // smaller (half the conversions at dk = 128, dv = 64), else K~.
@@ -156,37 +157,50 @@ __device__ __forceinline__ void split_pair(Two x, uint32_t (&part)[NP]) {
     part[NP - 1] = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// g log2 e in 2^-32, by a whole product of the mantissa (|g| at most 2839: 4096 log2 units); 0 for
-// a NaN.
+constexpr int kFrac = 40;  // bits below a log2 unit: 64 rows of 4096 units take 18 above
+
+// g log2 e in 2^-40, by a whole product of the mantissa (|g| at most 2839: 4096 log2 units); 0 for
+// a NaN.  Bits below are cut off, in the same direction for all rows of one slow decay: 65536 rows
+// of them are 4e-8 of a weight (in units of 2^-32 it would be 1e-5).
 __device__ __forceinline__ long long log2_fixed(float g) {
     const float x = fminf(fabsf(g), 2839.f);
     const uint32_t bits = __float_as_uint(x), m = (bits & 0x7FFFFFu) | 0x800000u;
     // x = m 2^(e - 150), log2 e = 3098164009 2^-31: the product's unit is 2^(e - 181)
-    const uint32_t shift = 149u - (bits >> 23);  // 11 at least (and subnormals end as zero)
-    const unsigned long long y = shift < 64 ? (unsigned long long)m * 3098164009u >> shift : 0;
+    const uint32_t shift = 181u - kFrac - (bits >> 23);  // 3 at least (and subnormals end as zero)
+    const unsigned long long p = (unsigned long long)m * 3098164009u;  // below 2^56
+    const unsigned long long y = shift < 64 ? p >> shift : 0;
     const long long z = g < 0.f ? -(long long)y : (long long)y;
     return g == g ? z : 0;
 }
 
-// 2^(x 2^-32) as a whole power and the rest of at most half a unit.
-__device__ __forceinline__ void split_exponent(long long x, int &n, float &f) {
-    const int low = (int)(uint32_t)x;  // of 2^-32; from a half on it counts as negative
-    n = (int)(x >> 32) + ((uint32_t)low >> 31);
-    f = (float)low * 2.3283064365386963e-10f;
-}
+// 2^(x 2^-40) as a pair: a whole power and the rest of at most half a unit, rounded to 2^-32.
+// (The plan's instructions are on the way from chunk to chunk: 16 prompts of 128 x 64 took 330 us
+// with rows rounded and a rest of 40 bits, 304 so.)
 __device__ __forceinline__ rec::Pair exp2_fixed(long long x) {
-    int n;
-    float f;
-    split_exponent(x, n, f);
-    return rec::exp2_pair((float)n, f);
+    x += 1LL << (kFrac - 33);
+    const int low = (int)(x >> (kFrac - 32));
+    const int n = (int)(x >> kFrac) + ((uint32_t)low >> 31);
+    return rec::exp2_pair((float)n, (float)low * 2.3283064365386963e-10f);
 }
 // The same as one float, by the hardware's exponential (2^-22) of the rest.
 __device__ __forceinline__ float exp2_single(long long x) {
-    int n;
-    float f, e;
-    split_exponent(x, n, f);
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
+    const int low = (int)(x >> (kFrac - 32));  // from a half on it counts as negative
+    const int n = (int)(x >> kFrac) + ((uint32_t)low >> 31);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((float)low * 2.3283064365386963e-10f));
     return e * __int_as_float((max(min(n, 128), -127) + 127) << 23);
+}
+
+// 2^x and 2^-x of rows within a chunk's span, by one split of x.
+__device__ __forceinline__ void exp2_both(long long x, float &up, float &down) {
+    const int low = (int)(x >> (kFrac - 32));
+    const int n = max(min((int)(x >> kFrac) + (int)((uint32_t)low >> 31), 127), -127);
+    const float f = (float)low * 2.3283064365386963e-10f;
+    float e0, e1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(-f));
+    up = e0 * __int_as_float((127 + n) << 23);
+    down = e1 * __int_as_float((127 - n) << 23);
 }
 
 // Segments of a request of n rows.
@@ -451,7 +465,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             }
             const long long l0 = sum - y1, l1 = sum;
             long long end = __shfl_sync(0xffffffffu, sum, 31);
-            const int h0 = (int)(l0 >> 32), h1 = (int)(l1 >> 32);
+            const int h0 = (int)(l0 >> kFrac), h1 = (int)(l1 >> kFrac);
             int lo = __reduce_min_sync(0xffffffffu, min(h0, h1));
             int hi = __reduce_max_sync(0xffffffffu, max(h0, h1));
             if (hi - lo > kSpan) {
@@ -471,7 +485,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                     hi = max(hi, h);
                 }
             }
-            const long long mid = (long long)((lo + hi) / 2) * (1LL << 32);
+            const long long mid = (long long)((lo + hi) / 2) * (1LL << kFrac);
             const bool first = w.first, last = row + cnt >= w.end;
             const long long unit_of = w.unit, ws = w.ws;
             const bool cut = w.pieces > 1, final_piece = w.piece == w.pieces - 1;
@@ -493,13 +507,15 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                            bad1 = __ballot_sync(0xffffffffu, nan1 && 2 * lane + 1 < cnt);
             const bool any = (bad0 | bad1) != 0;
             const float nanf = __int_as_float(0x7fffffff);
-            if (OUT)
-                *reinterpret_cast<float2 *>(s->factor[kB] + 2 * lane) =
-                    make_float2(exp2_single(mid - l0), exp2_single(mid - l1));
+            float2 ev = make_float2(0.f, 0.f), bv = ev;
+            if (OUT) {
+                exp2_both(l0 - mid, ev.x, bv.x);
+                exp2_both(l1 - mid, ev.y, bv.y);
+                *reinterpret_cast<float2 *>(s->factor[kB] + 2 * lane) = bv;
+            }
             *reinterpret_cast<float2 *>(s->factor[kW] + 2 * lane) =
                 make_float2(exp2_single(end - l0), exp2_single(end - l1));
             if (OUT) {
-                float2 ev = make_float2(exp2_single(l0 - mid), exp2_single(l1 - mid));
                 if (any) {
                     const uint32_t upto = 0xffffffffu >> (31 - lane);
                     if ((bad0 & upto) || (bad1 & (upto >> 1))) ev.x = nanf;
@@ -511,7 +527,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 total = 0;
                 total_nan = false;
             }
-            // (2^28 units either way are as good as any more, and many rows of 4096 may not wrap around)
+            // (2^20 units either way are as good as any more, and many rows of 4096 may not wrap around)
             total = max(min(total + end, 1LL << 60), -(1LL << 60));
             total_nan |= any;
             const rec::Pair d = exp2_fixed(end);
