@@ -799,8 +799,8 @@ typedef enum tv_rope {
  *   q_out, k_out   rows with strides of their own; q_out may be q and k_out k (in place, with
  *               the same stride), they must not overlap the inputs otherwise
  * Rows outside every request (behind the last one's) are left as they are.
- * Arithmetic: fp32, rounded once; the angle's turns are a 64-bit fixed-point product, so
- * far positions lose nothing.
+ * Arithmetic: fp32, rounded once (a row whose squares would leave fp32 is scaled by a power of two
+ * first); the angle's turns are a 64-bit fixed-point product, so far positions lose nothing.
  * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for sizes, strides and eps
  * out of range; TV_ERR_DTYPE for dtype and layout; TV_ERR_UNSUPPORTED for other d and
  * H + Hkv >= 2^23.

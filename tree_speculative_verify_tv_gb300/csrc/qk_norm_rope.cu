@@ -107,6 +107,22 @@ __device__ __forceinline__ float inv_sqrt(float x) {
     return x < 3.0e38f ? y * fmaf(-0.5f * x * y, y, 1.5f) : y;
 }
 
+// Means of squares outside of these come from values whose squares, or their sum, may have left
+// single precision.  Such a head's row is left out and done again, times a power of two.
+constexpr float kLeast = 1.0e-30f, kMost = 3.0e38f;
+constexpr float kShrink = 8.271806125530277e-25f, kGrow = 1.2676506002282294e30f;  // 2^-80, 2^100
+
+// The sum of squares of a row of D channels, eight of them in this lane.
+template <int D>
+__device__ __forceinline__ float square_sum(const Two (&x)[2], const Two (&y)[2]) {
+    const float2 q =
+        halves(fma2(x[0], x[0], fma2(x[1], x[1], fma2(y[0], y[0], mul2(y[1], y[1])))));
+    float sum = q.x + q.y;
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
 // A projection's weights with the rotation, for a lane's two quads (x: the first, y: the second).
 struct Turned {
     Two xc[2], xs[2], yc[2], ys[2];
@@ -206,60 +222,86 @@ __global__ void __launch_bounds__(kThreadsR, kPerSm<E>)
             in += cA;
             out += cA;
             const int over = cB - cA;
-            const auto some = [&](auto count) {
+            // a normed row rotated and stored
+            const auto put = [&](Two (&x)[2], Two (&y)[2], E *to) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const Two p = x[e], r = y[e];
+                    if (!turned) {
+                        x[e] = mul2(p, f.xc[e]);
+                        y[e] = mul2(r, f.yc[e]);
+                    } else if (PAIRS) {
+                        x[e] = fma2(p, f.xc[e], mul2(swap(p), f.xs[e]));
+                        y[e] = fma2(r, f.yc[e], mul2(swap(r), f.ys[e]));
+                    } else {
+                        x[e] = fma2(p, f.xc[e], mul2(r, f.ys[e]));
+                        y[e] = fma2(r, f.yc[e], mul2(p, f.xs[e]));
+                    }
+                }
+                Q o;
+                o.set(x);
+                *reinterpret_cast<Q *>(to) = o;
+                o.set(y);
+                *reinterpret_cast<Q *>(to + over) = o;
+            };
+            uint32_t again = 0;  // heads (fewer than 32 in an item) left out
+            const auto some = [&](auto count, int h) {
                 constexpr int kCount = decltype(count)::value;
                 Q A[kCount], B[kCount];
 #pragma unroll
                 for (int u = 0; u < kCount; ++u) {
-                    A[u] = *reinterpret_cast<const Q *>(in + u * D);
-                    B[u] = *reinterpret_cast<const Q *>(in + u * D + over);
+                    A[u] = *reinterpret_cast<const Q *>(in + (h + u) * D);
+                    B[u] = *reinterpret_cast<const Q *>(in + (h + u) * D + over);
                 }
 #pragma unroll
                 for (int u = 0; u < kCount; ++u) {
                     Two x[2], y[2];
                     A[u].get(x);
                     B[u].get(y);
-                    Two inv = two(1.f, 1.f);
+                    bool fits = true;
                     if (norm) {
-                        const float2 q = halves(
-                            fma2(x[0], x[0], fma2(x[1], x[1], fma2(y[0], y[0], mul2(y[1], y[1])))));
-                        float sum = q.x + q.y;
+                        const float mean = fmaf(square_sum<D>(x, y), 1.f / D, a.eps);
+                        fits = mean >= kLeast && mean <= kMost;
+                        if (!fits) again |= 1u << (h + u);
+                        const float i = inv_sqrt(mean);
+                        const Two inv = two(i, i);
 #pragma unroll
-                        for (int o = kLanes / 2; o > 0; o >>= 1)
-                            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                        const float i = inv_sqrt(fmaf(sum, 1.f / D, a.eps));
-                        inv = two(i, i);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const Two p = mul2(x[e], inv), r = mul2(y[e], inv);
-                        if (!turned) {
-                            x[e] = mul2(p, f.xc[e]);
-                            y[e] = mul2(r, f.yc[e]);
-                        } else if (PAIRS) {
-                            x[e] = fma2(p, f.xc[e], mul2(swap(p), f.xs[e]));
-                            y[e] = fma2(r, f.yc[e], mul2(swap(r), f.ys[e]));
-                        } else {
-                            x[e] = fma2(p, f.xc[e], mul2(r, f.ys[e]));
-                            y[e] = fma2(r, f.yc[e], mul2(p, f.xs[e]));
+                        for (int e = 0; e < 2; ++e) {
+                            x[e] = mul2(x[e], inv);
+                            y[e] = mul2(y[e], inv);
                         }
                     }
-                    if (live) {
-                        Q o;
-                        o.set(x);
-                        *reinterpret_cast<Q *>(out + u * D) = o;
-                        o.set(y);
-                        *reinterpret_cast<Q *>(out + u * D + over) = o;
-                    }
+                    if (live && fits) put(x, y, out + (h + u) * D);
                 }
-                in += kCount * D;
-                out += kCount * D;
             };
             int h = 0;
 #pragma unroll 1
-            for (; h + kUnroll <= n; h += kUnroll) some(std::integral_constant<int, kUnroll>());
+            for (; h + kUnroll <= n; h += kUnroll) some(std::integral_constant<int, kUnroll>(), h);
 #pragma unroll 1
-            for (; h < n; ++h) some(std::integral_constant<int, 1>());
+            for (; h < n; ++h) some(std::integral_constant<int, 1>(), h);
+            // (rows of one warp may differ in what is left; in place, what is done is not read again)
+            for (uint32_t rest = __reduce_or_sync(0xffffffffu, again); rest; rest &= rest - 1) {
+                const int at = __ffs(rest) - 1;
+                Two x[2], y[2];
+                reinterpret_cast<const Q *>(in + at * D)->get(x);
+                reinterpret_cast<const Q *>(in + at * D + over)->get(y);
+                const float mean = fmaf(square_sum<D>(x, y), 1.f / D, a.eps);
+                const float scale = mean < kLeast ? kGrow : kShrink;
+                const Two s2 = two(scale, scale);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[e] = mul2(x[e], s2);
+                    y[e] = mul2(y[e], s2);
+                }
+                const float i = inv_sqrt(fmaf(square_sum<D>(x, y), 1.f / D, a.eps * scale * scale));
+                const Two inv = two(i, i);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[e] = mul2(x[e], inv);
+                    y[e] = mul2(y[e], inv);
+                }
+                if (live && (again >> at & 1)) put(x, y, out + at * D);
+            }
         };
         if (h0 < a.H)
             project(static_cast<const E *>(a.q) + (size_t)row * a.q_stride + (size_t)h0 * D,
