@@ -1015,9 +1015,12 @@ long long most_chunks(const PrefillArgs &a) {
 }
 
 // Pieces that a request of that length is cut into: what makes the longest SM's work least,
-// counted in chunks.  A segment costs a few chunks to start, and its first launch half of what a
-// chunk costs (1.1 against 2.3 us at 128 x 128).  One prompt of 32768 rows and 32 heads, at an
-// earlier step: 466 us in 4 pieces, 433 in 9 (taken), 432 in 14, 463 in 28.
+// counted in chunks.  A segment costs a few chunks to start, and its first launch 0.6 of what a
+// chunk costs (with 0.5, which is what full SMs take, few and long segments look too cheap).
+// One prompt of 32768 rows and 32 heads of 128 x 128, at an earlier step: 466 us in 4 pieces, 433
+// in 9 (taken), 432 in 14, 463 in 28.  Two of 16384, bf16 outputs, in 7 pieces (taken) and in 2 (by
+// 0.5): 412 and 456 us, 128 x 64 324 and 364, 64 x 128 330 and 372, 64 x 64 294 and 344.  64 heads of
+// 4096 rows uncut (taken) and in 2: 144 and 138, 105 and 114, 105 and 113, 98 and 104.
 int best_pieces(const PrefillArgs &a) {
     const long long units = (long long)a.B * a.H, sms = device_sms(), chunks = most_chunks(a);
     if (units > 8 * sms) return 1;
@@ -1027,7 +1030,7 @@ int best_pieces(const PrefillArgs &a) {
     for (int s = 2; s <= 64 && s <= chunks; ++s) {
         const double per = (double)((chunks + s - 1) / s);
         const double cost =
-            waves(units * s) * (per + 4.0) + waves(units * (s - 1)) * (0.5 * per + 4.0) + 8.0;
+            waves(units * s) * (per + 4.0) + waves(units * (s - 1)) * (0.6 * per + 4.0) + 8.0;
         if (cost < 0.95 * least) {
             least = cost;
             best = s;
