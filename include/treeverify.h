@@ -721,6 +721,12 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
  * (2^-40; a row's g counts as at most 4096 log2 units), weights and states as two (bf16 outputs) or
  * three (fp32) bf16 parts, what is added to the state as three; factors within a chunk from the
  * hardware's exponential (2^-22).  Other cases: the recurrence row by row on CUDA cores.
+ * Range on tensor cores: within a chunk, weights and states are carried times up to 2^(s/2) and
+ * 2^(-s/2), s being the log2 units that the sums of its decays span (at most 120: it ends where
+ * they would span more).  Where they span s, a row's sum of q k v, over channels and rows, has to
+ * stay below 2^(127 - s/2) (2^67 at worst), and q . k and elements of a state below 2^(s/2 - 102)
+ * (2^-42 at worst) lose low bits, as does what a row adds to the state if it has fallen below 2^-102
+ * at the chunk's end.  Row by row there are fp32's limits alone.
  * NaN and infinity in a request's rows stay in that request and head, and those of v in their
  * column (on tensor cores they may reach its outputs of up to 63 rows ahead of theirs: a chunk's).
  * Infinite elements of a state stay infinite under decays above 0 (exp g in fp32, a segment's where
