@@ -801,12 +801,13 @@ typedef enum tv_rope {
  *               are >= heads * d and multiples of 8
  *   q_weight, k_weight   [d], or NULL for ones
  *   eps         >= 0 and finite; negative: no norm (rows are only rotated, weights not read)
- *   inv_freq    [rotary_dim / 2] fp64 (device): radians per position, finite
+ *   inv_freq    [rotary_dim / 2] fp64 (device): radians per position, of magnitude below 2^32
  *   q_out, k_out   rows with strides of their own; q_out may be q and k_out k (in place, with
  *               the same stride), they must not overlap the inputs otherwise
  * Rows outside every request (behind the last one's) are left as they are.
  * Arithmetic: fp32, rounded once (a row whose squares would leave fp32 is scaled by a power of two
- * first); the angle's turns are a 64-bit fixed-point product, so far positions lose nothing.
+ * first); an angle of t rad, before whole turns are left out, is off by 2^-52 |t| (2^-21 at 2^31 rad)
+ * and by its fraction's rounding.
  * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for sizes, strides and eps
  * out of range; TV_ERR_DTYPE for dtype and layout; TV_ERR_UNSUPPORTED for other d and
  * H + Hkv >= 2^23.

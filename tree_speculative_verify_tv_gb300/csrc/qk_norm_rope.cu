@@ -12,9 +12,10 @@
 // square and its conversions.
 //
 // Angles: t / 2 pi = position * f, f = inv_freq / 2 pi.  Only the fraction of the turns counts,
-// so f is held as a 64-bit fraction and the product is taken modulo 2^64: exact, whatever the
-// position.  The nearest quarter turn is taken off before the rest (at most 1/8 turn) becomes
-// a float.
+// so f is held as a 64-bit fraction and the product is taken modulo 2^64, which is exact.  f itself is
+// a double's: off by 2^-52 of itself, so an angle of t rad by 2^-52 t (2^-21 at 2^31 rad; f as two
+// doubles is better by that and takes 0.15 us more of a call of 4).  The nearest quarter turn is
+// taken off before the rest (at most 1/8 turn) becomes a float.
 #include <algorithm>
 #include <type_traits>
 
