@@ -729,9 +729,9 @@ tv_status tv_qcache_attention(int32_t B, int32_t total_nodes, int32_t max_nodes,
  * at the chunk's end.  Row by row there are fp32's limits alone.
  * NaN and infinity in a request's rows stay in that request and head, and those of v in their
  * column (on tensor cores they may reach its outputs of up to 63 rows ahead of theirs: a chunk's).
- * Infinite elements of a state stay infinite under decays above 0 (exp g in fp32, a segment's where
- * the prompt is cut); outputs of their column are infinite or NaN.  A decay of 2^128 and more makes
- * infinity of every element but 0, and NaN of that.
+ * Infinite elements of a state stay infinite under decays above 0 in fp32 (a row's, on tensor cores
+ * a chunk's or, where the prompt is cut, a segment's; else NaN); outputs of their column are infinite
+ * or NaN.  A decay of 2^128 and more makes infinity of every element but 0, and NaN of that.
  * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for
  * sizes and strides out of range (total_rows > B * max_rows too); TV_ERR_DTYPE;
  * TV_ERR_UNSUPPORTED for dk or dv > TV_MAX_DIM, total_rows > 0x7fff0000 and B * H >= 2^31.
@@ -850,7 +850,7 @@ tv_status tv_qk_norm_rope(int32_t B, int32_t total_rows, int32_t H, int32_t Hkv,
  * Logits of -inf (forbidden tokens) have probability 0 and log probability -inf.  In a row
  * with nothing else every log probability is -inf and the entropy 0; in a row with a NaN
  * or +inf all of them and the entropy are NaN (top_token is still in order).
- * Arithmetic: fp32 sums and exponentials; top_token is exact.
+ * Arithmetic: fp32 sums and exponentials (the hardware's, 2^-22); top_token is exact.
  * Host errors: TV_ERR_NULL, TV_ERR_ALIGN as usual; TV_ERR_SHAPE for sizes, row_stride and
  * scale out of range; TV_ERR_DTYPE; TV_ERR_UNSUPPORTED for top_k > TV_LOGPROBS_MAX_TOP.
  * Device-detected errors: a row >= num_rows or a token >= vocab gives TV_ERR_SHAPE, and what

@@ -8,8 +8,8 @@
 // column, each with 4 ceil(dk / 32) rows of the state in registers; blocks of kRows rows of
 // q, k, v land in shared memory by asynchronous copies a block ahead.  A pair of the state takes
 // four packed instructions (one for the decay's second part) against dk-sized loads: instructions
-// bound it.  8000 fp32 rows of 24 heads, 128 x 128: 725 us with two columns a thread, 64 x 64: 260;
-// with a decay per channel 1371.
+// bound it.  8000 fp32 rows of 24 heads, 128 x 128: 727 us with two columns a thread, 64 x 64: 260;
+// with a decay per channel 1375.
 #include "recurrence.cuh"
 #include "tc_ptx.cuh"
 

@@ -37,8 +37,8 @@
 // chunk.
 //
 // What bounds it.  That chain: D's product, its sums into H, the next D.  16 prompts of 4096 rows, 24
-// heads of 128 x 64, bf16 outputs: 300 us for 1.23 GB (181 us at the copy bandwidth); one of 32768
-// rows, 32 heads of 128 x 128: 394 us, about 125 of them for the segments' sums (1.1 us a chunk), 5
+// heads of 128 x 64, bf16 outputs: 307 us for 1.23 GB (181 us at the copy bandwidth); one of 32768
+// rows, 32 heads of 128 x 128: 398 us, about 125 of them for the segments' sums (1.1 us a chunk), 5
 // for their chain, 265 for the outputs (2.3 us a chunk).  Without conversions and most products a
 // chunk still takes three quarters of that, so neither tensor cores (50 to 69 % busy) nor issue slots
 // (51 to 58 %) are the limit, but signals from role to role.  Tried and not faster: H in eight warps

@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kThreadsR = 256;
 constexpr int kUnroll = 4;   // heads whose loads are in flight together
-// CTAs per SM that registers are kept to: three (78 registers a thread) for bf16, two for fp32.
+// CTAs per SM that registers are kept to: three (80 registers a thread) for bf16, two for fp32.
 // 32768 bf16 rows of 40 heads: 113 us, with four 121 (spills), with two 134.
 template <typename E>
 constexpr int kPerSm = sizeof(E) == 2 ? 3 : 2;
@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kThreadsR, kPerSm<E>)
 template <typename E, int D, bool PAIRS>
 cudaError_t launch(const RopeArgs &a, cudaStream_t s) {
     // Heads per item: about twenty where the rows alone fill the SMs twice, so that an angle serves
-    // many; down to four where rows are few, so that their heads spread over the SMs.
+    // many; down to four where rows are few, so that their heads spread over the SMs.  29 at most: the
+    // kernel has a bit for each.
     const long long heads = (long long)a.H + a.Hkv, warps = kThreadsR / 32;
     const long long rows = (a.R + 256 / D - 1LL) / (256 / D);
     const long long resident = device_sms() * kPerSm<E> * warps;
